@@ -33,6 +33,8 @@ __all__ = [
     "ERRF_SLOT_RANGE", "ERRF_BLOCK_RANGE", "ERRF_CONTEXT_RANGE",
     "CODES_E4M3", "CODES_E5M2", "quantize_scatter_unscaled", "paged_decode_codes",
     "paged_decode_codes_workspace_size",
+    "ERRF_POSITION_RANGE", "ERRF_SEQUENCE_RANGE", "ROPE_HALVES", "ROPE_INTERLEAVED",
+    "rope_quantize_scatter", "prompt_attention",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +50,11 @@ CODES_E5M2 = 1
 ERRF_SLOT_RANGE = 1
 ERRF_BLOCK_RANGE = 2
 ERRF_CONTEXT_RANGE = 4
+ERRF_POSITION_RANGE = 16
+ERRF_SEQUENCE_RANGE = 32
+
+ROPE_HALVES = 0
+ROPE_INTERLEAVED = 1
 
 _STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARGUMENT", 2: "KVQ_ERR_UNSUPPORTED",
            3: "KVQ_ERR_MISALIGNED", 4: "KVQ_ERR_WORKSPACE_TOO_SMALL", 5: "KVQ_ERR_CUDA"}
@@ -97,6 +104,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "kvq_abi_version": (i32, []),
             "kvq_cache_bytes": (sz, [i64, i32, i32]),
             "kvq_quantize_scatter": (ctypes.c_int, [CP, P, i64, P, i64, i64, P, P, P]),
+            "kvq_rope_quantize_scatter": (ctypes.c_int, [CP, P, i64, i32, P, i64, P, i64, i64, P,
+                                                         P, i64, i32, i32, P, P, i64, P, i64, P,
+                                                         P]),
+            "kvq_prompt_attention": (ctypes.c_int, [P, i64, P, i64, P, i64, i64, P, i32, i32, i32,
+                                                    i32, i32, ctypes.c_float, P, i64, P, P]),
             "kvq_paged_decode_partition_tokens": (i32, [i32, i32, i32, i32, i32, i32]),
             "kvq_paged_decode_workspace_size": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
             "kvq_paged_decode": (ctypes.c_int, [CP, P, i32, i32, i32, P, i32, P, i32,
@@ -238,6 +250,111 @@ def quantize_scatter(cache: Cache, k: torch.Tensor, v: torch.Tensor, slot_ids: t
     _check(load().kvq_quantize_scatter(ctypes.byref(st), _ptr(k), ks, _ptr(v), vs, T,
                                        _ptr(slot_ids), _ptr(err_flags), _stream(stream)),
            "kvq_quantize_scatter")
+
+
+def _on_device(device: torch.device, **tensors) -> None:
+    """Every tensor given is on ``device``, the current CUDA device: a pointer
+    of another device or of the host would fault in the kernel."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors must be on the current CUDA device, not on {device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _heads_view(x: torch.Tensor, name: str) -> int:
+    """Token stride (elements) of a [T, heads, D] bf16 view whose rows are
+    contiguous within a token (of one token: the stride it would have)."""
+    if x.dtype != torch.bfloat16 or x.dim() != 3:
+        raise ValueError(f"{name} must be a bfloat16 [T, heads, head_dim] view")
+    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2])):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def _check_flags(err_flags) -> None:
+    if err_flags is not None and (err_flags.dtype != torch.int32 or err_flags.numel() < 1):
+        raise ValueError("err_flags must be an int32 tensor of one element")
+
+
+def rope_quantize_scatter(cache: Cache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                          positions: torch.Tensor, rope_table: torch.Tensor,
+                          slot_ids: torch.Tensor, layout: int = ROPE_HALVES,
+                          q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                          err_flags: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor | None:
+    """kvq_rope_quantize_scatter: rotate query rows [T, Hq, D] and key rows
+    [T, H, D] by their int64 ``positions`` in ``rope_table`` (fp32 [P, rotary_dim]:
+    cosines, then sines) and quantise the rotated keys and the values into
+    ``cache`` at int64 ``slot_ids``.  The rotated queries go to ``q_out`` (may be
+    ``q`` itself; allocated here, by PyTorch, when not given), the rotated keys
+    also to ``k_out`` where given (may be ``k``).  Rows of skipped tokens
+    (slot id < 0) are not written.  Returns ``q_out`` (None without ``q``)."""
+    H, D, T = cache.num_kv_heads, cache.head_dim, k.shape[0]
+    for name, x in (("k", k), ("v", v), ("k_out", k_out)):
+        if x is not None and (x.dim() != 3 or tuple(x.shape) != (T, H, D)):
+            raise ValueError(f"{name}: expected [{T}, {H}, {D}]")
+    ks, vs = _heads_view(k, "k"), _heads_view(v, "v")
+    kos = 0 if k_out is None else _heads_view(k_out, "k_out")
+    for name, x in (("positions", positions), ("slot_ids", slot_ids)):
+        if x.dtype != torch.int64 or x.numel() != T or not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous int64 with one entry per token")
+    if rope_table.dtype != torch.float32 or rope_table.dim() != 2 or \
+            not rope_table.is_contiguous():
+        raise ValueError("rope_table must be contiguous fp32 [positions, rotary_dim]")
+    qs = qos = hq = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D:
+            raise ValueError(f"q: expected [{T}, num_q_heads, {D}]")
+        hq, qs = q.shape[1], _heads_view(q, "q")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        qos = _heads_view(q_out, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check_flags(err_flags)
+    _on_device(k.device, q=q, v=v, positions=positions, rope_table=rope_table, slot_ids=slot_ids,
+               q_out=q_out, k_out=k_out, err_flags=err_flags, k_codes=cache.k_codes,
+               v_codes=cache.v_codes, k_scales=cache.k_scales, v_scales=cache.v_scales)
+    st = cache.struct()
+    _check(load().kvq_rope_quantize_scatter(
+        ctypes.byref(st), _ptr(q), qs, hq, _ptr(k), ks, _ptr(v), vs, T, _ptr(positions),
+        _ptr(rope_table), rope_table.shape[0], rope_table.shape[1], layout, _ptr(slot_ids),
+        _ptr(q_out), qos, _ptr(k_out), kos, _ptr(err_flags), _stream(stream)),
+        "kvq_rope_quantize_scatter")
+    return q_out
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     max_seqlen: int, sm_scale: float, out: torch.Tensor | None = None,
+                     err_flags: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvq_prompt_attention: causal attention of packed prompts -- bf16 queries
+    [T, Hq, D] over keys and values [T, H, D] (views with their own token
+    strides), sequence s holding the tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1
+    (int32, on the device).  Returns ``out`` (bf16, shape of q; allocated here,
+    by PyTorch, when not given).  Rows outside the sequences are not written."""
+    qs, ks, vs = _heads_view(q, "q"), _heads_view(k, "k"), _heads_view(v, "v")
+    T, Hq, D = q.shape
+    H = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != D or v.shape != k.shape:
+        raise ValueError("k and v must be [T, num_kv_heads, head_dim] with q's T and head_dim")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or \
+            not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous int32 [num_seqs + 1]")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    os_ = _heads_view(out, "out")
+    _check_flags(err_flags)
+    _on_device(q.device, k=k, v=v, cu_seqlens=cu_seqlens, out=out, err_flags=err_flags)
+    _check(load().kvq_prompt_attention(
+        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, T, _ptr(cu_seqlens), cu_seqlens.numel() - 1,
+        max_seqlen, Hq, H, D, float(sm_scale), _ptr(out), os_, _ptr(err_flags), _stream(stream)),
+        "kvq_prompt_attention")
+    return out
 
 
 def paged_decode_partition_tokens(num_requests: int, rows_per_request: int, num_q_heads: int,

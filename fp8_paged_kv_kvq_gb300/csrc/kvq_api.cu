@@ -242,6 +242,56 @@ kvq_status kvq_quantize_scatter(const kvq_cache *cache, const void *k, int64_t k
                                                 reinterpret_cast<cudaStream_t>(stream)));
 }
 
+kvq_status kvq_rope_quantize_scatter(
+    const kvq_cache *cache, const void *q, int64_t q_token_stride, int32_t num_q_heads,
+    const void *k, int64_t k_token_stride, const void *v, int64_t v_token_stride,
+    int64_t num_tokens, const int64_t *positions, const float *rope_table, int64_t num_positions,
+    int32_t rotary_dim, int32_t rope_layout, const int64_t *slot_ids, void *q_out,
+    int64_t q_out_token_stride, void *k_out, int64_t k_out_token_stride, int32_t *err_flags,
+    kvq_stream_t stream) {
+  kvq_status st = check_cache(cache, false);
+  if (st != KVQ_OK) return st;
+  if (num_tokens < 0 || num_q_heads < 0 || num_positions < 0 || q_token_stride < 0 ||
+      k_token_stride < 0 || v_token_stride < 0 || q_out_token_stride < 0 ||
+      k_out_token_stride < 0)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (rope_layout != KVQ_ROPE_HALVES && rope_layout != KVQ_ROPE_INTERLEAVED)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (rotary_dim <= 0 || rotary_dim > cache->head_dim) return KVQ_ERR_INVALID_ARGUMENT;
+  if (rotary_dim % 16 != 0) return KVQ_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return KVQ_OK;
+  if (k == nullptr || v == nullptr || positions == nullptr || slot_ids == nullptr ||
+      (rope_table == nullptr && num_positions > 0))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if ((num_q_heads > 0) != (q != nullptr) || (num_q_heads > 0) != (q_out != nullptr))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(k_out, 16) || !aligned(rope_table, 16) || q_token_stride % 8 != 0 ||
+      k_token_stride % 8 != 0 || v_token_stride % 8 != 0 || q_out_token_stride % 8 != 0 ||
+      k_out_token_stride % 8 != 0 || !aligned(positions, 8) || !aligned(slot_ids, 8) ||
+      !aligned(err_flags, 4))
+    return KVQ_ERR_MISALIGNED;
+  // output rows of different tokens must not share memory, and a rotation in
+  // place keeps each row where it is read
+  const int64_t qw = static_cast<int64_t>(num_q_heads) * cache->head_dim;
+  const int64_t kw = static_cast<int64_t>(cache->num_kv_heads) * cache->head_dim;
+  if (num_tokens > 1 && ((q != nullptr && q_out_token_stride < qw) ||
+                         (k_out != nullptr && k_out_token_stride < kw)))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_tokens > 1 && ((q != nullptr && q_out == q && q_out_token_stride != q_token_stride) ||
+                         (k_out != nullptr && k_out == k && k_out_token_stride != k_token_stride)))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  // rows (token, query / key / value head) are numbered in 32 bits
+  const int64_t per_token = static_cast<int64_t>(num_q_heads) + 2 * int64_t(cache->num_kv_heads);
+  if (per_token > (1 << 20) || num_tokens > (int64_t(1) << 31) / per_token - 32)
+    return KVQ_ERR_UNSUPPORTED;
+  const kvq::RopeArgs a{q, q_token_stride, num_q_heads, k, k_token_stride, v, v_token_stride,
+                        num_tokens, positions, rope_table, num_positions, rotary_dim, rope_layout,
+                        slot_ids, q_out, q_out_token_stride, k_out, k_out_token_stride};
+  return from_cuda(kvq::launch_rope_quantize_scatter(*cache, a, err_flags,
+                                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int32_t kvq_paged_decode_partition_tokens(int32_t num_requests, int32_t rows_per_request,
                                           int32_t num_q_heads, int32_t num_kv_heads,
                                           int32_t block_size, int32_t max_context_len) {
@@ -507,6 +557,38 @@ kvq_status kvq_paged_decode_codes(const kvq_cache *cache, int32_t code_format, c
   return from_cuda(kvq::launch_attn_rows(*cache, s, q, block_tables, context_lens, sm_scale, out,
                                          workspace, err_flags,
                                          reinterpret_cast<cudaStream_t>(stream), code_format));
+}
+
+kvq_status kvq_prompt_attention(const void *q, int64_t q_token_stride, const void *k,
+                                int64_t k_token_stride, const void *v, int64_t v_token_stride,
+                                int64_t num_tokens, const int32_t *cu_seqlens, int32_t num_seqs,
+                                int32_t max_seqlen, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float sm_scale, void *out,
+                                int64_t out_token_stride, int32_t *err_flags,
+                                kvq_stream_t stream) {
+  if (num_tokens < 0 || num_seqs < 0 || max_seqlen < 0 || num_q_heads < 1 || num_kv_heads < 1 ||
+      head_dim < 1 || num_q_heads % num_kv_heads != 0)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(sm_scale) || sm_scale <= 0.0f) return KVQ_ERR_INVALID_ARGUMENT;
+  if (head_dim != kvq::kHeadDimAbi || num_q_heads / num_kv_heads > kvq::kPromptMaxGroup ||
+      num_tokens > 0x7FFFFFFF || num_seqs > 0x7FFFFFFE)
+    return KVQ_ERR_UNSUPPORTED;
+  const int64_t qw = static_cast<int64_t>(num_q_heads) * head_dim;
+  const int64_t kw = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q_token_stride < qw || out_token_stride < qw || k_token_stride < kw || v_token_stride < kw)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_tokens == 0 || num_seqs == 0) return KVQ_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || out == nullptr || cu_seqlens == nullptr)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+      q_token_stride % 8 != 0 || k_token_stride % 8 != 0 || v_token_stride % 8 != 0 ||
+      out_token_stride % 8 != 0 || !aligned(cu_seqlens, 4) || !aligned(err_flags, 4))
+    return KVQ_ERR_MISALIGNED;
+  const kvq::PromptArgs a{q, k, v, q_token_stride, k_token_stride, v_token_stride, num_tokens,
+                          cu_seqlens, num_seqs, max_seqlen, num_q_heads, num_kv_heads, sm_scale,
+                          out, out_token_stride, err_flags, current_sm_count()};
+  if (!kvq::prompt_attention_supported(a)) return KVQ_ERR_UNSUPPORTED;
+  return from_cuda(kvq::launch_prompt_attention(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kvq_status kvq_dequant_rows(const kvq_cache *cache, const int64_t *slot_ids, int64_t n,

@@ -115,6 +115,30 @@ cudaError_t launch_quantize_positions(const kvq_cache &c, const void *k, int64_t
                                      int32_t ctx_limit, int32_t log2_block, int32_t *err_flags,
                                      cudaStream_t stream);
 
+// The quantize-scatter with the rotary embedding on the way (kvq.h).
+struct RopeArgs {
+  const void *q;
+  int64_t q_stride;
+  int32_t num_q_heads;
+  const void *k;
+  int64_t k_stride;
+  const void *v;
+  int64_t v_stride;
+  int64_t num_tokens;
+  const int64_t *positions;
+  const float *table;
+  int64_t num_positions;
+  int32_t rotary_dim;
+  int32_t layout;
+  const int64_t *slot_ids;
+  void *q_out;
+  int64_t q_out_stride;
+  void *k_out;
+  int64_t k_out_stride;
+};
+cudaError_t launch_rope_quantize_scatter(const kvq_cache &c, const RopeArgs &a, int32_t *err_flags,
+                                         cudaStream_t stream);
+
 cudaError_t launch_dequant_rows(const kvq_cache &c, const int64_t *slot_ids, int64_t n,
                                 int32_t out_dtype, void *out_k, void *out_v,
                                 int32_t *err_flags, cudaStream_t stream);
@@ -188,6 +212,24 @@ cudaError_t launch_quantize_unscaled(const kvq_cache &c, int32_t code_format, co
                                      int64_t k_stride, const void *v, int64_t v_stride,
                                      int64_t num_tokens, const int64_t *slot_ids,
                                      int32_t *err_flags, cudaStream_t stream);
+
+// Causal attention of packed prompts over their own bf16 keys and values.
+struct PromptArgs {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;   // elements per token
+  int64_t num_tokens;
+  const int32_t *cu_seqlens;
+  int32_t num_seqs, max_seqlen, num_q_heads, num_kv_heads;
+  float sm_scale;
+  void *out;
+  int64_t out_stride;
+  int32_t *err_flags;
+  int32_t sms;
+};
+constexpr int32_t kPromptMaxGroup = 128;     // query heads per KV head
+// Whether the launch's units of work are numbered in 31 bits.
+bool prompt_attention_supported(const PromptArgs &a);
+cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream);
 
 // The tcgen05 partials kernel for 9..32 stacked rows per KV head.
 bool attn_tc_supported(const kvq_cache &c, const AttnShape &s);

@@ -88,6 +88,9 @@ typedef enum kvq_status {
                                             > max_blocks_per_req * block_size          */
 #define KVQ_ERRF_WAIT_TIMEOUT 8          /* a bounded in-kernel wait for an async copy
                                             gave up; that CTA's outputs are not written */
+#define KVQ_ERRF_POSITION_RANGE 16       /* token position outside the rotation table    */
+#define KVQ_ERRF_SEQUENCE_RANGE 32       /* a packed sequence's bounds decrease, leave the
+                                            token buffer or pass max_seqlen               */
 
 /* The cache: codes and scales always travel together (ATOM PR #2655,
  * "Motivation": a restore that drops the scale planes decodes rows under the
@@ -138,6 +141,52 @@ kvq_status kvq_quantize_scatter(const kvq_cache *cache,
                                 const void *v, int64_t v_token_stride,
                                 int64_t num_tokens, const int64_t *slot_ids,
                                 int32_t *err_flags, kvq_stream_t stream);
+
+/* Pairing of the rotated dims. */
+#define KVQ_ROPE_HALVES 0                /* dim i with dim i + rotary_dim / 2            */
+#define KVQ_ROPE_INTERLEAVED 1           /* dim 2i with dim 2i + 1                       */
+
+/* kvq_quantize_scatter with the rotary position embedding applied on the way
+ * (one launch, capturable): a step's query and key rows are rotated by their
+ * tokens' positions, the rotated keys and the values quantised into the cache.
+ * For token t at position p = positions[t], with c_i = rope_table[p][i] and
+ * s_i = rope_table[p][rotary_dim / 2 + i], i < rotary_dim / 2, each pair (a, b)
+ * of the row's first rotary_dim dims becomes
+ *     (fl(fl(a c_i) - fl(b s_i)), fl(fl(b c_i) + fl(a s_i)))
+ * in binary32 (six roundings, no contraction); the other dims pass through.
+ * The cache gets the row format of kvq_quantize_scatter from these binary32
+ * values -- they are not rounded to bf16 on the way; q_out and k_out get them
+ * rounded to bf16 (nearest-even).
+ *   q               device bf16, token t's row for query head h at element
+ *                   t*q_token_stride + h*head_dim; NULL with num_q_heads 0 to
+ *                   rotate and store keys only
+ *   k, v, strides   as for kvq_quantize_scatter
+ *   num_tokens      rows to store (0 launches nothing)
+ *   positions       device int64 [num_tokens]; one outside [0, num_positions)
+ *                   skips its token and sets KVQ_ERRF_POSITION_RANGE
+ *   rope_table      device fp32 [num_positions, rotary_dim], 16-byte aligned:
+ *                   each row rotary_dim / 2 cosines, then as many sines
+ *   rotary_dim      dims rotated: a multiple of 16 in [16, head_dim]
+ *   rope_layout     KVQ_ROPE_HALVES or KVQ_ROPE_INTERLEAVED
+ *   slot_ids        as for kvq_quantize_scatter; a skipped token (id < 0, or out
+ *                   of range with KVQ_ERRF_SLOT_RANGE) leaves its q_out and
+ *                   k_out rows as they were, and a negative id also leaves its
+ *                   position unread
+ *   q_out           device bf16 rows like q with their own token stride; may be
+ *                   q itself with q's stride (rotation in place); NULL iff q is
+ *   k_out           the same for k; NULL: the rotated keys go to the cache only
+ * Outputs that overlap inputs in any other way are not supported. */
+kvq_status kvq_rope_quantize_scatter(const kvq_cache *cache, const void *q,
+                                     int64_t q_token_stride, int32_t num_q_heads,
+                                     const void *k, int64_t k_token_stride,
+                                     const void *v, int64_t v_token_stride,
+                                     int64_t num_tokens, const int64_t *positions,
+                                     const float *rope_table, int64_t num_positions,
+                                     int32_t rotary_dim, int32_t rope_layout,
+                                     const int64_t *slot_ids, void *q_out,
+                                     int64_t q_out_token_stride, void *k_out,
+                                     int64_t k_out_token_stride, int32_t *err_flags,
+                                     kvq_stream_t stream);
 
 /* Tokens per split-K partition that kvq_paged_decode uses when passed 0 and
  * the shape takes a partitioned kernel: a power of two in [256, 8192] (up to
@@ -351,6 +400,46 @@ kvq_status kvq_paged_decode_codes(const kvq_cache *cache, int32_t code_format, c
                                   int32_t max_context_len, float sm_scale, void *out,
                                   void *workspace, size_t workspace_bytes, int32_t *err_flags,
                                   kvq_stream_t stream);
+
+/* Causal attention of whole prompts over their own keys and values, before
+ * anything of them is read from the cache: num_seqs sequences packed one after
+ * another in one token buffer.  Sequence s holds the tokens cu_seqlens[s] ..
+ * cu_seqlens[s + 1] - 1; with G = num_q_heads / num_kv_heads, token i of a
+ * sequence and query head hq (KV head hq / G)
+ *     out_i = sum_{j <= i} p_j v_j / sum_{j <= i} p_j,
+ *     p_j = exp(sm_scale (q_i . k_j - max_j q_i . k_j)),   j in its sequence.
+ * fp32 scores and sums; the probabilities are rounded to bf16 for the product
+ * with the values and not for the sum.  Tokens a row does not see do not reach
+ * it, whatever they hold (infinities and NaN included).
+ *   q               device bf16, token t's row for query head h at element
+ *                   t*q_token_stride + h*head_dim (a view of a fused qkv tensor,
+ *                   rotated); k and v the same with num_kv_heads heads
+ *   token strides   in elements, multiples of 8, >= heads * head_dim
+ *   num_tokens      rows of the token buffers
+ *   cu_seqlens      device int32 [num_seqs + 1], non-decreasing, in
+ *                   [0, num_tokens]; rows outside the sequences (in front, or
+ *                   padding behind the last) are left as they were in out.  A
+ *                   sequence that breaks this or is longer than max_seqlen is
+ *                   skipped and sets KVQ_ERRF_SEQUENCE_RANGE (the others'
+ *                   outputs are then unspecified, but every access stays in
+ *                   bounds)
+ *   max_seqlen      host bound on every sequence's length
+ *   num_q_heads     a multiple of num_kv_heads, at most 128 per KV head
+ *   head_dim        128
+ *   sm_scale        positive and finite
+ *   out             device bf16, rows like q with their own token stride; must
+ *                   not overlap q, k or v
+ *   err_flags       device int32, optional
+ * Needs no workspace. */
+kvq_status kvq_prompt_attention(const void *q, int64_t q_token_stride,
+                                const void *k, int64_t k_token_stride,
+                                const void *v, int64_t v_token_stride,
+                                int64_t num_tokens, const int32_t *cu_seqlens,
+                                int32_t num_seqs, int32_t max_seqlen,
+                                int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float sm_scale, void *out,
+                                int64_t out_token_stride, int32_t *err_flags,
+                                kvq_stream_t stream);
 
 /* Dequantise whole rows back to real values: out = fl32(e4m3(c) * scale), one
  * IEEE multiply, or that value rounded once more to bf16 (nearest-even).

@@ -1,0 +1,292 @@
+"""kvq_prompt_attention on the GPU against dense fp64 attention (oracle/prompt.py).
+
+Tolerance.  Of an output o = sum_j w_j v_j the kernel rounds: the output to
+bf16 (2^-8 |o|); every probability to bf16 for the product (2^-8 sum_j w_j |v_j|,
+the sum's denominator is not rounded); the score of 128 binary32 additions and
+its scaling, an absolute error of at most 130 2^-23 max_j sm_scale sum_d |q_d k_jd|
+=: e (one unit in the last place per addition, as the tensor cores may truncate),
+which moves numerator and denominator by a relative e each; the exponentials,
+2^-20 each; and the two sums of up to L terms, a unit in the last place per
+addition, L 2^-22 together.  In all
+    |err| <= 2^-8 |o| + (2^-8 + 2 e + 2^-19 + L 2^-22) sum_j w_j |v_j|."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_paged_kv_kvq_gb300 as kvq
+import oracle
+import oracle.prompt as plain
+import workloads
+from kvq_testlib import assert_attention_close
+
+pytestmark = pytest.mark.gpu
+SCALE = 128 ** -0.5
+
+
+def _inputs(T, hq, H, seed, spread=1.5):
+    """q, k, v [T, heads, 128] as views of one fused projection output on the GPU."""
+    g = workloads.generator(seed, 301)
+    qkv = torch.randn(T, (hq + 2 * H) * 128, generator=g)
+    qkv[:, :hq * 128] *= spread
+    qkv = qkv.to(torch.bfloat16).cuda()
+    return (qkv[:, :hq * 128].view(T, hq, 128), qkv[:, hq * 128:(hq + H) * 128].view(T, H, 128),
+            qkv[:, (hq + H) * 128:].view(T, H, 128))
+
+
+def _cu(lens, first=0):
+    return torch.tensor([first] + list(first + np.cumsum(lens)), dtype=torch.int32, device="cuda")
+
+
+def bound(ref, mag, dot, lens):
+    e = 130 * 2.0 ** -23 * dot
+    return 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * e + 2.0 ** -19 + max(lens) * 2.0 ** -22) * mag
+
+
+def assert_close(got, q, k, v, lens, scale=SCALE):
+    """Rows of the packed sequences (inputs already cut to them)."""
+    ref, mag, dot = plain.prompt_attention(q, k, v, lens, scale)
+    tol = bound(ref, mag, dot, lens)
+    err = (got.cpu().double() - ref).abs()
+    assert bool(torch.isfinite(got).all())
+    worst = float((err / tol.clamp(min=1e-300)).max()) if err.numel() else 0.0
+    print(f"worst |err| / bound {worst:.3f}")
+    assert worst <= 1.0
+
+
+def _run(lens, hq, H, seed, scale=SCALE, tail=0, first=0, spread=1.5, most=None):
+    T = first + int(sum(lens)) + tail
+    q, k, v = _inputs(T, hq, H, seed, spread)
+    out = torch.full((T, hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kvq.prompt_attention(q, k, v, _cu(lens, first), max(lens) if most is None else most, scale,
+                         out=out, err_flags=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    end = T - tail
+    assert torch.all(out[:first] == 7) and torch.all(out[end:] == 7)
+    assert_close(out[first:end], q[first:end], k[first:end], v[first:end], lens, scale)
+
+
+@pytest.mark.parametrize("lens", [
+    [1], [2], [63], [64], [65], [127], [128], [129], [255, 256, 257], [1, 1, 1, 1, 1],
+    [0, 5, 0, 0, 130, 0], [31, 32, 33, 383], [512, 1, 640], [1000],
+])
+@pytest.mark.parametrize("hq,H", [(32, 8), (3, 3), (7, 1)])
+def test_lengths(lens, hq, H):
+    _run(lens, hq, H, seed=sum(lens) + hq)
+
+
+@pytest.mark.parametrize("hq,H", [(1, 1), (2, 1), (6, 2), (10, 2), (12, 2), (14, 2), (16, 2), (9, 1),
+                                  (32, 2), (64, 1), (127, 1), (128, 1)])
+def test_head_groups(hq, H):
+    _run([200, 77, 300], hq, H, seed=hq)
+
+
+def test_longer_prompt():
+    _run([2333, 130], 8, 2, seed=4)
+
+
+def test_many_sequences():
+    """More sequences than one warp's search step covers, many empty ones among them."""
+    g = workloads.generator(6, 6)
+    lens = torch.randint(0, 12, (1500,), generator=g).tolist()
+    lens[700] = 300
+    _run(lens, 4, 2, seed=6)
+
+
+def test_rows_outside_the_sequences_stay():
+    _run([70, 0, 200], 16, 4, seed=7, tail=150, first=33)
+    _run([0, 0], 16, 4, seed=7, tail=9, most=0)
+
+
+@pytest.mark.parametrize("scale,spread", [(SCALE, 12.0), (1.0, 1.0), (1e-6, 1.0)])
+def test_score_ranges(scale, spread):
+    """Peaked rows (one probability near 1), and rows of nearly equal scores."""
+    _run([400, 150], 8, 2, seed=9, scale=scale, spread=spread)
+
+
+def test_climbing_and_falling_scores():
+    """Scores that rise (fall) by many powers of two along the keys, so that running maxima move
+    again and again (or never)."""
+    hq, H, L = 8, 2, 700
+    q, k, v = _inputs(L, hq, H, seed=11)
+    q.copy_(torch.ones_like(q))
+    step = (torch.arange(L, device="cuda") / 3.0)[:, None, None]
+    for sign in (1.0, -1.0):
+        noise = torch.randn(L, H, 128, generator=workloads.generator(12, 1)).cuda()
+        k.copy_((sign * step / 128 / SCALE + 0.05 * noise).to(torch.bfloat16))
+        out = kvq.prompt_attention(q, k, v, _cu([L]), L, SCALE)
+        torch.cuda.synchronize()
+        assert_close(out, q, k, v, [L])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("hq,H", [(8, 2), (2, 2)])
+def test_unseen_infinities_and_nans_do_not_reach_a_row(bad, hq, H):
+    """Keys and values of later tokens, of the next sequence and of the padding are infinite or
+    NaN: rows before them are exact, rows that see an infinite value get it."""
+    lens, tail = [150, 300, 37], 20
+    T = sum(lens) + tail
+    q, k, v = _inputs(T, hq, H, seed=13)
+    clean_q, clean_k, clean_v = q.clone(), k.clone(), v.clone()
+    spots = [100, 149, 150 + 130, 150 + 299, 486]       # tokens, one or two of each sequence
+    v[spots, :, 3] = bad
+    k[spots, :, 64] = bad
+    q[spots] = 0                                       # (their own scores are NaN all the same)
+    k[487:], v[487:], q[487:] = bad, bad, bad
+    out = kvq.prompt_attention(q, k, v, _cu(lens), 300, SCALE)
+    torch.cuda.synchronize()
+    ref, mag, dot = plain.prompt_attention(clean_q, clean_k, clean_v, lens + [0], SCALE)
+    tol = bound(ref, mag, dot, lens)
+    clean = torch.zeros(T, dtype=torch.bool)
+    clean[:100] = clean[150:280] = clean[450:486] = True
+    err = (out.cpu().double() - ref).abs()
+    assert bool(torch.isfinite(out[clean.cuda()]).all())
+    assert bool((err <= tol)[clean].all())
+
+
+def test_seen_infinite_values():
+    """Infinite and NaN values with finite keys: rows that see one have it in that dim (infinities
+    of both signs: NaN), every other element is the finite sum."""
+    lens = [333, 70]
+    T = sum(lens)
+    q, k, v = _inputs(T, 8, 2, seed=14)
+    clean = v.clone()
+    inf, nan = float("inf"), float("nan")
+    for tok, dim, x in ((10, 5, inf), (140, 6, -inf), (300, 5, -inf), (200, 7, nan), (332, 8, inf),
+                        (333, 9, nan), (400, 5, inf)):
+        v[tok, :, dim] = x
+        clean[tok, :, dim] = 0.0
+    out = kvq.prompt_attention(q, k, v, _cu(lens), 333, SCALE)
+    torch.cuda.synchronize()
+    ref, mag, dot = plain.prompt_attention(q, k, clean, lens, SCALE)
+    tol = bound(ref, mag, dot, lens)
+    want = ref.clone()
+    for tok, dim, x in ((10, 5, inf), (140, 6, -inf), (300, 5, -inf), (200, 7, nan), (332, 8, inf),
+                        (333, 9, nan), (400, 5, inf)):
+        want[tok:(333 if tok < 333 else T), :, dim] += x
+    got = out.cpu().double()
+    fin = torch.isfinite(want)
+    assert bool((((got - want).abs() <= tol) | ~fin).all())
+    assert bool((got[~fin].isnan() == want[~fin].isnan()).all())
+    both = ~fin & ~want.isnan()
+    assert bool((got[both] == want[both]).all())
+
+
+@pytest.mark.parametrize("cu,most", [
+    ([0, 50, 40, 100], 64),           # decreasing
+    ([0, 30, 60, 101], 64),           # past the buffer
+    ([-5, 30, 60, 100], 64),          # in front of it
+    ([0, 30, 100, 100], 64),          # longer than max_seqlen
+    ([0, 2_000_000_000, -2_000_000_000, 100], 2_000_000_000),
+    ([0, 30, 60, 100], 0),
+])
+def test_bad_bounds_are_flagged_and_stay_in_the_buffers(cu, most):
+    """Every access is checked against the buffers (shown by the kernel's own bounds checks); rows
+    of other tensors around them stay as they were."""
+    T, hq, H = 100, 8, 2
+    q, k, v = _inputs(T, hq, H, seed=15)
+    guard = torch.full((T + 400, hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = guard[200:200 + T]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kvq.prompt_attention(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"), most, SCALE,
+                         out=out, err_flags=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == kvq.ERRF_SEQUENCE_RANGE
+    assert torch.all(guard[:200] == 7) and torch.all(guard[200 + T:] == 7)
+
+
+def test_offsets_past_32_bits():
+    """A token buffer of more than 2^31 elements, the sequences at its end."""
+    hq, H, T = 32, 8, 360_000
+    qkv = torch.zeros(T, (hq + 2 * H) * 128, dtype=torch.bfloat16, device="cuda")
+    lens = [130, 300]
+    first = T - sum(lens)
+    g = workloads.generator(16, 1)
+    qkv[first:] = torch.randn(sum(lens), qkv.shape[1], generator=g).to(torch.bfloat16).cuda()
+    q = qkv[:, :hq * 128].view(T, hq, 128)
+    k = qkv[:, hq * 128:(hq + H) * 128].view(T, H, 128)
+    v = qkv[:, (hq + H) * 128:].view(T, H, 128)
+    out = torch.zeros(T, hq, 128, dtype=torch.bfloat16, device="cuda")
+    kvq.prompt_attention(q, k, v, _cu(lens, first), 300, SCALE, out=out)
+    torch.cuda.synchronize()
+    assert_close(out[first:], q[first:], k[first:], v[first:], lens)
+
+
+def test_captured_replayed_and_on_another_stream():
+    """A captured call replayed on new rows and other lengths below its bound; two streams at once."""
+    hq, H, T = 16, 4, 600
+    q, k, v = _inputs(T, hq, H, seed=17)
+    cu = _cu([100, 400])
+    out = torch.zeros(T, hq, 128, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        kvq.prompt_attention(q, k, v, cu, 500, SCALE, out=out)
+    for seed, lens in ((18, [500, 100]), (19, [3, 0]), (20, [255, 257])):
+        for x, y in zip((q, k, v), _inputs(T, hq, H, seed)):
+            x.copy_(y)
+        cu.copy_(_cu(lens))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        n = sum(lens)
+        assert torch.all(out[n:] == 7)
+        assert_close(out[:n], q[:n], k[:n], v[:n], lens)
+    other = torch.zeros_like(out)
+    out.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    kvq.prompt_attention(q, k, v, cu, 500, SCALE, out=other, stream=side)
+    kvq.prompt_attention(q, k, v, cu, 500, SCALE, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, other)                      # the same call gives the same bits
+    assert_close(out[:512], q[:512], k[:512], v[:512], [255, 257])
+
+
+def test_a_serving_step_of_both_operators():
+    """Prompts rotated in place and stored (kvq_rope_quantize_scatter), attended over
+    (kvq_prompt_attention), then one decode step of new tokens: rotated, stored, and attended over
+    the cache (kvq_paged_decode), each against the oracles."""
+    hq, H, bs = 16, 4, 16
+    lens = np.array([120, 33, 200], dtype=np.int32)
+    T, N = int(lens.sum()), len(lens)
+    q, k, v = _inputs(T, hq, H, seed=24)
+    qf, kf, vf = (x.float().cpu().numpy() for x in (q, k, v))
+    table = plain.rope_table(1024, 128)
+    bt, blocks = workloads.block_tables(lens + 1, bs, 3, spare_blocks=2)
+    slots = np.concatenate([workloads.token_slots(bt, r, int(L), bs) for r, L in enumerate(lens)])
+    pos = np.concatenate([np.arange(L) for L in lens])
+    cache = kvq.Cache.empty(blocks * bs, H, 128, bs)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()      # noqa: E731
+    kvq.rope_quantize_scatter(cache, q, k, v, dev(pos), table.cuda(), dev(slots), q_out=q, k_out=k,
+                              err_flags=err)
+    out = kvq.prompt_attention(q, k, v, _cu(lens), int(lens.max()), SCALE, err_flags=err)
+    # the decode step
+    q1, k1, v1 = _inputs(N, hq, H, seed=25)
+    new_slots = np.concatenate([workloads.token_slots(bt, r, int(L) + 1, bs)[-1:] for r, L in enumerate(lens)])
+    q1r = kvq.rope_quantize_scatter(cache, q1, k1, v1, dev(lens.astype(np.int64)), table.cuda(),
+                                    dev(new_slots), err_flags=err)
+    got = kvq.paged_decode(cache, q1r, dev(bt), dev(lens + 1), int(lens.max()) + 1, SCALE, err_flags=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    # rotation of the prompts, then the attention over the rotated bf16 rows
+    for x, xf in ((q, qf), (k, kf)):
+        want = torch.from_numpy(plain.rotate_rows(xf, table.numpy(), pos, False)).to(torch.bfloat16)
+        assert torch.equal(x.cpu(), want)
+    assert_close(out, q, k, v, lens)
+    # the cache, and the decode step over it
+    oc = oracle.empty_cache(blocks * bs, H, 128)
+    for at, kk, vv, pp in ((slots, kf, vf, pos),
+                           (new_slots, k1.float().cpu().numpy(), v1.float().cpu().numpy(), lens)):
+        rot = plain.rotate_rows(kk, table.numpy(), pp, False)
+        oc["k_codes"][at], oc["k_scales"][at] = plain.quantize_f32_rows(rot)
+        oc["v_codes"][at], oc["v_scales"][at] = plain.quantize_f32_rows(vv)
+    for name in ("k_codes", "v_codes", "k_scales", "v_scales"):
+        assert np.array_equal(getattr(cache, name).cpu().numpy(), oc[name]), name
+    want = torch.from_numpy(plain.rotate_rows(q1.float().cpu().numpy(), table.numpy(), lens, False)).to(torch.bfloat16)
+    assert torch.equal(q1r.cpu(), want)
+    ref, oerr = oracle.paged_attention(oc, workloads.bf16_bits(want), N, 1, hq, bt, lens + 1, bs, SCALE)
+    assert oerr == 0
+    assert_attention_close(got, ref, "decode after the rotary store")
