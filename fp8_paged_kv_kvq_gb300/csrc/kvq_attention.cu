@@ -981,6 +981,35 @@ bool encode_code_tensor_map_strided(CUtensorMap *map, const uint8_t *codes, int6
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_row_tensor_map(CUtensorMap *map, const void *rows, int64_t num_tokens, int heads,
+                           int64_t token_stride, int tokens) {
+  EncodeTiledFn f = encode_tiled_fn();
+  if (f == nullptr) return false;
+  const cuuint64_t dims[4] = {64u, static_cast<cuuint64_t>(num_tokens), 2u,
+                              static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(token_stride) * 2, 128u, kHeadDim * 2};
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(tokens), 2u, 1u};
+  const cuuint32_t estride[4] = {1u, 1u, 1u, 1u};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(rows), dims, strides, box,
+           estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_head_tensor_map(CUtensorMap *map, const void *rows, int64_t num_tokens, int heads,
+                            int64_t token_stride, int group, int tokens) {
+  EncodeTiledFn f = encode_tiled_fn();
+  if (f == nullptr) return false;
+  const cuuint64_t dims[4] = {64u, static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(num_tokens), 2u};
+  const cuuint64_t strides[3] = {kHeadDim * 2, static_cast<cuuint64_t>(token_stride) * 2, 128u};
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tokens),
+                             1u};
+  const cuuint32_t estride[4] = {1u, 1u, 1u, 1u};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(rows), dims, strides, box,
+           estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A map over one scale plane [num_slots, H] fp32: boxes of 4 consecutive heads
 // x `rows` slots, unswizzled (16 bytes per slot row in shared memory).
 bool encode_scale_tensor_map(CUtensorMap *map, const float *scales, int64_t num_slots, int H,

@@ -182,6 +182,17 @@ bool encode_scale_tensor_map(CUtensorMap *map, const float *scales, int64_t num_
 bool encode_code_tensor_map_strided(CUtensorMap *map, const uint8_t *codes, int64_t num_slots,
                                     int H);
 
+// Tensor map over bf16 rows [num_tokens, heads, 128] with a token stride in
+// elements: boxes of `tokens` tokens of one head as two halves of 64 dims
+// (coordinates: 0, token, 0, head), 128-byte swizzled.
+bool encode_row_tensor_map(CUtensorMap *map, const void *rows, int64_t num_tokens, int heads,
+                           int64_t token_stride, int tokens);
+
+// The same rows in boxes of 64 dims x `group` heads x `tokens` tokens
+// (coordinates: 0, head, token, half): rows ordered (token, head).
+bool encode_head_tensor_map(CUtensorMap *map, const void *rows, int64_t num_tokens, int heads,
+                            int64_t token_stride, int group, int tokens);
+
 // The page-major partials kernel for at most 8 stacked rows per KV head
 // (pages of >= 16 tokens, KV heads a multiple of 4).
 bool attn_page_supported(const kvq_cache &c, const AttnShape &s);

@@ -1,14 +1,44 @@
 // kvq_prompt.cu -- causal attention of packed prompts over their own bf16 keys
 // and values (grouped query heads, sequences of different lengths in one token
-// buffer), before anything is read from the cache.
+// buffer), before anything is read from the cache, on the 5th-generation
+// tensor cores.
 //
-// A unit of work is 64 of the stacked rows m = i G + g (token i, query head
-// h G + g) of one sequence and KV head h: the G heads that share a KV head use
-// the same keys, so a tile of few tokens fills the matrix product's rows.
-// Sequence s may use the units floor(cu[s] G / 64) + s up to the next
-// sequence's: at least as many as its rows need, and a unit finds its sequence
-// by a search over cu_seqlens with no plan made beforehand.
+//   out_i = sum_{j <= i} p_j v_j / sum_{j <= i} p_j,  p_j = 2^(c (q_i . k_j - m_i)),
+//   c = sm_scale log2(e), m_i a running reference within 8 / c of the row's maximum
+//
+//  * A unit of work is two 128-row tiles of one sequence and KV head.  The G
+//    query heads that share a KV head are stacked: row t G + g of a tile is
+//    token t, head h G + g, with floor(128 / G) tokens per tile, so short
+//    prompts fill the tensor core's rows and a key tile is read once for all G
+//    heads.  The unit's key tiles (128 keys) go from its diagonal down to 0.
+//  * Sequence s may use the unit numbers floor(cu[s] / TU) + s up to the next
+//    sequence's (TU tokens per unit): at least ceil(len / TU) of them, so a
+//    unit number finds its sequence by a search over cu_seqlens, with no plan
+//    launch, no workspace and no bound on the number of sequences.
+//  * Persistent CTAs of 512 threads, one per SM.  Warps 0-3 and 4-7: softmax of
+//    tile 0 and tile 1 (a thread owns a TMEM lane, a row); 8-11: the epilogue,
+//    which overlaps the next unit; 12: key/value TMA; 13: the MMAs; 14: clears
+//    what the edge value tiles must not contribute; 15: work numbers and query
+//    TMA.
+//  * S = Q K^T (128 x 128 x 128, both operands from shared memory) into TMEM;
+//    the softmax reads S, writes P as bf16 over S's own columns, and O += P V
+//    takes P from TMEM.  The two tiles alternate on the tensor core: PV and the
+//    next QK^T of one run while the other is in its softmax.
+//  * A row's reference m moves only when a score passes it by 2^8 in the
+//    exponent (P then stays below 2^8, and sums and outputs are fp32); the
+//    thread that moves it rescales its O row, with no PV in flight on it since
+//    the QK^T that it waited for was issued after it.
+//  * 0 times an infinity is not 0, so zero probabilities do not hide unseen
+//    values.  Of the value tiles that some row of the unit does not see whole
+//    warp 14 clears the rows past the sequence and every infinity and NaN; the
+//    epilogue adds those a row does see back (rare, one flag per unit).
+//  * Every wait is bounded; a role that gives up raises a shared abort flag,
+//    copies and MMAs in flight complete, the CTA frees its tensor memory
+//    (KVQ_ERRF_WAIT_TIMEOUT).
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
@@ -17,221 +47,651 @@ namespace kvq {
 
 namespace {
 
-constexpr int kPrRows = 64;                  // stacked rows of a unit
-constexpr int kPrKeys = 64;                  // keys of a tile
-constexpr int kPrWarps = 4;                  // 16 rows each
-constexpr int kPrPitch = kHeadDim + 8;       // elements: rows 16 bytes apart in the banks
+constexpr int kPtKeys = 128;                          // keys of a tile
+constexpr int kPtStages = 4;                          // ring: key tiles in even stages, values in odd
+constexpr int kPtWarpEpi = 8, kPtWarpKv = 12, kPtWarpMma = 13, kPtWarpClear = 14;
+constexpr int kPtThreads = 512;
+constexpr int kPtUnits = 4;                           // work numbers ahead
+constexpr float kPtLazy = 8.0f;                       // log2 of the largest unnormalised p
+
+// shared memory, offsets from a 1024-byte aligned base
+constexpr int kPtTileBytes = 128 * kHeadDim * 2;      // [2 halves of 64 dims][128 rows][128 B]
+constexpr int kPtHalf = kPtTileBytes / 2;
+constexpr int kPtOffQ = 0;
+constexpr int kPtOffKv = 2 * kPtTileBytes;
+constexpr int kPtOffOut = kPtOffKv + kPtStages * kPtTileBytes;   // 4 warps x 32 rows x 256 B
+constexpr int kPtOffSum = kPtOffOut + kPtTileBytes;              // [tile][128] denominators
+constexpr int kPtOffUnit = kPtOffSum + 2 * 128 * 4;
+constexpr int kPtOffDirty = kPtOffUnit + kPtUnits * 16;
+constexpr int kPtOffMisc = kPtOffDirty + kPtUnits * 4;           // tmem base, abort
+constexpr int kPtOffBar = kPtOffMisc + 16;
+enum : int {
+  kPtKvFull = 0,
+  kPtKvEmpty = kPtKvFull + kPtStages,
+  kPtQFull = kPtKvEmpty + kPtStages,                  // per tile, as the next six
+  kPtQEmpty = kPtQFull + 2,
+  kPtSFull = kPtQEmpty + 2,
+  kPtPReady = kPtSFull + 2,
+  kPtOFull = kPtPReady + 2,
+  kPtOEmpty = kPtOFull + 2,
+  kPtSumFull = kPtOEmpty + 2,
+  kPtVClear = kPtSumFull + 2,                         // per ring stage
+  kPtUnitFull = kPtVClear + kPtStages,
+  kPtUnitEmpty = kPtUnitFull + kPtUnits,
+  kPtDrain = kPtUnitEmpty + kPtUnits,
+  kPtBars
+};
+constexpr int kPtSmem = kPtOffBar + 8 * kPtBars + 1024;
+static_assert(kPtOffBar % 8 == 0 && kPtOffUnit % 16 == 0, "alignment");
+static_assert(kPtSmem <= 227 * 1024, "shared memory budget");
+
+// TMEM: S of tile a at 128 a (its P over the first 64 columns), O at 256 + 128 a
+constexpr uint32_t kPtTmemCols = 512;
+__device__ __forceinline__ uint32_t pt_s(int a) { return 128u * a; }
+__device__ __forceinline__ uint32_t pt_o(int a) { return 256u + 128u * a; }
+
+constexpr uint32_t kPtBf16 = (1u << 7) | (1u << 10);   // A and B bf16
+constexpr uint32_t kPtIdescQK = mma_idesc(128, kPtKeys, false, false) | kPtBf16;
+constexpr uint32_t kPtIdescPV = mma_idesc(128, kHeadDim, false, true) | kPtBf16;
 
 struct PromptParams {
-  const uint16_t *q, *k, *v;
+  const uint16_t *v;
   uint16_t *out;
-  int64_t q_stride, k_stride, v_stride, out_stride;
+  int64_t v_stride, out_stride;
   int32_t num_tokens;
   const int32_t *cu;
   int32_t N, max_seqlen, G, H;
-  float scale2;                              // sm_scale log2(e)
+  int32_t TQ;                                          // tokens of a tile: 128 / G
+  int32_t inv_g;                                       // ceil(65536 / G)
+  int64_t units;                                       // work numbers
+  float scale2;                                        // sm_scale log2(e)
   int32_t *err_flags;
 };
 
-__device__ __forceinline__ float pr_ex2(float x) {
+__device__ __forceinline__ float pt_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+__device__ __forceinline__ float pt_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pt_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
-// 16-bit lanes of w that hold an infinity or NaN become 0.
-__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
-  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
-  return w;
+// Bounded wait that also gives up once another role raised the abort flag.
+__device__ __forceinline__ bool pt_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort) {
+#pragma unroll 1
+  for (int i = 0; i < (1 << 19); ++i) {
+    if (mbar_try_wait_sleep(bar, parity, 2000u)) return true;
+    if ((i & 15) == 15 && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+  return mbar_try_wait(bar, parity) || pt_wait_slow(bar, parity, abort);
 }
 
-__global__ void __launch_bounds__(kPrWarps * 32)
-prompt_attention_kernel(const PromptParams p) {
-  __shared__ __align__(16) uint16_t ks[kPrKeys * kPrPitch];
-  __shared__ __align__(16) uint16_t vs[kPrKeys * kPrPitch];
-  __shared__ int dirty;
+// A unit: sequence rows [start, start + len), KV head h, tiles from token tok0
+// (within the sequence) on; len = 0 ends the work.
+struct PtUnit {
+  int start, len, h, tok0;
+  int n0, n1;                                          // key tiles of tile 0 and 1 (n1 = 0: none)
+  __device__ __forceinline__ void shape(const int4 e, int TQ) {
+    start = e.x;
+    len = e.y;
+    h = e.z;
+    tok0 = e.w;
+    const int t0 = min(len, tok0 + TQ), t1 = min(len, tok0 + 2 * TQ);
+    n0 = (t0 + kPtKeys - 1) / kPtKeys;
+    n1 = t1 > t0 ? (t1 + kPtKeys - 1) / kPtKeys : 0;
+  }
+  __device__ __forceinline__ int tiles() const { return max(n0, n1); }
+  // key tile j has a key that the unit's first row does not see
+  __device__ __forceinline__ bool edge(int j) const { return j * kPtKeys + kPtKeys - 1 > tok0; }
+  __device__ __forceinline__ bool active(int a, int j) const { return j < (a == 0 ? n0 : n1); }
+};
+
+// Work number w as a unit (len 0: none there).  All lanes of a warp.
+__device__ __forceinline__ int4 pt_find(const PromptParams &p, int64_t w, int lane) {
+  const int TU = 2 * p.TQ;
+  const int h = static_cast<int>(w % p.H);
+  const int64_t x = w / p.H;
+  int lo = 0, hi = p.N;
+  for (;;) {
+    const int step = (hi - lo + 31) / 32;
+    const int64_t i = lo + static_cast<int64_t>(lane) * step;
+    const bool below = i < hi && __ldg(p.cu + i) / TU + i <= x;
+    const int c = __ffs(~__ballot_sync(0xFFFFFFFFu, below)) - 1;   // leading lanes below (32: -1)
+    const int cnt = c < 0 ? 32 : c;
+    if (cnt == 0) return make_int4(0, 0, 0, 0);
+    lo += (cnt - 1) * step;
+    hi = min(hi, lo + step);
+    if (step == 1) break;
+  }
+  const int a = __ldg(p.cu + lo), b = __ldg(p.cu + lo + 1);
+  if (a < 0 || b < a || b > p.num_tokens || b - a > p.max_seqlen) return make_int4(0, 0, 0, 0);
+  const int64_t units = (static_cast<int64_t>(b - a) + TU - 1) / TU;
+  const int64_t u = units - 1 - (x - (a / TU + lo));                // the longest rows first
+  if (u < 0 || u >= units) return make_int4(0, 0, 0, 0);
+  return make_int4(a, b - a, h, static_cast<int>(u * TU));
+}
+
+__device__ __forceinline__ void pt_tma_4d(uint32_t dst, const void *tmap, int x, int y, int z,
+                                          int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n"
+      :: "r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
+}
+
+// One key tile of one row: S from TMEM, the reference and the denominator
+// brought up to date (the O row with them), P as bf16 over S's columns.
+// kMask: keys past `lim` (within the tile) are not seen.
+template <bool kMask>
+__device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, int lim, float scale2,
+                                           bool fresh, float &m_ref, float &lsum) {
+  float x[128];
+  tmem_ld64(scol, x);
+  tmem_ld64(scol + 64, x + 64);
+  if (kMask) {
+#pragma unroll
+    for (int i = 0; i < 128; ++i) x[i] = i <= lim ? x[i] : -INFINITY;
+  }
+  float mx[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) mx[q] = fmaxf(x[q], x[q + 4]);
+#pragma unroll
+  for (int i = 8; i < 128; i += 8)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
+  const float top = fmaxf(pt_max3(mx[0], mx[1], mx[2]), mx[3]);
+  const bool unset = m_ref == -INFINITY;
+  const bool move = unset ? top > -INFINITY : (top - m_ref) * scale2 > kPtLazy;
+  if (__any_sync(0xFFFFFFFFu, move && !unset)) {
+    // (rows of the warp that stay multiply by 1)
+    const float f = (move && !unset) ? pt_ex2((m_ref - top) * scale2) : 1.0f;
+    lsum *= f;
+    if (!fresh) {
+#pragma unroll 1
+      for (int c = 0; c < kHeadDim; c += 16) {
+        float o[16];
+        tmem_ld16(ocol + c, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] *= f;
+        tmem_st16(ocol + c, o);
+      }
+    }
+  }
+  if (move) m_ref = top;
+  const float shift = m_ref == -INFINITY ? 0.0f : -m_ref * scale2;
+  const uint64_t sc = pack_f32x2(scale2, scale2), sh = pack_f32x2(shift, shift);
+  uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
+#pragma unroll
+  for (int c = 0; c < 128; c += 32) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float a, b;
+      unpack_f32x2(fma_f32x2(pack_f32x2(x[c + 2 * i], x[c + 2 * i + 1]), sc, sh), a, b);
+      a = pt_ex2(a);
+      b = pt_ex2(b);
+      sum[i & 1] = pt_add2(sum[i & 1], pack_f32x2(a, b));
+      w[i] = pack_bf16x2(a, b);
+    }
+    tmem_st16u(scol + c / 2, w);
+  }
+  float a, b;
+  unpack_f32x2(pt_add2(sum[0], sum[1]), a, b);
+  lsum += a + b;
+}
+
+__global__ void __launch_bounds__(kPtThreads, 1)
+prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMap tm_q,
+                        const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t bar0 = smem_addr(smem + kPtOffBar);
+  auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kPtOffMisc);
+  volatile int *abort_s = reinterpret_cast<volatile int *>(smem + kPtOffMisc + 4);
+  volatile int *dirty_s = reinterpret_cast<volatile int *>(smem + kPtOffDirty);
+  int4 *unit_s = reinterpret_cast<int4 *>(smem + kPtOffUnit);
+  volatile float *sum_s = reinterpret_cast<volatile float *>(smem + kPtOffSum);
+
   allow_dependents_launch();
+  if (tid == 0) {
+    for (int s = 0; s < kPtStages; ++s) {
+      mbar_init(BAR(kPtKvFull + s), 1);
+      mbar_init(BAR(kPtKvEmpty + s), 1 + (s & 1));     // value tiles: warp 14 too
+      mbar_init(BAR(kPtVClear + s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(BAR(kPtQFull + a), 1);
+      mbar_init(BAR(kPtQEmpty + a), 1);
+      mbar_init(BAR(kPtSFull + a), 1);
+      mbar_init(BAR(kPtPReady + a), 4);
+      mbar_init(BAR(kPtOFull + a), 1);
+      mbar_init(BAR(kPtOEmpty + a), 4);
+      mbar_init(BAR(kPtSumFull + a), 4);
+    }
+    for (int e = 0; e < kPtUnits; ++e) {
+      mbar_init(BAR(kPtUnitFull + e), 1);
+      mbar_init(BAR(kPtUnitEmpty + e), 8 + 4 + 3);     // softmax, epilogue, warps 12-14
+    }
+    mbar_init(BAR(kPtDrain), 1);
+    *abort_s = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kPtWarpMma) {
+    tmem_alloc(smem_addr(tmem_slot), kPtTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();
-  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.H));
-  const int64_t x = blockIdx.x / static_cast<unsigned>(p.H);
-  auto base = [&](int s) -> int64_t {
-    return static_cast<int64_t>(p.cu[s]) * p.G / kPrRows + s;
+
+  // Unit `t` of this CTA; the caller's warp (or lone lane) releases its entry.
+  auto take_unit = [&](int t, PtUnit &u) -> bool {
+    const int e = t % kPtUnits;
+    if (!pt_wait(BAR(kPtUnitFull + e), (t / kPtUnits) & 1, abort_s)) return false;
+    u.shape(unit_s[e], p.TQ);
+    return true;
   };
-  if (p.err_flags) {
-    for (int64_t s = static_cast<int64_t>(blockIdx.x) * (kPrWarps * 32) + tid; s < p.N;
-         s += static_cast<int64_t>(gridDim.x) * (kPrWarps * 32)) {
-      const int a = p.cu[s], b = p.cu[s + 1];
-      if (a < 0 || b < a || b > p.num_tokens || b - a > p.max_seqlen)
-        atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
-    }
-  }
-  int lo = 0, hi = p.N - 1;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo + 1) / 2;
-    if (base(mid) <= x) lo = mid;
-    else hi = mid - 1;
-  }
-  const int start = p.cu[lo], end = p.cu[lo + 1];
-  if (start < 0 || end < start || end > p.num_tokens || end - start > p.max_seqlen) return;
-  const int len = end - start;
-  const int64_t rows = static_cast<int64_t>(len) * p.G;
-  const int64_t units = (rows + kPrRows - 1) / kPrRows;
-  const int64_t u = units - 1 - (x - base(lo));          // heaviest first
-  if (u < 0 || u >= units) return;
-  const int64_t row0 = u * kPrRows;
-  const int g4 = lane >> 2, c4 = lane & 3;
+  bool gave_up = false;
 
-  // this thread's two rows (g4 and g4 + 8 of its warp's 16)
-  int tok[2];
-  const uint16_t *qp[2];
-  uint16_t *op[2];
-  bool ok[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t m = row0 + 16 * warp + g4 + 8 * i;
-    ok[i] = m < rows;
-    const int64_t mm = ok[i] ? m : rows - 1;
-    tok[i] = static_cast<int>(mm / p.G);
-    const int64_t head = static_cast<int64_t>(h) * p.G + (mm - static_cast<int64_t>(tok[i]) * p.G);
-    qp[i] = p.q + (start + tok[i]) * p.q_stride + head * kHeadDim;
-    op[i] = p.out + (start + tok[i]) * p.out_stride + head * kHeadDim;
-  }
-  uint32_t qf[8][4];
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    qf[kk][0] = *reinterpret_cast<const uint32_t *>(qp[0] + 16 * kk + 2 * c4);
-    qf[kk][1] = *reinterpret_cast<const uint32_t *>(qp[1] + 16 * kk + 2 * c4);
-    qf[kk][2] = *reinterpret_cast<const uint32_t *>(qp[0] + 16 * kk + 8 + 2 * c4);
-    qf[kk][3] = *reinterpret_cast<const uint32_t *>(qp[1] + 16 * kk + 8 + 2 * c4);
-  }
-  float o[16][4];
-#pragma unroll
-  for (int n = 0; n < 16; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
-
-  const int first_tok = static_cast<int>(row0 / p.G);
-  const int64_t last_row = (row0 + kPrRows < rows ? row0 + kPrRows : rows) - 1;
-  const int keys = static_cast<int>(last_row / p.G) + 1;  // keys the unit's last row sees
-  for (int j0 = 0; j0 < keys; j0 += kPrKeys) {
-    // a tile some row does not see whole: its values with infinities and NaN
-    // taken out (a zero probability would not), those are added at the end
-    const bool edge = j0 + kPrKeys - 1 > first_tok;
-    __syncthreads();
-    if (tid == 0) dirty = 0;
-    __syncthreads();
-    for (int i = tid; i < kPrKeys * (kHeadDim / 8); i += kPrWarps * 32) {
-      const int r = i / (kHeadDim / 8), c = i % (kHeadDim / 8);
-      uint4 kw = make_uint4(0u, 0u, 0u, 0u), vw = kw;
-      if (j0 + r < keys) {
-        kw = *reinterpret_cast<const uint4 *>(p.k + (start + j0 + r) * p.k_stride + h * kHeadDim + 8 * c);
-        vw = *reinterpret_cast<const uint4 *>(p.v + (start + j0 + r) * p.v_stride + h * kHeadDim + 8 * c);
+  if (warp < kPtWarpEpi) {
+    // ------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
+    const int a = warp >> 2;
+    const int m = tid & 127;                           // row of the tile, TMEM lane
+    const int t_row = (m * p.inv_g) >> 16;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    uint32_t steps = 0, done = 0;                      // key tiles and units of tile a
+    for (int t = 0;; ++t) {
+      PtUnit u;
+      const bool ok = take_unit(t, u);
+      if (__any_sync(0xFFFFFFFFu, !ok)) {
+        gave_up = true;
+        break;
       }
-      if (edge) {
-        const uint4 f = make_uint4(finite_or_zero(vw.x), finite_or_zero(vw.y),
-                                   finite_or_zero(vw.z), finite_or_zero(vw.w));
-        if (f.x != vw.x || f.y != vw.y || f.z != vw.z || f.w != vw.w) dirty = 1;
-        vw = f;
+      if (lane == 0) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
+      if (u.len == 0) break;
+      const int n = a == 0 ? u.n0 : u.n1;
+      if (n == 0) continue;
+      const int first = u.tok0 + a * p.TQ;             // the tile's first token
+      const int tok = first + t_row;
+      float m_ref = -INFINITY, lsum = 0.0f;
+      for (int j = n - 1; j >= 0; --j, ++steps) {
+        if (__any_sync(0xFFFFFFFFu, !pt_wait(BAR(kPtSFull + a), steps & 1, abort_s))) {
+          gave_up = true;
+          break;
+        }
+        tc_fence_after();
+        if (j * kPtKeys + kPtKeys - 1 > first)
+          pt_softmax<true>(tl + pt_s(a), tl + pt_o(a), tok - j * kPtKeys, p.scale2, j == n - 1,
+                           m_ref, lsum);
+        else
+          pt_softmax<false>(tl + pt_s(a), tl + pt_o(a), 0, p.scale2, j == n - 1, m_ref, lsum);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(kPtPReady + a));
       }
-      *reinterpret_cast<uint4 *>(ks + r * kPrPitch + 8 * c) = kw;
-      *reinterpret_cast<uint4 *>(vs + r * kPrPitch + 8 * c) = vw;
+      if (gave_up) break;
+      // the denominators, once the epilogue has read the last unit's
+      if (done > 0 &&
+          __any_sync(0xFFFFFFFFu, !pt_wait(BAR(kPtOEmpty + a), (done - 1) & 1, abort_s))) {
+        gave_up = true;
+        break;
+      }
+      sum_s[128 * a + m] = lsum;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(kPtSumFull + a));
+      ++done;
     }
-    __syncthreads();
-    float s[8][4];
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = 0.0f;
-#pragma unroll
-      for (int kk = 0; kk < 8; kk += 2) {
-        uint32_t b[4];
-        ldsm_x4(smem_addr(ks + (8 * n + (lane & 7)) * kPrPitch + 16 * kk + 8 * (lane >> 3)), b);
-        mma_bf16_16816(s[n], qf[kk], b[0], b[1]);
-        mma_bf16_16816(s[n], qf[kk + 1], b[2], b[3]);
+  } else if (warp < kPtWarpKv) {
+    // ------------------------------------------------------------ epilogue
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
+    if (p.err_flags) {
+      for (int64_t s = static_cast<int64_t>(blockIdx.x) * 128 + (tid - 32 * kPtWarpEpi); s < p.N;
+           s += static_cast<int64_t>(gridDim.x) * 128) {
+        const int b0 = __ldg(p.cu + s), b1 = __ldg(p.cu + s + 1);
+        if (b0 < 0 || b1 < b0 || b1 > p.num_tokens || b1 - b0 > p.max_seqlen)
+          atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
       }
     }
-    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = j0 + 8 * n + 2 * c4 + (i & 1);
-        if (key > tok[i >> 1]) s[n][i] = -INFINITY;
-        mx[i >> 1] = fmaxf(mx[i >> 1], s[n][i]);
+    const int q4 = warp & 3;
+    const int m = 32 * q4 + lane;
+    const int t_row = (m * p.inv_g) >> 16;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
+    uint8_t *stage = smem + kPtOffOut + q4 * (32 * 2 * kHeadDim);
+    uint32_t done[2] = {0, 0};
+    for (int t = 0;; ++t) {
+      PtUnit u;
+      const bool ok = take_unit(t, u);
+      if (__any_sync(0xFFFFFFFFu, !ok)) {
+        gave_up = true;
+        break;
       }
-    float shift[2];
+      if (u.len == 0) break;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
-      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
-      const float m_new = fmaxf(m_run[i], mx[i]);
-      const float f = m_run[i] == -INFINITY ? 0.0f : pr_ex2((m_run[i] - m_new) * p.scale2);
-      m_run[i] = m_new;
-      shift[i] = m_new == -INFINITY ? 0.0f : m_new * p.scale2;
-      l_run[i] *= f;
+      for (int a = 0; a < 2; ++a) {
+        if ((a == 0 ? u.n0 : u.n1) == 0) continue;
+        const bool got = pt_wait(BAR(kPtSumFull + a), done[a] & 1, abort_s) &&
+                         pt_wait(BAR(kPtOFull + a), done[a] & 1, abort_s);
+        if (__any_sync(0xFFFFFFFFu, !got)) {
+          gave_up = true;
+          break;
+        }
+        tc_fence_after();
+        ++done[a];
+        const float inv = 1.0f / sum_s[128 * a + m];
+        const int tok = u.tok0 + a * p.TQ + t_row;
+        const bool dirty = dirty_s[t % kPtUnits] != 0;
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim; c += 32) {
+          float o[32];
+          tmem_ld32(tl + pt_o(a) + c, o);
 #pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        o[n][2 * i] *= f;
-        o[n][2 * i + 1] *= f;
-      }
-    }
+          for (int i = 0; i < 32; ++i) o[i] *= inv;
+          if (dirty) {
+            // the infinities and NaN this row sees in the edge tiles
+            const int last = min(tok, u.len - 1);
+            for (int j = max(0, u.tok0 - (kPtKeys - 2)) / kPtKeys * kPtKeys; j <= last; ++j) {
+              const uint16_t *vr = p.v + (static_cast<int64_t>(u.start) + j) * p.v_stride +
+                                   u.h * kHeadDim + c;
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[n][i] = pr_ex2(fmaf(s[n][i], p.scale2, -shift[i >> 1]));
-        l_run[i >> 1] += s[n][i];
-      }
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const uint32_t a[4] = {pack_bf16x2(s[2 * kk][0], s[2 * kk][1]),
-                             pack_bf16x2(s[2 * kk][2], s[2 * kk][3]),
-                             pack_bf16x2(s[2 * kk + 1][0], s[2 * kk + 1][1]),
-                             pack_bf16x2(s[2 * kk + 1][2], s[2 * kk + 1][3])};
-#pragma unroll
-      for (int n = 0; n < 16; n += 2) {
-        uint32_t b[4];
-        ldsm_x4_trans(smem_addr(vs + (16 * kk + (lane & 15)) * kPrPitch + 8 * n + 8 * (lane >> 4)), b);
-        mma_bf16_16816(o[n], a, b[0], b[1]);
-        mma_bf16_16816(o[n + 1], a, b[2], b[3]);
-      }
-    }
-    if (dirty) {
-      // the infinities and NaN that a row does see, as the sum has them
-      for (int r = 0; r < kPrKeys && j0 + r < keys; ++r)
-#pragma unroll
-        for (int n = 0; n < 16; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t e = p.v[(start + j0 + r) * p.v_stride + h * kHeadDim + 8 * n + 2 * c4 + (i & 1)];
-            if ((e & 0x7F80u) == 0x7F80u && j0 + r <= tok[i >> 1]) o[n][i] += bf16_lo(e);
+              for (int i = 0; i < 32; ++i) {
+                const uint32_t e = vr[i];
+                if ((e & 0x7F80u) == 0x7F80u) o[i] += bf16_lo(e);
+              }
+            }
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4 *>(stage + lane * 256 + (((c / 8 + k) ^ (lane & 7)) << 4)) =
+                make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                           pack_bf16x2(o[8 * k + 4], o[8 * k + 5]),
+                           pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(kPtOEmpty + a));
+        // rows of 256 contiguous bytes, two per store
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int r = 2 * i + (lane >> 4), mr = 32 * q4 + r, c = lane & 15;
+          const int tr = (mr * p.inv_g) >> 16, g = mr - tr * p.G;
+          const int tk = u.tok0 + a * p.TQ + tr;
+          if (tr < p.TQ && tk < u.len)
+            *reinterpret_cast<uint4 *>(p.out + (static_cast<int64_t>(u.start) + tk) * p.out_stride +
+                                       (static_cast<int64_t>(u.h) * p.G + g) * kHeadDim + 8 * c) =
+                *reinterpret_cast<const uint4 *>(stage + r * 256 + ((c ^ (r & 7)) << 4));
+        }
+        __syncwarp();
+      }
+      if (gave_up) break;
+      // (held to here: the entry's dirty flag is the unit's until it is taken again)
+      if (lane == 0) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    if (warp == kPtWarpKv) {
+      // ------------------------------------------------------ key, value TMA
+      if (lane == 0) {
+        uint32_t idx = 0;                              // ring entries issued
+        for (int t = 0; !gave_up; ++t) {
+          PtUnit u;
+          if (!take_unit(t, u)) {
+            gave_up = true;
+            break;
+          }
+          mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
+          if (u.len == 0) break;
+          for (int j = u.tiles() - 1; j >= 0 && !gave_up; --j)
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv, ++idx) {
+              const int b = idx % kPtStages;
+              if (idx >= kPtStages &&
+                  !pt_wait(BAR(kPtKvEmpty + b), (idx / kPtStages - 1) & 1, abort_s)) {
+                gave_up = true;
+                break;
+              }
+              mbar_arrive_expect_tx(BAR(kPtKvFull + b), kPtTileBytes);
+              pt_tma_4d(smem_addr(smem + kPtOffKv + b * kPtTileBytes), kv == 0 ? &tm_k : &tm_v, 0,
+                        u.start + j * kPtKeys, 0, u.h, BAR(kPtKvFull + b));
+            }
+        }
+        // copies in flight land before the CTA leaves
+        for (uint32_t v = idx > kPtStages ? idx - kPtStages : 0; v < idx; ++v)
+          mbar_wait_sleep_bounded(BAR(kPtKvFull + v % kPtStages), (v / kPtStages) & 1);
+      }
+    } else if (warp == kPtWarpMma) {
+      // ---------------------------------------------------------------- MMA
+      if (lane == 0) {
+        const uint32_t q0 = smem_addr(smem + kPtOffQ), kv0 = smem_addr(smem + kPtOffKv);
+        uint32_t step = 0;                             // key tiles so far: ring entries 2 step, + 1
+        uint32_t pr[2] = {0, 0};                       // PV steps of each tile
+        uint32_t units[2] = {0, 0};                    // units whose first QK^T / PV was issued
+        uint32_t o_units[2] = {0, 0};
+        uint32_t clears = 0;                           // parity of edge tiles per ring stage
+        // QK^T of tile a with the key tile of step st
+        auto qk = [&](const PtUnit &u, int a, int j, uint32_t st) -> bool {
+          const uint32_t e = 2 * st, b = e % kPtStages;
+          if (!pt_wait(BAR(kPtKvFull + b), (e / kPtStages) & 1, abort_s)) return false;
+          if (j == (a == 0 ? u.n0 : u.n1) - 1 &&
+              !pt_wait(BAR(kPtQFull + a), units[a]++ & 1, abort_s))
+            return false;
+          tc_fence_after();
+          const uint64_t qd = smem_desc(q0 + a * kPtTileBytes, 16, 1024, kSmemSwizzle128);
+          const uint64_t kd = smem_desc(kv0 + b * kPtTileBytes, 16, 1024, kSmemSwizzle128);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk & 3) * 2 + (kk >> 2) * (kPtHalf >> 4);
+            tc_mma_f16(tmem + pt_s(a), qd + off, kd + off, kPtIdescQK, kk != 0);
+          }
+          tc_commit(BAR(kPtSFull + a));
+          if (j == 0) tc_commit(BAR(kPtQEmpty + a));
+          return true;
+        };
+        PtUnit u, nx;
+        int t = 0;
+        bool ok = take_unit(t, u);
+        if (ok) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
+        if (ok && u.len > 0) {
+          const int j = u.tiles() - 1;
+#pragma unroll
+          for (int a = 0; a < 2 && ok; ++a)
+            if (u.active(a, j)) ok = qk(u, a, j, 0);
+          if (ok) tc_commit(BAR(kPtKvEmpty + 0));
+        }
+        while (ok && u.len > 0) {
+          const int n = u.tiles();
+          for (int j = n - 1; j >= 0 && ok; --j, ++step) {
+            int jn = j - 1;
+            if (j == 0) {
+              ok = take_unit(++t, nx);
+              if (!ok) break;
+              mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
+              jn = nx.len > 0 ? nx.tiles() - 1 : -1;
+            } else {
+              nx = u;
+            }
+            const uint32_t e = 2 * step + 1, b = e % kPtStages;
+#pragma unroll
+            for (int a = 0; a < 2 && ok; ++a) {
+              if (u.active(a, j)) {
+                const bool first = j == (a == 0 ? u.n0 : u.n1) - 1;
+                ok = pt_wait(BAR(kPtPReady + a), pr[a]++ & 1, abort_s) &&
+                     pt_wait(BAR(kPtKvFull + b), (e / kPtStages) & 1, abort_s);
+                if (ok && first && o_units[a]++ > 0)
+                  ok = pt_wait(BAR(kPtOEmpty + a), (o_units[a] - 2) & 1, abort_s);
+                if (ok && u.edge(j)) ok = pt_wait(BAR(kPtVClear + b), (clears >> b) & 1, abort_s);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vd = smem_desc(kv0 + b * kPtTileBytes, kPtHalf, 1024, kSmemSwizzle128);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  tc_mma_f16_tmem_a(tmem + pt_o(a), tmem + pt_s(a) + 8 * kk, vd + (2048 >> 4) * kk,
+                                    kPtIdescPV, (first && kk == 0) ? 0u : 1u);
+                if (j == 0) tc_commit(BAR(kPtOFull + a));
+              }
+              if (jn >= 0 && nx.active(a, jn)) ok = qk(nx, a, jn, step + 1);
+            }
+            if (!ok) break;
+            if (u.edge(j)) clears ^= 1u << b;
+            tc_commit(BAR(kPtKvEmpty + b));
+            if (jn >= 0) tc_commit(BAR(kPtKvEmpty + (2 * (step + 1)) % kPtStages));
+          }
+          u = nx;
+        }
+        gave_up = !ok;
+        // every MMA issued has completed before the tensor memory is freed
+        tc_commit(BAR(kPtDrain));
+        mbar_wait_sleep_bounded(BAR(kPtDrain), 0);
+      }
+    } else if (warp == kPtWarpClear) {
+      // ------------------------------------------- edge value tiles cleared
+      uint32_t step = 0;
+      for (int t = 0; !gave_up; ++t) {
+        PtUnit u;
+        const bool ok = take_unit(t, u);
+        if (__any_sync(0xFFFFFFFFu, !ok)) {
+          gave_up = true;
+          break;
+        }
+        if (lane == 0) {
+          dirty_s[t % kPtUnits] = 0;
+          mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
+        }
+        __syncwarp();
+        if (u.len == 0) break;
+        // (every value tile is waited for and released, or this warp could be
+        // phases ahead of the ring or behind it)
+        for (int j = u.tiles() - 1; j >= 0; --j, ++step) {
+          const uint32_t e = 2 * step + 1, b = e % kPtStages;
+          if (__any_sync(0xFFFFFFFFu, !pt_wait(BAR(kPtKvFull + b), (e / kPtStages) & 1, abort_s))) {
+            gave_up = true;
+            break;
+          }
+          if (!u.edge(j)) {
+            if (lane == 0) mbar_arrive(BAR(kPtKvEmpty + b));
+            continue;
+          }
+          uint8_t *tile = smem + kPtOffKv + b * kPtTileBytes;
+          const int rows = min(kPtKeys, u.len - j * kPtKeys);   // of this sequence
+          // every 16-byte piece: the largest magnitude of its 16-bit lanes
+          uint32_t top = 0;
+          for (int r0 = 0; r0 < 2 * rows; r0 += 16) {            // half-rows of 128 bytes
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = r0 + 4 * i + (lane >> 3);
+              w[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (r < 2 * rows)
+                w[i] = *reinterpret_cast<const uint4 *>(tile + (r < rows ? r * 128 : kPtHalf + (r - rows) * 128) +
+                                                         16 * (lane & 7));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t mk = 0x7FFF7FFFu;
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & mk, w[i].y & mk),
+                                           __vmaxu2(w[i].z & mk, w[i].w & mk)));
+            }
+          }
+          const bool bad = (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
+          if (__any_sync(0xFFFFFFFFu, bad)) {
+            if (lane == 0) dirty_s[t % kPtUnits] = 1;
+            for (int r = 0; r < 2 * rows; ++r) {
+              uint32_t *w = reinterpret_cast<uint32_t *>(tile + (r < rows ? r * 128 : kPtHalf + (r - rows) * 128)) + lane;
+              uint32_t x = *w;
+              if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+              if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
+              *w = x;
+            }
+          }
+          // rows past the sequence
+          for (int r = rows + (lane >> 3); r < kPtKeys; r += 4) {
+            *reinterpret_cast<uint4 *>(tile + r * 128 + 16 * (lane & 7)) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(tile + kPtHalf + r * 128 + 16 * (lane & 7)) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(BAR(kPtVClear + b));
+            mbar_arrive(BAR(kPtKvEmpty + b));
+          }
+        }
+      }
+    } else {
+      // --------------------------------------------- work numbers, query TMA
+      uint32_t loads[2] = {0, 0};
+      int64_t w = blockIdx.x;
+      for (int t = 0;; ++t) {
+        int4 e = make_int4(0, 0, 0, 0);
+        for (; w < p.units && e.y == 0; w += gridDim.x) e = pt_find(p, w, lane);
+        const int b = t % kPtUnits;
+        bool ok = t < kPtUnits || pt_wait(BAR(kPtUnitEmpty + b), (t / kPtUnits - 1) & 1, abort_s);
+        if (__any_sync(0xFFFFFFFFu, !ok)) {
+          gave_up = true;
+          break;
+        }
+        if (lane == 0) {
+          unit_s[b] = e;
+          mbar_arrive(BAR(kPtUnitFull + b));
+          PtUnit u;
+          u.shape(e, p.TQ);
+          for (int a = 0; a < 2 && e.y > 0; ++a) {
+            if ((a == 0 ? u.n0 : u.n1) == 0) continue;
+            if (loads[a] > 0 && !pt_wait(BAR(kPtQEmpty + a), (loads[a] - 1) & 1, abort_s)) {
+              ok = false;
+              break;
+            }
+            ++loads[a];
+            const uint32_t dst = smem_addr(smem + kPtOffQ + a * kPtTileBytes);
+            mbar_arrive_expect_tx(BAR(kPtQFull + a), 2u * 128u * p.TQ * p.G);
+            for (int half = 0; half < 2; ++half)
+              pt_tma_4d(dst + half * kPtHalf, &tm_q, 0, u.h * p.G, u.start + u.tok0 + a * p.TQ, half,
+                        BAR(kPtQFull + a));
+          }
+        }
+        gave_up = __any_sync(0xFFFFFFFFu, !ok);
+        if (gave_up || e.y == 0) break;
+      }
+      if (lane == 0)
+        for (int a = 0; a < 2; ++a)
+          if (loads[a] > 0) mbar_wait_sleep_bounded(BAR(kPtQFull + a), (loads[a] - 1) & 1);
     }
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l_run[i] += __shfl_xor_sync(0xFFFFFFFFu, l_run[i], 1);
-    l_run[i] += __shfl_xor_sync(0xFFFFFFFFu, l_run[i], 2);
-    const float inv = 1.0f / l_run[i];
-    if (!ok[i]) continue;
-#pragma unroll
-    for (int n = 0; n < 16; ++n)
-      *reinterpret_cast<uint32_t *>(op[i] + 8 * n + 2 * c4) =
-          pack_bf16x2(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+  if (gave_up) {
+    *abort_s = 1;
+    if (lane == 0 && p.err_flags) atomicOr(p.err_flags, KVQ_ERRF_WAIT_TIMEOUT);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPtWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kPtTmemCols);
   }
 }
 
 int64_t prompt_units(const PromptArgs &a) {
-  const int64_t G = a.num_q_heads / a.num_kv_heads;
-  return (a.num_tokens * G / kPrRows + a.num_seqs) * a.num_kv_heads;
+  const int64_t TU = 2 * (128 / (a.num_q_heads / a.num_kv_heads));
+  return (a.num_tokens / TU + a.num_seqs) * a.num_kv_heads;
 }
 
 }  // namespace
@@ -239,25 +699,42 @@ int64_t prompt_units(const PromptArgs &a) {
 bool prompt_attention_supported(const PromptArgs &a) { return prompt_units(a) <= 0x7FFFFFFF; }
 
 cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
+  const int G = a.num_q_heads / a.num_kv_heads;
   PromptParams p;
-  p.q = static_cast<const uint16_t *>(a.q);
-  p.k = static_cast<const uint16_t *>(a.k);
   p.v = static_cast<const uint16_t *>(a.v);
   p.out = static_cast<uint16_t *>(a.out);
-  p.q_stride = a.q_stride;
-  p.k_stride = a.k_stride;
   p.v_stride = a.v_stride;
   p.out_stride = a.out_stride;
   p.num_tokens = static_cast<int32_t>(a.num_tokens);
   p.cu = a.cu_seqlens;
   p.N = a.num_seqs;
   p.max_seqlen = a.max_seqlen;
-  p.G = a.num_q_heads / a.num_kv_heads;
+  p.G = G;
   p.H = a.num_kv_heads;
+  p.TQ = 128 / G;
+  p.inv_g = (65536 + G - 1) / G;
+  p.units = prompt_units(a);
   p.scale2 = a.sm_scale * 1.4426950408889634f;
   p.err_flags = a.err_flags;
-  return launch_overlapped(prompt_attention_kernel, dim3(static_cast<unsigned>(prompt_units(a))),
-                           dim3(kPrWarps * 32), 0, stream, p);
+  CUtensorMap mq, mk, mv;
+  if (!encode_head_tensor_map(&mq, a.q, a.num_tokens, a.num_q_heads, a.q_stride, G, p.TQ) ||
+      !encode_row_tensor_map(&mk, a.k, a.num_tokens, a.num_kv_heads, a.k_stride, kPtKeys) ||
+      !encode_row_tensor_map(&mv, a.v, a.num_tokens, a.num_kv_heads, a.v_stride, kPtKeys))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = (dev >= 0 && dev < 64) ? (uint64_t(1) << dev) : 0;
+  if (bit == 0 || !(configured.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(prompt_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kPtSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int64_t grid = p.units < a.sms ? p.units : a.sms;
+  return launch_overlapped(prompt_attention_kernel, dim3(static_cast<unsigned>(grid)),
+                           dim3(kPtThreads), kPtSmem, stream, p, mq, mk, mv);
 }
 
 }  // namespace kvq

@@ -86,6 +86,13 @@ def test_longer_prompt():
     _run([2333, 130], 8, 2, seed=4)
 
 
+@pytest.mark.parametrize("lens,hq,H", [([2900, 1500, 40, 700], 32, 8), ([1999, 1999], 28, 4),
+                                       ([130] * 150, 16, 4)])
+def test_many_units_per_cta(lens, hq, H):
+    """Several times more units of work than the GPU has SMs, of very different lengths."""
+    _run(lens, hq, H, seed=5)
+
+
 def test_many_sequences():
     """More sequences than one warp's search step covers, many empty ones among them."""
     g = workloads.generator(6, 6)
