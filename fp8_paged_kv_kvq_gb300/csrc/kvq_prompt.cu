@@ -17,20 +17,23 @@
 //    launch, no workspace and no bound on the number of sequences.
 //  * Persistent CTAs of 512 threads, one per SM.  Warps 0-3 and 4-7: softmax of
 //    tile 0 and tile 1 (a thread owns a TMEM lane, a row); 8-11: the epilogue,
-//    which overlaps the next unit; 12: key/value TMA; 13: the MMAs; 14: clears
-//    what the edge value tiles must not contribute; 15: work numbers and query
-//    TMA.
+//    which overlaps the next unit; 12: work numbers and TMA; 13 and 14: the MMAs
+//    of tile 0 and tile 1; 15: clears what the edge value tiles must not
+//    contribute.
 //  * S = Q K^T (128 x 128 x 128, both operands from shared memory) into TMEM;
 //    the softmax reads S, writes P as bf16 over S's own columns, and O += P V
 //    takes P from TMEM.  The two tiles alternate on the tensor core: PV and the
-//    next QK^T of one run while the other is in its softmax.
+//    next QK^T of one run while the other is in its softmax.  Each tile has an
+//    issuing warp of its own, since the pipe takes an MMA about when it starts:
+//    whatever one warp spends on barriers, the other's MMAs fill (one warp for
+//    both left the tensor core idle for 60% of the time).
 //  * A row's reference m moves only when a score passes it by 2^8 in the
 //    exponent (P then stays below 2^8, and sums and outputs are fp32); the
 //    thread that moves it rescales its O row, with no PV in flight on it since
 //    the QK^T that it waited for was issued after it.
 //  * 0 times an infinity is not 0, so zero probabilities do not hide unseen
 //    values.  Of the value tiles that some row of the unit does not see whole
-//    warp 14 clears the rows past the sequence and every infinity and NaN; the
+//    warp 15 clears the rows past the sequence and every infinity and NaN; the
 //    epilogue adds those a row does see back (rare, one flag per unit).
 //  * Every wait is bounded; a role that gives up raises a shared abort flag,
 //    copies and MMAs in flight complete, the CTA frees its tensor memory
@@ -49,7 +52,7 @@ namespace {
 
 constexpr int kPtKeys = 128;                          // keys of a tile
 constexpr int kPtStages = 4;                          // ring: key tiles in even stages, values in odd
-constexpr int kPtWarpEpi = 8, kPtWarpKv = 12, kPtWarpMma = 13, kPtWarpClear = 14;
+constexpr int kPtWarpEpi = 8, kPtWarpLoad = 12, kPtWarpMma = 13, kPtWarpClear = 15;
 constexpr int kPtThreads = 512;
 constexpr int kPtUnits = 4;                           // work numbers ahead
 constexpr float kPtLazy = 8.0f;                       // log2 of the largest unnormalised p
@@ -72,14 +75,14 @@ enum : int {
   kPtQEmpty = kPtQFull + 2,
   kPtSFull = kPtQEmpty + 2,
   kPtPReady = kPtSFull + 2,
-  kPtOFull = kPtPReady + 2,
+  kPtOFull = kPtPReady + 4,                           // (P: per tile and half of the keys)
   kPtOEmpty = kPtOFull + 2,
   kPtSumFull = kPtOEmpty + 2,
   kPtVClear = kPtSumFull + 2,                         // per ring stage
   kPtUnitFull = kPtVClear + kPtStages,
   kPtUnitEmpty = kPtUnitFull + kPtUnits,
-  kPtDrain = kPtUnitEmpty + kPtUnits,
-  kPtBars
+  kPtDrain = kPtUnitEmpty + kPtUnits,                 // per tile
+  kPtBars = kPtDrain + 2
 };
 constexpr int kPtSmem = kPtOffBar + 8 * kPtBars + 1024;
 static_assert(kPtOffBar % 8 == 0 && kPtOffUnit % 16 == 0, "alignment");
@@ -192,15 +195,16 @@ __device__ __forceinline__ void pt_tma_4d(uint32_t dst, const void *tmap, int x,
 }
 
 // One key tile of one row: S from TMEM, the reference and the denominator
-// brought up to date (the O row with them), P as bf16 over S's columns.
-// kMask: keys past `lim` (within the tile) are not seen.
-template <bool kMask>
-__device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, int lim, float scale2,
-                                           bool fresh, float &m_ref, float &lsum) {
+// brought up to date (the O row with them), P as bf16 over S's columns, its two
+// halves announced one after the other.  Keys past `lim` (within the tile) are
+// not seen where `masked`.
+__device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, bool masked, int lim,
+                                           float scale2, bool fresh, uint32_t ready, int lane,
+                                           float &m_ref, float &lsum) {
   float x[128];
   tmem_ld64(scol, x);
   tmem_ld64(scol + 64, x + 64);
-  if (kMask) {
+  if (masked) {
 #pragma unroll
     for (int i = 0; i < 128; ++i) x[i] = i <= lim ? x[i] : -INFINITY;
   }
@@ -246,6 +250,12 @@ __device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, int lim
       w[i] = pack_bf16x2(a, b);
     }
     tmem_st16u(scol + c / 2, w);
+    if (c % 64 == 32) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ready + 8 * (c / 64));
+    }
   }
   float a, b;
   unpack_f32x2(pt_add2(sum[0], sum[1]), a, b);
@@ -272,27 +282,29 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   if (tid == 0) {
     for (int s = 0; s < kPtStages; ++s) {
       mbar_init(BAR(kPtKvFull + s), 1);
-      mbar_init(BAR(kPtKvEmpty + s), 1 + (s & 1));     // value tiles: warp 14 too
+      mbar_init(BAR(kPtKvEmpty + s), 2 + (s & 1));     // both tiles; value tiles: warp 15 too
       mbar_init(BAR(kPtVClear + s), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(BAR(kPtQFull + a), 1);
       mbar_init(BAR(kPtQEmpty + a), 1);
       mbar_init(BAR(kPtSFull + a), 1);
-      mbar_init(BAR(kPtPReady + a), 4);
+      mbar_init(BAR(kPtPReady + 2 * a), 4);
+      mbar_init(BAR(kPtPReady + 2 * a + 1), 4);
       mbar_init(BAR(kPtOFull + a), 1);
       mbar_init(BAR(kPtOEmpty + a), 4);
       mbar_init(BAR(kPtSumFull + a), 4);
     }
     for (int e = 0; e < kPtUnits; ++e) {
       mbar_init(BAR(kPtUnitFull + e), 1);
-      mbar_init(BAR(kPtUnitEmpty + e), 8 + 4 + 3);     // softmax, epilogue, warps 12-14
+      mbar_init(BAR(kPtUnitEmpty + e), 8 + 4 + 3);     // softmax, epilogue, warps 13-15
     }
     mbar_init(BAR(kPtDrain), 1);
+    mbar_init(BAR(kPtDrain + 1), 1);
     *abort_s = 0;
     fence_mbarrier_init();
   }
-  if (warp == kPtWarpMma) {
+  if (warp == kPtWarpLoad) {
     tmem_alloc(smem_addr(tmem_slot), kPtTmemCols);
     tmem_relinquish();
   }
@@ -339,15 +351,9 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
           break;
         }
         tc_fence_after();
-        if (j * kPtKeys + kPtKeys - 1 > first)
-          pt_softmax<true>(tl + pt_s(a), tl + pt_o(a), tok - j * kPtKeys, p.scale2, j == n - 1,
-                           m_ref, lsum);
-        else
-          pt_softmax<false>(tl + pt_s(a), tl + pt_o(a), 0, p.scale2, j == n - 1, m_ref, lsum);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(kPtPReady + a));
+        pt_softmax(tl + pt_s(a), tl + pt_o(a), j * kPtKeys + kPtKeys - 1 > first,
+                   tok - j * kPtKeys, p.scale2, j == n - 1, BAR(kPtPReady + 2 * a), lane, m_ref,
+                   lsum);
       }
       if (gave_up) break;
       // the denominators, once the epilogue has read the last unit's
@@ -361,7 +367,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       if (lane == 0) mbar_arrive(BAR(kPtSumFull + a));
       ++done;
     }
-  } else if (warp < kPtWarpKv) {
+  } else if (warp < kPtWarpLoad) {
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
     if (p.err_flags) {
@@ -448,121 +454,172 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-    if (warp == kPtWarpKv) {
-      // ------------------------------------------------------ key, value TMA
-      if (lane == 0) {
-        uint32_t idx = 0;                              // ring entries issued
-        for (int t = 0; !gave_up; ++t) {
-          PtUnit u;
-          if (!take_unit(t, u)) {
-            gave_up = true;
-            break;
-          }
-          mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
-          if (u.len == 0) break;
-          for (int j = u.tiles() - 1; j >= 0 && !gave_up; --j)
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++idx) {
-              const int b = idx % kPtStages;
-              if (idx >= kPtStages &&
-                  !pt_wait(BAR(kPtKvEmpty + b), (idx / kPtStages - 1) & 1, abort_s)) {
-                gave_up = true;
-                break;
-              }
-              mbar_arrive_expect_tx(BAR(kPtKvFull + b), kPtTileBytes);
-              pt_tma_4d(smem_addr(smem + kPtOffKv + b * kPtTileBytes), kv == 0 ? &tm_k : &tm_v, 0,
-                        u.start + j * kPtKeys, 0, u.h, BAR(kPtKvFull + b));
-            }
+    if (warp == kPtWarpLoad) {
+      // ----------------------------------------------- work numbers and TMA
+      uint32_t idx = 0;                                // ring entries issued
+      uint32_t loads[2] = {0, 0};                      // query tiles
+      int64_t w = blockIdx.x;
+      // the next unit of this CTA, announced in entry t
+      auto next_unit = [&](int t, int4 &e) -> bool {
+        e = make_int4(0, 0, 0, 0);
+        for (; w < p.units && e.y == 0; w += gridDim.x) e = pt_find(p, w, lane);
+        const int b = t % kPtUnits;
+        const bool ok =
+            t < kPtUnits || pt_wait(BAR(kPtUnitEmpty + b), (t / kPtUnits - 1) & 1, abort_s);
+        if (__any_sync(0xFFFFFFFFu, !ok)) return false;
+        if (lane == 0) {
+          unit_s[b] = e;
+          mbar_arrive(BAR(kPtUnitFull + b));
         }
-        // copies in flight land before the CTA leaves
+        return true;
+      };
+      // key tile j and value tile j of the unit
+      auto load_kv = [&](const PtUnit &u, int j) -> bool {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++idx) {
+          const int b = idx % kPtStages;
+          if (idx >= kPtStages && !pt_wait(BAR(kPtKvEmpty + b), (idx / kPtStages - 1) & 1, abort_s))
+            return false;
+          mbar_arrive_expect_tx(BAR(kPtKvFull + b), kPtTileBytes);
+          pt_tma_4d(smem_addr(smem + kPtOffKv + b * kPtTileBytes), kv == 0 ? &tm_k : &tm_v, 0,
+                    u.start + j * kPtKeys, 0, u.h, BAR(kPtKvFull + b));
+        }
+        return true;
+      };
+      auto load_q = [&](const PtUnit &u) -> bool {
+#pragma unroll 1
+        for (int a = 0; a < 2; ++a) {
+          if ((a == 0 ? u.n0 : u.n1) == 0) continue;
+          if (loads[a] > 0 && !pt_wait(BAR(kPtQEmpty + a), (loads[a] - 1) & 1, abort_s)) return false;
+          ++loads[a];
+          const uint32_t dst = smem_addr(smem + kPtOffQ + a * kPtTileBytes);
+          mbar_arrive_expect_tx(BAR(kPtQFull + a), 2u * 128u * p.TQ * p.G);
+          for (int half = 0; half < 2; ++half)
+            pt_tma_4d(dst + half * kPtHalf, &tm_q, 0, u.h * p.G, u.start + u.tok0 + a * p.TQ, half,
+                      BAR(kPtQFull + a));
+        }
+        return true;
+      };
+      int4 e;
+      gave_up = !next_unit(0, e);
+      for (int t = 0; !gave_up && e.y > 0; ++t) {
+        PtUnit u;
+        u.shape(e, p.TQ);
+        // the first keys and values ahead of the queries, whose tiles are free
+        // only once the last unit's products with them are done
+        bool ok = true;
+        int j = u.tiles() - 1;
+        if (lane == 0) ok = load_kv(u, j) && load_q(u);
+        if (__any_sync(0xFFFFFFFFu, !ok) || !next_unit(t + 1, e)) {
+          gave_up = true;
+          break;
+        }
+        if (lane == 0)
+          while (ok && --j >= 0) ok = load_kv(u, j);
+        gave_up = __any_sync(0xFFFFFFFFu, !ok);
+      }
+      // copies in flight land before the CTA leaves
+      if (lane == 0) {
         for (uint32_t v = idx > kPtStages ? idx - kPtStages : 0; v < idx; ++v)
           mbar_wait_sleep_bounded(BAR(kPtKvFull + v % kPtStages), (v / kPtStages) & 1);
+        for (int a = 0; a < 2; ++a)
+          if (loads[a] > 0) mbar_wait_sleep_bounded(BAR(kPtQFull + a), (loads[a] - 1) & 1);
       }
-    } else if (warp == kPtWarpMma) {
-      // ---------------------------------------------------------------- MMA
+    } else if (warp < kPtWarpClear) {
+      // ----------------------------------------------------- MMAs of a tile
+      // Each turn: PV of the present step and QK^T of the next.  Everything but
+      // P is waited for before P, so the turn's MMAs follow one another.
       if (lane == 0) {
-        const uint32_t q0 = smem_addr(smem + kPtOffQ), kv0 = smem_addr(smem + kPtOffKv);
-        uint32_t step = 0;                             // key tiles so far: ring entries 2 step, + 1
-        uint32_t pr[2] = {0, 0};                       // PV steps of each tile
-        uint32_t units[2] = {0, 0};                    // units whose first QK^T / PV was issued
-        uint32_t o_units[2] = {0, 0};
-        uint32_t clears = 0;                           // parity of edge tiles per ring stage
-        // QK^T of tile a with the key tile of step st
-        auto qk = [&](const PtUnit &u, int a, int j, uint32_t st) -> bool {
-          const uint32_t e = 2 * st, b = e % kPtStages;
-          if (!pt_wait(BAR(kPtKvFull + b), (e / kPtStages) & 1, abort_s)) return false;
-          if (j == (a == 0 ? u.n0 : u.n1) - 1 &&
-              !pt_wait(BAR(kPtQFull + a), units[a]++ & 1, abort_s))
-            return false;
-          tc_fence_after();
-          const uint64_t qd = smem_desc(q0 + a * kPtTileBytes, 16, 1024, kSmemSwizzle128);
-          const uint64_t kd = smem_desc(kv0 + b * kPtTileBytes, 16, 1024, kSmemSwizzle128);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk & 3) * 2 + (kk >> 2) * (kPtHalf >> 4);
-            tc_mma_f16(tmem + pt_s(a), qd + off, kd + off, kPtIdescQK, kk != 0);
-          }
-          tc_commit(BAR(kPtSFull + a));
-          if (j == 0) tc_commit(BAR(kPtQEmpty + a));
-          return true;
-        };
+        const int a = warp - kPtWarpMma;
+        const uint32_t q0 = smem_addr(smem + kPtOffQ + a * kPtTileBytes);
+        const uint32_t kv0 = smem_addr(smem + kPtOffKv);
+        const uint32_t s_col = tmem + pt_s(a), o_col = tmem + pt_o(a);
+        uint32_t step = ~0u;                           // ring entries 2 step, 2 step + 1
+        uint32_t par_q = 0, par_p = 0, par_o = 1;      // barrier parities
+        uint32_t par_clear = 0;                        // bit per ring stage
         PtUnit u, nx;
-        int t = 0;
-        bool ok = take_unit(t, u);
-        if (ok) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
-        if (ok && u.len > 0) {
-          const int j = u.tiles() - 1;
-#pragma unroll
-          for (int a = 0; a < 2 && ok; ++a)
-            if (u.active(a, j)) ok = qk(u, a, j, 0);
-          if (ok) tc_commit(BAR(kPtKvEmpty + 0));
+        int t = 0, j = 0, jn = 0;
+        u.n0 = u.n1 = 0;
+        bool ok = take_unit(t, nx);
+        if (ok) {
+          mbar_arrive(BAR(kPtUnitEmpty));
+          jn = nx.tiles() - 1;
         }
-        while (ok && u.len > 0) {
-          const int n = u.tiles();
-          for (int j = n - 1; j >= 0 && ok; --j, ++step) {
-            int jn = j - 1;
-            if (j == 0) {
-              ok = take_unit(++t, nx);
-              if (!ok) break;
-              mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
-              jn = nx.len > 0 ? nx.tiles() - 1 : -1;
-            } else {
-              nx = u;
+        while (ok) {
+          const uint32_t ev = 2 * step + 1, bv = ev % kPtStages;       // values of this step
+          const uint32_t ek = 2 * step + 2, bk = ek % kPtStages;       // keys of the next
+          const bool pv = u.active(a, j), next = nx.len > 0, qk = next && nx.active(a, jn);
+          const bool pv_first = j == (a == 0 ? u.n0 : u.n1) - 1;
+          const bool qk_first = jn == (a == 0 ? nx.n0 : nx.n1) - 1;
+          const uint64_t vd = smem_desc(kv0 + bv * kPtTileBytes, kPtHalf, 1024, kSmemSwizzle128);
+          const uint64_t qd = smem_desc(q0, 16, 1024, kSmemSwizzle128);
+          const uint64_t kd = smem_desc(kv0 + bk * kPtTileBytes, 16, 1024, kSmemSwizzle128);
+          if (step != ~0u) {
+            ok = pt_wait(BAR(kPtKvFull + bv), (ev / kPtStages) & 1, abort_s);
+            if (ok && pv && u.edge(j))
+              ok = pt_wait(BAR(kPtVClear + bv), (par_clear >> bv) & 1, abort_s);
+            if (u.edge(j)) par_clear ^= 1u << bv;
+          }
+          if (ok && next) ok = pt_wait(BAR(kPtKvFull + bk), (ek / kPtStages) & 1, abort_s);
+          if (ok && pv) {
+            if (pv_first) {
+              ok = pt_wait(BAR(kPtOEmpty + a), par_o, abort_s);
+              par_o ^= 1u;
             }
-            const uint32_t e = 2 * step + 1, b = e % kPtStages;
+            // 64 keys at a time, as the softmax has them ready
+            ok = ok && pt_wait(BAR(kPtPReady + 2 * a), par_p, abort_s);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-            for (int a = 0; a < 2 && ok; ++a) {
-              if (u.active(a, j)) {
-                const bool first = j == (a == 0 ? u.n0 : u.n1) - 1;
-                ok = pt_wait(BAR(kPtPReady + a), pr[a]++ & 1, abort_s) &&
-                     pt_wait(BAR(kPtKvFull + b), (e / kPtStages) & 1, abort_s);
-                if (ok && first && o_units[a]++ > 0)
-                  ok = pt_wait(BAR(kPtOEmpty + a), (o_units[a] - 2) & 1, abort_s);
-                if (ok && u.edge(j)) ok = pt_wait(BAR(kPtVClear + b), (clears >> b) & 1, abort_s);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t vd = smem_desc(kv0 + b * kPtTileBytes, kPtHalf, 1024, kSmemSwizzle128);
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16_tmem_a(o_col, s_col + 8 * kk, vd + (2048 >> 4) * kk, kPtIdescPV,
+                                (pv_first && kk == 0) ? 0u : 1u);
+            ok = pt_wait(BAR(kPtPReady + 2 * a + 1), par_p, abort_s);
+            if (!ok) break;
+            par_p ^= 1u;
+            tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                  tc_mma_f16_tmem_a(tmem + pt_o(a), tmem + pt_s(a) + 8 * kk, vd + (2048 >> 4) * kk,
-                                    kPtIdescPV, (first && kk == 0) ? 0u : 1u);
-                if (j == 0) tc_commit(BAR(kPtOFull + a));
-              }
-              if (jn >= 0 && nx.active(a, jn)) ok = qk(nx, a, jn, step + 1);
+            for (int kk = 4; kk < 8; ++kk)
+              tc_mma_f16_tmem_a(o_col, s_col + 8 * kk, vd + (2048 >> 4) * kk, kPtIdescPV, 1u);
+            if (j == 0) tc_commit(BAR(kPtOFull + a));
+          }
+          if (ok && qk) {
+            if (qk_first) {
+              ok = pt_wait(BAR(kPtQFull + a), par_q, abort_s);
+              par_q ^= 1u;
             }
             if (!ok) break;
-            if (u.edge(j)) clears ^= 1u << b;
-            tc_commit(BAR(kPtKvEmpty + b));
-            if (jn >= 0) tc_commit(BAR(kPtKvEmpty + (2 * (step + 1)) % kPtStages));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (kk & 3) * 2 + (kk >> 2) * (kPtHalf >> 4);
+              tc_mma_f16(s_col, qd + off, kd + off, kPtIdescQK, kk != 0);
+            }
+            tc_commit(BAR(kPtSFull + a));
+            if (jn == 0) tc_commit(BAR(kPtQEmpty + a));
           }
+          if (!ok) break;
+          if (step != ~0u) tc_commit(BAR(kPtKvEmpty + bv));
+          if (!next) break;
+          tc_commit(BAR(kPtKvEmpty + bk));
           u = nx;
+          j = jn;
+          ++step;
+          if (j == 0) {
+            ok = take_unit(++t, nx);
+            if (ok) {
+              mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
+              jn = nx.tiles() - 1;
+            }
+          } else {
+            --jn;
+          }
         }
         gave_up = !ok;
         // every MMA issued has completed before the tensor memory is freed
-        tc_commit(BAR(kPtDrain));
-        mbar_wait_sleep_bounded(BAR(kPtDrain), 0);
+        tc_commit(BAR(kPtDrain + a));
+        mbar_wait_sleep_bounded(BAR(kPtDrain + a), 0);
       }
-    } else if (warp == kPtWarpClear) {
+    } else {
       // ------------------------------------------- edge value tiles cleared
       uint32_t step = 0;
       for (int t = 0; !gave_up; ++t) {
@@ -636,44 +693,6 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
           }
         }
       }
-    } else {
-      // --------------------------------------------- work numbers, query TMA
-      uint32_t loads[2] = {0, 0};
-      int64_t w = blockIdx.x;
-      for (int t = 0;; ++t) {
-        int4 e = make_int4(0, 0, 0, 0);
-        for (; w < p.units && e.y == 0; w += gridDim.x) e = pt_find(p, w, lane);
-        const int b = t % kPtUnits;
-        bool ok = t < kPtUnits || pt_wait(BAR(kPtUnitEmpty + b), (t / kPtUnits - 1) & 1, abort_s);
-        if (__any_sync(0xFFFFFFFFu, !ok)) {
-          gave_up = true;
-          break;
-        }
-        if (lane == 0) {
-          unit_s[b] = e;
-          mbar_arrive(BAR(kPtUnitFull + b));
-          PtUnit u;
-          u.shape(e, p.TQ);
-          for (int a = 0; a < 2 && e.y > 0; ++a) {
-            if ((a == 0 ? u.n0 : u.n1) == 0) continue;
-            if (loads[a] > 0 && !pt_wait(BAR(kPtQEmpty + a), (loads[a] - 1) & 1, abort_s)) {
-              ok = false;
-              break;
-            }
-            ++loads[a];
-            const uint32_t dst = smem_addr(smem + kPtOffQ + a * kPtTileBytes);
-            mbar_arrive_expect_tx(BAR(kPtQFull + a), 2u * 128u * p.TQ * p.G);
-            for (int half = 0; half < 2; ++half)
-              pt_tma_4d(dst + half * kPtHalf, &tm_q, 0, u.h * p.G, u.start + u.tok0 + a * p.TQ, half,
-                        BAR(kPtQFull + a));
-          }
-        }
-        gave_up = __any_sync(0xFFFFFFFFu, !ok);
-        if (gave_up || e.y == 0) break;
-      }
-      if (lane == 0)
-        for (int a = 0; a < 2; ++a)
-          if (loads[a] > 0) mbar_wait_sleep_bounded(BAR(kPtQFull + a), (loads[a] - 1) & 1);
     }
   }
   if (gave_up) {
@@ -683,7 +702,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kPtWarpMma) {
+  if (warp == kPtWarpLoad) {
     tc_fence_after();
     tmem_dealloc(tmem, kPtTmemCols);
   }
