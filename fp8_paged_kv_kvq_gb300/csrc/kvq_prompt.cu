@@ -82,7 +82,8 @@ enum : int {
   kPtUnitFull = kPtVClear + kPtStages,
   kPtUnitEmpty = kPtUnitFull + kPtUnits,
   kPtDrain = kPtUnitEmpty + kPtUnits,                 // per tile
-  kPtBars = kPtDrain + 2
+  kPtTurn = kPtDrain + 2,                             // per tile
+  kPtBars = kPtTurn + 2
 };
 constexpr int kPtSmem = kPtOffBar + 8 * kPtBars + 1024;
 static_assert(kPtOffBar % 8 == 0 && kPtOffUnit % 16 == 0, "alignment");
@@ -294,13 +295,13 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       mbar_init(BAR(kPtOFull + a), 1);
       mbar_init(BAR(kPtOEmpty + a), 4);
       mbar_init(BAR(kPtSumFull + a), 4);
+      mbar_init(BAR(kPtDrain + a), 1);
+      mbar_init(BAR(kPtTurn + a), 1);
     }
     for (int e = 0; e < kPtUnits; ++e) {
       mbar_init(BAR(kPtUnitFull + e), 1);
       mbar_init(BAR(kPtUnitEmpty + e), 8 + 4 + 3);     // softmax, epilogue, warps 13-15
     }
-    mbar_init(BAR(kPtDrain), 1);
-    mbar_init(BAR(kPtDrain + 1), 1);
     *abort_s = 0;
     fence_mbarrier_init();
   }
@@ -537,6 +538,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         uint32_t step = ~0u;                           // ring entries 2 step, 2 step + 1
         uint32_t par_q = 0, par_p = 0, par_o = 1;      // barrier parities
         uint32_t par_clear = 0;                        // bit per ring stage
+        uint32_t par_turn = a ^ 1;                     // tile 0 goes first
         PtUnit u, nx;
         int t = 0, j = 0, jn = 0;
         u.n0 = u.n1 = 0;
@@ -566,9 +568,12 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
               ok = pt_wait(BAR(kPtOEmpty + a), par_o, abort_s);
               par_o ^= 1u;
             }
-            // 64 keys at a time, as the softmax has them ready
             ok = ok && pt_wait(BAR(kPtPReady + 2 * a), par_p, abort_s);
-            if (!ok) break;
+          }
+          ok = ok && pt_wait(BAR(kPtTurn + a), par_turn, abort_s);
+          par_turn ^= 1u;
+          if (ok && pv) {
+            // 64 keys at a time, as the softmax has them ready
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -581,7 +586,6 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
 #pragma unroll
             for (int kk = 4; kk < 8; ++kk)
               tc_mma_f16_tmem_a(o_col, s_col + 8 * kk, vd + (2048 >> 4) * kk, kPtIdescPV, 1u);
-            if (j == 0) tc_commit(BAR(kPtOFull + a));
           }
           if (ok && qk) {
             if (qk_first) {
@@ -595,9 +599,11 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
               tc_mma_f16(s_col, qd + off, kd + off, kPtIdescQK, kk != 0);
             }
             tc_commit(BAR(kPtSFull + a));
-            if (jn == 0) tc_commit(BAR(kPtQEmpty + a));
           }
           if (!ok) break;
+          mbar_arrive(BAR(kPtTurn + (a ^ 1)));
+          if (pv && j == 0) tc_commit(BAR(kPtOFull + a));
+          if (qk && jn == 0) tc_commit(BAR(kPtQEmpty + a));
           if (step != ~0u) tc_commit(BAR(kPtKvEmpty + bv));
           if (!next) break;
           tc_commit(BAR(kPtKvEmpty + bk));
