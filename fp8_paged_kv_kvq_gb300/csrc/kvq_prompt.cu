@@ -98,6 +98,37 @@ constexpr uint32_t kPtBf16 = (1u << 7) | (1u << 10);   // A and B bf16
 constexpr uint32_t kPtIdescQK = mma_idesc(128, kPtKeys, false, false) | kPtBf16;
 constexpr uint32_t kPtIdescPV = mma_idesc(128, kHeadDim, false, true) | kPtBf16;
 
+
+// The upper word of every operand's shared-memory descriptor (smem_desc:
+// stride offset 1024, version 1, 128-byte swizzle) and the two leading offsets.
+constexpr uint32_t kPtDescHi = (1024u >> 4) | (1u << 14) | (kSmemSwizzle128 << 29);
+constexpr uint32_t kPtKMajor = 1u << 16, kPtMnMajor = (kPtHalf >> 4) << 16;
+
+// S (+)= Q K^T and O (+)= P V, 16 dims or keys each: the descriptors' lower
+// words vary, the rest is constant (an issuing warp's time goes by the
+// instructions around each MMA).
+__device__ __forceinline__ void pt_mma_qk(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n"
+      :: "r"(d), "r"(a_lo), "r"(b_lo), "n"(kPtIdescQK), "r"(acc), "n"(kPtDescHi) : "memory");
+}
+__device__ __forceinline__ void pt_mma_pv(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n"
+      :: "r"(d), "r"(a_tmem), "r"(b_lo), "n"(kPtIdescPV), "r"(acc), "n"(kPtDescHi) : "memory");
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool pt_elect() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(r));
+  return r != 0;
+}
+
 struct PromptParams {
   const uint16_t *v;
   uint16_t *out;
@@ -140,6 +171,11 @@ __device__ __forceinline__ bool pt_wait_slow(uint32_t bar, uint32_t parity, vola
 }
 __device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
   return mbar_try_wait(bar, parity) || pt_wait_slow(bar, parity, abort);
+}
+
+// The whole warp's (every lane tries; one that gives up speaks for all).
+__device__ __forceinline__ bool pt_wait_all(uint32_t bar, uint32_t parity, volatile int *abort) {
+  return __all_sync(0xFFFFFFFFu, pt_wait(bar, parity, abort));
 }
 
 // A unit: sequence rows [start, start + len), KV head h, tiles from token tok0
@@ -202,20 +238,24 @@ __device__ __forceinline__ void pt_tma_4d(uint32_t dst, const void *tmap, int x,
 __device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, bool masked, int lim,
                                            float scale2, bool fresh, uint32_t ready, int lane,
                                            float &m_ref, float &lsum) {
-  float x[128];
-  tmem_ld64(scol, x);
-  tmem_ld64(scol + 64, x + 64);
-  if (masked) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 64) {
+    float x[64];
+    tmem_ld64(scol + c, x);
+    if (masked) {
 #pragma unroll
-    for (int i = 0; i < 128; ++i) x[i] = i <= lim ? x[i] : -INFINITY;
+      for (int i = 0; i < 64; ++i) x[i] = i <= lim - c ? x[i] : -INFINITY;
+      tmem_st64(scol + c, x);
+    }
+#pragma unroll
+    for (int i = 0; i < 64; i += 8)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
   }
-  float mx[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) mx[q] = fmaxf(x[q], x[q + 4]);
-#pragma unroll
-  for (int i = 8; i < 128; i += 8)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
+  if (masked) tmem_wait_st();
+  uint32_t x0[32], x1[32];
+  tmem_ld32_start(scol, x0);
   const float top = fmaxf(pt_max3(mx[0], mx[1], mx[2]), mx[3]);
   const bool unset = m_ref == -INFINITY;
   const bool move = unset ? top > -INFINITY : (top - m_ref) * scale2 > kPtLazy;
@@ -238,25 +278,34 @@ __device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, bool ma
   const float shift = m_ref == -INFINITY ? 0.0f : -m_ref * scale2;
   const uint64_t sc = pack_f32x2(scale2, scale2), sh = pack_f32x2(shift, shift);
   uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
-#pragma unroll
-  for (int c = 0; c < 128; c += 32) {
+  // 32 keys: P and their share of the denominator
+  auto part = [&](const uint32_t (&x)[32], uint32_t col) {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float a, b;
-      unpack_f32x2(fma_f32x2(pack_f32x2(x[c + 2 * i], x[c + 2 * i + 1]), sc, sh), a, b);
+      unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                             sc, sh), a, b);
       a = pt_ex2(a);
       b = pt_ex2(b);
       sum[i & 1] = pt_add2(sum[i & 1], pack_f32x2(a, b));
       w[i] = pack_bf16x2(a, b);
     }
-    tmem_st16u(scol + c / 2, w);
-    if (c % 64 == 32) {
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ready + 8 * (c / 64));
-    }
+    tmem_st16u(col, w);
+  };
+  tmem_ld32_done(x0);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    tmem_ld32_start(scol + 64 * h + 32, x1);
+    part(x0, scol + 32 * h);
+    tmem_ld32_done(x1);
+    if (h == 0) tmem_ld32_start(scol + 64, x0);
+    part(x1, scol + 32 * h + 16);
+    if (h == 0) tmem_ld32_done(x0);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(ready + 8 * h);
   }
   float a, b;
   unpack_f32x2(pt_add2(sum[0], sum[1]), a, b);
@@ -528,103 +577,111 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       }
     } else if (warp < kPtWarpClear) {
       // ----------------------------------------------------- MMAs of a tile
-      // Each turn: PV of the present step and QK^T of the next.  Everything but
-      // P is waited for before P, so the turn's MMAs follow one another.
-      if (lane == 0) {
-        const int a = warp - kPtWarpMma;
-        const uint32_t q0 = smem_addr(smem + kPtOffQ + a * kPtTileBytes);
-        const uint32_t kv0 = smem_addr(smem + kPtOffKv);
-        const uint32_t s_col = tmem + pt_s(a), o_col = tmem + pt_o(a);
-        uint32_t step = ~0u;                           // ring entries 2 step, 2 step + 1
-        uint32_t par_q = 0, par_p = 0, par_o = 1;      // barrier parities
-        uint32_t par_clear = 0;                        // bit per ring stage
-        uint32_t par_turn = a ^ 1;                     // tile 0 goes first
-        PtUnit u, nx;
-        int t = 0, j = 0, jn = 0;
-        u.n0 = u.n1 = 0;
-        bool ok = take_unit(t, nx);
-        if (ok) {
-          mbar_arrive(BAR(kPtUnitEmpty));
-          jn = nx.tiles() - 1;
+      // Each turn: PV of the present step and QK^T of the next, tile 0's and
+      // tile 1's bursts one after the other (free to interleave, the tiles fell
+      // into step: both in the softmax, then both at the tensor core).
+      // Everything but P is waited for before the turn.  The warp stays
+      // converged and elects a lane for each group of MMAs: addresses stay
+      // uniform, 8 instructions an MMA instead of 11 for a lone lane.
+      const int a = warp - kPtWarpMma;
+      const uint32_t q_lo = (smem_addr(smem + kPtOffQ + a * kPtTileBytes) >> 4) | kPtKMajor;
+      const uint32_t kv0 = smem_addr(smem + kPtOffKv) >> 4;
+      const uint32_t s_col = tmem + pt_s(a), o_col = tmem + pt_o(a);
+      uint32_t step = ~0u;                             // ring entries 2 step, 2 step + 1
+      uint32_t par_q = 0, par_p = 0, par_o = 1;        // barrier parities
+      uint32_t par_clear = 0;                          // bit per ring stage
+      uint32_t par_turn = a ^ 1;                       // tile 0 goes first
+      PtUnit u, nx;
+      int t = 0, j = 0, jn = 0;
+      u.n0 = u.n1 = 0;
+      auto next_unit = [&]() -> bool {
+        if (!__all_sync(0xFFFFFFFFu, take_unit(t, nx))) return false;
+        if (lane == 0) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
+        jn = nx.tiles() - 1;
+        ++t;
+        return true;
+      };
+      bool ok = next_unit();
+      while (ok) {
+        const uint32_t ev = 2 * step + 1, bv = ev % kPtStages;         // values of this step
+        const uint32_t ek = 2 * step + 2, bk = ek % kPtStages;         // keys of the next
+        const bool pv = u.active(a, j), next = nx.len > 0, qk = next && nx.active(a, jn);
+        const bool pv_first = j == (a == 0 ? u.n0 : u.n1) - 1;
+        const bool qk_first = jn == (a == 0 ? nx.n0 : nx.n1) - 1;
+        const uint32_t v_lo = (kv0 + bv * (kPtTileBytes >> 4)) | kPtMnMajor;
+        const uint32_t k_lo = (kv0 + bk * (kPtTileBytes >> 4)) | kPtKMajor;
+        if (step != ~0u) {
+          ok = pt_wait_all(BAR(kPtKvFull + bv), (ev / kPtStages) & 1, abort_s);
+          if (ok && pv && u.edge(j))
+            ok = pt_wait_all(BAR(kPtVClear + bv), (par_clear >> bv) & 1, abort_s);
+          if (u.edge(j)) par_clear ^= 1u << bv;
         }
-        while (ok) {
-          const uint32_t ev = 2 * step + 1, bv = ev % kPtStages;       // values of this step
-          const uint32_t ek = 2 * step + 2, bk = ek % kPtStages;       // keys of the next
-          const bool pv = u.active(a, j), next = nx.len > 0, qk = next && nx.active(a, jn);
-          const bool pv_first = j == (a == 0 ? u.n0 : u.n1) - 1;
-          const bool qk_first = jn == (a == 0 ? nx.n0 : nx.n1) - 1;
-          const uint64_t vd = smem_desc(kv0 + bv * kPtTileBytes, kPtHalf, 1024, kSmemSwizzle128);
-          const uint64_t qd = smem_desc(q0, 16, 1024, kSmemSwizzle128);
-          const uint64_t kd = smem_desc(kv0 + bk * kPtTileBytes, 16, 1024, kSmemSwizzle128);
-          if (step != ~0u) {
-            ok = pt_wait(BAR(kPtKvFull + bv), (ev / kPtStages) & 1, abort_s);
-            if (ok && pv && u.edge(j))
-              ok = pt_wait(BAR(kPtVClear + bv), (par_clear >> bv) & 1, abort_s);
-            if (u.edge(j)) par_clear ^= 1u << bv;
+        if (ok && next) ok = pt_wait_all(BAR(kPtKvFull + bk), (ek / kPtStages) & 1, abort_s);
+        if (ok && pv) {
+          if (pv_first) {
+            ok = pt_wait_all(BAR(kPtOEmpty + a), par_o, abort_s);
+            par_o ^= 1u;
           }
-          if (ok && next) ok = pt_wait(BAR(kPtKvFull + bk), (ek / kPtStages) & 1, abort_s);
-          if (ok && pv) {
-            if (pv_first) {
-              ok = pt_wait(BAR(kPtOEmpty + a), par_o, abort_s);
-              par_o ^= 1u;
-            }
-            ok = ok && pt_wait(BAR(kPtPReady + 2 * a), par_p, abort_s);
-          }
-          ok = ok && pt_wait(BAR(kPtTurn + a), par_turn, abort_s);
-          par_turn ^= 1u;
-          if (ok && pv) {
-            // 64 keys at a time, as the softmax has them ready
-            tc_fence_after();
+          ok = ok && pt_wait_all(BAR(kPtPReady + 2 * a), par_p, abort_s);
+        }
+        ok = ok && pt_wait_all(BAR(kPtTurn + a), par_turn, abort_s);
+        par_turn ^= 1u;
+        if (ok && pv) {
+          // 64 keys at a time, as the softmax has them ready
+          tc_fence_after();
+          if (pt_elect()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f16_tmem_a(o_col, s_col + 8 * kk, vd + (2048 >> 4) * kk, kPtIdescPV,
-                                (pv_first && kk == 0) ? 0u : 1u);
-            ok = pt_wait(BAR(kPtPReady + 2 * a + 1), par_p, abort_s);
-            if (!ok) break;
-            par_p ^= 1u;
-            tc_fence_after();
+              pt_mma_pv(o_col, s_col + 8 * kk, v_lo + (2048 >> 4) * kk,
+                        (pv_first && kk == 0) ? 0u : 1u);
+          }
+          ok = pt_wait_all(BAR(kPtPReady + 2 * a + 1), par_p, abort_s);
+          if (!ok) break;
+          par_p ^= 1u;
+          tc_fence_after();
+          if (pt_elect()) {
 #pragma unroll
             for (int kk = 4; kk < 8; ++kk)
-              tc_mma_f16_tmem_a(o_col, s_col + 8 * kk, vd + (2048 >> 4) * kk, kPtIdescPV, 1u);
+              pt_mma_pv(o_col, s_col + 8 * kk, v_lo + (2048 >> 4) * kk, 1u);
           }
-          if (ok && qk) {
-            if (qk_first) {
-              ok = pt_wait(BAR(kPtQFull + a), par_q, abort_s);
-              par_q ^= 1u;
-            }
-            if (!ok) break;
+        }
+        if (ok && qk) {
+          if (qk_first) {
+            ok = pt_wait_all(BAR(kPtQFull + a), par_q, abort_s);
+            par_q ^= 1u;
+          }
+          if (!ok) break;
+          if (pt_elect()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
               const uint32_t off = (kk & 3) * 2 + (kk >> 2) * (kPtHalf >> 4);
-              tc_mma_f16(s_col, qd + off, kd + off, kPtIdescQK, kk != 0);
+              pt_mma_qk(s_col, q_lo + off, k_lo + off, kk != 0);
             }
             tc_commit(BAR(kPtSFull + a));
           }
-          if (!ok) break;
+        }
+        if (!ok) break;
+        if (pt_elect()) {
           mbar_arrive(BAR(kPtTurn + (a ^ 1)));
           if (pv && j == 0) tc_commit(BAR(kPtOFull + a));
           if (qk && jn == 0) tc_commit(BAR(kPtQEmpty + a));
           if (step != ~0u) tc_commit(BAR(kPtKvEmpty + bv));
-          if (!next) break;
-          tc_commit(BAR(kPtKvEmpty + bk));
-          u = nx;
-          j = jn;
-          ++step;
-          if (j == 0) {
-            ok = take_unit(++t, nx);
-            if (ok) {
-              mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
-              jn = nx.tiles() - 1;
-            }
-          } else {
-            --jn;
-          }
+          if (next) tc_commit(BAR(kPtKvEmpty + bk));
         }
-        gave_up = !ok;
-        // every MMA issued has completed before the tensor memory is freed
-        tc_commit(BAR(kPtDrain + a));
-        mbar_wait_sleep_bounded(BAR(kPtDrain + a), 0);
+        if (!next) break;
+        u = nx;
+        j = jn;
+        ++step;
+        if (j == 0)
+          ok = next_unit();
+        else
+          --jn;
       }
+      gave_up = !ok;
+      // every MMA issued has completed before the tensor memory is freed
+      __syncwarp();
+      if (pt_elect()) tc_commit(BAR(kPtDrain + a));
+      mbar_wait_sleep_bounded(BAR(kPtDrain + a), 0);
     } else {
       // ------------------------------------------- edge value tiles cleared
       uint32_t step = 0;
