@@ -15,7 +15,9 @@
 //    sequence's (TU tokens per unit): at least ceil(len / TU) of them, so a
 //    unit number finds its sequence by a search over cu_seqlens, with no plan
 //    launch, no workspace and no bound on the number of sequences.
-//  * Persistent CTAs of 512 threads, one per SM.  Warps 0-3 and 4-7: softmax of
+//  * CTAs of 512 threads, one per SM, that go on with the units of blocks that
+//    have not started (cluster launch control) until there are none, longest
+//    rows of a sequence first.  Warps 0-3 and 4-7: softmax of
 //    tile 0 and tile 1 (a thread owns a TMEM lane, a row); 8-11: the epilogue,
 //    which overlaps the next unit; 12: work numbers and TMA; 13 and 14: the MMAs
 //    of tile 0 and tile 1; 15: clears what the edge value tiles must not
@@ -66,7 +68,8 @@ constexpr int kPtOffOut = kPtOffKv + kPtStages * kPtTileBytes;   // 4 warps x 32
 constexpr int kPtOffSum = kPtOffOut + kPtTileBytes;              // [tile][128] denominators
 constexpr int kPtOffUnit = kPtOffSum + 2 * 128 * 4;
 constexpr int kPtOffDirty = kPtOffUnit + kPtUnits * 16;
-constexpr int kPtOffMisc = kPtOffDirty + kPtUnits * 4;           // tmem base, abort
+constexpr int kPtOffSteal = kPtOffDirty + kPtUnits * 4;          // two answers of 16 bytes
+constexpr int kPtOffMisc = kPtOffSteal + 32;                     // tmem base, abort
 constexpr int kPtOffBar = kPtOffMisc + 16;
 enum : int {
   kPtKvFull = 0,
@@ -83,10 +86,11 @@ enum : int {
   kPtUnitEmpty = kPtUnitFull + kPtUnits,
   kPtDrain = kPtUnitEmpty + kPtUnits,                 // per tile
   kPtTurn = kPtDrain + 2,                             // per tile
-  kPtBars = kPtTurn + 2
+  kPtSteal = kPtTurn + 2,
+  kPtBars
 };
 constexpr int kPtSmem = kPtOffBar + 8 * kPtBars + 1024;
-static_assert(kPtOffBar % 8 == 0 && kPtOffUnit % 16 == 0, "alignment");
+static_assert(kPtOffBar % 8 == 0 && kPtOffUnit % 16 == 0 && kPtOffSteal % 16 == 0, "alignment");
 static_assert(kPtSmem <= 227 * 1024, "shared memory budget");
 
 // TMEM: S of tile a at 128 a (its P over the first 64 columns), O at 256 + 128 a
@@ -198,6 +202,10 @@ struct PtUnit {
   __device__ __forceinline__ bool active(int a, int j) const { return j < (a == 0 ? n0 : n1); }
 };
 
+__device__ __forceinline__ bool pt_bounds_ok(const PromptParams &p, int begin, int end) {
+  return begin >= 0 && end >= begin && end <= p.num_tokens && end - begin <= p.max_seqlen;
+}
+
 // Work number w as a unit (len 0: none there).  All lanes of a warp.
 __device__ __forceinline__ int4 pt_find(const PromptParams &p, int64_t w, int lane) {
   const int TU = 2 * p.TQ;
@@ -216,7 +224,7 @@ __device__ __forceinline__ int4 pt_find(const PromptParams &p, int64_t w, int la
     if (step == 1) break;
   }
   const int a = __ldg(p.cu + lo), b = __ldg(p.cu + lo + 1);
-  if (a < 0 || b < a || b > p.num_tokens || b - a > p.max_seqlen) return make_int4(0, 0, 0, 0);
+  if (!pt_bounds_ok(p, a, b)) return make_int4(0, 0, 0, 0);
   const int64_t units = (static_cast<int64_t>(b - a) + TU - 1) / TU;
   const int64_t u = units - 1 - (x - (a / TU + lo));                // the longest rows first
   if (u < 0 || u >= units) return make_int4(0, 0, 0, 0);
@@ -229,6 +237,26 @@ __device__ __forceinline__ void pt_tma_4d(uint32_t dst, const void *tmap, int x,
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5}], [%6];\n"
       :: "r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
+}
+
+// Asks for the number of a block of this grid that has not started, which then
+// never starts; the answer (16 bytes) completes on `bar`.
+__device__ __forceinline__ void pt_steal(uint32_t answer, uint32_t bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+      " [%0], [%1];\n" :: "r"(answer), "r"(bar) : "memory");
+}
+// The answer: a block number, or -1 once every block has started.
+__device__ __forceinline__ int64_t pt_stolen(uint32_t answer) {
+  uint32_t some, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+      " selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+      : "=r"(some), "=r"(x) : "r"(answer) : "memory");
+  return some != 0 ? static_cast<int64_t>(x) : -1;
 }
 
 // One key tile of one row: S from TMEM, the reference and the denominator
@@ -347,6 +375,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       mbar_init(BAR(kPtDrain + a), 1);
       mbar_init(BAR(kPtTurn + a), 1);
     }
+    mbar_init(BAR(kPtSteal), 1);
     for (int e = 0; e < kPtUnits; ++e) {
       mbar_init(BAR(kPtUnitFull + e), 1);
       mbar_init(BAR(kPtUnitEmpty + e), 8 + 4 + 3);     // softmax, epilogue, warps 13-15
@@ -420,14 +449,6 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   } else if (warp < kPtWarpLoad) {
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
-    if (p.err_flags) {
-      for (int64_t s = static_cast<int64_t>(blockIdx.x) * 128 + (tid - 32 * kPtWarpEpi); s < p.N;
-           s += static_cast<int64_t>(gridDim.x) * 128) {
-        const int b0 = __ldg(p.cu + s), b1 = __ldg(p.cu + s + 1);
-        if (b0 < 0 || b1 < b0 || b1 > p.num_tokens || b1 - b0 > p.max_seqlen)
-          atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
-      }
-    }
     const int q4 = warp & 3;
     const int m = 32 * q4 + lane;
     const int t_row = (m * p.inv_g) >> 16;
@@ -508,11 +529,30 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       // ----------------------------------------------- work numbers and TMA
       uint32_t idx = 0;                                // ring entries issued
       uint32_t loads[2] = {0, 0};                      // query tiles
+      // the next unit of this CTA, announced in entry t: its own block's first,
+      // then those of blocks that have not started, asked for one ahead
+      const uint32_t steal = smem_addr(smem + kPtOffSteal);
       int64_t w = blockIdx.x;
-      // the next unit of this CTA, announced in entry t
+      uint32_t asked = 0, heard = 0;
+      auto ask = [&]() {
+        if (lane == 0) pt_steal(steal + 16 * (asked & 1), BAR(kPtSteal));
+        ++asked;
+      };
+      ask();
       auto next_unit = [&](int t, int4 &e) -> bool {
         e = make_int4(0, 0, 0, 0);
-        for (; w < p.units && e.y == 0; w += gridDim.x) e = pt_find(p, w, lane);
+        while (w >= 0 && e.y == 0) {
+          e = pt_find(p, w, lane);
+          // (every work number is somebody's, and there are more than sequences)
+          if (lane == 0 && w < p.N && p.err_flags && !pt_bounds_ok(p, __ldg(p.cu + w), __ldg(p.cu + w + 1)))
+            atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
+          if (!pt_wait_all(BAR(kPtSteal), heard & 1, abort_s)) return false;
+          w = pt_stolen(steal + 16 * (heard & 1));
+          ++heard;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (w >= 0) ask();
+        }
         const int b = t % kPtUnits;
         const bool ok =
             t < kPtUnits || pt_wait(BAR(kPtUnitEmpty + b), (t / kPtUnits - 1) & 1, abort_s);
@@ -574,6 +614,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
           mbar_wait_sleep_bounded(BAR(kPtKvFull + v % kPtStages), (v / kPtStages) & 1);
         for (int a = 0; a < 2; ++a)
           if (loads[a] > 0) mbar_wait_sleep_bounded(BAR(kPtQFull + a), (loads[a] - 1) & 1);
+        if (asked > heard) mbar_wait_sleep_bounded(BAR(kPtSteal), heard & 1);
       }
     } else if (warp < kPtWarpClear) {
       // ----------------------------------------------------- MMAs of a tile
@@ -814,8 +855,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  const int64_t grid = p.units < a.sms ? p.units : a.sms;
-  return launch_overlapped(prompt_attention_kernel, dim3(static_cast<unsigned>(grid)),
+  return launch_overlapped(prompt_attention_kernel, dim3(static_cast<unsigned>(p.units)),
                            dim3(kPtThreads), kPtSmem, stream, p, mq, mk, mv);
 }
 
