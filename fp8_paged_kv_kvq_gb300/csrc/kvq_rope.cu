@@ -21,10 +21,17 @@ namespace kvq {
 
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeWarps = 4;
 constexpr int kRopeLanes = 4;                       // lanes of a row
-constexpr int kRopeRows = kRopeThreads / kRopeLanes;   // rows of a CTA
+constexpr int kRopeGroups = 32 / kRopeLanes;        // rows of a warp at a time
 constexpr int kRopeChunks = kHeadDim / 8 / kRopeLanes;  // 16-byte pieces of a lane
+constexpr int64_t kRopeManyWarps = 152 * 24;
+
+// Where a pair's dims lie: a lane holds the row's 16-byte pieces sub + 4 j.
+constexpr int kRopeHalves128 = 0;   // halves of 64 dims: pieces j and j + 2 of the same lane
+constexpr int kRopeHalves64 = 1;    // halves of 32 dims: pieces 0 and 1 of the same lane
+constexpr int kRopePairs = 2;       // neighbours: within a piece
+constexpr int kRopeHalvesAny = 3;   // other halves: the partner's piece is read as well
 
 struct RopeParams {
   const uint16_t *q, *k, *v;
@@ -40,8 +47,7 @@ struct RopeParams {
   int64_t num_slots;
   int32_t num_q_heads, num_kv_heads, rotary_dim;
   int32_t *err_flags;
-  uint64_t rows_magic;      // row id / rows per token by a multiply
-  int32_t rows_shift;
+  int32_t warps_per_token;
 };
 
 __device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
@@ -90,124 +96,180 @@ __device__ __forceinline__ uint32_t encode4_f32(const float *x, float s, float y
   return e4m3x2_rn(q[0], q[1]) | (e4m3x2_rn(q[2], q[3]) << 16) | signs;
 }
 
-// One row per 4-lane group, rows ordered (token; query heads, key heads, value
-// heads).  Lane `sub` holds the row's 16-byte pieces sub + 4 j, j < 4, so each
-// of its loads and stores is part of a contiguous 64 bytes, and for a rotation
-// of 128 or 64 dims in halves both dims of a pair lie in one lane (pieces 8 or
-// 4 apart: j with j + 2 or j + 1).
-template <int kLayout>
-__global__ void __launch_bounds__(kRopeThreads)
+// The angles of a lane's pieces, in registers for all of a token's rows (for
+// kRopeHalvesAny they are read again for each row).
+template <int kMode>
+struct RopeAngles {
+  static constexpr int kN = kMode == kRopeHalves128 ? 16 : (kMode == kRopeHalves64 ? 8 : 16);
+  float c[kN], s[kN];
+  __device__ __forceinline__ void load(const float *cs, int r, int sub) {
+    const int half = r >> 1;
+    if (kMode == kRopeHalves128 || kMode == kRopeHalves64) {
+#pragma unroll
+      for (int j = 0; j < kN / 8; ++j) {
+        load8(cs + 8 * (sub + kRopeLanes * j), *reinterpret_cast<float (*)[8]>(c + 8 * j));
+        load8(cs + half + 8 * (sub + kRopeLanes * j), *reinterpret_cast<float (*)[8]>(s + 8 * j));
+      }
+    } else if (kMode == kRopePairs) {
+#pragma unroll
+      for (int j = 0; j < kRopeChunks; ++j) {
+        const int i0 = 4 * (sub + kRopeLanes * j);      // the piece's first pair
+        if (i0 < half) {
+          const float4 a = __ldg(reinterpret_cast<const float4 *>(cs + i0));
+          const float4 b = __ldg(reinterpret_cast<const float4 *>(cs + half + i0));
+          c[4 * j] = a.x; c[4 * j + 1] = a.y; c[4 * j + 2] = a.z; c[4 * j + 3] = a.w;
+          s[4 * j] = b.x; s[4 * j + 1] = b.y; s[4 * j + 2] = b.z; s[4 * j + 3] = b.w;
+        }
+      }
+    }
+  }
+};
+
+// A lane's pieces of one row, rotated in place (src: the row, for kRopeHalvesAny).
+template <int kMode>
+__device__ __forceinline__ void rotate_row(float (&x)[kRopeChunks][8], const RopeAngles<kMode> &ang,
+                                           const uint16_t *src, const float *cs, int r, int sub) {
+  if (kMode == kRopeHalves128 || kMode == kRopeHalves64) {
+    constexpr int kFar = kMode == kRopeHalves128 ? 2 : 1;
+#pragma unroll
+    for (int j = 0; j < kFar; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = x[j][i], b = x[j + kFar][i];
+        x[j][i] = turn_first(a, b, ang.c[8 * j + i], ang.s[8 * j + i]);
+        x[j + kFar][i] = turn_second(a, b, ang.c[8 * j + i], ang.s[8 * j + i]);
+      }
+  } else if (kMode == kRopePairs) {
+#pragma unroll
+    for (int j = 0; j < kRopeChunks; ++j)
+      if (8 * (sub + kRopeLanes * j) < r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = x[j][2 * i], b = x[j][2 * i + 1];
+          x[j][2 * i] = turn_first(a, b, ang.c[4 * j + i], ang.s[4 * j + i]);
+          x[j][2 * i + 1] = turn_second(a, b, ang.c[4 * j + i], ang.s[4 * j + i]);
+        }
+  } else {
+    const int half = r >> 1;
+#pragma unroll
+    for (int j = 0; j < kRopeChunks; ++j) {
+      const int e0 = 8 * (sub + kRopeLanes * j);        // the piece's first dim
+      if (e0 >= r) continue;
+      const bool first = e0 < half;
+      const int i0 = first ? e0 : e0 - half;
+      float o[8], c[8], s[8];
+      unpack8(*reinterpret_cast<const uint4 *>(src + (first ? e0 + half : i0)), o);
+      load8(cs + i0, c);
+      load8(cs + half + i0, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[j][i] = first ? turn_first(x[j][i], o[i], c[i], s[i])
+                        : turn_second(o[i], x[j][i], c[i], s[i]);
+    }
+  }
+}
+
+// A warp, or warps_per_token of them, takes one token's rows, ordered (query
+// heads, key heads, value heads), eight at a time, each on four lanes: the
+// lane's loads and stores of a row are parts of contiguous 64 bytes, the
+// token's angles stay in registers, and the next row is fetched while this one
+// is worked on.
+template <int kMode>
+__global__ void __launch_bounds__(kRopeWarps * 32)
 rope_quantize_kernel(const RopeParams p) {
   const int sub = threadIdx.x & (kRopeLanes - 1);
   const unsigned gmask = ((1u << kRopeLanes) - 1u) << (threadIdx.x & 31 & ~(kRopeLanes - 1));
-  const uint32_t rid = blockIdx.x * kRopeRows + threadIdx.x / kRopeLanes;
-  const int Hq = p.num_q_heads, H = p.num_kv_heads;
-  const uint32_t t32 =
-      static_cast<uint32_t>((static_cast<uint64_t>(rid) * p.rows_magic) >> p.rows_shift);
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
+  const int64_t t = warp / p.warps_per_token;
+  const int part = static_cast<int>(warp - t * p.warps_per_token);
+  const int Hq = p.num_q_heads, H = p.num_kv_heads, rows = Hq + 2 * H;
+  const int stride = kRopeGroups * p.warps_per_token;
+  const int h0 = kRopeGroups * part + ((threadIdx.x & 31) / kRopeLanes);
   grid_dependency_wait();
   allow_dependents_launch();
-  if (t32 >= p.num_tokens) return;
-  const int64_t t = t32;
-  int h = static_cast<int>(rid - t32 * static_cast<uint32_t>(Hq + 2 * H));
-  const bool flagger = sub == 0 && h == 0 && p.err_flags != nullptr;
-  const int kind = h < Hq ? 0 : (h < Hq + H ? 1 : 2);   // query, key, value
-  h -= kind == 0 ? 0 : (kind == 1 ? Hq : Hq + H);
-  const uint16_t *src = (kind == 0 ? p.q + t * p.q_stride
-                                   : (kind == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride)) +
-                        h * kHeadDim;
+  if (t >= p.num_tokens || h0 >= rows) return;
+  auto row_at = [&](int h) -> const uint16_t * {
+    return h < Hq ? p.q + t * p.q_stride + static_cast<int64_t>(h) * kHeadDim
+                  : (h < Hq + H ? p.k + t * p.k_stride + static_cast<int64_t>(h - Hq) * kHeadDim
+                                : p.v + t * p.v_stride + static_cast<int64_t>(h - Hq - H) * kHeadDim);
+  };
   // (plain loads: the rotation may be in place)
   uint4 w[kRopeChunks];
+  auto fetch = [&](int h) {
+    const uint16_t *src = row_at(h);
 #pragma unroll
-  for (int j = 0; j < kRopeChunks; ++j)
-    w[j] = *reinterpret_cast<const uint4 *>(src + 8 * (sub + kRopeLanes * j));
+    for (int j = 0; j < kRopeChunks; ++j)
+      w[j] = *reinterpret_cast<const uint4 *>(src + 8 * (sub + kRopeLanes * j));
+  };
+  fetch(h0);
   const int64_t slot = p.slot_ids[t];
   if (slot < 0) return;
   const int64_t pos = p.positions[t];
   if (slot >= p.num_slots || pos < 0 || pos >= p.num_positions) {
-    if (flagger) {
+    if (sub == 0 && h0 == 0 && p.err_flags) {
       int32_t f = slot >= p.num_slots ? KVQ_ERRF_SLOT_RANGE : 0;
       if (pos < 0 || pos >= p.num_positions) f |= KVQ_ERRF_POSITION_RANGE;
       atomicOr(p.err_flags, f);
     }
     return;
   }
-  float x[kRopeChunks][8];
+  const float *cs = p.table + pos * p.rotary_dim;
+  RopeAngles<kMode> ang;
+  ang.load(cs, p.rotary_dim, sub);
+  for (int hh = h0; hh < rows; hh += stride) {
+    float x[kRopeChunks][8];
 #pragma unroll
-  for (int j = 0; j < kRopeChunks; ++j) unpack8(w[j], x[j]);
-  if (kind != 2) {
-    const int r = p.rotary_dim, half = r >> 1;
-    const float *cs = p.table + pos * r;
+    for (int j = 0; j < kRopeChunks; ++j) unpack8(w[j], x[j]);
+    if (hh + stride < rows) fetch(hh + stride);
+    const bool is_q = hh < Hq, is_v = hh >= Hq + H;
+    const int h = is_q ? hh : (is_v ? hh - Hq - H : hh - Hq);
+    if (!is_v) {
+      rotate_row<kMode>(x, ang, row_at(hh), cs, p.rotary_dim, sub);
+      uint16_t *dst = is_q ? p.q_out + t * p.q_out_stride
+                           : (p.k_out ? p.k_out + t * p.k_out_stride : nullptr);
+      // (every lane has read the row before any of it is overwritten in place)
+      if (kMode == kRopeHalvesAny) __syncwarp(gmask);
+      if (dst != nullptr) {
 #pragma unroll
-    for (int j = 0; j < kRopeChunks; ++j) {
-      const int e0 = 8 * (sub + kRopeLanes * j);        // the piece's first dim
-      if (e0 >= r) continue;
-      if (kLayout == KVQ_ROPE_INTERLEAVED) {
-        const float4 c = __ldg(reinterpret_cast<const float4 *>(cs + (e0 >> 1)));
-        const float4 s = __ldg(reinterpret_cast<const float4 *>(cs + half + (e0 >> 1)));
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+        for (int j = 0; j < kRopeChunks; ++j)
+          *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(h) * kHeadDim +
+                                     8 * (sub + kRopeLanes * j)) = pack8(x[j]);
+      }
+      if (is_q) continue;
+    }
+    float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[j][2 * i], b = x[j][2 * i + 1];
-          x[j][2 * i] = turn_first(a, b, cc[i], ss[i]);
-          x[j][2 * i + 1] = turn_second(a, b, cc[i], ss[i]);
-        }
+    for (int j = 0; j < kRopeChunks; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[j][i]));
+#pragma unroll
+    for (int off = 1; off < kRopeLanes; off <<= 1)
+      amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, off));
+    uint2 codes[kRopeChunks];
+#pragma unroll
+    for (int j = 0; j < kRopeChunks; ++j) codes[j] = make_uint2(0u, 0u);
+    float s = 0.0f;
+    if (amax != 0.0f) {
+      s = row_scale(amax);
+      if (s >= kMarksteinMinScale) {
+        const float y = __frcp_rn(s);
+#pragma unroll
+        for (int j = 0; j < kRopeChunks; ++j)
+          codes[j] = make_uint2(encode4_f32<true>(&x[j][0], s, y), encode4_f32<true>(&x[j][4], s, y));
       } else {
-        // the piece of the pairs' other dims, half a rotation away
-        const bool first = e0 < half;
-        const int i0 = first ? e0 : e0 - half;
-        float o[8], c[8], s[8];
-        unpack8(*reinterpret_cast<const uint4 *>(src + (first ? e0 + half : i0)), o);
-        load8(cs + i0, c);
-        load8(cs + half + i0, s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[j][i] = first ? turn_first(x[j][i], o[i], c[i], s[i])
-                          : turn_second(o[i], x[j][i], c[i], s[i]);
+        for (int j = 0; j < kRopeChunks; ++j)
+          codes[j] = make_uint2(encode4_f32<false>(&x[j][0], s, 0.0f),
+                                encode4_f32<false>(&x[j][4], s, 0.0f));
       }
     }
-    uint16_t *dst = kind == 0 ? p.q_out + t * p.q_out_stride
-                              : (p.k_out ? p.k_out + t * p.k_out_stride : nullptr);
-    // (every lane has read the row before any of it is overwritten in place)
-    __syncwarp(gmask);
-    if (dst != nullptr) {
+    const int64_t row = slot * H + h;
+    uint8_t *dst = (is_v ? p.v_codes : p.k_codes) + row * kHeadDim;
 #pragma unroll
-      for (int j = 0; j < kRopeChunks; ++j)
-        *reinterpret_cast<uint4 *>(dst + h * kHeadDim + 8 * (sub + kRopeLanes * j)) = pack8(x[j]);
-    }
-    if (kind == 0) return;
+    for (int j = 0; j < kRopeChunks; ++j)
+      *reinterpret_cast<uint2 *>(dst + 8 * (sub + kRopeLanes * j)) = codes[j];
+    if (sub == 0) (is_v ? p.v_scales : p.k_scales)[row] = s;
   }
-  float amax = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kRopeChunks; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[j][i]));
-#pragma unroll
-  for (int off = 1; off < kRopeLanes; off <<= 1)
-    amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, off));
-  uint2 codes[kRopeChunks];
-#pragma unroll
-  for (int j = 0; j < kRopeChunks; ++j) codes[j] = make_uint2(0u, 0u);
-  float s = 0.0f;
-  if (amax != 0.0f) {
-    s = row_scale(amax);
-    if (s >= kMarksteinMinScale) {
-      const float y = __frcp_rn(s);
-#pragma unroll
-      for (int j = 0; j < kRopeChunks; ++j)
-        codes[j] = make_uint2(encode4_f32<true>(&x[j][0], s, y), encode4_f32<true>(&x[j][4], s, y));
-    } else {
-#pragma unroll
-      for (int j = 0; j < kRopeChunks; ++j)
-        codes[j] = make_uint2(encode4_f32<false>(&x[j][0], s, 0.0f),
-                              encode4_f32<false>(&x[j][4], s, 0.0f));
-    }
-  }
-  const int64_t row = slot * H + h;
-  uint8_t *dst = (kind == 2 ? p.v_codes : p.k_codes) + row * kHeadDim;
-#pragma unroll
-  for (int j = 0; j < kRopeChunks; ++j)
-    *reinterpret_cast<uint2 *>(dst + 8 * (sub + kRopeLanes * j)) = codes[j];
-  if (sub == 0) (kind == 2 ? p.v_scales : p.k_scales)[row] = s;
 }
 
 }  // namespace
@@ -239,19 +301,23 @@ cudaError_t launch_rope_quantize_scatter(const kvq_cache &c, const RopeArgs &a, 
   p.num_kv_heads = c.num_kv_heads;
   p.rotary_dim = a.rotary_dim;
   p.err_flags = err_flags;
-  // n / d == (n * ceil(2^S / d)) >> S for every n < 2^31 when S = 32 + ceil(log2 d)
-  const uint64_t d = static_cast<uint64_t>(a.num_q_heads) + 2u * static_cast<uint64_t>(c.num_kv_heads);
-  int l = 0;
-  while ((uint64_t(1) << l) < d) ++l;
-  p.rows_shift = 32 + l;
-  p.rows_magic = ((uint64_t(1) << (32 + l)) + d - 1) / d;
-  const int64_t rows = a.num_tokens * static_cast<int64_t>(d);
-  const dim3 grid(static_cast<unsigned>((rows + kRopeRows - 1) / kRopeRows));
+  // few tokens: their rows over more warps; many: one warp a token, which reads
+  // its angles once
+  const int64_t rows = static_cast<int64_t>(a.num_q_heads) + 2 * int64_t(c.num_kv_heads);
+  const int64_t most = (rows + kRopeGroups - 1) / kRopeGroups;
+  int64_t per_token = (kRopeManyWarps + a.num_tokens - 1) / a.num_tokens;
+  per_token = per_token < 1 ? 1 : (per_token > most ? most : per_token);
+  p.warps_per_token = static_cast<int32_t>(per_token);
+  const int64_t warps = a.num_tokens * per_token;
+  const dim3 grid(static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps));
+  const dim3 block(kRopeWarps * 32);
   if (a.layout == KVQ_ROPE_INTERLEAVED)
-    return launch_overlapped(rope_quantize_kernel<KVQ_ROPE_INTERLEAVED>, grid, dim3(kRopeThreads),
-                             0, stream, p);
-  return launch_overlapped(rope_quantize_kernel<KVQ_ROPE_HALVES>, grid, dim3(kRopeThreads), 0,
-                           stream, p);
+    return launch_overlapped(rope_quantize_kernel<kRopePairs>, grid, block, 0, stream, p);
+  if (a.rotary_dim == 128)
+    return launch_overlapped(rope_quantize_kernel<kRopeHalves128>, grid, block, 0, stream, p);
+  if (a.rotary_dim == 64)
+    return launch_overlapped(rope_quantize_kernel<kRopeHalves64>, grid, block, 0, stream, p);
+  return launch_overlapped(rope_quantize_kernel<kRopeHalvesAny>, grid, block, 0, stream, p);
 }
 
 }  // namespace kvq
