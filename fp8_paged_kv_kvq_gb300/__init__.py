@@ -87,6 +87,8 @@ _lib = None
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load libkvq.so (built by ``fp8_paged_kv_kvq_gb300.build.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -162,6 +164,11 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _raw_stream(stream, device: int) -> int:
+    """The cudaStream_t of ``stream``, or of ``device``'s current one."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -252,28 +259,44 @@ def quantize_scatter(cache: Cache, k: torch.Tensor, v: torch.Tensor, slot_ids: t
            "kvq_quantize_scatter")
 
 
-def _on_device(device: torch.device, **tensors) -> None:
-    """Every tensor given is on ``device``, the current CUDA device: a pointer
-    of another device or of the host would fault in the kernel."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors must be on the current CUDA device, not on {device}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+# The two operators below are called once per layer and step, on few tokens too,
+# so their checks keep to a few tensor attribute reads each.
 
-
-def _heads_view(x: torch.Tensor, name: str) -> int:
-    """Token stride (elements) of a [T, heads, D] bf16 view whose rows are
+def _heads(x: torch.Tensor, name: str, T: int, heads: int, D: int) -> int:
+    """Token stride (elements) of a bf16 view [T, heads, D] whose rows are
     contiguous within a token (of one token: the stride it would have)."""
-    if x.dtype != torch.bfloat16 or x.dim() != 3:
-        raise ValueError(f"{name} must be a bfloat16 [T, heads, head_dim] view")
-    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2])):
+    if x.dtype is not torch.bfloat16 or x.shape != (T, heads, D):
+        raise ValueError(f"{name} must be a bfloat16 view [{T}, {heads}, {D}], "
+                         f"not {x.dtype} {tuple(x.shape)}")
+    s0, s1, s2 = x.stride()
+    if T and (s2 != 1 or (heads > 1 and s1 != D)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+    return s0 if T > 1 else heads * D
 
 
-def _check_flags(err_flags) -> None:
-    if err_flags is not None and (err_flags.dtype != torch.int32 or err_flags.numel() < 1):
+def _flat(x: torch.Tensor, name: str, dtype, n: int) -> None:
+    if x.dtype is not dtype or x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} with {n} entries")
+
+
+def _one_device(tensors) -> int:
+    """The index of the current CUDA device, on which every tensor (None: not
+    given) has to be: a pointer of the host or of another device would fault in
+    the kernel."""
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"every tensor must be on the current CUDA device ({device}), "
+                             f"not on {t.device}")
+    return device
+
+
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _flags(err_flags) -> None:
+    if err_flags is not None and (err_flags.dtype is not torch.int32 or err_flags.numel() < 1):
         raise ValueError("err_flags must be an int32 tensor of one element")
 
 
@@ -290,40 +313,36 @@ def rope_quantize_scatter(cache: Cache, q: torch.Tensor | None, k: torch.Tensor,
     ``q`` itself; allocated here, by PyTorch, when not given), the rotated keys
     also to ``k_out`` where given (may be ``k``).  Rows of skipped tokens
     (slot id < 0) are not written.  Returns ``q_out`` (None without ``q``)."""
-    H, D, T = cache.num_kv_heads, cache.head_dim, k.shape[0]
-    for name, x in (("k", k), ("v", v), ("k_out", k_out)):
-        if x is not None and (x.dim() != 3 or tuple(x.shape) != (T, H, D)):
-            raise ValueError(f"{name}: expected [{T}, {H}, {D}]")
-    ks, vs = _heads_view(k, "k"), _heads_view(v, "v")
-    kos = 0 if k_out is None else _heads_view(k_out, "k_out")
-    for name, x in (("positions", positions), ("slot_ids", slot_ids)):
-        if x.dtype != torch.int64 or x.numel() != T or not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous int64 with one entry per token")
-    if rope_table.dtype != torch.float32 or rope_table.dim() != 2 or \
+    T, H, D = k.shape[0], cache.num_kv_heads, cache.head_dim
+    ks, vs = _heads(k, "k", T, H, D), _heads(v, "v", T, H, D)
+    kos = 0 if k_out is None else _heads(k_out, "k_out", T, H, D)
+    _flat(positions, "positions", torch.int64, T)
+    _flat(slot_ids, "slot_ids", torch.int64, T)
+    if rope_table.dtype is not torch.float32 or rope_table.dim() != 2 or \
             not rope_table.is_contiguous():
         raise ValueError("rope_table must be contiguous fp32 [positions, rotary_dim]")
     qs = qos = hq = 0
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D:
-            raise ValueError(f"q: expected [{T}, num_q_heads, {D}]")
-        hq, qs = q.shape[1], _heads_view(q, "q")
+        if q.dim() != 3:
+            raise ValueError(f"q must be a bfloat16 view [{T}, num_q_heads, {D}]")
+        hq = q.shape[1]
+        qs = _heads(q, "q", T, hq, D)
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        qos = _heads_view(q_out, "q_out")
+        qos = _heads(q_out, "q_out", T, hq, D)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _check_flags(err_flags)
-    _on_device(k.device, q=q, v=v, positions=positions, rope_table=rope_table, slot_ids=slot_ids,
-               q_out=q_out, k_out=k_out, err_flags=err_flags, k_codes=cache.k_codes,
-               v_codes=cache.v_codes, k_scales=cache.k_scales, v_scales=cache.v_scales)
+    _flags(err_flags)
+    device = _one_device((k, v, positions, rope_table, slot_ids, q, q_out, k_out, err_flags,
+                          cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales))
     st = cache.struct()
-    _check(load().kvq_rope_quantize_scatter(
-        ctypes.byref(st), _ptr(q), qs, hq, _ptr(k), ks, _ptr(v), vs, T, _ptr(positions),
-        _ptr(rope_table), rope_table.shape[0], rope_table.shape[1], layout, _ptr(slot_ids),
-        _ptr(q_out), qos, _ptr(k_out), kos, _ptr(err_flags), _stream(stream)),
-        "kvq_rope_quantize_scatter")
+    P, r = rope_table.shape
+    status = load().kvq_rope_quantize_scatter(
+        ctypes.byref(st), _addr(q), qs, hq, k.data_ptr(), ks, v.data_ptr(), vs, T,
+        positions.data_ptr(), rope_table.data_ptr(), P, r, layout, slot_ids.data_ptr(),
+        _addr(q_out), qos, _addr(k_out), kos, _addr(err_flags), _raw_stream(stream, device))
+    if status:
+        raise KvqError(status, "kvq_rope_quantize_scatter")
     return q_out
 
 
@@ -335,25 +354,26 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     strides), sequence s holding the tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1
     (int32, on the device).  Returns ``out`` (bf16, shape of q; allocated here,
     by PyTorch, when not given).  Rows outside the sequences are not written."""
-    qs, ks, vs = _heads_view(q, "q"), _heads_view(k, "k"), _heads_view(v, "v")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be bfloat16 views [T, heads, head_dim]")
     T, Hq, D = q.shape
     H = k.shape[1]
-    if k.shape[0] != T or k.shape[2] != D or v.shape != k.shape:
-        raise ValueError("k and v must be [T, num_kv_heads, head_dim] with q's T and head_dim")
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or \
-            not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be contiguous int32 [num_seqs + 1]")
+    qs, ks, vs = _heads(q, "q", T, Hq, D), _heads(k, "k", T, H, D), _heads(v, "v", T, H, D)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be int32 [num_seqs + 1]")
+    N = cu_seqlens.numel() - 1
+    _flat(cu_seqlens, "cu_seqlens", torch.int32, N + 1)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    os_ = _heads_view(out, "out")
-    _check_flags(err_flags)
-    _on_device(q.device, k=k, v=v, cu_seqlens=cu_seqlens, out=out, err_flags=err_flags)
-    _check(load().kvq_prompt_attention(
-        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, T, _ptr(cu_seqlens), cu_seqlens.numel() - 1,
-        max_seqlen, Hq, H, D, float(sm_scale), _ptr(out), os_, _ptr(err_flags), _stream(stream)),
-        "kvq_prompt_attention")
+    outs = _heads(out, "out", T, Hq, D)
+    _flags(err_flags)
+    device = _one_device((q, k, v, cu_seqlens, out, err_flags))
+    status = load().kvq_prompt_attention(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, cu_seqlens.data_ptr(), N,
+        max_seqlen, Hq, H, D, sm_scale, out.data_ptr(), outs, _addr(err_flags),
+        _raw_stream(stream, device))
+    if status:
+        raise KvqError(status, "kvq_prompt_attention")
     return out
 
 

@@ -287,7 +287,8 @@ kvq_status kvq_rope_quantize_scatter(
     return KVQ_ERR_UNSUPPORTED;
   const kvq::RopeArgs a{q, q_token_stride, num_q_heads, k, k_token_stride, v, v_token_stride,
                         num_tokens, positions, rope_table, num_positions, rotary_dim, rope_layout,
-                        slot_ids, q_out, q_out_token_stride, k_out, k_out_token_stride};
+                        slot_ids, q_out, q_out_token_stride, k_out, k_out_token_stride,
+                        current_sm_count()};
   return from_cuda(kvq::launch_rope_quantize_scatter(*cache, a, err_flags,
                                                      reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -135,6 +135,7 @@ struct RopeArgs {
   int64_t q_out_stride;
   void *k_out;
   int64_t k_out_stride;
+  int32_t sms;
 };
 cudaError_t launch_rope_quantize_scatter(const kvq_cache &c, const RopeArgs &a, int32_t *err_flags,
                                          cudaStream_t stream);

@@ -25,7 +25,6 @@ constexpr int kRopeWarps = 4;
 constexpr int kRopeLanes = 4;                       // lanes of a row
 constexpr int kRopeGroups = 32 / kRopeLanes;        // rows of a warp at a time
 constexpr int kRopeChunks = kHeadDim / 8 / kRopeLanes;  // 16-byte pieces of a lane
-constexpr int64_t kRopeManyWarps = 152 * 24;
 
 // Where a pair's dims lie: a lane holds the row's 16-byte pieces sub + 4 j.
 constexpr int kRopeHalves128 = 0;   // halves of 64 dims: pieces j and j + 2 of the same lane
@@ -174,7 +173,7 @@ __device__ __forceinline__ void rotate_row(float (&x)[kRopeChunks][8], const Rop
 // lane's loads and stores of a row are parts of contiguous 64 bytes, the
 // token's angles stay in registers, and the next row is fetched while this one
 // is worked on.
-template <int kMode>
+template <int kMode, bool kLoop>
 __global__ void __launch_bounds__(kRopeWarps * 32)
 rope_quantize_kernel(const RopeParams p) {
   const int sub = threadIdx.x & (kRopeLanes - 1);
@@ -220,7 +219,7 @@ rope_quantize_kernel(const RopeParams p) {
     float x[kRopeChunks][8];
 #pragma unroll
     for (int j = 0; j < kRopeChunks; ++j) unpack8(w[j], x[j]);
-    if (hh + stride < rows) fetch(hh + stride);
+    if (kLoop && hh + stride < rows) fetch(hh + stride);
     const bool is_q = hh < Hq, is_v = hh >= Hq + H;
     const int h = is_q ? hh : (is_v ? hh - Hq - H : hh - Hq);
     if (!is_v) {
@@ -232,10 +231,13 @@ rope_quantize_kernel(const RopeParams p) {
       if (dst != nullptr) {
 #pragma unroll
         for (int j = 0; j < kRopeChunks; ++j)
-          *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(h) * kHeadDim +
-                                     8 * (sub + kRopeLanes * j)) = pack8(x[j]);
+          __stcs(reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(h) * kHeadDim +
+                                           8 * (sub + kRopeLanes * j)), pack8(x[j]));
       }
-      if (is_q) continue;
+      if (is_q) {
+        if (!kLoop) return;
+        continue;
+      }
     }
     float amax = 0.0f;
 #pragma unroll
@@ -269,6 +271,7 @@ rope_quantize_kernel(const RopeParams p) {
     for (int j = 0; j < kRopeChunks; ++j)
       *reinterpret_cast<uint2 *>(dst + 8 * (sub + kRopeLanes * j)) = codes[j];
     if (sub == 0) (is_v ? p.v_scales : p.k_scales)[row] = s;
+    if (!kLoop) return;
   }
 }
 
@@ -301,23 +304,30 @@ cudaError_t launch_rope_quantize_scatter(const kvq_cache &c, const RopeArgs &a, 
   p.num_kv_heads = c.num_kv_heads;
   p.rotary_dim = a.rotary_dim;
   p.err_flags = err_flags;
-  // few tokens: their rows over more warps; many: one warp a token, which reads
-  // its angles once
+  // few tokens: their rows over more warps; many (8 an SM and up): one warp a
+  // token, which reads its angles once and fetches ahead.  With 24 for 8, 1,021
+  // tokens of 32 rows take 5.3 us instead of 3.6, 2,048 of 48 rows 9.3 instead
+  // of 8.3; below 512 tokens the two differ by less than 0.2 us.
   const int64_t rows = static_cast<int64_t>(a.num_q_heads) + 2 * int64_t(c.num_kv_heads);
   const int64_t most = (rows + kRopeGroups - 1) / kRopeGroups;
-  int64_t per_token = (kRopeManyWarps + a.num_tokens - 1) / a.num_tokens;
+  int64_t per_token = (8 * static_cast<int64_t>(a.sms) + a.num_tokens - 1) / a.num_tokens;
   per_token = per_token < 1 ? 1 : (per_token > most ? most : per_token);
   p.warps_per_token = static_cast<int32_t>(per_token);
   const int64_t warps = a.num_tokens * per_token;
   const dim3 grid(static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps));
   const dim3 block(kRopeWarps * 32);
-  if (a.layout == KVQ_ROPE_INTERLEAVED)
-    return launch_overlapped(rope_quantize_kernel<kRopePairs>, grid, block, 0, stream, p);
-  if (a.rotary_dim == 128)
-    return launch_overlapped(rope_quantize_kernel<kRopeHalves128>, grid, block, 0, stream, p);
-  if (a.rotary_dim == 64)
-    return launch_overlapped(rope_quantize_kernel<kRopeHalves64>, grid, block, 0, stream, p);
-  return launch_overlapped(rope_quantize_kernel<kRopeHalvesAny>, grid, block, 0, stream, p);
+  const int mode = a.layout == KVQ_ROPE_INTERLEAVED
+                       ? kRopePairs
+                       : (a.rotary_dim == 128 ? kRopeHalves128
+                                              : (a.rotary_dim == 64 ? kRopeHalves64 : kRopeHalvesAny));
+  const bool loop = per_token < most;
+  using Kernel = void (*)(RopeParams);
+  static constexpr Kernel kernels[4][2] = {
+      {rope_quantize_kernel<kRopeHalves128, false>, rope_quantize_kernel<kRopeHalves128, true>},
+      {rope_quantize_kernel<kRopeHalves64, false>, rope_quantize_kernel<kRopeHalves64, true>},
+      {rope_quantize_kernel<kRopePairs, false>, rope_quantize_kernel<kRopePairs, true>},
+      {rope_quantize_kernel<kRopeHalvesAny, false>, rope_quantize_kernel<kRopeHalvesAny, true>}};
+  return launch_overlapped(kernels[mode][loop ? 1 : 0], grid, block, 0, stream, p);
 }
 
 }  // namespace kvq
