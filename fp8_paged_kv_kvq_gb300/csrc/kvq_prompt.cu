@@ -157,6 +157,11 @@ __device__ __forceinline__ float pt_max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+__device__ __forceinline__ uint32_t pt_fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 __device__ __forceinline__ uint64_t pt_add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -532,26 +537,29 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       // the next unit of this CTA, announced in entry t: its own block's first,
       // then those of blocks that have not started, asked for one ahead
       const uint32_t steal = smem_addr(smem + kPtOffSteal);
-      int64_t w = blockIdx.x;
       uint32_t asked = 0, heard = 0;
       auto ask = [&]() {
         if (lane == 0) pt_steal(steal + 16 * (asked & 1), BAR(kPtSteal));
         ++asked;
       };
-      ask();
       auto next_unit = [&](int t, int4 &e) -> bool {
         e = make_int4(0, 0, 0, 0);
-        while (w >= 0 && e.y == 0) {
+        while (e.y == 0) {
+          int64_t w = blockIdx.x;
+          if (asked > 0) {
+            if (!pt_wait_all(BAR(kPtSteal), heard & 1, abort_s)) return false;
+            w = pt_stolen(steal + 16 * (heard & 1));
+            ++heard;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (w < 0) break;
+          }
+          ask();
           e = pt_find(p, w, lane);
           // (every work number is somebody's, and there are more than sequences)
-          if (lane == 0 && w < p.N && p.err_flags && !pt_bounds_ok(p, __ldg(p.cu + w), __ldg(p.cu + w + 1)))
+          if (lane == 0 && w < p.N && p.err_flags &&
+              !pt_bounds_ok(p, __ldg(p.cu + w), __ldg(p.cu + w + 1)))
             atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
-          if (!pt_wait_all(BAR(kPtSteal), heard & 1, abort_s)) return false;
-          w = pt_stolen(steal + 16 * (heard & 1));
-          ++heard;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (w >= 0) ask();
         }
         const int b = t % kPtUnits;
         const bool ok =
@@ -753,30 +761,32 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
           }
           uint8_t *tile = smem + kPtOffKv + b * kPtTileBytes;
           const int rows = min(kPtKeys, u.len - j * kPtKeys);   // of this sequence
-          // every 16-byte piece: the largest magnitude of its 16-bit lanes
-          uint32_t top = 0;
-          for (int r0 = 0; r0 < 2 * rows; r0 += 16) {            // half-rows of 128 bytes
-            uint4 w[4];
+          // 0 times the values, summed: NaN where one of them is not finite
+          uint32_t sum0 = 0u, sum1 = 0u;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half)
+#pragma unroll 1
+            for (int r0 = 0; r0 < rows; r0 += 32) {
+              uint4 w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = r0 + 4 * i + (lane >> 3);
-              w[i] = make_uint4(0u, 0u, 0u, 0u);
-              if (r < 2 * rows)
-                w[i] = *reinterpret_cast<const uint4 *>(tile + (r < rows ? r * 128 : kPtHalf + (r - rows) * 128) +
+              for (int i = 0; i < 8; ++i) {
+                const int r = min(r0 + 4 * i + (lane >> 3), rows - 1);
+                w[i] = *reinterpret_cast<const uint4 *>(tile + half * kPtHalf + r * 128 +
                                                          16 * (lane & 7));
-            }
+              }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t mk = 0x7FFF7FFFu;
-              top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & mk, w[i].y & mk),
-                                           __vmaxu2(w[i].z & mk, w[i].w & mk)));
+              for (int i = 0; i < 8; ++i) {
+                sum0 = pt_fma_bf16x2(w[i].x, 0u, sum0);
+                sum1 = pt_fma_bf16x2(w[i].y, 0u, sum1);
+                sum0 = pt_fma_bf16x2(w[i].z, 0u, sum0);
+                sum1 = pt_fma_bf16x2(w[i].w, 0u, sum1);
+              }
             }
-          }
-          const bool bad = (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
-          if (__any_sync(0xFFFFFFFFu, bad)) {
+          if (__any_sync(0xFFFFFFFFu, ((sum0 | sum1) & 0x7FFF7FFFu) != 0u)) {
             if (lane == 0) dirty_s[t % kPtUnits] = 1;
             for (int r = 0; r < 2 * rows; ++r) {
-              uint32_t *w = reinterpret_cast<uint32_t *>(tile + (r < rows ? r * 128 : kPtHalf + (r - rows) * 128)) + lane;
+              uint32_t *w = reinterpret_cast<uint32_t *>(
+                                tile + (r < rows ? r * 128 : kPtHalf + (r - rows) * 128)) + lane;
               uint32_t x = *w;
               if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
               if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
