@@ -64,8 +64,7 @@ constexpr int kPtTileBytes = 128 * kHeadDim * 2;      // [2 halves of 64 dims][1
 constexpr int kPtHalf = kPtTileBytes / 2;
 constexpr int kPtOffQ = 0;
 constexpr int kPtOffKv = 2 * kPtTileBytes;
-constexpr int kPtOffOut = kPtOffKv + kPtStages * kPtTileBytes;   // 4 warps x 32 rows x 256 B
-constexpr int kPtOffSum = kPtOffOut + kPtTileBytes;              // [tile][128] denominators
+constexpr int kPtOffSum = kPtOffKv + kPtStages * kPtTileBytes;   // [tile][128] denominators
 constexpr int kPtOffUnit = kPtOffSum + 2 * 128 * 4;
 constexpr int kPtOffDirty = kPtOffUnit + kPtUnits * 16;
 constexpr int kPtOffSteal = kPtOffDirty + kPtUnits * 4;          // two answers of 16 bytes
@@ -86,8 +85,8 @@ enum : int {
   kPtUnitEmpty = kPtUnitFull + kPtUnits,
   kPtDrain = kPtUnitEmpty + kPtUnits,                 // per tile
   kPtTurn = kPtDrain + 2,                             // per tile
-  kPtSteal = kPtTurn + 2,
-  kPtBars
+  kPtSteal = kPtTurn + 2,                             // per answer
+  kPtBars = kPtSteal + 2
 };
 constexpr int kPtSmem = kPtOffBar + 8 * kPtBars + 1024;
 static_assert(kPtOffBar % 8 == 0 && kPtOffUnit % 16 == 0 && kPtOffSteal % 16 == 0, "alignment");
@@ -144,6 +143,7 @@ struct PromptParams {
   int32_t inv_g;                                       // ceil(65536 / G)
   int64_t units;                                       // work numbers
   float scale2;                                        // sm_scale log2(e)
+  int32_t out_by_32;                                   // out rows are 32-byte aligned
   int32_t *err_flags;
 };
 
@@ -204,7 +204,6 @@ struct PtUnit {
   __device__ __forceinline__ int tiles() const { return max(n0, n1); }
   // key tile j has a key that the unit's first row does not see
   __device__ __forceinline__ bool edge(int j) const { return j * kPtKeys + kPtKeys - 1 > tok0; }
-  __device__ __forceinline__ bool active(int a, int j) const { return j < (a == 0 ? n0 : n1); }
 };
 
 __device__ __forceinline__ bool pt_bounds_ok(const PromptParams &p, int begin, int end) {
@@ -212,10 +211,11 @@ __device__ __forceinline__ bool pt_bounds_ok(const PromptParams &p, int begin, i
 }
 
 // Work number w as a unit (len 0: none there).  All lanes of a warp.
-__device__ __forceinline__ int4 pt_find(const PromptParams &p, int64_t w, int lane) {
+__device__ __forceinline__ int4 pt_find(const PromptParams &p, uint32_t w, int lane) {
   const int TU = 2 * p.TQ;
-  const int h = static_cast<int>(w % p.H);
-  const int64_t x = w / p.H;
+  const uint32_t H = static_cast<uint32_t>(p.H), xq = w / H;
+  const int h = static_cast<int>(w - xq * H);
+  const int64_t x = xq;
   int lo = 0, hi = p.N;
   for (;;) {
     const int step = (hi - lo + 31) / 32;
@@ -230,10 +230,10 @@ __device__ __forceinline__ int4 pt_find(const PromptParams &p, int64_t w, int la
   }
   const int a = __ldg(p.cu + lo), b = __ldg(p.cu + lo + 1);
   if (!pt_bounds_ok(p, a, b)) return make_int4(0, 0, 0, 0);
-  const int64_t units = (static_cast<int64_t>(b - a) + TU - 1) / TU;
-  const int64_t u = units - 1 - (x - (a / TU + lo));                // the longest rows first
+  const int units = (b - a) / TU + ((b - a) % TU != 0 ? 1 : 0);
+  const int64_t u = units - 1 - (x - (static_cast<int64_t>(a / TU) + lo));   // longest rows first
   if (u < 0 || u >= units) return make_int4(0, 0, 0, 0);
-  return make_int4(a, b - a, h, static_cast<int>(u * TU));
+  return make_int4(a, b - a, h, static_cast<int>(u) * TU);
 }
 
 __device__ __forceinline__ void pt_tma_4d(uint32_t dst, const void *tmap, int x, int y, int z,
@@ -242,6 +242,25 @@ __device__ __forceinline__ void pt_tma_4d(uint32_t dst, const void *tmap, int x,
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5}], [%6];\n"
       :: "r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void pt_prefetch_map(const void *tmap) {
+  asm volatile("prefetch.tensormap [%0];\n" :: "l"(tmap) : "memory");
+}
+
+// 64 bytes of an output row, in whole 32-byte sectors where it is aligned.
+__device__ __forceinline__ void pt_store64(uint16_t *dst, const uint32_t (&w)[16], bool by_32) {
+  if (by_32) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n"
+                   :: "l"(dst + 2 * i), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]),
+                      "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7]) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<uint4 *>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
 }
 
 // Asks for the number of a block of this grid that has not started, which then
@@ -267,26 +286,33 @@ __device__ __forceinline__ int64_t pt_stolen(uint32_t answer) {
 // One key tile of one row: S from TMEM, the reference and the denominator
 // brought up to date (the O row with them), P as bf16 over S's columns, its two
 // halves announced one after the other.  Keys past `lim` (within the tile) are
-// not seen where `masked`.
-__device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, bool masked, int lim,
-                                           float scale2, bool fresh, uint32_t ready, int lane,
+// not seen.
+__device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, int lim, float scale2,
+                                           bool fresh, uint32_t ready, int lane,
                                            float &m_ref, float &lsum) {
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  // (lane 0 has the warp's first token, the one that sees the least)
+  const int lim0 = __shfl_sync(0xFFFFFFFFu, lim, 0);
 #pragma unroll 1
   for (int c = 0; c < 128; c += 64) {
     float x[64];
     tmem_ld64(scol + c, x);
-    if (masked) {
+    if (lim0 < c + 63) {
+      // unseen keys, 32 at a time where the warp has any
+      if (lim0 < c + 31) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) x[i] = i <= lim - c ? x[i] : -INFINITY;
+        for (int i = 0; i < 32; ++i) x[i] = i <= lim - c ? x[i] : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 32; i < 64; ++i) x[i] = i <= lim - c ? x[i] : -INFINITY;
       tmem_st64(scol + c, x);
+      tmem_wait_st();
     }
 #pragma unroll
     for (int i = 0; i < 64; i += 8)
 #pragma unroll
       for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
   }
-  if (masked) tmem_wait_st();
   uint32_t x0[32], x1[32];
   tmem_ld32_start(scol, x0);
   const float top = fmaxf(pt_max3(mx[0], mx[1], mx[2]), mx[3]);
@@ -381,12 +407,18 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       mbar_init(BAR(kPtTurn + a), 1);
     }
     mbar_init(BAR(kPtSteal), 1);
+    mbar_init(BAR(kPtSteal + 1), 1);
     for (int e = 0; e < kPtUnits; ++e) {
       mbar_init(BAR(kPtUnitFull + e), 1);
       mbar_init(BAR(kPtUnitEmpty + e), 8 + 4 + 3);     // softmax, epilogue, warps 13-15
     }
     *abort_s = 0;
     fence_mbarrier_init();
+  }
+  if (tid == 32) {
+    pt_prefetch_map(&tm_q);
+    pt_prefetch_map(&tm_k);
+    pt_prefetch_map(&tm_v);
   }
   if (warp == kPtWarpLoad) {
     tmem_alloc(smem_addr(tmem_slot), kPtTmemCols);
@@ -426,8 +458,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       if (u.len == 0) break;
       const int n = a == 0 ? u.n0 : u.n1;
       if (n == 0) continue;
-      const int first = u.tok0 + a * p.TQ;             // the tile's first token
-      const int tok = first + t_row;
+      const int tok = u.tok0 + a * p.TQ + t_row;
       float m_ref = -INFINITY, lsum = 0.0f;
       for (int j = n - 1; j >= 0; --j, ++steps) {
         if (__any_sync(0xFFFFFFFFu, !pt_wait(BAR(kPtSFull + a), steps & 1, abort_s))) {
@@ -435,9 +466,8 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
           break;
         }
         tc_fence_after();
-        pt_softmax(tl + pt_s(a), tl + pt_o(a), j * kPtKeys + kPtKeys - 1 > first,
-                   tok - j * kPtKeys, p.scale2, j == n - 1, BAR(kPtPReady + 2 * a), lane, m_ref,
-                   lsum);
+        pt_softmax(tl + pt_s(a), tl + pt_o(a), tok - j * kPtKeys, p.scale2, j == n - 1,
+                   BAR(kPtPReady + 2 * a), lane, m_ref, lsum);
       }
       if (gave_up) break;
       // the denominators, once the epilogue has read the last unit's
@@ -458,7 +488,6 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
     const int m = 32 * q4 + lane;
     const int t_row = (m * p.inv_g) >> 16;
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
-    uint8_t *stage = smem + kPtOffOut + q4 * (32 * 2 * kHeadDim);
     uint32_t done[2] = {0, 0};
     for (int t = 0;; ++t) {
       PtUnit u;
@@ -482,6 +511,9 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         const float inv = 1.0f / sum_s[128 * a + m];
         const int tok = u.tok0 + a * p.TQ + t_row;
         const bool dirty = dirty_s[t % kPtUnits] != 0;
+        const bool mine = t_row < p.TQ && tok < u.len;
+        uint16_t *dst = p.out + (static_cast<int64_t>(u.start) + tok) * p.out_stride +
+                        (static_cast<int64_t>(u.h) * p.G + (m - t_row * p.G)) * kHeadDim;
 #pragma unroll 1
         for (int c = 0; c < kHeadDim; c += 32) {
           float o[32];
@@ -501,28 +533,14 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
               }
             }
           }
+          uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4 *>(stage + lane * 256 + (((c / 8 + k) ^ (lane & 7)) << 4)) =
-                make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                           pack_bf16x2(o[8 * k + 4], o[8 * k + 5]),
-                           pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+          for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+          if (mine) pt_store64(dst + c, w, p.out_by_32);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(kPtOEmpty + a));
-        // rows of 256 contiguous bytes, two per store
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-          const int r = 2 * i + (lane >> 4), mr = 32 * q4 + r, c = lane & 15;
-          const int tr = (mr * p.inv_g) >> 16, g = mr - tr * p.G;
-          const int tk = u.tok0 + a * p.TQ + tr;
-          if (tr < p.TQ && tk < u.len)
-            *reinterpret_cast<uint4 *>(p.out + (static_cast<int64_t>(u.start) + tk) * p.out_stride +
-                                       (static_cast<int64_t>(u.h) * p.G + g) * kHeadDim + 8 * c) =
-                *reinterpret_cast<const uint4 *>(stage + r * 256 + ((c ^ (r & 7)) << 4));
-        }
-        __syncwarp();
       }
       if (gave_up) break;
       // (held to here: the entry's dirty flag is the unit's until it is taken again)
@@ -534,37 +552,50 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       // ----------------------------------------------- work numbers and TMA
       uint32_t idx = 0;                                // ring entries issued
       uint32_t loads[2] = {0, 0};                      // query tiles
-      // the next unit of this CTA, announced in entry t: its own block's first,
-      // then those of blocks that have not started, asked for one ahead
+      // Units: the own block's first, then those of blocks that have not
+      // started.  Answers are asked for while a unit's last two tiles are loaded
+      // (any earlier, and the CTAs that ask first hold work back from those that
+      // finish first), two of them if it has no more.
       const uint32_t steal = smem_addr(smem + kPtOffSteal);
       uint32_t asked = 0, heard = 0;
-      auto ask = [&]() {
-        if (lane == 0) pt_steal(steal + 16 * (asked & 1), BAR(kPtSteal));
-        ++asked;
+      bool more = true;
+      auto ask = [&](uint32_t ahead) {
+        for (; more && asked - heard < ahead; ++asked)
+          if (lane == 0) pt_steal(steal + 16 * (asked & 1), BAR(kPtSteal + (asked & 1)));
+        __syncwarp();
       };
-      auto next_unit = [&](int t, int4 &e) -> bool {
+      auto find = [&](int64_t w) -> int4 {
+        // (every work number is somebody's, and there are more than sequences)
+        if (lane == 0 && w < p.N && p.err_flags &&
+            !pt_bounds_ok(p, __ldg(p.cu + w), __ldg(p.cu + w + 1)))
+          atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
+        return pt_find(p, static_cast<uint32_t>(w), lane);
+      };
+      // the next answer with work in it, or none (length 0)
+      auto next_unit = [&](int4 &e) -> bool {
         e = make_int4(0, 0, 0, 0);
         while (e.y == 0) {
-          int64_t w = blockIdx.x;
-          if (asked > 0) {
-            if (!pt_wait_all(BAR(kPtSteal), heard & 1, abort_s)) return false;
-            w = pt_stolen(steal + 16 * (heard & 1));
-            ++heard;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (w < 0) break;
+          ask(1);
+          if (asked == heard) break;
+          if (!pt_wait_all(BAR(kPtSteal + (heard & 1)), (heard >> 1) & 1, abort_s)) return false;
+          const int64_t w = pt_stolen(steal + 16 * (heard & 1));
+          ++heard;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (w < 0) {
+            more = false;                              // (an answer may still be under way)
+          } else {
+            ask(1);
+            e = find(w);
           }
-          ask();
-          e = pt_find(p, w, lane);
-          // (every work number is somebody's, and there are more than sequences)
-          if (lane == 0 && w < p.N && p.err_flags &&
-              !pt_bounds_ok(p, __ldg(p.cu + w), __ldg(p.cu + w + 1)))
-            atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
         }
+        return true;
+      };
+      auto announce = [&](int t, const int4 e) -> bool {
         const int b = t % kPtUnits;
-        const bool ok =
-            t < kPtUnits || pt_wait(BAR(kPtUnitEmpty + b), (t / kPtUnits - 1) & 1, abort_s);
-        if (__any_sync(0xFFFFFFFFu, !ok)) return false;
+        if (t >= kPtUnits &&
+            !pt_wait_all(BAR(kPtUnitEmpty + b), (t / kPtUnits - 1) & 1, abort_s))
+          return false;
         if (lane == 0) {
           unit_s[b] = e;
           mbar_arrive(BAR(kPtUnitFull + b));
@@ -598,36 +629,37 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         }
         return true;
       };
-      int4 e;
-      gave_up = !next_unit(0, e);
-      for (int t = 0; !gave_up && e.y > 0; ++t) {
+      int4 e = find(blockIdx.x);
+      bool ok = e.y > 0 || next_unit(e);
+      for (int t = 0; ok; ++t) {
+        ok = announce(t, e);
+        if (!ok || e.y == 0) break;
         PtUnit u;
         u.shape(e, p.TQ);
-        // the first keys and values ahead of the queries, whose tiles are free
-        // only once the last unit's products with them are done
-        bool ok = true;
-        int j = u.tiles() - 1;
-        if (lane == 0) ok = load_kv(u, j) && load_q(u);
-        if (__any_sync(0xFFFFFFFFu, !ok) || !next_unit(t + 1, e)) {
-          gave_up = true;
-          break;
+        const int nt = u.tiles();
+        for (int j = nt - 1; j >= 0 && ok; --j) {
+          if (j == (nt > 1 ? 1 : 0)) ask(nt > 2 ? 1 : 2);
+          // the first keys and values ahead of the queries, whose tiles are free
+          // only once the last unit's products with them are done
+          if (lane == 0) ok = load_kv(u, j) && (j < nt - 1 || load_q(u));
+          ok = __all_sync(0xFFFFFFFFu, ok);
         }
-        if (lane == 0)
-          while (ok && --j >= 0) ok = load_kv(u, j);
-        gave_up = __any_sync(0xFFFFFFFFu, !ok);
+        ok = ok && next_unit(e);
       }
+      gave_up = !ok;
       // copies in flight land before the CTA leaves
       if (lane == 0) {
         for (uint32_t v = idx > kPtStages ? idx - kPtStages : 0; v < idx; ++v)
           mbar_wait_sleep_bounded(BAR(kPtKvFull + v % kPtStages), (v / kPtStages) & 1);
         for (int a = 0; a < 2; ++a)
           if (loads[a] > 0) mbar_wait_sleep_bounded(BAR(kPtQFull + a), (loads[a] - 1) & 1);
-        if (asked > heard) mbar_wait_sleep_bounded(BAR(kPtSteal), heard & 1);
+        for (; asked > heard; ++heard)
+          mbar_wait_sleep_bounded(BAR(kPtSteal + (heard & 1)), (heard >> 1) & 1);
       }
     } else if (warp < kPtWarpClear) {
       // ----------------------------------------------------- MMAs of a tile
-      // Each turn: PV of the present step and QK^T of the next, tile 0's and
-      // tile 1's bursts one after the other (free to interleave, the tiles fell
+      // Each turn: PV of one key tile and QK^T of the next (a unit's first turn
+      // has no PV, its last no QK^T), tile 0's and tile 1's bursts one after the other (free to interleave, the tiles fell
       // into step: both in the softmax, then both at the tensor core).
       // Everything but P is waited for before the turn.  The warp stays
       // converged and elects a lane for each group of MMAs: addresses stay
@@ -636,71 +668,67 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       const uint32_t q_lo = (smem_addr(smem + kPtOffQ + a * kPtTileBytes) >> 4) | kPtKMajor;
       const uint32_t kv0 = smem_addr(smem + kPtOffKv) >> 4;
       const uint32_t s_col = tmem + pt_s(a), o_col = tmem + pt_o(a);
-      uint32_t step = ~0u;                             // ring entries 2 step, 2 step + 1
+      uint32_t base = 0;                               // ring entries of earlier units
       uint32_t par_q = 0, par_p = 0, par_o = 1;        // barrier parities
       uint32_t par_clear = 0;                          // bit per ring stage
       uint32_t par_turn = a ^ 1;                       // tile 0 goes first
-      PtUnit u, nx;
-      int t = 0, j = 0, jn = 0;
-      u.n0 = u.n1 = 0;
-      auto next_unit = [&]() -> bool {
-        if (!__all_sync(0xFFFFFFFFu, take_unit(t, nx))) return false;
+      bool ok = true;
+      for (int t = 0; ok; ++t) {
+        PtUnit u;
+        ok = __all_sync(0xFFFFFFFFu, take_unit(t, u));
+        if (!ok) break;
         if (lane == 0) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
-        jn = nx.tiles() - 1;
-        ++t;
-        return true;
-      };
-      bool ok = next_unit();
-      while (ok) {
-        const uint32_t ev = 2 * step + 1, bv = ev % kPtStages;         // values of this step
-        const uint32_t ek = 2 * step + 2, bk = ek % kPtStages;         // keys of the next
-        const bool pv = u.active(a, j), next = nx.len > 0, qk = next && nx.active(a, jn);
-        const bool pv_first = j == (a == 0 ? u.n0 : u.n1) - 1;
-        const bool qk_first = jn == (a == 0 ? nx.n0 : nx.n1) - 1;
-        const uint32_t v_lo = (kv0 + bv * (kPtTileBytes >> 4)) | kPtMnMajor;
-        const uint32_t k_lo = (kv0 + bk * (kPtTileBytes >> 4)) | kPtKMajor;
-        if (step != ~0u) {
-          ok = pt_wait_all(BAR(kPtKvFull + bv), (ev / kPtStages) & 1, abort_s);
-          if (ok && pv && u.edge(j))
-            ok = pt_wait_all(BAR(kPtVClear + bv), (par_clear >> bv) & 1, abort_s);
-          if (u.edge(j)) par_clear ^= 1u << bv;
-        }
-        if (ok && next) ok = pt_wait_all(BAR(kPtKvFull + bk), (ek / kPtStages) & 1, abort_s);
-        if (ok && pv) {
-          if (pv_first) {
-            ok = pt_wait_all(BAR(kPtOEmpty + a), par_o, abort_s);
-            par_o ^= 1u;
+        if (u.len == 0) break;
+        const int nt = u.tiles(), n = a == 0 ? u.n0 : u.n1;
+        // turn j: PV of key tile j and QK^T of key tile j - 1
+        for (int j = nt; j >= 0; --j) {
+          const uint32_t ek = base + 2 * (nt - j), bk = ek % kPtStages;      // keys of j - 1
+          const uint32_t ev = ek - 1, bv = ev % kPtStages;                   // values of j
+          const bool pv = j < n, qk = j > 0 && j - 1 < n;
+          const uint32_t v_lo = (kv0 + bv * (kPtTileBytes >> 4)) | kPtMnMajor;
+          const uint32_t k_lo = (kv0 + bk * (kPtTileBytes >> 4)) | kPtKMajor;
+          if (j < nt) {
+            ok = pt_wait_all(BAR(kPtKvFull + bv), (ev / kPtStages) & 1, abort_s);
+            if (u.edge(j)) {
+              if (ok && pv) ok = pt_wait_all(BAR(kPtVClear + bv), (par_clear >> bv) & 1, abort_s);
+              par_clear ^= 1u << bv;
+            }
           }
-          ok = ok && pt_wait_all(BAR(kPtPReady + 2 * a), par_p, abort_s);
-        }
-        ok = ok && pt_wait_all(BAR(kPtTurn + a), par_turn, abort_s);
-        par_turn ^= 1u;
-        if (ok && pv) {
-          // 64 keys at a time, as the softmax has them ready
-          tc_fence_after();
-          if (pt_elect()) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              pt_mma_pv(o_col, s_col + 8 * kk, v_lo + (2048 >> 4) * kk,
-                        (pv_first && kk == 0) ? 0u : 1u);
-          }
-          ok = pt_wait_all(BAR(kPtPReady + 2 * a + 1), par_p, abort_s);
-          if (!ok) break;
-          par_p ^= 1u;
-          tc_fence_after();
-          if (pt_elect()) {
-#pragma unroll
-            for (int kk = 4; kk < 8; ++kk)
-              pt_mma_pv(o_col, s_col + 8 * kk, v_lo + (2048 >> 4) * kk, 1u);
-          }
-        }
-        if (ok && qk) {
-          if (qk_first) {
+          if (ok && j > 0) ok = pt_wait_all(BAR(kPtKvFull + bk), (ek / kPtStages) & 1, abort_s);
+          if (ok && qk && j == n) {
             ok = pt_wait_all(BAR(kPtQFull + a), par_q, abort_s);
             par_q ^= 1u;
           }
+          if (ok && pv) {
+            if (j == n - 1) {
+              ok = pt_wait_all(BAR(kPtOEmpty + a), par_o, abort_s);
+              par_o ^= 1u;
+            }
+            ok = ok && pt_wait_all(BAR(kPtPReady + 2 * a), par_p, abort_s);
+          }
+          ok = ok && pt_wait_all(BAR(kPtTurn + a), par_turn, abort_s);
           if (!ok) break;
-          if (pt_elect()) {
+          par_turn ^= 1u;
+          if (pv) {
+            // 64 keys at a time, as the softmax has them ready
+            tc_fence_after();
+            if (pt_elect()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                pt_mma_pv(o_col, s_col + 8 * kk, v_lo + (2048 >> 4) * kk,
+                          (j == n - 1 && kk == 0) ? 0u : 1u);
+            }
+            ok = pt_wait_all(BAR(kPtPReady + 2 * a + 1), par_p, abort_s);
+            if (!ok) break;
+            par_p ^= 1u;
+            tc_fence_after();
+            if (pt_elect()) {
+#pragma unroll
+              for (int kk = 4; kk < 8; ++kk)
+                pt_mma_pv(o_col, s_col + 8 * kk, v_lo + (2048 >> 4) * kk, 1u);
+            }
+          }
+          if (qk && pt_elect()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
               const uint32_t off = (kk & 3) * 2 + (kk >> 2) * (kPtHalf >> 4);
@@ -708,23 +736,17 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
             }
             tc_commit(BAR(kPtSFull + a));
           }
+          __syncwarp();
+          if (pt_elect()) {
+            mbar_arrive(BAR(kPtTurn + (a ^ 1)));
+            if (pv && j == 0) tc_commit(BAR(kPtOFull + a));
+            if (qk && j == 1) tc_commit(BAR(kPtQEmpty + a));
+            if (j < nt) tc_commit(BAR(kPtKvEmpty + bv));
+            if (j > 0) tc_commit(BAR(kPtKvEmpty + bk));
+          }
+          __syncwarp();
         }
-        if (!ok) break;
-        if (pt_elect()) {
-          mbar_arrive(BAR(kPtTurn + (a ^ 1)));
-          if (pv && j == 0) tc_commit(BAR(kPtOFull + a));
-          if (qk && jn == 0) tc_commit(BAR(kPtQEmpty + a));
-          if (step != ~0u) tc_commit(BAR(kPtKvEmpty + bv));
-          if (next) tc_commit(BAR(kPtKvEmpty + bk));
-        }
-        if (!next) break;
-        u = nx;
-        j = jn;
-        ++step;
-        if (j == 0)
-          ok = next_unit();
-        else
-          --jn;
+        base += 2 * nt;
       }
       gave_up = !ok;
       // every MMA issued has completed before the tensor memory is freed
@@ -848,6 +870,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
   p.inv_g = (65536 + G - 1) / G;
   p.units = prompt_units(a);
   p.scale2 = a.sm_scale * 1.4426950408889634f;
+  p.out_by_32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0;
   p.err_flags = a.err_flags;
   CUtensorMap mq, mk, mv;
   if (!encode_head_tensor_map(&mq, a.q, a.num_tokens, a.num_q_heads, a.q_stride, G, p.TQ) ||
