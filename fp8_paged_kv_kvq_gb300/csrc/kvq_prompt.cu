@@ -11,10 +11,13 @@
 //    token t, head h G + g, with floor(128 / G) tokens per tile, so short
 //    prompts fill the tensor core's rows and a key tile is read once for all G
 //    heads.  The unit's key tiles (128 keys) go from its diagonal down to 0.
-//  * Sequence s may use the unit numbers floor(cu[s] / TU) + s up to the next
-//    sequence's (TU tokens per unit): at least ceil(len / TU) of them, so a
-//    unit number finds its sequence by a search over cu_seqlens, with no plan
-//    launch, no workspace and no bound on the number of sequences.
+//  * Units are numbered through the sequences (TU tokens per unit); every CTA
+//    sums their counts in shared memory, so there is no plan launch and no
+//    workspace.  Of more than kPtSeqs sequences, s uses the numbers
+//    floor(cu[s] / TU) + s up to the next one's, at least ceil(len / TU) of them,
+//    and a number finds its sequence by a search over cu_seqlens itself, with no
+//    bound on their count; the numbers left over cost a look each (64 prompts of
+//    one unit would have as many of those as units).
 //  * CTAs of 512 threads, one per SM, that go on with the units of blocks that
 //    have not started (cluster launch control) until there are none, longest
 //    rows of a sequence first.  Warps 0-3 and 4-7: softmax of
@@ -35,7 +38,7 @@
 //    the QK^T that it waited for was issued after it.
 //  * 0 times an infinity is not 0, so zero probabilities do not hide unseen
 //    values.  Of the value tiles that some row of the unit does not see whole
-//    warp 15 clears the rows past the sequence and every infinity and NaN; the
+//    warp 15 clears the rows that none sees and every infinity and NaN; the
 //    epilogue adds those a row does see back (rare, one flag per unit).
 //  * Every wait is bounded; a role that gives up raises a shared abort flag,
 //    copies and MMAs in flight complete, the CTA frees its tensor memory
@@ -43,6 +46,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "kvq_device.cuh"
@@ -56,7 +60,8 @@ constexpr int kPtKeys = 128;                          // keys of a tile
 constexpr int kPtStages = 4;                          // ring: key tiles in even stages, values in odd
 constexpr int kPtWarpEpi = 8, kPtWarpLoad = 12, kPtWarpMma = 13, kPtWarpClear = 15;
 constexpr int kPtThreads = 512;
-constexpr int kPtUnits = 4;                           // work numbers ahead
+constexpr int kPtUnits = 4;                           // units ahead
+constexpr int kPtSeqs = 2048;                         // sequences whose units are summed
 constexpr float kPtLazy = 8.0f;                       // log2 of the largest unnormalised p
 
 // shared memory, offsets from a 1024-byte aligned base
@@ -69,7 +74,10 @@ constexpr int kPtOffUnit = kPtOffSum + 2 * 128 * 4;
 constexpr int kPtOffDirty = kPtOffUnit + kPtUnits * 16;
 constexpr int kPtOffSteal = kPtOffDirty + kPtUnits * 4;          // two answers of 16 bytes
 constexpr int kPtOffMisc = kPtOffSteal + 32;                     // tmem base, abort
-constexpr int kPtOffBar = kPtOffMisc + 16;
+constexpr int kPtOffScan = kPtOffMisc + 16;                      // a warp's sum each
+constexpr int kPtOffPre = kPtOffScan + 16 * 4;                   // units before each sequence
+constexpr int kPtOffCu = kPtOffPre + (kPtSeqs + 1) * 4;          // cu_seqlens
+constexpr int kPtOffBar = (kPtOffCu + (kPtSeqs + 1) * 4 + 7) / 8 * 8;
 enum : int {
   kPtKvFull = 0,
   kPtKvEmpty = kPtKvFull + kPtStages,
@@ -141,6 +149,8 @@ struct PromptParams {
   int32_t N, max_seqlen, G, H;
   int32_t TQ;                                          // tokens of a tile: 128 / G
   int32_t inv_g;                                       // ceil(65536 / G)
+  uint64_t h_magic;                                    // ceil(2^h_shift / H): n / H for n < 2^31
+  int32_t h_shift;                                     // 32 + ceil(log2(H))
   int64_t units;                                       // work numbers
   float scale2;                                        // sm_scale log2(e)
   int32_t out_by_32;                                   // out rows are 32-byte aligned
@@ -202,6 +212,10 @@ struct PtUnit {
     n1 = t1 > t0 ? (t1 + kPtKeys - 1) / kPtKeys : 0;
   }
   __device__ __forceinline__ int tiles() const { return max(n0, n1); }
+  // keys of key tile j that some row sees
+  __device__ __forceinline__ int keys(int j, int TQ) const {
+    return min(kPtKeys, min(len, tok0 + 2 * TQ) - j * kPtKeys);
+  }
   // key tile j has a key that the unit's first row does not see
   __device__ __forceinline__ bool edge(int j) const { return j * kPtKeys + kPtKeys - 1 > tok0; }
 };
@@ -210,29 +224,51 @@ __device__ __forceinline__ bool pt_bounds_ok(const PromptParams &p, int begin, i
   return begin >= 0 && end >= begin && end <= p.num_tokens && end - begin <= p.max_seqlen;
 }
 
-// Work number w as a unit (len 0: none there).  All lanes of a warp.
-__device__ __forceinline__ int4 pt_find(const PromptParams &p, uint32_t w, int lane) {
-  const int TU = 2 * p.TQ;
-  const uint32_t H = static_cast<uint32_t>(p.H), xq = w / H;
-  const int h = static_cast<int>(w - xq * H);
-  const int64_t x = xq;
-  int lo = 0, hi = p.N;
+// The last i in [lo, hi) with below(i), which holds up to some i; -1 if none.
+// All lanes of a warp.
+template <typename F>
+__device__ __forceinline__ int pt_last(int lo, int hi, int lane, F below) {
   for (;;) {
-    const int step = (hi - lo + 31) / 32;
-    const int64_t i = lo + static_cast<int64_t>(lane) * step;
-    const bool below = i < hi && __ldg(p.cu + i) / TU + i <= x;
-    const int c = __ffs(~__ballot_sync(0xFFFFFFFFu, below)) - 1;   // leading lanes below (32: -1)
-    const int cnt = c < 0 ? 32 : c;
-    if (cnt == 0) return make_int4(0, 0, 0, 0);
+    const int step = (hi - lo + 31) >> 5;
+    const int i = lo + lane * step;
+    const int c = __ffs(~__ballot_sync(0xFFFFFFFFu, i < hi && below(i))) - 1;
+    const int cnt = c < 0 ? 32 : c;                    // leading lanes below
+    if (cnt == 0) return -1;
     lo += (cnt - 1) * step;
     hi = min(hi, lo + step);
-    if (step == 1) break;
+    if (step == 1) return lo;
   }
-  const int a = __ldg(p.cu + lo), b = __ldg(p.cu + lo + 1);
-  if (!pt_bounds_ok(p, a, b)) return make_int4(0, 0, 0, 0);
-  const int units = (b - a) / TU + ((b - a) % TU != 0 ? 1 : 0);
-  const int64_t u = units - 1 - (x - (static_cast<int64_t>(a / TU) + lo));   // longest rows first
-  if (u < 0 || u >= units) return make_int4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ int pt_units_of(int len, int TU) {
+  return len / TU + (len % TU != 0 ? 1 : 0);
+}
+
+// Work number w as a unit (len 0: none there).  All lanes of a warp.
+__device__ __forceinline__ int4 pt_find(const PromptParams &p, const int *pre, const int *cu_s,
+                                        uint32_t w, int lane) {
+  const int TU = 2 * p.TQ;
+  const uint32_t x = static_cast<uint32_t>((static_cast<uint64_t>(w) * p.h_magic) >> p.h_shift);
+  const int h = static_cast<int>(w - x * static_cast<uint32_t>(p.H));      // w % H
+  int s, a, b;
+  int64_t u;                                           // within the sequence, longest rows first
+  if (p.N <= kPtSeqs) {
+    if (x >= static_cast<uint32_t>(pre[p.N])) return make_int4(0, 0, 0, 0);
+    s = pt_last(0, p.N, lane, [&](int i) { return static_cast<uint32_t>(pre[i]) <= x; });
+    a = cu_s[s];
+    b = cu_s[s + 1];
+    u = static_cast<int64_t>(pre[s + 1]) - 1 - x;
+  } else {
+    s = pt_last(0, p.N, lane, [&](int i) {
+      return static_cast<int64_t>(__ldg(p.cu + i) / TU) + i <= x;
+    });
+    if (s < 0) return make_int4(0, 0, 0, 0);
+    a = __ldg(p.cu + s);
+    b = __ldg(p.cu + s + 1);
+    if (!pt_bounds_ok(p, a, b)) return make_int4(0, 0, 0, 0);
+    u = pt_units_of(b - a, TU) - 1 - (x - (static_cast<int64_t>(a / TU) + s));
+  }
+  if (u < 0 || u * TU >= b - a) return make_int4(0, 0, 0, 0);
   return make_int4(a, b - a, h, static_cast<int>(u) * TU);
 }
 
@@ -388,34 +424,20 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   volatile float *sum_s = reinterpret_cast<volatile float *>(smem + kPtOffSum);
 
   allow_dependents_launch();
-  if (tid == 0) {
-    for (int s = 0; s < kPtStages; ++s) {
-      mbar_init(BAR(kPtKvFull + s), 1);
-      mbar_init(BAR(kPtKvEmpty + s), 2 + (s & 1));     // both tiles; value tiles: warp 15 too
-      mbar_init(BAR(kPtVClear + s), 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(BAR(kPtQFull + a), 1);
-      mbar_init(BAR(kPtQEmpty + a), 1);
-      mbar_init(BAR(kPtSFull + a), 1);
-      mbar_init(BAR(kPtPReady + 2 * a), 4);
-      mbar_init(BAR(kPtPReady + 2 * a + 1), 4);
-      mbar_init(BAR(kPtOFull + a), 1);
-      mbar_init(BAR(kPtOEmpty + a), 4);
-      mbar_init(BAR(kPtSumFull + a), 4);
-      mbar_init(BAR(kPtDrain + a), 1);
-      mbar_init(BAR(kPtTurn + a), 1);
-    }
-    mbar_init(BAR(kPtSteal), 1);
-    mbar_init(BAR(kPtSteal + 1), 1);
-    for (int e = 0; e < kPtUnits; ++e) {
-      mbar_init(BAR(kPtUnitFull + e), 1);
-      mbar_init(BAR(kPtUnitEmpty + e), 8 + 4 + 3);     // softmax, epilogue, warps 13-15
-    }
-    *abort_s = 0;
+  if (tid < kPtBars) {
+    uint32_t count = 1;
+    if (tid >= kPtKvEmpty && tid < kPtKvEmpty + kPtStages)
+      count = 2 + ((tid - kPtKvEmpty) & 1);            // both tiles; value tiles: warp 15 too
+    if ((tid >= kPtPReady && tid < kPtPReady + 4) || (tid >= kPtOEmpty && tid < kPtOEmpty + 2) ||
+        (tid >= kPtSumFull && tid < kPtSumFull + 2))
+      count = 4;                                       // a warp each of the softmax or epilogue
+    if (tid >= kPtUnitEmpty && tid < kPtUnitEmpty + kPtUnits)
+      count = 8 + 4 + 3;                               // softmax, epilogue, warps 13-15
+    mbar_init(BAR(tid), count);
     fence_mbarrier_init();
   }
-  if (tid == 32) {
+  if (tid == 0) *abort_s = 0;
+  if (tid == 64) {
     pt_prefetch_map(&tm_q);
     pt_prefetch_map(&tm_k);
     pt_prefetch_map(&tm_v);
@@ -429,6 +451,41 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();
+  int *pre = reinterpret_cast<int *>(smem + kPtOffPre);
+  int *cu_s = reinterpret_cast<int *>(smem + kPtOffCu);
+  if (p.N <= kPtSeqs) {
+    int *warp_sum = reinterpret_cast<int *>(smem + kPtOffScan);
+    int carry = 0;
+    for (int s0 = 0; s0 < p.N; s0 += kPtThreads) {
+      const int i = s0 + tid;
+      int a = 0, b = 0;
+      if (i < p.N) {
+        a = __ldg(p.cu + i);
+        b = __ldg(p.cu + i + 1);
+        cu_s[i] = a;
+        cu_s[i + 1] = b;
+      }
+      int n = i < p.N && pt_bounds_ok(p, a, b) ? pt_units_of(b - a, 2 * p.TQ) : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, n, off);
+        if (lane >= off) n += v;
+      }
+      if (lane == 31) warp_sum[warp] = n;
+      __syncthreads();
+      int before = carry;
+#pragma unroll
+      for (int k = 0; k < kPtThreads / 32; ++k) {
+        const int v = warp_sum[k];
+        if (k < warp) before += v;
+        carry += v;
+      }
+      if (i < p.N) pre[i + 1] = before + n;
+      __syncthreads();
+    }
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+  }
 
   // Unit `t` of this CTA; the caller's warp (or lone lane) releases its entry.
   auto take_unit = [&](int t, PtUnit &u) -> bool {
@@ -553,7 +610,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       uint32_t idx = 0;                                // ring entries issued
       uint32_t loads[2] = {0, 0};                      // query tiles
       // Units: the own block's first, then those of blocks that have not
-      // started.  Answers are asked for while a unit's last two tiles are loaded
+      // started.  Answers are asked for before a unit's last two tiles are loaded
       // (any earlier, and the CTAs that ask first hold work back from those that
       // finish first), two of them if it has no more.
       const uint32_t steal = smem_addr(smem + kPtOffSteal);
@@ -569,7 +626,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         if (lane == 0 && w < p.N && p.err_flags &&
             !pt_bounds_ok(p, __ldg(p.cu + w), __ldg(p.cu + w + 1)))
           atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
-        return pt_find(p, static_cast<uint32_t>(w), lane);
+        return pt_find(p, pre, cu_s, static_cast<uint32_t>(w), lane);
       };
       // the next answer with work in it, or none (length 0)
       auto next_unit = [&](int4 &e) -> bool {
@@ -632,17 +689,23 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       int4 e = find(blockIdx.x);
       bool ok = e.y > 0 || next_unit(e);
       for (int t = 0; ok; ++t) {
-        ok = announce(t, e);
-        if (!ok || e.y == 0) break;
+        if (e.y == 0) {
+          ok = announce(t, e);
+          break;
+        }
         PtUnit u;
         u.shape(e, p.TQ);
         const int nt = u.tiles();
         for (int j = nt - 1; j >= 0 && ok; --j) {
-          if (j == (nt > 1 ? 1 : 0)) ask(nt > 2 ? 1 : 2);
           // the first keys and values ahead of the queries, whose tiles are free
           // only once the last unit's products with them are done
-          if (lane == 0) ok = load_kv(u, j) && (j < nt - 1 || load_q(u));
+          if (lane == 0) ok = load_kv(u, j);
+          if (j == nt - 1) {
+            ok = __all_sync(0xFFFFFFFFu, ok) && announce(t, e);
+            if (ok && lane == 0) ok = load_q(u);
+          }
           ok = __all_sync(0xFFFFFFFFu, ok);
+          if (ok && j == (nt > 2 ? 2 : 0)) ask(nt > 2 ? 1 : 2);
         }
         ok = ok && next_unit(e);
       }
@@ -782,7 +845,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
             continue;
           }
           uint8_t *tile = smem + kPtOffKv + b * kPtTileBytes;
-          const int rows = min(kPtKeys, u.len - j * kPtKeys);   // of this sequence
+          const int rows = u.keys(j, p.TQ);
           // 0 times the values, summed: NaN where one of them is not finite
           uint32_t sum0 = 0u, sum1 = 0u;
 #pragma unroll 1
@@ -815,8 +878,8 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
               *w = x;
             }
           }
-          // rows past the sequence
-          for (int r = rows + (lane >> 3); r < kPtKeys; r += 4) {
+          // the rows after them
+          for (int r = rows + (lane >> 3); r < 128; r += 4) {
             *reinterpret_cast<uint4 *>(tile + r * 128 + 16 * (lane & 7)) = make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4 *>(tile + kPtHalf + r * 128 + 16 * (lane & 7)) =
                 make_uint4(0u, 0u, 0u, 0u);
@@ -844,14 +907,22 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   }
 }
 
+// Work numbers of a call: at least its units.
 int64_t prompt_units(const PromptArgs &a) {
   const int64_t TU = 2 * (128 / (a.num_q_heads / a.num_kv_heads));
-  return (a.num_tokens / TU + a.num_seqs) * a.num_kv_heads;
+  int64_t n = a.num_tokens / TU + a.num_seqs;
+  if (a.num_seqs <= kPtSeqs) {
+    const int64_t most = (static_cast<int64_t>(a.max_seqlen) + TU - 1) / TU;
+    n = std::min(n, a.num_seqs * std::max<int64_t>(most, 1));
+  }
+  return n * a.num_kv_heads;
 }
 
 }  // namespace
 
-bool prompt_attention_supported(const PromptArgs &a) { return prompt_units(a) <= 0x7FFFFFFF; }
+bool prompt_attention_supported(const PromptArgs &a) {
+  return a.num_seqs <= 0x7FFFFF00 && prompt_units(a) <= 0x7FFFFFFF;
+}
 
 cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
   const int G = a.num_q_heads / a.num_kv_heads;
@@ -868,6 +939,10 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
   p.H = a.num_kv_heads;
   p.TQ = 128 / G;
   p.inv_g = (65536 + G - 1) / G;
+  int l = 0;
+  while ((int64_t(1) << l) < p.H) ++l;
+  p.h_shift = 32 + l;
+  p.h_magic = ((uint64_t(1) << p.h_shift) + p.H - 1) / p.H;
   p.units = prompt_units(a);
   p.scale2 = a.sm_scale * 1.4426950408889634f;
   p.out_by_32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0;
