@@ -327,27 +327,36 @@ __device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, int lim
                                            bool fresh, uint32_t ready, int lane,
                                            float &m_ref, float &lsum) {
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  // (lane 0 has the warp's first token, the one that sees the least)
-  const int lim0 = __shfl_sync(0xFFFFFFFFu, lim, 0);
+  // the warp's first row sees the least, its last the most: keys past 32 `parts`
+  // are nobody's
+  const int lim0 = __shfl_sync(0xFFFFFFFFu, lim, 0), lim31 = __shfl_sync(0xFFFFFFFFu, lim, 31);
+  const int parts = lim31 < 0 ? 0 : min(4, lim31 / 32 + 1);
+  if (lim0 >= 127) {
 #pragma unroll 1
-  for (int c = 0; c < 128; c += 64) {
-    float x[64];
-    tmem_ld64(scol + c, x);
-    if (lim0 < c + 63) {
-      // unseen keys, 32 at a time where the warp has any
+    for (int c = 0; c < 128; c += 64) {
+      float x[64];
+      tmem_ld64(scol + c, x);
+#pragma unroll
+      for (int i = 0; i < 64; i += 8)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
+    }
+  } else {
+#pragma unroll 1
+    for (int c = 0; c < 32 * parts; c += 32) {
+      float x[32];
+      tmem_ld32(scol + c, x);
       if (lim0 < c + 31) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = i <= lim - c ? x[i] : -INFINITY;
+        tmem_st32(scol + c, x);
       }
 #pragma unroll
-      for (int i = 32; i < 64; ++i) x[i] = i <= lim - c ? x[i] : -INFINITY;
-      tmem_st64(scol + c, x);
-      tmem_wait_st();
+      for (int i = 0; i < 32; i += 8)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
     }
-#pragma unroll
-    for (int i = 0; i < 64; i += 8)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
+    tmem_wait_st();
   }
   uint32_t x0[32], x1[32];
   tmem_ld32_start(scol, x0);
@@ -374,28 +383,33 @@ __device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, int lim
   const uint64_t sc = pack_f32x2(scale2, scale2), sh = pack_f32x2(shift, shift);
   uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
   // 32 keys: P and their share of the denominator
-  auto part = [&](const uint32_t (&x)[32], uint32_t col) {
+  auto part = [&](const uint32_t (&x)[32], int i0) {
     uint32_t w[16];
+    if (i0 < parts) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float a, b;
-      unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
-                             sc, sh), a, b);
-      a = pt_ex2(a);
-      b = pt_ex2(b);
-      sum[i & 1] = pt_add2(sum[i & 1], pack_f32x2(a, b));
-      w[i] = pack_bf16x2(a, b);
+      for (int i = 0; i < 16; ++i) {
+        float a, b;
+        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                               sc, sh), a, b);
+        a = pt_ex2(a);
+        b = pt_ex2(b);
+        sum[i & 1] = pt_add2(sum[i & 1], pack_f32x2(a, b));
+        w[i] = pack_bf16x2(a, b);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = 0u;
     }
-    tmem_st16u(col, w);
+    tmem_st16u(scol + 16 * i0, w);
   };
   tmem_ld32_done(x0);
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     tmem_ld32_start(scol + 64 * h + 32, x1);
-    part(x0, scol + 32 * h);
+    part(x0, 2 * h);
     tmem_ld32_done(x1);
     if (h == 0) tmem_ld32_start(scol + 64, x0);
-    part(x1, scol + 32 * h + 16);
+    part(x1, 2 * h + 1);
     if (h == 0) tmem_ld32_done(x0);
     tmem_wait_st();
     tc_fence_before();
