@@ -479,7 +479,13 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         cu_s[i] = a;
         cu_s[i + 1] = b;
       }
-      int n = i < p.N && pt_bounds_ok(p, a, b) ? pt_units_of(b - a, 2 * p.TQ) : 0;
+      int n = 0;
+      if (i < p.N) {
+        if (pt_bounds_ok(p, a, b))
+          n = pt_units_of(b - a, 2 * p.TQ);
+        else if (blockIdx.x == 0 && p.err_flags)
+          atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
+      }
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, n, off);
@@ -589,8 +595,10 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         for (int c = 0; c < kHeadDim; c += 32) {
           float o[32];
           tmem_ld32(tl + pt_o(a) + c, o);
+          const uint64_t inv2 = pack_f32x2(inv, inv);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= inv;
+          for (int i = 0; i < 32; i += 2)
+            unpack_f32x2(mul_f32x2(pack_f32x2(o[i], o[i + 1]), inv2), o[i], o[i + 1]);
           if (dirty) {
             // the infinities and NaN this row sees in the edge tiles
             const int last = min(tok, u.len - 1);
@@ -637,7 +645,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       };
       auto find = [&](int64_t w) -> int4 {
         // (every work number is somebody's, and there are more than sequences)
-        if (lane == 0 && w < p.N && p.err_flags &&
+        if (p.N > kPtSeqs && lane == 0 && w < p.N && p.err_flags &&
             !pt_bounds_ok(p, __ldg(p.cu + w), __ldg(p.cu + w + 1)))
           atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
         return pt_find(p, pre, cu_s, static_cast<uint32_t>(w), lane);
@@ -757,6 +765,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         if (lane == 0) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
         if (u.len == 0) break;
         const int nt = u.tiles(), n = a == 0 ? u.n0 : u.n1;
+        const bool turns = u.n1 > 0;                   // (a lone tile 0 need not pass them)
         // turn j: PV of key tile j and QK^T of key tile j - 1
         for (int j = nt; j >= 0; --j) {
           const uint32_t ek = base + 2 * (nt - j), bk = ek % kPtStages;      // keys of j - 1
@@ -783,9 +792,11 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
             }
             ok = ok && pt_wait_all(BAR(kPtPReady + 2 * a), par_p, abort_s);
           }
-          ok = ok && pt_wait_all(BAR(kPtTurn + a), par_turn, abort_s);
+          if (turns) {
+            ok = ok && pt_wait_all(BAR(kPtTurn + a), par_turn, abort_s);
+            par_turn ^= 1u;
+          }
           if (!ok) break;
-          par_turn ^= 1u;
           if (pv) {
             // 64 keys at a time, as the softmax has them ready
             tc_fence_after();
@@ -815,7 +826,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
           }
           __syncwarp();
           if (pt_elect()) {
-            mbar_arrive(BAR(kPtTurn + (a ^ 1)));
+            if (turns) mbar_arrive(BAR(kPtTurn + (a ^ 1)));
             if (pv && j == 0) tc_commit(BAR(kPtOFull + a));
             if (qk && j == 1) tc_commit(BAR(kPtQEmpty + a));
             if (j < nt) tc_commit(BAR(kPtKvEmpty + bv));
