@@ -13,7 +13,10 @@
 //    heads.  The unit's key tiles (128 keys) go from its diagonal down to 0.
 //  * Units are numbered through the sequences (TU tokens per unit); every CTA
 //    sums their counts in shared memory, so there is no plan launch and no
-//    workspace.  Of more than kPtSeqs sequences, s uses the numbers
+//    workspace.  (Cutting the packed tokens instead, with rows of several
+//    sequences in one tile, took 9 us instead of 15 for 64 prompts of 16 tokens,
+//    but 348 us instead of 322 for 8 of 355 to 4,096 and 64 heads: diagonals that
+//    no longer end with a key tile.)  Of more than kPtSeqs sequences, s uses the numbers
 //    floor(cu[s] / TU) + s up to the next one's, at least ceil(len / TU) of them,
 //    and a number finds its sequence by a search over cu_seqlens itself, with no
 //    bound on their count; the numbers left over cost a look each (64 prompts of
@@ -244,6 +247,16 @@ __device__ __forceinline__ int pt_units_of(int len, int TU) {
   return len / TU + (len % TU != 0 ? 1 : 0);
 }
 
+// Inclusive sums over a warp.
+__device__ __forceinline__ int pt_scan(int n, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, n, off);
+    if (lane >= off) n += v;
+  }
+  return n;
+}
+
 // Work number w as a unit (len 0: none there).  All lanes of a warp.
 __device__ __forceinline__ int4 pt_find(const PromptParams &p, const int *pre, const int *cu_s,
                                         uint32_t w, int lane) {
@@ -319,106 +332,146 @@ __device__ __forceinline__ int64_t pt_stolen(uint32_t answer) {
   return some != 0 ? static_cast<int64_t>(x) : -1;
 }
 
-// One key tile of one row: S from TMEM, the reference and the denominator
-// brought up to date (the O row with them), P as bf16 over S's columns, its two
-// halves announced one after the other.  Keys past `lim` (within the tile) are
-// not seen.
-__device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, int lim, float scale2,
-                                           bool fresh, uint32_t ready, int lane,
-                                           float &m_ref, float &lsum) {
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  // the warp's first row sees the least, its last the most: keys past 32 `parts`
-  // are nobody's
-  const int lim0 = __shfl_sync(0xFFFFFFFFu, lim, 0), lim31 = __shfl_sync(0xFFFFFFFFu, lim, 31);
-  const int parts = lim31 < 0 ? 0 : min(4, lim31 / 32 + 1);
-  if (lim0 >= 127) {
+// The running statistics of one row.
+struct PtRow {
+  float m = -INFINITY;                                 // reference
+  float sum = 0.0f;                                    // denominator under it
+
+  // The reference moved to a tile's maximum `top` where that is far above it,
+  // the denominator and (unless fresh) the O row brought under the new one;
+  // returns the shift of the exponents.
+  __device__ __forceinline__ float meet(float top, float scale2, bool fresh, uint32_t ocol) {
+    const bool unset = m == -INFINITY;
+    const bool move = unset ? top > -INFINITY : (top - m) * scale2 > kPtLazy;
+    if (__any_sync(0xFFFFFFFFu, move && !unset)) {
+      // (rows of the warp that stay multiply by 1)
+      const float f = (move && !unset) ? pt_ex2((m - top) * scale2) : 1.0f;
+      sum *= f;
+      if (!fresh) {
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 64) {
-      float x[64];
-      tmem_ld64(scol + c, x);
+        for (int c = 0; c < kHeadDim; c += 16) {
+          float o[16];
+          tmem_ld16(ocol + c, o);
 #pragma unroll
-      for (int i = 0; i < 64; i += 8)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
-    }
-  } else {
-#pragma unroll 1
-    for (int c = 0; c < 32 * parts; c += 32) {
-      float x[32];
-      tmem_ld32(scol + c, x);
-      if (lim0 < c + 31) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = i <= lim - c ? x[i] : -INFINITY;
-        tmem_st32(scol + c, x);
+          for (int i = 0; i < 16; ++i) o[i] *= f;
+          tmem_st16(ocol + c, o);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 32; i += 8)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
     }
-    tmem_wait_st();
+    if (move) m = top;
+    return m == -INFINITY ? 0.0f : -m * scale2;
+  }
+};
+
+// P of 32 scores as bf16 in 16 columns, its sum added to `sum`.
+__device__ __forceinline__ void pt_part(const uint32_t (&x)[32], uint32_t col, uint64_t scale,
+                                        uint64_t shift, uint64_t (&sum)[2]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a, b;
+    unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                           scale, shift), a, b);
+    a = pt_ex2(a);
+    b = pt_ex2(b);
+    sum[i & 1] = pt_add2(sum[i & 1], pack_f32x2(a, b));
+    w[i] = pack_bf16x2(a, b);
+  }
+  tmem_st16u(col, w);
+}
+
+// 64 keys of P are in TMEM.
+__device__ __forceinline__ void pt_announce(uint32_t bar, int lane) {
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// One key tile of one row whose warp sees all its keys: S from TMEM, the row's
+// statistics brought up to date, P as bf16 over S's columns, its two halves
+// announced one after the other.
+__device__ __forceinline__ void pt_softmax(uint32_t scol, uint32_t ocol, float scale2, bool fresh,
+                                           uint32_t ready, int lane, PtRow &row) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 64) {
+    float x[64];
+    tmem_ld64(scol + c, x);
+#pragma unroll
+    for (int i = 0; i < 64; i += 8)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
   }
   uint32_t x0[32], x1[32];
   tmem_ld32_start(scol, x0);
   const float top = fmaxf(pt_max3(mx[0], mx[1], mx[2]), mx[3]);
-  const bool unset = m_ref == -INFINITY;
-  const bool move = unset ? top > -INFINITY : (top - m_ref) * scale2 > kPtLazy;
-  if (__any_sync(0xFFFFFFFFu, move && !unset)) {
-    // (rows of the warp that stay multiply by 1)
-    const float f = (move && !unset) ? pt_ex2((m_ref - top) * scale2) : 1.0f;
-    lsum *= f;
-    if (!fresh) {
-#pragma unroll 1
-      for (int c = 0; c < kHeadDim; c += 16) {
-        float o[16];
-        tmem_ld16(ocol + c, o);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] *= f;
-        tmem_st16(ocol + c, o);
-      }
-    }
-  }
-  if (move) m_ref = top;
-  const float shift = m_ref == -INFINITY ? 0.0f : -m_ref * scale2;
+  const float shift = row.meet(top, scale2, fresh, ocol);
   const uint64_t sc = pack_f32x2(scale2, scale2), sh = pack_f32x2(shift, shift);
   uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
-  // 32 keys: P and their share of the denominator
-  auto part = [&](const uint32_t (&x)[32], int i0) {
-    uint32_t w[16];
-    if (i0 < parts) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float a, b;
-        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
-                               sc, sh), a, b);
-        a = pt_ex2(a);
-        b = pt_ex2(b);
-        sum[i & 1] = pt_add2(sum[i & 1], pack_f32x2(a, b));
-        w[i] = pack_bf16x2(a, b);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = 0u;
-    }
-    tmem_st16u(scol + 16 * i0, w);
-  };
   tmem_ld32_done(x0);
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     tmem_ld32_start(scol + 64 * h + 32, x1);
-    part(x0, 2 * h);
+    pt_part(x0, scol + 32 * h, sc, sh, sum);
     tmem_ld32_done(x1);
     if (h == 0) tmem_ld32_start(scol + 64, x0);
-    part(x1, 2 * h + 1);
+    pt_part(x1, scol + 32 * h + 16, sc, sh, sum);
     if (h == 0) tmem_ld32_done(x0);
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(ready + 8 * h);
+    pt_announce(ready + 8 * h, lane);
   }
   float a, b;
   unpack_f32x2(pt_add2(sum[0], sum[1]), a, b);
-  lsum += a + b;
+  row.sum += a + b;
+}
+
+// The same for a tile whose keys some of the warp's rows do not see: the row
+// sees the keys lo .. hi, counted within the tile, and both rise along the rows.
+// 32 keys at a time; the scores of parts that no row sees are not read and
+// their P is 0.
+__device__ __forceinline__ void pt_softmax_edge(uint32_t scol, uint32_t ocol, int hi,
+                                                float scale2, bool fresh, uint32_t ready, int lane,
+                                                PtRow &row) {
+  const int hi0 = __shfl_sync(0xFFFFFFFFu, hi, 0), hi31 = __shfl_sync(0xFFFFFFFFu, hi, 31);
+  const int parts = hi31 < 0 ? 0 : min(4, hi31 / 32 + 1);
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int c = 0; c < 32 * parts; c += 32) {
+    float x[32];
+    tmem_ld32(scol + c, x);
+    if (hi0 < c + 31) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = i <= hi - c ? x[i] : -INFINITY;
+      tmem_st32(scol + c, x);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) mx[q] = pt_max3(mx[q], x[i + q], x[i + q + 4]);
+  }
+  tmem_wait_st();
+  const float top = fmaxf(pt_max3(mx[0], mx[1], mx[2]), mx[3]);
+  const float shift = row.meet(top, scale2, fresh, ocol);
+  const uint64_t sc = pack_f32x2(scale2, scale2), sh = pack_f32x2(shift, shift);
+  uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    if (i < parts) {
+      uint32_t x[32];
+      tmem_ld32_start(scol + 32 * i, x);
+      tmem_ld32_done(x);
+      pt_part(x, scol + 16 * i, sc, sh, sum);
+    } else {
+      uint32_t w[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) w[k] = 0u;
+      tmem_st16u(scol + 16 * i, w);
+    }
+    if (i & 1) pt_announce(ready + 8 * (i >> 1), lane);
+  }
+  float a, b;
+  unpack_f32x2(pt_add2(sum[0], sum[1]), a, b);
+  row.sum += a + b;
 }
 
 __global__ void __launch_bounds__(kPtThreads, 1)
@@ -467,30 +520,30 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   grid_dependency_wait();
   int *pre = reinterpret_cast<int *>(smem + kPtOffPre);
   int *cu_s = reinterpret_cast<int *>(smem + kPtOffCu);
-  if (p.N <= kPtSeqs) {
+  // Units of sequence i, which is flagged if it is not to be computed.
+  auto count_units = [&](int i) -> int {
+    const int a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1);
+    cu_s[i] = a;
+    cu_s[i + 1] = b;
+    if (pt_bounds_ok(p, a, b)) return pt_units_of(b - a, 2 * p.TQ);
+    if (blockIdx.x == 0 && p.err_flags) atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
+    return 0;
+  };
+  if (p.N <= 32) {
+    // the loading warp alone, which is the one to use them
+    if (warp == kPtWarpLoad) {
+      int n = lane < p.N ? count_units(lane) : 0;
+      n = pt_scan(n, lane);
+      if (lane < p.N) pre[lane + 1] = n;
+      if (lane == 0) pre[0] = 0;
+      __syncwarp();
+    }
+  } else if (p.N <= kPtSeqs) {
     int *warp_sum = reinterpret_cast<int *>(smem + kPtOffScan);
     int carry = 0;
     for (int s0 = 0; s0 < p.N; s0 += kPtThreads) {
       const int i = s0 + tid;
-      int a = 0, b = 0;
-      if (i < p.N) {
-        a = __ldg(p.cu + i);
-        b = __ldg(p.cu + i + 1);
-        cu_s[i] = a;
-        cu_s[i + 1] = b;
-      }
-      int n = 0;
-      if (i < p.N) {
-        if (pt_bounds_ok(p, a, b))
-          n = pt_units_of(b - a, 2 * p.TQ);
-        else if (blockIdx.x == 0 && p.err_flags)
-          atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
-      }
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, n, off);
-        if (lane >= off) n += v;
-      }
+      const int n = pt_scan(i < p.N ? count_units(i) : 0, lane);
       if (lane == 31) warp_sum[warp] = n;
       __syncthreads();
       int before = carry;
@@ -536,15 +589,21 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       const int n = a == 0 ? u.n0 : u.n1;
       if (n == 0) continue;
       const int tok = u.tok0 + a * p.TQ + t_row;
-      float m_ref = -INFINITY, lsum = 0.0f;
+      // the key tiles that all of the warp's rows see whole (the first row sees least)
+      const int whole = (__shfl_sync(0xFFFFFFFFu, tok, 0) + 1) / kPtKeys;
+      PtRow row;
       for (int j = n - 1; j >= 0; --j, ++steps) {
         if (__any_sync(0xFFFFFFFFu, !pt_wait(BAR(kPtSFull + a), steps & 1, abort_s))) {
           gave_up = true;
           break;
         }
         tc_fence_after();
-        pt_softmax(tl + pt_s(a), tl + pt_o(a), tok - j * kPtKeys, p.scale2, j == n - 1,
-                   BAR(kPtPReady + 2 * a), lane, m_ref, lsum);
+        if (j < whole)
+          pt_softmax(tl + pt_s(a), tl + pt_o(a), p.scale2, j == n - 1, BAR(kPtPReady + 2 * a), lane,
+                     row);
+        else
+          pt_softmax_edge(tl + pt_s(a), tl + pt_o(a), tok - j * kPtKeys, p.scale2, j == n - 1,
+                          BAR(kPtPReady + 2 * a), lane, row);
       }
       if (gave_up) break;
       // the denominators, once the epilogue has read the last unit's
@@ -553,7 +612,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         gave_up = true;
         break;
       }
-      sum_s[128 * a + m] = lsum;
+      sum_s[128 * a + m] = row.sum;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(kPtSumFull + a));
       ++done;

@@ -82,6 +82,18 @@ def test_head_groups(hq, H):
     _run([200, 77, 300], hq, H, seed=hq)
 
 
+@pytest.mark.parametrize("hq,H", [(8, 2), (2, 2), (14, 2)])
+def test_mixed_lengths(hq, H):
+    """Tails, heads and whole short prompts side by side, among empty ones."""
+    g = workloads.generator(31, hq)
+    lens = []
+    for _ in range(20):
+        lens += torch.randint(0, 9, (4,), generator=g).tolist()
+        lens += torch.randint(20, 200, (1,), generator=g).tolist()
+    lens[7] = 700
+    _run(lens, hq, H, seed=31, tail=5, first=3)
+
+
 def test_longer_prompt():
     _run([2333, 130], 8, 2, seed=4)
 
