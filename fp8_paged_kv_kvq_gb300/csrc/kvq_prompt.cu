@@ -73,7 +73,8 @@ constexpr int kPtHalf = kPtTileBytes / 2;
 constexpr int kPtOffQ = 0;
 constexpr int kPtOffKv = 2 * kPtTileBytes;
 constexpr int kPtOffSum = kPtOffKv + kPtStages * kPtTileBytes;   // [tile][128] denominators
-constexpr int kPtOffUnit = kPtOffSum + 2 * 128 * 4;
+constexpr int kPtOffRef = kPtOffSum + 2 * 128 * 4;               // [chain][128] references
+constexpr int kPtOffUnit = kPtOffRef + 2 * 128 * 4;
 constexpr int kPtOffDirty = kPtOffUnit + kPtUnits * 16;
 constexpr int kPtOffSteal = kPtOffDirty + kPtUnits * 4;          // two answers of 16 bytes
 constexpr int kPtOffMisc = kPtOffSteal + 32;                     // tmem base, abort
@@ -150,7 +151,8 @@ struct PromptParams {
   int32_t num_tokens;
   const int32_t *cu;
   int32_t N, max_seqlen, G, H;
-  int32_t TQ;                                          // tokens of a tile: 128 / G
+  int32_t TQ;                                          // tokens of a row tile: 128 / G
+  int32_t TU;                                          // of a unit: one or two tiles
   int32_t inv_g;                                       // ceil(65536 / G)
   uint64_t h_magic;                                    // ceil(2^h_shift / H): n / H for n < 2^31
   int32_t h_shift;                                     // 32 + ceil(log2(H))
@@ -200,11 +202,14 @@ __device__ __forceinline__ bool pt_wait_all(uint32_t bar, uint32_t parity, volat
   return __all_sync(0xFFFFFFFFu, pt_wait(bar, parity, abort));
 }
 
-// A unit: sequence rows [start, start + len), KV head h, tiles from token tok0
-// (within the sequence) on; len = 0 ends the work.
+// A unit: sequence rows [start, start + len), KV head h, queries from token tok0
+// (within the sequence) on; len = 0 ends the work.  `a` is one of the two chains
+// (QK^T, softmax, PV, O): a row tile each over all the key tiles or, where the
+// keys are split, the same row tile over every other key tile.
+template <bool kSplit>
 struct PtUnit {
   int start, len, h, tok0;
-  int n0, n1;                                          // key tiles of tile 0 and 1 (n1 = 0: none)
+  int n0, n1;                                          // key tiles of row tile 0 and 1
   __device__ __forceinline__ void shape(const int4 e, int TQ) {
     start = e.x;
     len = e.y;
@@ -212,12 +217,20 @@ struct PtUnit {
     tok0 = e.w;
     const int t0 = min(len, tok0 + TQ), t1 = min(len, tok0 + 2 * TQ);
     n0 = (t0 + kPtKeys - 1) / kPtKeys;
-    n1 = t1 > t0 ? (t1 + kPtKeys - 1) / kPtKeys : 0;
+    n1 = !kSplit && t1 > t0 ? (t1 + kPtKeys - 1) / kPtKeys : 0;
   }
-  __device__ __forceinline__ int tiles() const { return max(n0, n1); }
+  __device__ __forceinline__ int tiles() const { return kSplit ? n0 : max(n0, n1); }
+  // steps: key tiles, or pairs of them
+  __device__ __forceinline__ int steps() const { return kSplit ? (n0 + 1) / 2 : max(n0, n1); }
+  // chain a's key tiles, from the top: top(a) (-1: none), ..., bottom(a)
+  __device__ __forceinline__ int top(int a) const {
+    return kSplit ? n0 - 1 - a : (a == 0 ? n0 : n1) - 1;
+  }
+  __device__ __forceinline__ int bottom(int a) const { return kSplit ? (n0 - 1 - a) & 1 : 0; }
+  __device__ __forceinline__ int row_tile(int a) const { return kSplit ? 0 : a; }
   // keys of key tile j that some row sees
   __device__ __forceinline__ int keys(int j, int TQ) const {
-    return min(kPtKeys, min(len, tok0 + 2 * TQ) - j * kPtKeys);
+    return min(kPtKeys, min(len, tok0 + (kSplit ? 1 : 2) * TQ) - j * kPtKeys);
   }
   // key tile j has a key that the unit's first row does not see
   __device__ __forceinline__ bool edge(int j) const { return j * kPtKeys + kPtKeys - 1 > tok0; }
@@ -260,7 +273,7 @@ __device__ __forceinline__ int pt_scan(int n, int lane) {
 // Work number w as a unit (len 0: none there).  All lanes of a warp.
 __device__ __forceinline__ int4 pt_find(const PromptParams &p, const int *pre, const int *cu_s,
                                         uint32_t w, int lane) {
-  const int TU = 2 * p.TQ;
+  const int TU = p.TU;
   const uint32_t x = static_cast<uint32_t>((static_cast<uint64_t>(w) * p.h_magic) >> p.h_shift);
   const int h = static_cast<int>(w - x * static_cast<uint32_t>(p.H));      // w % H
   int s, a, b;
@@ -474,6 +487,7 @@ __device__ __forceinline__ void pt_softmax_edge(uint32_t scol, uint32_t ocol, in
   row.sum += a + b;
 }
 
+template <bool kSplit>
 __global__ void __launch_bounds__(kPtThreads, 1)
 prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
@@ -488,13 +502,14 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   volatile int *abort_s = reinterpret_cast<volatile int *>(smem + kPtOffMisc + 4);
   volatile int *dirty_s = reinterpret_cast<volatile int *>(smem + kPtOffDirty);
   int4 *unit_s = reinterpret_cast<int4 *>(smem + kPtOffUnit);
+  volatile float *ref_s = reinterpret_cast<volatile float *>(smem + kPtOffRef);
   volatile float *sum_s = reinterpret_cast<volatile float *>(smem + kPtOffSum);
 
   allow_dependents_launch();
   if (tid < kPtBars) {
     uint32_t count = 1;
     if (tid >= kPtKvEmpty && tid < kPtKvEmpty + kPtStages)
-      count = 2 + ((tid - kPtKvEmpty) & 1);            // both tiles; value tiles: warp 15 too
+      count = (kSplit ? 1 : 2) + ((tid - kPtKvEmpty) & 1);   // the chains; value tiles: warp 15 too
     if ((tid >= kPtPReady && tid < kPtPReady + 4) || (tid >= kPtOEmpty && tid < kPtOEmpty + 2) ||
         (tid >= kPtSumFull && tid < kPtSumFull + 2))
       count = 4;                                       // a warp each of the softmax or epilogue
@@ -525,7 +540,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
     const int a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1);
     cu_s[i] = a;
     cu_s[i + 1] = b;
-    if (pt_bounds_ok(p, a, b)) return pt_units_of(b - a, 2 * p.TQ);
+    if (pt_bounds_ok(p, a, b)) return pt_units_of(b - a, p.TU);
     if (blockIdx.x == 0 && p.err_flags) atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
     return 0;
   };
@@ -561,7 +576,8 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   }
 
   // Unit `t` of this CTA; the caller's warp (or lone lane) releases its entry.
-  auto take_unit = [&](int t, PtUnit &u) -> bool {
+  using Unit = PtUnit<kSplit>;
+  auto take_unit = [&](int t, Unit &u) -> bool {
     const int e = t % kPtUnits;
     if (!pt_wait(BAR(kPtUnitFull + e), (t / kPtUnits) & 1, abort_s)) return false;
     u.shape(unit_s[e], p.TQ);
@@ -571,14 +587,14 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
 
   if (warp < kPtWarpEpi) {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
     const int a = warp >> 2;
     const int m = tid & 127;                           // row of the tile, TMEM lane
     const int t_row = (m * p.inv_g) >> 16;
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     uint32_t steps = 0, done = 0;                      // key tiles and units of tile a
     for (int t = 0;; ++t) {
-      PtUnit u;
+      Unit u;
       const bool ok = take_unit(t, u);
       if (__any_sync(0xFFFFFFFFu, !ok)) {
         gave_up = true;
@@ -586,33 +602,34 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       }
       if (lane == 0) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
       if (u.len == 0) break;
-      const int n = a == 0 ? u.n0 : u.n1;
-      if (n == 0) continue;
-      const int tok = u.tok0 + a * p.TQ + t_row;
+      const int top = u.top(a), bottom = u.bottom(a);
+      if (top < 0) continue;
+      const int tok = u.tok0 + u.row_tile(a) * p.TQ + t_row;
       // the key tiles that all of the warp's rows see whole (the first row sees least)
       const int whole = (__shfl_sync(0xFFFFFFFFu, tok, 0) + 1) / kPtKeys;
       PtRow row;
-      for (int j = n - 1; j >= 0; --j, ++steps) {
+      for (int j = top; j >= bottom; j -= kSplit ? 2 : 1, ++steps) {
         if (__any_sync(0xFFFFFFFFu, !pt_wait(BAR(kPtSFull + a), steps & 1, abort_s))) {
           gave_up = true;
           break;
         }
         tc_fence_after();
         if (j < whole)
-          pt_softmax(tl + pt_s(a), tl + pt_o(a), p.scale2, j == n - 1, BAR(kPtPReady + 2 * a), lane,
+          pt_softmax(tl + pt_s(a), tl + pt_o(a), p.scale2, j == top, BAR(kPtPReady + 2 * a), lane,
                      row);
         else
-          pt_softmax_edge(tl + pt_s(a), tl + pt_o(a), tok - j * kPtKeys, p.scale2, j == n - 1,
+          pt_softmax_edge(tl + pt_s(a), tl + pt_o(a), tok - j * kPtKeys, p.scale2, j == top,
                           BAR(kPtPReady + 2 * a), lane, row);
       }
       if (gave_up) break;
-      // the denominators, once the epilogue has read the last unit's
+      // the row's statistics, once the epilogue has read the last unit's
       if (done > 0 &&
           __any_sync(0xFFFFFFFFu, !pt_wait(BAR(kPtOEmpty + a), (done - 1) & 1, abort_s))) {
         gave_up = true;
         break;
       }
       sum_s[128 * a + m] = row.sum;
+      if (kSplit) ref_s[128 * a + m] = row.m;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(kPtSumFull + a));
       ++done;
@@ -626,7 +643,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     uint32_t done[2] = {0, 0};
     for (int t = 0;; ++t) {
-      PtUnit u;
+      Unit u;
       const bool ok = take_unit(t, u);
       if (__any_sync(0xFFFFFFFFu, !ok)) {
         gave_up = true;
@@ -634,18 +651,35 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       }
       if (u.len == 0) break;
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        if ((a == 0 ? u.n0 : u.n1) == 0) continue;
-        const bool got = pt_wait(BAR(kPtSumFull + a), done[a] & 1, abort_s) &&
-                         pt_wait(BAR(kPtOFull + a), done[a] & 1, abort_s);
+      for (int a = 0; a < (kSplit ? 1 : 2); ++a) {
+        if (u.top(a) < 0) continue;
+        const bool both = kSplit && u.top(1) >= 0;
+        bool got = pt_wait(BAR(kPtSumFull + a), done[a] & 1, abort_s) &&
+                   pt_wait(BAR(kPtOFull + a), done[a] & 1, abort_s);
+        if (both)
+          got = got && pt_wait(BAR(kPtSumFull + 1), done[1] & 1, abort_s) &&
+                pt_wait(BAR(kPtOFull + 1), done[1] & 1, abort_s);
         if (__any_sync(0xFFFFFFFFu, !got)) {
           gave_up = true;
           break;
         }
         tc_fence_after();
         ++done[a];
-        const float inv = 1.0f / sum_s[128 * a + m];
-        const int tok = u.tok0 + a * p.TQ + t_row;
+        float inv = sum_s[128 * a + m], inv_b = 0.0f;
+        if (both) {
+          // the two chains' sums and outputs under the larger reference (of a row
+          // that saw no key of a chain, nothing)
+          ++done[1];
+          const float m0 = ref_s[m], m1 = ref_s[128 + m], top = fmaxf(m0, m1);
+          const float f0 = m0 == -INFINITY ? 0.0f : pt_ex2((m0 - top) * p.scale2);
+          const float f1 = m1 == -INFINITY ? 0.0f : pt_ex2((m1 - top) * p.scale2);
+          const float all = 1.0f / (f0 * inv + f1 * sum_s[128 + m]);
+          inv = f0 * all;
+          inv_b = f1 * all;
+        } else {
+          inv = 1.0f / inv;
+        }
+        const int tok = u.tok0 + u.row_tile(a) * p.TQ + t_row;
         const bool dirty = dirty_s[t % kPtUnits] != 0;
         const bool mine = t_row < p.TQ && tok < u.len;
         uint16_t *dst = p.out + (static_cast<int64_t>(u.start) + tok) * p.out_stride +
@@ -658,6 +692,12 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
             unpack_f32x2(mul_f32x2(pack_f32x2(o[i], o[i + 1]), inv2), o[i], o[i + 1]);
+          if (both) {
+            float o1[32];
+            tmem_ld32(tl + pt_o(1) + c, o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], inv_b, o[i]);
+          }
           if (dirty) {
             // the infinities and NaN this row sees in the edge tiles
             const int last = min(tok, u.len - 1);
@@ -678,18 +718,20 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(kPtOEmpty + a));
+        if (lane == 0) {
+          mbar_arrive(BAR(kPtOEmpty + a));
+          if (both) mbar_arrive(BAR(kPtOEmpty + 1));
+        }
       }
       if (gave_up) break;
       // (held to here: the entry's dirty flag is the unit's until it is taken again)
       if (lane == 0) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
     if (warp == kPtWarpLoad) {
       // ----------------------------------------------- work numbers and TMA
-      uint32_t idx = 0;                                // ring entries issued
-      uint32_t loads[2] = {0, 0};                      // query tiles
+      uint32_t loads0 = 0, loads1 = 0;                 // query tiles of each chain
       // Units: the own block's first, then those of blocks that have not
       // started.  Answers are asked for before a unit's last two tiles are loaded
       // (any earlier, and the CTAs that ask first hold work back from those that
@@ -740,25 +782,47 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         }
         return true;
       };
-      // key tile j and value tile j of the unit
-      auto load_kv = [&](const PtUnit &u, int j) -> bool {
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++idx) {
-          const int b = idx % kPtStages;
-          if (idx >= kPtStages && !pt_wait(BAR(kPtKvEmpty + b), (idx / kPtStages - 1) & 1, abort_s))
-            return false;
-          mbar_arrive_expect_tx(BAR(kPtKvFull + b), kPtTileBytes);
-          pt_tma_4d(smem_addr(smem + kPtOffKv + b * kPtTileBytes), kv == 0 ? &tm_k : &tm_v, 0,
-                    u.start + j * kPtKeys, 0, u.h, BAR(kPtKvFull + b));
-        }
+      // key (kv = 0) or value tile j of the unit into ring stage b, round by round
+      auto load_tile = [&](const Unit &u, int j, int kv, uint32_t b, uint32_t round) -> bool {
+        if (round > 0 && !pt_wait(BAR(kPtKvEmpty + b), (round - 1) & 1, abort_s)) return false;
+        mbar_arrive_expect_tx(BAR(kPtKvFull + b), kPtTileBytes);
+        pt_tma_4d(smem_addr(smem + kPtOffKv + b * kPtTileBytes), kv == 0 ? &tm_k : &tm_v, 0,
+                  u.start + j * kPtKeys, 0, u.h, BAR(kPtKvFull + b));
         return true;
       };
-      auto load_q = [&](const PtUnit &u) -> bool {
+      // the tiles of the unit's step i
+      // ring entries issued (split: each chain's tiles; no arrays: they would be in
+      // local memory, a cold miss at the kernel's start)
+      uint32_t idx0 = 0, idx1 = 0;
+      auto load_step = [&](const Unit &u, int i) -> bool {
+        bool ok = true;
+        if constexpr (kSplit) {
+          // both chains' keys first: their stages are free before the values'
 #pragma unroll 1
-        for (int a = 0; a < 2; ++a) {
-          if ((a == 0 ? u.n0 : u.n1) == 0) continue;
-          if (loads[a] > 0 && !pt_wait(BAR(kPtQEmpty + a), (loads[a] - 1) & 1, abort_s)) return false;
-          ++loads[a];
+          for (int x = 0; x < 4 && ok; ++x) {
+            const int a = x & 1, kv = x >> 1, j = u.top(a) - 2 * i;
+            if (j >= 0) ok = load_tile(u, j, kv, 2 * a + kv, a == 0 ? idx0 : idx1);
+          }
+          idx0 += u.top(0) >= 2 * i;
+          idx1 += u.top(1) >= 2 * i;
+        } else {
+#pragma unroll 1
+          for (int kv = 0; kv < 2 && ok; ++kv, ++idx0)
+            ok = load_tile(u, u.tiles() - 1 - i, kv, idx0 % kPtStages, idx0 / kPtStages);
+        }
+        return ok;
+      };
+      auto load_q = [&](const Unit &u) -> bool {
+        // the chains' last products with the tiles are done
+        if (loads0 > 0 && !pt_wait(BAR(kPtQEmpty), (loads0 - 1) & 1, abort_s)) return false;
+        if ((kSplit || u.top(1) >= 0) && loads1 > 0 &&
+            !pt_wait(BAR(kPtQEmpty + 1), (loads1 - 1) & 1, abort_s))
+          return false;
+        ++loads0;
+        loads1 += u.top(1) >= 0;
+#pragma unroll 1
+        for (int a = 0; a < (kSplit ? 1 : 2); ++a) {
+          if (u.top(a) < 0) continue;
           const uint32_t dst = smem_addr(smem + kPtOffQ + a * kPtTileBytes);
           mbar_arrive_expect_tx(BAR(kPtQFull + a), 2u * 128u * p.TQ * p.G);
           for (int half = 0; half < 2; ++half)
@@ -774,34 +838,38 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
           ok = announce(t, e);
           break;
         }
-        PtUnit u;
+        Unit u;
         u.shape(e, p.TQ);
-        const int nt = u.tiles();
-        for (int j = nt - 1; j >= 0 && ok; --j) {
+        const int steps = u.steps();
+        for (int i = 0; i < steps && ok; ++i) {
           // the first keys and values ahead of the queries, whose tiles are free
           // only once the last unit's products with them are done
-          if (lane == 0) ok = load_kv(u, j);
-          if (j == nt - 1) {
+          if (lane == 0) ok = load_step(u, i);
+          if (i == 0) {
             ok = __all_sync(0xFFFFFFFFu, ok) && announce(t, e);
             if (ok && lane == 0) ok = load_q(u);
           }
           ok = __all_sync(0xFFFFFFFFu, ok);
-          if (ok && j == (nt > 2 ? 2 : 0)) ask(nt > 2 ? 1 : 2);
+          if (ok && i == max(steps - 3, 0)) ask(steps > 2 ? 1 : 2);
         }
         ok = ok && next_unit(e);
       }
       gave_up = !ok;
       // copies in flight land before the CTA leaves
       if (lane == 0) {
-        for (uint32_t v = idx > kPtStages ? idx - kPtStages : 0; v < idx; ++v)
-          mbar_wait_sleep_bounded(BAR(kPtKvFull + v % kPtStages), (v / kPtStages) & 1);
-        for (int a = 0; a < 2; ++a)
-          if (loads[a] > 0) mbar_wait_sleep_bounded(BAR(kPtQFull + a), (loads[a] - 1) & 1);
+#pragma unroll
+        for (uint32_t b = 0; b < kPtStages; ++b) {
+          // rounds of this stage so far
+          const uint32_t n = kSplit ? (b < 2 ? idx0 : idx1) : (idx0 + kPtStages - 1 - b) / kPtStages;
+          if (n > 0) mbar_wait_sleep_bounded(BAR(kPtKvFull + b), (n - 1) & 1);
+        }
+        if (loads0 > 0) mbar_wait_sleep_bounded(BAR(kPtQFull), (loads0 - 1) & 1);
+        if (!kSplit && loads1 > 0) mbar_wait_sleep_bounded(BAR(kPtQFull + 1), (loads1 - 1) & 1);
         for (; asked > heard; ++heard)
           mbar_wait_sleep_bounded(BAR(kPtSteal + (heard & 1)), (heard >> 1) & 1);
       }
     } else if (warp < kPtWarpClear) {
-      // ----------------------------------------------------- MMAs of a tile
+      // ---------------------------------------------------- MMAs of a chain
       // Each turn: PV of one key tile and QK^T of the next (a unit's first turn
       // has no PV, its last no QK^T), tile 0's and tile 1's bursts one after the other (free to interleave, the tiles fell
       // into step: both in the softmax, then both at the tensor core).
@@ -809,43 +877,65 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       // converged and elects a lane for each group of MMAs: addresses stay
       // uniform, 8 instructions an MMA instead of 11 for a lone lane.
       const int a = warp - kPtWarpMma;
-      const uint32_t q_lo = (smem_addr(smem + kPtOffQ + a * kPtTileBytes) >> 4) | kPtKMajor;
+      const uint32_t q_lo = (smem_addr(smem + kPtOffQ + (kSplit ? 0 : a) * kPtTileBytes) >> 4) | kPtKMajor;
       const uint32_t kv0 = smem_addr(smem + kPtOffKv) >> 4;
       const uint32_t s_col = tmem + pt_s(a), o_col = tmem + pt_o(a);
-      uint32_t base = 0;                               // ring entries of earlier units
+      uint32_t base = 0;                               // ring entries (split: tiles) of earlier units
       uint32_t par_q = 0, par_p = 0, par_o = 1;        // barrier parities
       uint32_t par_clear = 0;                          // bit per ring stage
-      uint32_t par_turn = a ^ 1;                       // tile 0 goes first
+      uint32_t par_turn = a ^ 1;                       // chain 0 goes first
       bool ok = true;
       for (int t = 0; ok; ++t) {
-        PtUnit u;
+        Unit u;
         ok = __all_sync(0xFFFFFFFFu, take_unit(t, u));
         if (!ok) break;
         if (lane == 0) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
         if (u.len == 0) break;
-        const int nt = u.tiles(), n = a == 0 ? u.n0 : u.n1;
-        const bool turns = u.n1 > 0;                   // (a lone tile 0 need not pass them)
-        // turn j: PV of key tile j and QK^T of key tile j - 1
-        for (int j = nt; j >= 0; --j) {
-          const uint32_t ek = base + 2 * (nt - j), bk = ek % kPtStages;      // keys of j - 1
-          const uint32_t ev = ek - 1, bv = ev % kPtStages;                   // values of j
-          const bool pv = j < n, qk = j > 0 && j - 1 < n;
+        const int steps = u.steps(), top = u.top(a);
+        const bool turns = u.top(1) >= 0;              // (a lone chain 0 need not pass them)
+        // turn j: PV of one of the chain's key tiles (jv, none in the first turn) and
+        // QK^T of the next (none in the last)
+        for (int j = steps; j >= 0; --j) {
+          int jv = j;
+          bool pv = j <= top, qk = j > 0 && j - 1 <= top;
+          bool pv_first = j == top, pv_last = j == 0, qk_first = j - 1 == top, qk_last = j == 1;
+          // (not split: tiles that are only the other chain's are waited for and
+          // released too)
+          bool use_v = j < steps, use_k = j > 0;
+          uint32_t ek = base + 2 * (steps - j);        // its entry in the ring; the values' is before
+          uint32_t bk = ek % kPtStages, bv = (ek - 1) % kPtStages;
+          uint32_t pk = ek / kPtStages, pvv = (ek - 1) / kPtStages;
+          if (kSplit) {
+            jv = top - 2 * (steps - j) + 2;
+            const int jk = jv - 2, bottom = u.bottom(a);
+            pv = use_v = j < steps && jv >= 0;
+            qk = use_k = j > 0 && jk >= 0;
+            pv_first = jv == top;
+            pv_last = jv == bottom;
+            qk_first = jk == top;
+            qk_last = jk == bottom;
+            bk = 2 * a;
+            bv = bk + 1;
+            pk = base + (steps - j);
+            pvv = pk - 1;
+          }
           const uint32_t v_lo = (kv0 + bv * (kPtTileBytes >> 4)) | kPtMnMajor;
           const uint32_t k_lo = (kv0 + bk * (kPtTileBytes >> 4)) | kPtKMajor;
-          if (j < nt) {
-            ok = pt_wait_all(BAR(kPtKvFull + bv), (ev / kPtStages) & 1, abort_s);
-            if (u.edge(j)) {
+          if (use_v) {
+            ok = pt_wait_all(BAR(kPtKvFull + bv), pvv & 1, abort_s);
+            if (u.edge(jv)) {
               if (ok && pv) ok = pt_wait_all(BAR(kPtVClear + bv), (par_clear >> bv) & 1, abort_s);
               par_clear ^= 1u << bv;
             }
           }
-          if (ok && j > 0) ok = pt_wait_all(BAR(kPtKvFull + bk), (ek / kPtStages) & 1, abort_s);
-          if (ok && qk && j == n) {
-            ok = pt_wait_all(BAR(kPtQFull + a), par_q, abort_s);
+          if (ok && use_k) ok = pt_wait_all(BAR(kPtKvFull + bk), pk & 1, abort_s);
+          if (ok && qk && qk_first) {
+            // (split: the one tile of every unit)
+            ok = pt_wait_all(BAR(kPtQFull + (kSplit ? 0 : a)), kSplit ? t & 1 : par_q, abort_s);
             par_q ^= 1u;
           }
           if (ok && pv) {
-            if (j == n - 1) {
+            if (pv_first) {
               ok = pt_wait_all(BAR(kPtOEmpty + a), par_o, abort_s);
               par_o ^= 1u;
             }
@@ -863,7 +953,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 pt_mma_pv(o_col, s_col + 8 * kk, v_lo + (2048 >> 4) * kk,
-                          (j == n - 1 && kk == 0) ? 0u : 1u);
+                          (pv_first && kk == 0) ? 0u : 1u);
             }
             ok = pt_wait_all(BAR(kPtPReady + 2 * a + 1), par_p, abort_s);
             if (!ok) break;
@@ -886,14 +976,14 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
           __syncwarp();
           if (pt_elect()) {
             if (turns) mbar_arrive(BAR(kPtTurn + (a ^ 1)));
-            if (pv && j == 0) tc_commit(BAR(kPtOFull + a));
-            if (qk && j == 1) tc_commit(BAR(kPtQEmpty + a));
-            if (j < nt) tc_commit(BAR(kPtKvEmpty + bv));
-            if (j > 0) tc_commit(BAR(kPtKvEmpty + bk));
+            if (pv && pv_last) tc_commit(BAR(kPtOFull + a));
+            if (qk && qk_last) tc_commit(BAR(kPtQEmpty + a));
+            if (use_v) tc_commit(BAR(kPtKvEmpty + bv));
+            if (use_k) tc_commit(BAR(kPtKvEmpty + bk));
           }
           __syncwarp();
         }
-        base += 2 * nt;
+        base += kSplit ? (top >= 0 ? top / 2 + 1 : 0) : 2 * steps;
       }
       gave_up = !ok;
       // every MMA issued has completed before the tensor memory is freed
@@ -902,9 +992,9 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       mbar_wait_sleep_bounded(BAR(kPtDrain + a), 0);
     } else {
       // ------------------------------------------- edge value tiles cleared
-      uint32_t step = 0;
+      uint32_t tiles0 = 0, tiles1 = 0;                 // of each chain (not split: of both)
       for (int t = 0; !gave_up; ++t) {
-        PtUnit u;
+        Unit u;
         const bool ok = take_unit(t, u);
         if (__any_sync(0xFFFFFFFFu, !ok)) {
           gave_up = true;
@@ -918,9 +1008,19 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         if (u.len == 0) break;
         // (every value tile is waited for and released, or this warp could be
         // phases ahead of the ring or behind it)
-        for (int j = u.tiles() - 1; j >= 0; --j, ++step) {
-          const uint32_t e = 2 * step + 1, b = e % kPtStages;
-          if (__any_sync(0xFFFFFFFFu, !pt_wait(BAR(kPtKvFull + b), (e / kPtStages) & 1, abort_s))) {
+        for (int j = u.tiles() - 1; j >= 0; --j) {
+          const uint32_t e = 2 * tiles0 + 1;
+          uint32_t b = e % kPtStages, round = e / kPtStages;
+          if (kSplit) {
+            const int a = (u.tiles() - 1 - j) & 1;
+            b = 2 * a + 1;
+            round = a == 0 ? tiles0 : tiles1;
+            tiles0 += a ^ 1;
+            tiles1 += a;
+          } else {
+            ++tiles0;
+          }
+          if (__any_sync(0xFFFFFFFFu, !pt_wait(BAR(kPtKvFull + b), round & 1, abort_s))) {
             gave_up = true;
             break;
           }
@@ -991,9 +1091,9 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   }
 }
 
-// Work numbers of a call: at least its units.
-int64_t prompt_units(const PromptArgs &a) {
-  const int64_t TU = 2 * (128 / (a.num_q_heads / a.num_kv_heads));
+// Work numbers of a call with units of `tiles` row tiles: at least those.
+int64_t prompt_units(const PromptArgs &a, int tiles) {
+  const int64_t TU = tiles * (128 / (a.num_q_heads / a.num_kv_heads));
   int64_t n = a.num_tokens / TU + a.num_seqs;
   if (a.num_seqs <= kPtSeqs) {
     const int64_t most = (static_cast<int64_t>(a.max_seqlen) + TU - 1) / TU;
@@ -1005,7 +1105,7 @@ int64_t prompt_units(const PromptArgs &a) {
 }  // namespace
 
 bool prompt_attention_supported(const PromptArgs &a) {
-  return a.num_seqs <= 0x7FFFFF00 && prompt_units(a) <= 0x7FFFFFFF;
+  return a.num_seqs <= 0x7FFFFF00 && prompt_units(a, 1) <= 0x7FFFFFFF;
 }
 
 cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
@@ -1027,7 +1127,13 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
   while ((int64_t(1) << l) < p.H) ++l;
   p.h_shift = 32 + l;
   p.h_magic = ((uint64_t(1) << p.h_shift) + p.H - 1) / p.H;
-  p.units = prompt_units(a);
+  // Where units of one row tile all start at once: its keys split between the two
+  // chains -- twice the units of half the steps, which only pays while SMs would
+  // stand idle (8 KV heads of 4 query heads: 512 tokens, 128 units, 10.0 us against
+  // 12.2; 1,024 tokens, 256 units, 22.5 against 18.5).
+  const bool split = prompt_units(a, 1) <= a.sms;
+  p.TU = (split ? 1 : 2) * p.TQ;
+  p.units = prompt_units(a, split ? 1 : 2);
   p.scale2 = a.sm_scale * 1.4426950408889634f;
   p.out_by_32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0;
   p.err_flags = a.err_flags;
@@ -1036,19 +1142,19 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
       !encode_row_tensor_map(&mk, a.k, a.num_tokens, a.num_kv_heads, a.k_stride, kPtKeys) ||
       !encode_row_tensor_map(&mv, a.v, a.num_tokens, a.num_kv_heads, a.v_stride, kPtKeys))
     return cudaErrorInvalidValue;
-  static std::atomic<uint64_t> configured{0};
+  const auto kernel = split ? prompt_attention_kernel<true> : prompt_attention_kernel<false>;
+  static std::atomic<uint64_t> configured[2];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = (dev >= 0 && dev < 64) ? (uint64_t(1) << dev) : 0;
-  if (bit == 0 || !(configured.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(prompt_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kPtSmem);
+  if (bit == 0 || !(configured[split].load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPtSmem);
     if (e != cudaSuccess) return e;
-    configured.fetch_or(bit, std::memory_order_acq_rel);
+    configured[split].fetch_or(bit, std::memory_order_acq_rel);
   }
-  return launch_overlapped(prompt_attention_kernel, dim3(static_cast<unsigned>(p.units)),
-                           dim3(kPtThreads), kPtSmem, stream, p, mq, mk, mv);
+  return launch_overlapped(kernel, dim3(static_cast<unsigned>(p.units)), dim3(kPtThreads), kPtSmem,
+                           stream, p, mq, mk, mv);
 }
 
 }  // namespace kvq
