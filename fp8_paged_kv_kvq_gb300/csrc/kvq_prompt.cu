@@ -11,38 +11,49 @@
 //    token t, head h G + g, with floor(128 / G) tokens per tile, so short
 //    prompts fill the tensor core's rows and a key tile is read once for all G
 //    heads.  The unit's key tiles (128 keys) go from its diagonal down to 0.
-//  * Units are numbered through the sequences (TU tokens per unit); every CTA
-//    sums their counts in shared memory, so there is no plan launch and no
-//    workspace.  (Cutting the packed tokens instead, with rows of several
-//    sequences in one tile, took 9 us instead of 15 for 64 prompts of 16 tokens,
-//    but 348 us instead of 322 for 8 of 355 to 4,096 and 64 heads: diagonals that
-//    no longer end with a key tile.)  Of more than kPtSeqs sequences, s uses the numbers
-//    floor(cu[s] / TU) + s up to the next one's, at least ceil(len / TU) of them,
-//    and a number finds its sequence by a search over cu_seqlens itself, with no
-//    bound on their count; the numbers left over cost a look each (64 prompts of
-//    one unit would have as many of those as units).
+//    Two chains (QK^T -> softmax -> PV) work on it, one per row tile; where a
+//    call has few units, on one row tile, each over every other key tile, their
+//    sums and outputs joined at the end (launch_prompt_attention has the rule).
+//  * Units are numbered through the sequences; every CTA sums their counts in
+//    shared memory, so there is no plan launch and no workspace.  (Cutting the
+//    packed tokens instead, with rows of several sequences in one tile, took 9 us
+//    instead of 15 for 64 prompts of 16 tokens, but 348 us instead of 322 for 8
+//    of 355 to 4,096 and 64 heads: diagonals that no longer end with a key
+//    tile.)  Of more than kPtSeqs sequences, s uses the numbers
+//    floor(cu[s] / TU) + s up to the next one's (TU tokens a unit), at least
+//    ceil(len / TU) of them, and a number finds its sequence by a search over
+//    cu_seqlens itself, with no bound on their count; the numbers left over cost
+//    a look each.
 //  * CTAs of 512 threads, one per SM, that go on with the units of blocks that
 //    have not started (cluster launch control) until there are none, longest
-//    rows of a sequence first.  Warps 0-3 and 4-7: softmax of
-//    tile 0 and tile 1 (a thread owns a TMEM lane, a row); 8-11: the epilogue,
-//    which overlaps the next unit; 12: work numbers and TMA; 13 and 14: the MMAs
-//    of tile 0 and tile 1; 15: clears what the edge value tiles must not
-//    contribute.
+//    rows of a sequence first.  Warps 0-3 and 4-7: softmax of chain 0 and 1 (a
+//    thread owns a TMEM lane, a row); 8-11: the epilogue, which overlaps the next
+//    unit; 12: work numbers and TMA; 13 and 14: the MMAs of chain 0 and 1; 15:
+//    clears what the edge value tiles must not contribute.
 //  * S = Q K^T (128 x 128 x 128, both operands from shared memory) into TMEM;
 //    the softmax reads S, writes P as bf16 over S's own columns, and O += P V
-//    takes P from TMEM.  The two tiles alternate on the tensor core: PV and the
-//    next QK^T of one run while the other is in its softmax.  Each tile has an
-//    issuing warp of its own, since the pipe takes an MMA about when it starts:
-//    whatever one warp spends on barriers, the other's MMAs fill (one warp for
-//    both left the tensor core idle for 60% of the time).
+//    takes P from TMEM.  The chains alternate on the tensor core: PV and the next
+//    QK^T of one run while the other is in its softmax.  Each has an issuing warp
+//    of its own, since the pipe takes an MMA about when it starts: whatever one
+//    warp spends on barriers, the other's MMAs fill (one warp for both left the
+//    tensor core idle for 60% of the time).
 //  * A row's reference m moves only when a score passes it by 2^8 in the
 //    exponent (P then stays below 2^8, and sums and outputs are fp32); the
 //    thread that moves it rescales its O row, with no PV in flight on it since
-//    the QK^T that it waited for was issued after it.
+//    the QK^T that it waited for was issued after it.  P is rounded to bf16 for
+//    the product (2^-8 of each term at most, the tensor core's operand type) and
+//    not for the sum.
 //  * 0 times an infinity is not 0, so zero probabilities do not hide unseen
 //    values.  Of the value tiles that some row of the unit does not see whole
 //    warp 15 clears the rows that none sees and every infinity and NaN; the
 //    epilogue adds those a row does see back (rare, one flag per unit).
+//  * What bounds it: the tensor core, and from 4,096 tokens on the card's 1.4 kW
+//    (1.83-1.86 GHz in a loop): 16,381 tokens of 32 heads 1.33 ms, 1,650 TFLOP/s,
+//    86% of what a bf16 library product reaches in a burst; 4 x 8,192 tokens
+//    1.37 ms.  A step of two row tiles over a key tile takes about 2,700 cycles, of
+//    which its MMAs need 2,048; the rest is the chain of one tile (QK^T, 128
+//    scores a thread, PV) that the other's MMAs do not cover.  Short prompts are
+//    bound by latency: 2 us to the first MMA, 1.5 us a step, 1 us for the rows.
 //  * Every wait is bounded; a role that gives up raises a shared abort flag,
 //    copies and MMAs in flight complete, the CTA frees its tensor memory
 //    (KVQ_ERRF_WAIT_TIMEOUT).
@@ -72,7 +83,7 @@ constexpr int kPtTileBytes = 128 * kHeadDim * 2;      // [2 halves of 64 dims][1
 constexpr int kPtHalf = kPtTileBytes / 2;
 constexpr int kPtOffQ = 0;
 constexpr int kPtOffKv = 2 * kPtTileBytes;
-constexpr int kPtOffSum = kPtOffKv + kPtStages * kPtTileBytes;   // [tile][128] denominators
+constexpr int kPtOffSum = kPtOffKv + kPtStages * kPtTileBytes;   // [chain][128] denominators
 constexpr int kPtOffRef = kPtOffSum + 2 * 128 * 4;               // [chain][128] references
 constexpr int kPtOffUnit = kPtOffRef + 2 * 128 * 4;
 constexpr int kPtOffDirty = kPtOffUnit + kPtUnits * 16;
@@ -85,18 +96,18 @@ constexpr int kPtOffBar = (kPtOffCu + (kPtSeqs + 1) * 4 + 7) / 8 * 8;
 enum : int {
   kPtKvFull = 0,
   kPtKvEmpty = kPtKvFull + kPtStages,
-  kPtQFull = kPtKvEmpty + kPtStages,                  // per tile, as the next six
+  kPtQFull = kPtKvEmpty + kPtStages,                  // per chain, as the next six
   kPtQEmpty = kPtQFull + 2,
   kPtSFull = kPtQEmpty + 2,
   kPtPReady = kPtSFull + 2,
-  kPtOFull = kPtPReady + 4,                           // (P: per tile and half of the keys)
+  kPtOFull = kPtPReady + 4,                           // (P: per chain and half of the keys)
   kPtOEmpty = kPtOFull + 2,
   kPtSumFull = kPtOEmpty + 2,
   kPtVClear = kPtSumFull + 2,                         // per ring stage
   kPtUnitFull = kPtVClear + kPtStages,
   kPtUnitEmpty = kPtUnitFull + kPtUnits,
-  kPtDrain = kPtUnitEmpty + kPtUnits,                 // per tile
-  kPtTurn = kPtDrain + 2,                             // per tile
+  kPtDrain = kPtUnitEmpty + kPtUnits,                 // per chain
+  kPtTurn = kPtDrain + 2,                             // per chain
   kPtSteal = kPtTurn + 2,                             // per answer
   kPtBars = kPtSteal + 2
 };
@@ -104,7 +115,7 @@ constexpr int kPtSmem = kPtOffBar + 8 * kPtBars + 1024;
 static_assert(kPtOffBar % 8 == 0 && kPtOffUnit % 16 == 0 && kPtOffSteal % 16 == 0, "alignment");
 static_assert(kPtSmem <= 227 * 1024, "shared memory budget");
 
-// TMEM: S of tile a at 128 a (its P over the first 64 columns), O at 256 + 128 a
+// TMEM: S of chain a at 128 a (its P over the first 64 columns), O at 256 + 128 a
 constexpr uint32_t kPtTmemCols = 512;
 __device__ __forceinline__ uint32_t pt_s(int a) { return 128u * a; }
 __device__ __forceinline__ uint32_t pt_o(int a) { return 256u + 128u * a; }
@@ -112,7 +123,6 @@ __device__ __forceinline__ uint32_t pt_o(int a) { return 256u + 128u * a; }
 constexpr uint32_t kPtBf16 = (1u << 7) | (1u << 10);   // A and B bf16
 constexpr uint32_t kPtIdescQK = mma_idesc(128, kPtKeys, false, false) | kPtBf16;
 constexpr uint32_t kPtIdescPV = mma_idesc(128, kHeadDim, false, true) | kPtBf16;
-
 
 // The upper word of every operand's shared-memory descriptor (smem_desc:
 // stride offset 1024, version 1, 128-byte swizzle) and the two leading offsets.
@@ -871,8 +881,9 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
     } else if (warp < kPtWarpClear) {
       // ---------------------------------------------------- MMAs of a chain
       // Each turn: PV of one key tile and QK^T of the next (a unit's first turn
-      // has no PV, its last no QK^T), tile 0's and tile 1's bursts one after the other (free to interleave, the tiles fell
-      // into step: both in the softmax, then both at the tensor core).
+      // has no PV, its last no QK^T), chain 0's and chain 1's bursts one after the
+      // other (free to interleave, the chains fell into step: both in the softmax,
+      // then both at the tensor core; 4 x 8,192 tokens 1.98 ms instead of 1.66).
       // Everything but P is waited for before the turn.  The warp stays
       // converged and elects a lane for each group of MMAs: addresses stay
       // uniform, 8 instructions an MMA instead of 11 for a lone lane.
@@ -1105,6 +1116,9 @@ int64_t prompt_units(const PromptArgs &a, int tiles) {
 }  // namespace
 
 bool prompt_attention_supported(const PromptArgs &a) {
+  // (a tensor map's strides are below 2^40 bytes)
+  const int64_t most = int64_t(1) << 39;
+  if (a.q_stride >= most || a.k_stride >= most || a.v_stride >= most) return false;
   return a.num_seqs <= 0x7FFFFF00 && prompt_units(a, 1) <= 0x7FFFFFFF;
 }
 

@@ -82,6 +82,7 @@ def _prompt(lib, **changes):
     (dict(scale=0.0), INVALID), (dict(scale=-0.1), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(d=64), UNSUPPORTED),
     (dict(hq=8 * 129, qs=8 * 129 * 128, os=8 * 129 * 128), UNSUPPORTED),
+    (dict(qs=1 << 40), UNSUPPORTED), (dict(ks=1 << 40), UNSUPPORTED), (dict(vs=1 << 40), UNSUPPORTED),
     (dict(T=1 << 31), UNSUPPORTED), (dict(N=0x7FFFFFFE), UNSUPPORTED),
     (dict(qs=4088), INVALID), (dict(ks=1016), INVALID), (dict(vs=1016), INVALID),
     (dict(os=4088), INVALID), (dict(q=0), INVALID), (dict(k=0), INVALID), (dict(v=0), INVALID),

@@ -82,6 +82,14 @@ def test_head_groups(hq, H):
     _run([200, 77, 300], hq, H, seed=hq)
 
 
+@pytest.mark.parametrize("lens,hq,H", [([640], 4, 1), ([1290], 4, 1), ([129, 500], 6, 2),
+                                       ([128, 256, 384], 4, 2), ([2500], 2, 1), ([257], 128, 1)])
+def test_split_keys(lens, hq, H):
+    """So few units that two chains share a row tile, each over every other key tile (one, two, an
+    odd and an even number of them)."""
+    _run(lens, hq, H, seed=sum(lens))
+
+
 @pytest.mark.parametrize("hq,H", [(8, 2), (2, 2), (14, 2)])
 def test_mixed_lengths(hq, H):
     """Tails, heads and whole short prompts side by side, among empty ones."""
@@ -105,12 +113,23 @@ def test_many_units_per_cta(lens, hq, H):
     _run(lens, hq, H, seed=5)
 
 
-def test_many_sequences():
-    """More sequences than one warp's search step covers, many empty ones among them."""
-    g = workloads.generator(6, 6)
-    lens = torch.randint(0, 12, (1500,), generator=g).tolist()
-    lens[700] = 300
-    _run(lens, 4, 2, seed=6)
+@pytest.mark.parametrize("n", [32, 33, 600, 1500, 2048, 2049, 3000])
+def test_many_sequences(n):
+    """Many sequences, empty ones among them: counted by a warp, by all threads in one or several
+    rounds, and so many that a unit is found over cu_seqlens itself."""
+    g = workloads.generator(6, n)
+    lens = torch.randint(0, 12, (n,), generator=g).tolist()
+    lens[n // 2] = 300
+    _run(lens, 4, 2, seed=6, tail=3, first=2)
+    # one of them out of bounds: flagged
+    T = int(sum(lens))
+    q, k, v = _inputs(T, 4, 2, seed=6)
+    cu = _cu(lens)
+    cu[n // 2 + 1] = T + 1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kvq.prompt_attention(q, k, v, cu, 300, SCALE, err_flags=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == kvq.ERRF_SEQUENCE_RANGE
 
 
 def test_rows_outside_the_sequences_stay():
@@ -118,16 +137,18 @@ def test_rows_outside_the_sequences_stay():
     _run([0, 0], 16, 4, seed=7, tail=9, most=0)
 
 
+@pytest.mark.parametrize("hq,H", [(8, 2), (64, 16)])
 @pytest.mark.parametrize("scale,spread", [(SCALE, 12.0), (1.0, 1.0), (1e-6, 1.0)])
-def test_score_ranges(scale, spread):
+def test_score_ranges(scale, spread, hq, H):
     """Peaked rows (one probability near 1), and rows of nearly equal scores."""
-    _run([400, 150], 8, 2, seed=9, scale=scale, spread=spread)
+    _run([400, 150], hq, H, seed=9, scale=scale, spread=spread)
 
 
-def test_climbing_and_falling_scores():
+@pytest.mark.parametrize("hq,H", [(8, 2), (64, 32)])
+def test_climbing_and_falling_scores(hq, H):
     """Scores that rise (fall) by many powers of two along the keys, so that running maxima move
     again and again (or never)."""
-    hq, H, L = 8, 2, 700
+    L = 700
     q, k, v = _inputs(L, hq, H, seed=11)
     q.copy_(torch.ones_like(q))
     step = (torch.arange(L, device="cuda") / 3.0)[:, None, None]
@@ -140,7 +161,7 @@ def test_climbing_and_falling_scores():
 
 
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
-@pytest.mark.parametrize("hq,H", [(8, 2), (2, 2)])
+@pytest.mark.parametrize("hq,H", [(8, 2), (2, 2), (64, 16)])
 def test_unseen_infinities_and_nans_do_not_reach_a_row(bad, hq, H):
     """Keys and values of later tokens, of the next sequence and of the padding are infinite or
     NaN: rows before them are exact, rows that see an infinite value get it."""
@@ -164,12 +185,13 @@ def test_unseen_infinities_and_nans_do_not_reach_a_row(bad, hq, H):
     assert bool((err <= tol)[clean].all())
 
 
-def test_seen_infinite_values():
+@pytest.mark.parametrize("hq,H", [(8, 2), (64, 16)])
+def test_seen_infinite_values(hq, H):
     """Infinite and NaN values with finite keys: rows that see one have it in that dim (infinities
     of both signs: NaN), every other element is the finite sum."""
     lens = [333, 70]
     T = sum(lens)
-    q, k, v = _inputs(T, 8, 2, seed=14)
+    q, k, v = _inputs(T, hq, H, seed=14)
     clean = v.clone()
     inf, nan = float("inf"), float("nan")
     for tok, dim, x in ((10, 5, inf), (140, 6, -inf), (300, 5, -inf), (200, 7, nan), (332, 8, inf),
