@@ -168,7 +168,11 @@ def _stream(stream) -> ctypes.c_void_p:
 
 def _raw_stream(stream, device: int) -> int:
     """The cudaStream_t of ``stream``, or of ``device``'s current one."""
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"stream of device {stream.device_index}, not of the current one ({device})")
+    return stream.cuda_stream
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -291,6 +295,15 @@ def _one_device(tensors) -> int:
     return device
 
 
+def _rows_like(x: torch.Tensor, stream) -> torch.Tensor:
+    """An output like ``x``, allocated on the stream that writes it: memory that
+    another stream has freed may still be read by work queued there."""
+    if stream is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def _addr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -328,7 +341,7 @@ def rope_quantize_scatter(cache: Cache, q: torch.Tensor | None, k: torch.Tensor,
         hq = q.shape[1]
         qs = _heads(q, "q", T, hq, D)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _rows_like(q, stream)
         qos = _heads(q_out, "q_out", T, hq, D)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -364,7 +377,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     N = cu_seqlens.numel() - 1
     _flat(cu_seqlens, "cu_seqlens", torch.int32, N + 1)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _rows_like(q, stream)
     outs = _heads(out, "out", T, Hq, D)
     _flags(err_flags)
     device = _one_device((q, k, v, cu_seqlens, out, err_flags))

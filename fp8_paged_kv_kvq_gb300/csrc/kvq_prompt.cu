@@ -166,7 +166,6 @@ struct PromptParams {
   int32_t inv_g;                                       // ceil(65536 / G)
   uint64_t h_magic;                                    // ceil(2^h_shift / H): n / H for n < 2^31
   int32_t h_shift;                                     // 32 + ceil(log2(H))
-  int64_t units;                                       // work numbers
   float scale2;                                        // sm_scale log2(e)
   int32_t out_by_32;                                   // out rows are 32-byte aligned
   int32_t *err_flags;
@@ -551,7 +550,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
     cu_s[i] = a;
     cu_s[i + 1] = b;
     if (pt_bounds_ok(p, a, b)) return pt_units_of(b - a, p.TU);
-    if (blockIdx.x == 0 && p.err_flags) atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
+    if (p.err_flags) atomicOr(p.err_flags, KVQ_ERRF_SEQUENCE_RANGE);
     return 0;
   };
   if (p.N <= 32) {
@@ -800,10 +799,10 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
                   u.start + j * kPtKeys, 0, u.h, BAR(kPtKvFull + b));
         return true;
       };
-      // the tiles of the unit's step i
       // ring entries issued (split: each chain's tiles; no arrays: they would be in
       // local memory, a cold miss at the kernel's start)
       uint32_t idx0 = 0, idx1 = 0;
+      // the tiles of the unit's step i
       auto load_step = [&](const Unit &u, int i) -> bool {
         bool ok = true;
         if constexpr (kSplit) {
@@ -1147,7 +1146,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
   // 12.2; 1,024 tokens, 256 units, 22.5 against 18.5).
   const bool split = prompt_units(a, 1) <= a.sms;
   p.TU = (split ? 1 : 2) * p.TQ;
-  p.units = prompt_units(a, split ? 1 : 2);
+  const int64_t units = prompt_units(a, split ? 1 : 2);
   p.scale2 = a.sm_scale * 1.4426950408889634f;
   p.out_by_32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0;
   p.err_flags = a.err_flags;
@@ -1167,7 +1166,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured[split].fetch_or(bit, std::memory_order_acq_rel);
   }
-  return launch_overlapped(kernel, dim3(static_cast<unsigned>(p.units)), dim3(kPtThreads), kPtSmem,
+  return launch_overlapped(kernel, dim3(static_cast<unsigned>(units)), dim3(kPtThreads), kPtSmem,
                            stream, p, mq, mk, mv);
 }
 

@@ -178,9 +178,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32)
 rope_quantize_kernel(const RopeParams p) {
   const int sub = threadIdx.x & (kRopeLanes - 1);
   const unsigned gmask = ((1u << kRopeLanes) - 1u) << (threadIdx.x & 31 & ~(kRopeLanes - 1));
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
-  const int64_t t = warp / p.warps_per_token;
-  const int part = static_cast<int>(warp - t * p.warps_per_token);
+  const uint32_t warp = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);   // (below 2^31)
+  const uint32_t token = warp / static_cast<uint32_t>(p.warps_per_token);
+  const int part = static_cast<int>(warp - token * static_cast<uint32_t>(p.warps_per_token));
+  const int64_t t = token;
   const int Hq = p.num_q_heads, H = p.num_kv_heads, rows = Hq + 2 * H;
   const int stride = kRopeGroups * p.warps_per_token;
   const int h0 = kRopeGroups * part + ((threadIdx.x & 31) / kRopeLanes);

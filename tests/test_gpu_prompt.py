@@ -285,6 +285,32 @@ def test_captured_replayed_and_on_another_stream():
     assert_close(out[:512], q[:512], k[:512], v[:512], [255, 257])
 
 
+@pytest.mark.parametrize("which", ["prompt", "rope"])
+def test_output_allocated_for_another_stream(which):
+    """A call on a side stream that allocates its output does not write over memory that the
+    current stream has freed but has yet to read."""
+    hq, H, T = 16, 4, 100
+    q, k, v = _inputs(T, hq, H, seed=25)
+    cache = kvq.Cache.empty(128, H)
+    pos = torch.arange(T).cuda()
+    table = plain.rope_table(T, 128).cuda()
+    cu = _cu([T])
+    side = torch.cuda.Stream()
+    kept = torch.zeros_like(q)
+    old = torch.full_like(q, 3.0)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                      # some 50 ms
+    kept.copy_(old)
+    del old
+    if which == "prompt":
+        out = kvq.prompt_attention(q, k, v, cu, T, SCALE, stream=side)
+    else:
+        out = kvq.rope_quantize_scatter(cache, q, k, v, pos, table, pos, stream=side)
+    torch.cuda.synchronize()
+    assert torch.all(kept == 3.0)
+    assert out.shape == q.shape
+
+
 def test_a_serving_step_of_both_operators():
     """Prompts rotated in place and stored (kvq_rope_quantize_scatter), attended over
     (kvq_prompt_attention), then one decode step of new tokens: rotated, stored, and attended over
