@@ -4,7 +4,7 @@
 // tensor cores.
 //
 //   out_i = sum_{j <= i} p_j v_j / sum_{j <= i} p_j,  p_j = 2^(c (q_i . k_j - m_i)),
-//   c = sm_scale log2(e), m_i a running reference within 8 / c of the row's maximum
+//   c = sm_scale log2(e), m_i a running reference within 16 / c of the row's maximum
 //
 //  * A unit of work is two 128-row tiles of one sequence and KV head.  The G
 //    query heads that share a KV head are stacked: row t G + g of a tile is
@@ -37,16 +37,18 @@
 //    of its own, since the pipe takes an MMA about when it starts: whatever one
 //    warp spends on barriers, the other's MMAs fill (one warp for both left the
 //    tensor core idle for 60% of the time).
-//  * A row's reference m moves only when a score passes it by 2^8 in the
-//    exponent (P then stays below 2^8, and sums and outputs are fp32); the
+//  * A row's reference m moves only when a score passes it by 2^16 in the
+//    exponent (P then stays below 2^16, and sums and outputs are fp32; with 2^8
+//    the rows of the ragged batch moved often enough to take 328 us, not 323); the
 //    thread that moves it rescales its O row, with no PV in flight on it since
 //    the QK^T that it waited for was issued after it.  P is rounded to bf16 for
 //    the product (2^-8 of each term at most, the tensor core's operand type) and
 //    not for the sum.
 //  * 0 times an infinity is not 0, so zero probabilities do not hide unseen
 //    values.  Of the value tiles that some row of the unit does not see whole
-//    warp 15 clears the rows that none sees and every infinity and NaN; the
-//    epilogue adds those a row does see back (rare, one flag per unit).
+//    warp 15 clears the rows that none sees, and in the rows that some see every
+//    infinity and NaN; the epilogue adds those a row does see back (rare, one
+//    flag per unit).
 //  * What bounds it: the tensor core, and from 4,096 tokens on the card's 1.4 kW
 //    (1.83-1.86 GHz in a loop): 16,381 tokens of 32 heads 1.33 ms, 1,650 TFLOP/s,
 //    86% of what a bf16 library product reaches in a burst; 4 x 8,192 tokens
@@ -76,7 +78,7 @@ constexpr int kPtWarpEpi = 8, kPtWarpLoad = 12, kPtWarpMma = 13, kPtWarpClear = 
 constexpr int kPtThreads = 512;
 constexpr int kPtUnits = 4;                           // units ahead
 constexpr int kPtSeqs = 2048;                         // sequences whose units are summed
-constexpr float kPtLazy = 8.0f;                       // log2 of the largest unnormalised p
+constexpr float kPtLazy = 16.0f;                       // log2 of the largest unnormalised p
 
 // shared memory, offsets from a 1024-byte aligned base
 constexpr int kPtTileBytes = 128 * kHeadDim * 2;      // [2 halves of 64 dims][128 rows][128 B]
@@ -708,9 +710,9 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
             for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], inv_b, o[i]);
           }
           if (dirty) {
-            // the infinities and NaN this row sees in the edge tiles
+            // the infinities and NaN this row sees of the cleared rows
             const int last = min(tok, u.len - 1);
-            for (int j = max(0, u.tok0 - (kPtKeys - 2)) / kPtKeys * kPtKeys; j <= last; ++j) {
+            for (int j = u.tok0 + 1; j <= last; ++j) {
               const uint16_t *vr = p.v + (static_cast<int64_t>(u.start) + j) * p.v_stride +
                                    u.h * kHeadDim + c;
 #pragma unroll
@@ -744,7 +746,8 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       // Units: the own block's first, then those of blocks that have not
       // started.  Answers are asked for before a unit's last two tiles are loaded
       // (any earlier, and the CTAs that ask first hold work back from those that
-      // finish first), two of them if it has no more.
+      // finish first: asked one unit earlier, 1,999 tokens take 33.1 us instead of
+      // 31.6), two of them if it has no more.
       const uint32_t steal = smem_addr(smem + kPtOffSteal);
       uint32_t asked = 0, heard = 0;
       bool more = true;
@@ -774,7 +777,6 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
           if (w < 0) {
             more = false;                              // (an answer may still be under way)
           } else {
-            ask(1);
             e = find(w);
           }
         }
@@ -895,12 +897,17 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
       uint32_t par_clear = 0;                          // bit per ring stage
       uint32_t par_turn = a ^ 1;                       // chain 0 goes first
       bool ok = true;
-      for (int t = 0; ok; ++t) {
-        Unit u;
-        ok = __all_sync(0xFFFFFFFFu, take_unit(t, u));
-        if (!ok) break;
+      // The next unit is taken while this one's last softmax runs (after its last
+      // product, the ragged batch of 64 heads takes 320 us instead of 312); where the
+      // keys are split there hardly is one.
+      auto take = [&](int t, Unit &u) -> bool {
+        if (!__all_sync(0xFFFFFFFFu, take_unit(t, u))) return false;
         if (lane == 0) mbar_arrive(BAR(kPtUnitEmpty + t % kPtUnits));
-        if (u.len == 0) break;
+        return true;
+      };
+      Unit u, next;
+      ok = take(0, u);
+      for (int t = 0; ok && u.len != 0; ++t, u = next) {
         const int steps = u.steps(), top = u.top(a);
         const bool turns = u.top(1) >= 0;              // (a lone chain 0 need not pass them)
         // turn j: PV of one of the chain's key tiles (jv, none in the first turn) and
@@ -944,6 +951,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
             ok = pt_wait_all(BAR(kPtQFull + (kSplit ? 0 : a)), kSplit ? t & 1 : par_q, abort_s);
             par_q ^= 1u;
           }
+          if (!kSplit && ok && j == 0) ok = take(t + 1, next);
           if (ok && pv) {
             if (pv_first) {
               ok = pt_wait_all(BAR(kPtOEmpty + a), par_o, abort_s);
@@ -994,6 +1002,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
           __syncwarp();
         }
         base += kSplit ? (top >= 0 ? top / 2 + 1 : 0) : 2 * steps;
+        if (kSplit && ok) ok = take(t + 1, next);
       }
       gave_up = !ok;
       // every MMA issued has completed before the tensor memory is freed
@@ -1039,13 +1048,14 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
             continue;
           }
           uint8_t *tile = smem + kPtOffKv + b * kPtTileBytes;
-          const int rows = u.keys(j, p.TQ);
+          // the rows that some rows of the unit see and some do not
+          const int lo = max(0, u.tok0 + 1 - j * kPtKeys), rows = u.keys(j, p.TQ);
           // 0 times the values, summed: NaN where one of them is not finite
           uint32_t sum0 = 0u, sum1 = 0u;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half)
 #pragma unroll 1
-            for (int r0 = 0; r0 < rows; r0 += 32) {
+            for (int r0 = lo; r0 < rows; r0 += 32) {
               uint4 w[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -1063,9 +1073,8 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
             }
           if (__any_sync(0xFFFFFFFFu, ((sum0 | sum1) & 0x7FFF7FFFu) != 0u)) {
             if (lane == 0) dirty_s[t % kPtUnits] = 1;
-            for (int r = 0; r < 2 * rows; ++r) {
-              uint32_t *w = reinterpret_cast<uint32_t *>(
-                                tile + (r < rows ? r * 128 : kPtHalf + (r - rows) * 128)) + lane;
+            for (int r = 2 * lo; r < 2 * rows; ++r) {
+              uint32_t *w = reinterpret_cast<uint32_t *>(tile + (r & 1) * kPtHalf + (r >> 1) * 128) + lane;
               uint32_t x = *w;
               if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
               if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
