@@ -349,7 +349,7 @@ __device__ __forceinline__ void pt_steal(uint32_t answer, uint32_t bar) {
       " [%0], [%1];\n" :: "r"(answer), "r"(bar) : "memory");
 }
 // The answer: a block number, or -1 once every block has started.
-__device__ __forceinline__ int64_t pt_stolen(uint32_t answer) {
+__device__ __forceinline__ int pt_stolen(uint32_t answer) {
   uint32_t some, x;
   asm volatile(
       "{\n .reg .pred p;\n .reg .b128 r;\n ld.shared.b128 r, [%2];\n"
@@ -357,7 +357,7 @@ __device__ __forceinline__ int64_t pt_stolen(uint32_t answer) {
       " selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
       " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
       : "=r"(some), "=r"(x) : "r"(answer) : "memory");
-  return some != 0 ? static_cast<int64_t>(x) : -1;
+  return some != 0 ? static_cast<int>(x) : -1;
 }
 
 // The running statistics of one row.
@@ -713,23 +713,29 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], inv_b, o[i]);
           }
-          if (dirty) {
-            // the infinities and NaN this row sees of the cleared rows
-            const int last = min(tok, u.len - 1);
-            for (int j = u.tok0 + 1; j <= last; ++j) {
-              const uint16_t *vr = p.v + (static_cast<int64_t>(u.start) + j) * p.v_stride +
-                                   u.h * kHeadDim + c;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const uint32_t e = vr[i];
-                if ((e & 0x7F80u) == 0x7F80u) o[i] += bf16_lo(e);
-              }
-            }
-          }
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
           if (mine) pt_store64(dst + c, w, p.out_by_32);
+        }
+        if (dirty && mine) {
+          // the infinities and NaN this row sees of the cleared rows, added to what
+          // was stored (rare, and little code)
+#pragma unroll 1
+          for (int j = u.tok0 + 1; j <= tok; ++j) {
+            const uint16_t *vr = p.v + (static_cast<int64_t>(u.start) + j) * p.v_stride + u.h * kHeadDim;
+#pragma unroll 1
+            for (int d = 0; d < kHeadDim; d += 8) {
+              const uint4 x = __ldg(reinterpret_cast<const uint4 *>(vr + d));
+              const uint32_t sum = pt_fma_bf16x2(x.x, 0u, 0u) | pt_fma_bf16x2(x.y, 0u, 0u) |
+                                   pt_fma_bf16x2(x.z, 0u, 0u) | pt_fma_bf16x2(x.w, 0u, 0u);
+              if ((sum & 0x7FFF7FFFu) == 0u) continue;
+#pragma unroll 1
+              for (int i = d; i < d + 8; ++i)
+                if ((vr[i] & 0x7F80u) == 0x7F80u)
+                  dst[i] = static_cast<uint16_t>(pack_bf16x2(bf16_lo(dst[i]) + bf16_lo(vr[i]), 0.0f));
+            }
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -761,7 +767,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         __syncwarp();
       };
       // the unit of work number w (none: the next answer's), or none (length 0)
-      auto next_unit = [&](int64_t w, int4 &e) -> bool {
+      auto next_unit = [&](int w, int4 &e) -> bool {
         e = make_int4(0, 0, 0, 0);
 #pragma unroll 1
         for (;;) {
@@ -844,7 +850,7 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         return true;
       };
       bool ok = true;
-      int64_t w = blockIdx.x;
+      int w = static_cast<int>(blockIdx.x);
       for (int t = 0; ok; ++t, w = -1) {
         int4 e;
         ok = next_unit(w, e);
