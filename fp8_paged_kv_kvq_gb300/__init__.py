@@ -214,13 +214,15 @@ class Cache:
         return self.k_codes.shape[2]
 
     def struct(self) -> _CacheStruct:
-        for t, dt in ((self.k_codes, torch.uint8), (self.v_codes, torch.uint8),
-                      (self.k_scales, torch.float32), (self.v_scales, torch.float32)):
-            if t.dtype != dt or not t.is_contiguous():
-                raise ValueError("cache tensors must be contiguous uint8 codes / fp32 scales")
-        return _CacheStruct(self.k_codes.data_ptr(), self.v_codes.data_ptr(),
-                            self.k_scales.data_ptr(), self.v_scales.data_ptr(),
-                            self.num_slots, self.num_kv_heads, self.head_dim, self.block_size)
+        kc, vc, ks, vs = self.k_codes, self.v_codes, self.k_scales, self.v_scales
+        u8, f32 = torch.uint8, torch.float32
+        if not (kc.dtype is u8 and vc.dtype is u8 and ks.dtype is f32 and vs.dtype is f32 and
+                kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and
+                vs.is_contiguous()):
+            raise ValueError("cache tensors must be contiguous uint8 codes / fp32 scales")
+        shape = kc.shape
+        return _CacheStruct(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                            shape[0], shape[1], shape[2], self.block_size)
 
 
 def abi_version() -> int:
@@ -287,7 +289,7 @@ def _one_device(tensors) -> int:
     """The index of the current CUDA device, on which every tensor (None: not
     given) has to be: a pointer of the host or of another device would fault in
     the kernel."""
-    device = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError(f"every tensor must be on the current CUDA device ({device}), "
@@ -326,7 +328,7 @@ def rope_quantize_scatter(cache: Cache, q: torch.Tensor | None, k: torch.Tensor,
     ``q`` itself; allocated here, by PyTorch, when not given), the rotated keys
     also to ``k_out`` where given (may be ``k``).  Rows of skipped tokens
     (slot id < 0) are not written.  Returns ``q_out`` (None without ``q``)."""
-    T, H, D = k.shape[0], cache.num_kv_heads, cache.head_dim
+    T, (_, H, D) = k.shape[0], cache.k_codes.shape
     ks, vs = _heads(k, "k", T, H, D), _heads(v, "v", T, H, D)
     kos = 0 if k_out is None else _heads(k_out, "k_out", T, H, D)
     _flat(positions, "positions", torch.int64, T)
