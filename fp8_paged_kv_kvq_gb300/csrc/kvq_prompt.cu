@@ -1160,11 +1160,17 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
   while ((int64_t(1) << l) < p.H) ++l;
   p.h_shift = 32 + l;
   p.h_magic = ((uint64_t(1) << p.h_shift) + p.H - 1) / p.H;
-  // Where units of one row tile all start at once: its keys split between the two
-  // chains -- twice the units of half the steps, which only pays while SMs would
-  // stand idle (8 KV heads of 4 query heads: 512 tokens, 128 units, 10.0 us against
-  // 12.2; 1,024 tokens, 256 units, 22.5 against 18.5).
-  const bool split = prompt_units(a, 1) <= a.sms;
+  // Units of one row tile, its keys split between the two chains: twice the units
+  // of half the steps.  That pays where they all start at once (8 KV heads of 4
+  // query heads, 512 tokens, 128 units: 9.7 us against 12.3) and, while a second
+  // unit hides behind the longest, somewhat beyond: the room grows with the key
+  // tiles of a sequence, and falls with their number (numbers go sequence by
+  // sequence, so long units start late).  152 SMs, not split against split: 1 x
+  // 4,800 tokens, 300 units, 58 and 55 us; 1 x 640, 160 units, 13.9 and 12.2; 1 x
+  // 900, 232 units, 16.8 and 17.5; 2 x 1,500, 188 units, 23.1 and 20.2; 3 x 1,000,
+  // 192 units, 17.9 and 20.8; 4 x 350, 176 units, 11.0 and 12.8.
+  const int64_t room = 7 * a.num_tokens / kPtKeys / a.num_seqs / a.num_seqs;
+  const bool split = prompt_units(a, 1) <= a.sms + std::min<int64_t>(a.sms, room);
   p.TU = (split ? 1 : 2) * p.TQ;
   const int64_t units = prompt_units(a, split ? 1 : 2);
   p.scale2 = a.sm_scale * 1.4426950408889634f;

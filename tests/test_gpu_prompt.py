@@ -90,6 +90,14 @@ def test_split_keys(lens, hq, H):
     _run(lens, hq, H, seed=sum(lens))
 
 
+@pytest.mark.parametrize("lens,hq,H", [([650], 32, 8), ([2000], 16, 2), ([1500, 1500], 8, 2),
+                                       ([3700], 8, 1), ([2900, 1], 8, 1)])
+def test_split_keys_of_more_units_than_sms(lens, hq, H):
+    """Split keys where some SMs take a second unit (and where the last of two sequences is one
+    row, whose second chain has no key)."""
+    _run(lens, hq, H, seed=sum(lens) + 1)
+
+
 @pytest.mark.parametrize("hq,H", [(8, 2), (2, 2), (14, 2)])
 def test_mixed_lengths(hq, H):
     """Tails, heads and whole short prompts side by side, among empty ones."""
