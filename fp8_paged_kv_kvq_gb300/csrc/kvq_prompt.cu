@@ -808,25 +808,31 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
                   u.start + j * kPtKeys, 0, u.h, BAR(kPtKvFull + b));
         return true;
       };
-      // ring entries issued (split: each chain's tiles; no arrays: they would be in
-      // local memory, a cold miss at the kernel's start)
-      uint32_t idx0 = 0, idx1 = 0;
-      // the tiles of the unit's step i
+      // ring entries issued (split: each chain's keys and values; no arrays: they
+      // would be in local memory, a cold miss at the kernel's start)
+      uint32_t idx = 0, k0 = 0, k1 = 0, v0 = 0, v1 = 0;
+      // the tiles of the unit's step i (split: from -1 on, with the first keys)
       auto load_step = [&](const Unit &u, int i) -> bool {
         bool ok = true;
         if constexpr (kSplit) {
-          // both chains' keys first: their stages are free before the values'
-#pragma unroll 1
-          for (int x = 0; x < 4 && ok; ++x) {
-            const int a = x & 1, kv = x >> 1, j = u.top(a) - 2 * i;
-            if (j >= 0) ok = load_tile(u, j, kv, 2 * a + kv, a == 0 ? idx0 : idx1);
+          // chain 0's values of this step, its keys of the next, the same of chain 1:
+          // the order in which their places come free (all keys, then all values: 1 x
+          // 4,096 tokens of 4 heads take 43.4 us instead of 30.0; in a loop, 31.6)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int a = x >> 1, keys = x & 1;
+            const int step = i + keys, j = u.top(a) - 2 * step;
+            uint32_t &n = a == 0 ? (keys ? k0 : v0) : (keys ? k1 : v1);
+            if (!ok || step < 0 || j < 0) continue;
+            ok = load_tile(u, j, 1 - keys, 2 * a + 1 - keys, n);
+            n += ok;
           }
-          idx0 += u.top(0) >= 2 * i;
-          idx1 += u.top(1) >= 2 * i;
         } else {
 #pragma unroll 1
-          for (int kv = 0; kv < 2 && ok; ++kv, ++idx0)
-            ok = load_tile(u, u.tiles() - 1 - i, kv, idx0 % kPtStages, idx0 / kPtStages);
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            ok = load_tile(u, u.tiles() - 1 - i, kv, idx % kPtStages, idx / kPtStages);
+            idx += ok;
+          }
         }
         return ok;
       };
@@ -862,8 +868,8 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
         // wait for)
         if (kSplit || steps == 0) ok = announce(t, e);
         if (steps == 0) break;
-        for (int i = 0; i < steps && ok; ++i) {
-          if (kSplit && i == 0 && lane == 0) ok = load_q(u);
+        for (int i = kSplit ? -1 : 0; i < steps && ok; ++i) {
+          if (kSplit && i < 0 && lane == 0) ok = load_q(u);
           if (ok && lane == 0) ok = load_step(u, i);
           if (!kSplit && i == 0) {
             // the first keys and values ahead of the queries, whose tiles are free
@@ -882,7 +888,8 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
 #pragma unroll
         for (uint32_t b = 0; b < kPtStages; ++b) {
           // rounds of this stage so far
-          const uint32_t n = kSplit ? (b < 2 ? idx0 : idx1) : (idx0 + kPtStages - 1 - b) / kPtStages;
+          const uint32_t n = kSplit ? (b == 0 ? k0 : (b == 1 ? v0 : (b == 2 ? k1 : v1)))
+                                    : (idx + kPtStages - 1 - b) / kPtStages;
           if (n > 0) mbar_wait_sleep_bounded(BAR(kPtKvFull + b), (n - 1) & 1);
         }
         if (loads0 > 0) mbar_wait_sleep_bounded(BAR(kPtQFull), (loads0 - 1) & 1);
@@ -1166,10 +1173,10 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
   // unit hides behind the longest, somewhat beyond: the room grows with the key
   // tiles of a sequence, and falls with their number (numbers go sequence by
   // sequence, so long units start late).  152 SMs, not split against split: 1 x
-  // 4,800 tokens, 300 units, 58 and 55 us; 1 x 640, 160 units, 13.9 and 12.2; 1 x
-  // 900, 232 units, 16.8 and 17.5; 2 x 1,500, 188 units, 23.1 and 20.2; 3 x 1,000,
-  // 192 units, 17.9 and 20.8; 4 x 350, 176 units, 11.0 and 12.8.
-  const int64_t room = 7 * a.num_tokens / kPtKeys / a.num_seqs / a.num_seqs;
+  // 4,800 tokens, 300 units, 58 and 40 us; 1 x 640, 160 units, 13.9 and 11.5; 1 x
+  // 900, 232 units, 16.9 and 18.4; 2 x 1,500, 188 units, 23.1 and 19.2; 3 x 1,000,
+  // 192 units, 18.0 and 19.4; 4 x 350, 176 units, 11.0 and 12.6.
+  const int64_t room = 8 * a.num_tokens / kPtKeys / a.num_seqs / a.num_seqs;
   const bool split = prompt_units(a, 1) <= a.sms + std::min<int64_t>(a.sms, room);
   p.TU = (split ? 1 : 2) * p.TQ;
   const int64_t units = prompt_units(a, split ? 1 : 2);
