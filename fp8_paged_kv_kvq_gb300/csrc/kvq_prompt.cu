@@ -18,7 +18,7 @@
 //    shared memory, so there is no plan launch and no workspace.  (Cutting the
 //    packed tokens instead, with rows of several sequences in one tile, took 9 us
 //    instead of 15 for 64 prompts of 16 tokens, but 348 us instead of 322 for 8
-//    of 355 to 4,096 and 64 heads: diagonals that no longer end with a key
+//    of 355 to 4,096 and 64 heads (both before later steps): diagonals that no longer end with a key
 //    tile.)  Of more than kPtSeqs sequences, s uses the numbers
 //    floor(cu[s] / TU) + s up to the next one's (TU tokens a unit), at least
 //    ceil(len / TU) of them, and a number finds its sequence by a search over
@@ -49,13 +49,15 @@
 //    warp 15 clears the rows that none sees, and in the rows that some see every
 //    infinity and NaN; the epilogue adds those a row does see back (rare, one
 //    flag per unit).
-//  * What bounds it: the tensor core, and from 4,096 tokens on the card's 1.4 kW
-//    (1.83-1.86 GHz in a loop): 16,381 tokens of 32 heads 1.33 ms, 1,650 TFLOP/s,
+//  * What bounds it: the tensor core, and on large calls the card's 1.4 kW
+//    (1.78-1.94 GHz in a loop): 16,381 tokens of 32 heads 1.33 ms, 1,650 TFLOP/s,
 //    86% of what a bf16 library product reaches in a burst; 4 x 8,192 tokens
-//    1.37 ms.  A step of two row tiles over a key tile takes about 2,700 cycles, of
-//    which its MMAs need 2,048; the rest is the chain of one tile (QK^T, 128
-//    scores a thread, PV) that the other's MMAs do not cover.  Short prompts are
-//    bound by latency: 2 us to the first MMA, 1.5 us a step, 1 us for the rows.
+//    1.30-1.37 ms.  A step of two row tiles over a key tile takes about 2,700
+//    cycles: MMAs of 2,048, and at each of the two hand-overs some 300 of waiting
+//    for the turn and for the second half of P.  A change of units takes some 5,000
+//    more (queries from memory, a masked softmax, an epilogue of 2,500 a tile).
+//    Short prompts are bound by latency: 2 us to the first MMA, 1.5 us a step, 1 us
+//    for the rows.
 //  * Code that runs once a unit is kept in one copy (one search for units, one
 //    epilogue for both chains): the roles share an instruction cache, and with
 //    two copies 8 x 1,024 tokens take 86 us instead of 83, the short ragged batch
