@@ -17,9 +17,9 @@
 //  * Units are numbered through the sequences; every CTA sums their counts in
 //    shared memory, so there is no plan launch and no workspace.  (Cutting the
 //    packed tokens instead, with rows of several sequences in one tile, took 9 us
-//    instead of 15 for 64 prompts of 16 tokens, but 348 us instead of 322 for 8
-//    of 355 to 4,096 and 64 heads (both before later steps): diagonals that no longer end with a key
-//    tile.)  Of more than kPtSeqs sequences, s uses the numbers
+//    instead of 15 for 64 prompts of 16 tokens, but 348 us instead of the 322 of
+//    the time for 8 of 355 to 4,096 and 64 heads: diagonals that no longer end with
+//    a key tile.)  Of more than kPtSeqs sequences, s uses the numbers
 //    floor(cu[s] / TU) + s up to the next one's (TU tokens a unit), at least
 //    ceil(len / TU) of them, and a number finds its sequence by a search over
 //    cu_seqlens itself, with no bound on their count; the numbers left over cost

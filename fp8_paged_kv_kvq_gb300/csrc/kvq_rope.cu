@@ -179,7 +179,7 @@ __device__ __forceinline__ void rotate_row(float (&x)[kRopeChunks][8], const Rop
 // token's angles stay in registers, and the next row is fetched while this one
 // is worked on.  (16,384 tokens: blocks of 32 rows, whosever they are, with the
 // angles read for each row 98.5 us; this 79.5; with streaming stores of the
-// bf16 rows, which would else push the rows to be read out of L2, 71.)
+// bf16 rows, 71.)
 template <int kMode, bool kLoop>
 __global__ void __launch_bounds__(kRopeWarps * 32)
 rope_quantize_kernel(const RopeParams p) {
