@@ -409,12 +409,15 @@ kvq_status kvq_paged_decode_codes(const kvq_cache *cache, int32_t code_format, c
  *     out_i = sum_{j <= i} p_j v_j / sum_{j <= i} p_j,
  *     p_j = exp(sm_scale (q_i . k_j - max_j q_i . k_j)),   j in its sequence.
  * fp32 scores and sums; the probabilities are rounded to bf16 for the product
- * with the values and not for the sum.  Tokens a row does not see do not reach
- * it, whatever they hold (infinities and NaN included).
+ * with the values and not for the sum.  (The sums run under a reference that may
+ * trail the maximum by 2^16, so values of 2^112 / length and more can overflow.)
+ * Tokens a row does not see do not reach it, whatever they hold (infinities and
+ * NaN included).
  *   q               device bf16, token t's row for query head h at element
  *                   t*q_token_stride + h*head_dim (a view of a fused qkv tensor,
  *                   rotated); k and v the same with num_kv_heads heads
- *   token strides   in elements, multiples of 8, >= heads * head_dim
+ *   token strides   in elements, multiples of 8, >= heads * head_dim (q, k, v:
+ *                   below 2^39)
  *   num_tokens      rows of the token buffers
  *   cu_seqlens      device int32 [num_seqs + 1], non-decreasing, in
  *                   [0, num_tokens]; rows outside the sequences (in front, or

@@ -293,6 +293,65 @@ def test_captured_replayed_and_on_another_stream():
     assert_close(out[:512], q[:512], k[:512], v[:512], [255, 257])
 
 
+@pytest.mark.parametrize("hq,H", [(4, 1), (64, 16)])
+def test_strides_and_alignment_of_their_own(hq, H):
+    """q, k, v and out with four different token strides, none a multiple of 32 bytes, each 16 bytes
+    off a 32-byte boundary; what lies between the rows of out stays."""
+    lens = [130, 9, 261]
+    T = sum(lens)
+    views = []
+    for x, gap in zip(_inputs(T, hq, H, seed=26), (8, 24, 40)):
+        heads = x.shape[1]
+        buf = torch.full((T * (heads * 128 + gap) + 8,), 3.0, dtype=torch.bfloat16, device="cuda")
+        views.append(buf.as_strided((T, heads, 128), (heads * 128 + gap, 128, 1), 8))
+        views[-1].copy_(x)
+    buf = torch.full((T, hq * 128 + 56), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf.as_strided((T, hq, 128), (hq * 128 + 56, 128, 1), 8)
+    kvq.prompt_attention(*views, _cu(lens), 300, SCALE, out=out)
+    torch.cuda.synchronize()
+    assert torch.all(buf[:, :8] == 7) and torch.all(buf[:, hq * 128 + 8:] == 7)
+    assert_close(out, *views, lens)
+
+
+@pytest.mark.parametrize("hq,H", [(4, 1), (64, 16)])
+def test_large_values(hq, H):
+    """Values around 2^100, whose sums the unnormalised probabilities (below 2^16) may not push out
+    of binary32: 2^100 2^16 350 < 2^125."""
+    lens = [350, 40]
+    q, k, v = _inputs(390, hq, H, seed=27, spread=8.0)
+    v = (v.double() * 2.0 ** 97).clamp(-2.0 ** 100, 2.0 ** 100).to(torch.bfloat16)
+    out = kvq.prompt_attention(q, k, v, _cu(lens), 350, SCALE)
+    torch.cuda.synchronize()
+    assert_close(out, q, k, v, lens)
+
+
+def test_calls_that_follow_one_another():
+    """Calls in a row that read what the last one wrote (rotated in place and stored, attended over,
+    the outputs the next queries), of few units and of many, give the bits that they give with a
+    wait after each."""
+    def steps(wait):
+        got = []
+        for lens, hq, H in (([200, 90], 8, 2), ([300, 300, 41], 64, 16)):
+            T = sum(lens)
+            q, k, v = (x.clone() for x in _inputs(T, hq, H, seed=28))
+            pos = torch.arange(T).cuda()
+            cu, table = _cu(lens), plain.rope_table(T, 128).cuda()
+            cache = kvq.Cache.empty(T, H)
+            torch.cuda.synchronize()
+            for _ in range(4):
+                kvq.rope_quantize_scatter(cache, q, k, v, pos, table, pos, q_out=q, k_out=k)
+                if wait:
+                    torch.cuda.synchronize()
+                q = kvq.prompt_attention(q, k, v, cu, 300, SCALE)
+                if wait:
+                    torch.cuda.synchronize()
+            torch.cuda.synchronize()
+            got += [q, k, cache.k_codes, cache.k_scales]
+        return got
+    for a, b in zip(steps(True), steps(False)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("which", ["prompt", "rope"])
 def test_output_allocated_for_another_stream(which):
     """A call on a side stream that allocates its output does not write over memory that the
