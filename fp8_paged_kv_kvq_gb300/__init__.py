@@ -325,9 +325,10 @@ def rope_quantize_scatter(cache: Cache, q: torch.Tensor | None, k: torch.Tensor,
     [T, H, D] by their int64 ``positions`` in ``rope_table`` (fp32 [P, rotary_dim]:
     cosines, then sines) and quantise the rotated keys and the values into
     ``cache`` at int64 ``slot_ids``.  The rotated queries go to ``q_out`` (may be
-    ``q`` itself; allocated here, by PyTorch, when not given), the rotated keys
-    also to ``k_out`` where given (may be ``k``).  Rows of skipped tokens
-    (slot id < 0) are not written.  Returns ``q_out`` (None without ``q``)."""
+    ``q`` itself; allocated here, by PyTorch on the call's stream, when not
+    given), the rotated keys also to ``k_out`` where given (may be ``k``).  Rows
+    of skipped tokens (slot id < 0) are not written.  Returns ``q_out`` (None
+    without ``q``)."""
     T, (_, H, D) = k.shape[0], cache.k_codes.shape
     ks, vs = _heads(k, "k", T, H, D), _heads(v, "v", T, H, D)
     kos = 0 if k_out is None else _heads(k_out, "k_out", T, H, D)
@@ -368,7 +369,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     [T, Hq, D] over keys and values [T, H, D] (views with their own token
     strides), sequence s holding the tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1
     (int32, on the device).  Returns ``out`` (bf16, shape of q; allocated here,
-    by PyTorch, when not given).  Rows outside the sequences are not written."""
+    by PyTorch on the call's stream, when not given).  Rows outside the sequences
+    are not written."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be bfloat16 views [T, heads, head_dim]")
     T, Hq, D = q.shape

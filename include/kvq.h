@@ -429,7 +429,7 @@ kvq_status kvq_paged_decode_codes(const kvq_cache *cache, int32_t code_format, c
  *   max_seqlen      host bound on every sequence's length
  *   num_q_heads     a multiple of num_kv_heads, at most 128 per KV head
  *   head_dim        128
- *   sm_scale        positive and finite
+ *   sm_scale        positive and finite, as are the scores times log2(e) sm_scale
  *   out             device bf16, rows like q with their own token stride; must
  *                   not overlap q, k or v
  *   err_flags       device int32, optional
