@@ -19,11 +19,12 @@
 //    packed tokens instead, with rows of several sequences in one tile, took 9 us
 //    instead of 15 for 64 prompts of 16 tokens, but 348 us instead of the 322 of
 //    the time for 8 of 355 to 4,096 and 64 heads: diagonals that no longer end with
-//    a key tile.)  Of more than kPtSeqs sequences, s uses the numbers
-//    floor(cu[s] / TU) + s up to the next one's (TU tokens a unit), at least
-//    ceil(len / TU) of them, and a number finds its sequence by a search over
-//    cu_seqlens itself, with no bound on their count; the numbers left over cost
-//    a look each.
+//    a key tile.)  Of more than kPtSeqs sequences, whose counts would not fit, s
+//    uses the numbers floor(cu[s] / TU) + s up to the next one's (TU tokens a
+//    unit), at least ceil(len / TU) of them, and a number finds its sequence by a
+//    search over cu_seqlens itself, with no bound on their count; the numbers left
+//    over cost a look each.  (Searched so, 64 prompts of 16 tokens take 16.3 us,
+//    not 14.1, and 2,048 of up to 64 tokens 105, not 79.)
 //  * CTAs of 512 threads, one per SM, that go on with the units of blocks that
 //    have not started (cluster launch control) until there are none, longest
 //    rows of a sequence first.  Warps 0-3 and 4-7: softmax of chain 0 and 1 (a
@@ -122,6 +123,7 @@ enum : int {
 constexpr int kPtSmem = kPtOffBar + 8 * kPtBars + 1024;
 static_assert(kPtOffBar % 8 == 0 && kPtOffUnit % 16 == 0 && kPtOffSteal % 16 == 0, "alignment");
 static_assert(kPtSmem <= 227 * 1024, "shared memory budget");
+static_assert(kPtSeqs >= 32, "a warp counts the units of up to 32 sequences");
 
 // TMEM: S of chain a at 128 a (its P over the first 64 columns), O at 256 + 128 a
 constexpr uint32_t kPtTmemCols = 512;
