@@ -329,7 +329,8 @@ __device__ __forceinline__ void pt_prefetch_map(const void *tmap) {
   asm volatile("prefetch.tensormap [%0];\n" :: "l"(tmap) : "memory");
 }
 
-// 64 bytes of an output row, in whole 32-byte sectors where it is aligned.
+// 64 bytes of an output row, in whole 32-byte sectors where it is aligned (in
+// halves of them, the ragged batch of 64 heads takes 319 us, not 309).
 __device__ __forceinline__ void pt_store64(uint16_t *dst, const uint32_t (&w)[16], bool by_32) {
   if (by_32) {
 #pragma unroll
@@ -564,7 +565,8 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
     return 0;
   };
   if (p.N <= 32) {
-    // the loading warp alone, which is the one to use them
+    // the loading warp alone, which is the one to use them (with every warp and
+    // its barriers, one prompt of 64 tokens took 7.5 us, not 7.1)
     if (warp == kPtWarpLoad) {
       int n = lane < p.N ? count_units(lane) : 0;
       n = pt_scan(n, lane);
