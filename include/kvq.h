@@ -15,7 +15,9 @@
  *    ([num_slots, num_kv_heads, head_dim]); the scales in a sidecar
  *    [num_slots, num_kv_heads] fp32.  Division and rounding are IEEE binary32,
  *    round-to-nearest-even; |x / scale| >= 448 saturates to 448; an all-zero
- *    row stores scale 0 and codes 0x00; a NaN code is never written.
+ *    row stores scale 0 and codes 0x00; a row of finite values gets no NaN
+ *    code.  Rows are expected to be finite: one with a NaN or an infinity gets
+ *    a NaN scale and reads back as NaN.
  *
  *  - Attention.  ATOM PR #2655, PR description (K/V bullet): attention runs
  *    on the E4M3 tiles; a token's key scale is applied to its score after the
@@ -156,7 +158,8 @@ kvq_status kvq_quantize_scatter(const kvq_cache *cache,
  * in binary32 (six roundings, no contraction); the other dims pass through.
  * The cache gets the row format of kvq_quantize_scatter from these binary32
  * values -- they are not rounded to bf16 on the way; q_out and k_out get them
- * rounded to bf16 (nearest-even).
+ * rounded to bf16 (nearest-even).  A rotated key that is not finite (inputs that
+ * are not, or pairs of magnitudes whose turn passes FLT_MAX) gets a NaN scale.
  *   q               device bf16, token t's row for query head h at element
  *                   t*q_token_stride + h*head_dim; NULL with num_q_heads 0 to
  *                   rotate and store keys only

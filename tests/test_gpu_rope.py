@@ -155,6 +155,52 @@ def test_rotation_zero_is_the_plain_store():
         assert np.array_equal(x, y)
 
 
+@pytest.mark.parametrize("T", [32, 1301])
+def test_rows_that_are_not_finite_are_stored_as_the_store_stores_them(T):
+    """A NaN or an infinity anywhere in a value row, or in a key's dims that are not rotated, gives
+    the codes and the NaN scale of kvq_quantize_scatter, so that the row reads back as NaN; one in
+    the rotated dims, or a rotation that leaves binary32, gives a NaN scale too; other rows stay
+    finite."""
+    H = 8
+    inf, nan = float("inf"), float("nan")
+    _, q, k, v = _inputs(T, 8, H, seed=31)
+    k, v = k.contiguous(), v.contiguous()
+    every = torch.tensor([nan, -nan] * 64, dtype=torch.bfloat16, device="cuda")
+    for x in (k, v):
+        x[1, 2, 20:] = every[20:]
+        for token, head, dim, bad in ((3, 0, 77, nan), (4, 7, 127, -nan), (5, 1, 20, inf),
+                                      (6, 3, 99, -inf), (7, 5, 64, inf), (7, 5, 65, nan)):
+            x[token, head, dim] = bad
+    v[9, 4] = every                                     # a row of nothing else
+    v[10, 6, 0], v[11, 6, 3] = nan, inf
+    slots = torch.randperm(T, generator=workloads.generator(31, T)).cuda()
+    table = torch.cat([torch.ones(1, 8), torch.zeros(1, 8)], dim=1).cuda()      # no turn
+    pos = torch.zeros(T, dtype=torch.int64, device="cuda")
+    a, b = _cache(T, H), _cache(T, H)
+    kvq.rope_quantize_scatter(a, q, k, v, pos, table, slots)
+    kvq.quantize_scatter(b, k, v, slots)
+    torch.cuda.synchronize()
+    got, want = _planes(a), _planes(b)
+    for x, y in zip(got[:2], want[:2]):
+        assert np.array_equal(x, y)
+    for x, y, rows in zip(got[2:], want[2:], (6, 9)):
+        assert np.isnan(y).sum() == rows                # the existing store's NaN scales
+        assert np.array_equal(x, y, equal_nan=True)
+
+    k2 = k.clone()
+    k2[:, :, 16:] = 1.0
+    k2[12, 0, 3], k2[13, 1, 5] = nan, inf
+    k2[14, 2, :16] = 3.0e38                             # a c + b s beyond FLT_MAX
+    turn = torch.full((1, 16), 0.5 ** 0.5, device="cuda")
+    for layout in (kvq.ROPE_HALVES, kvq.ROPE_INTERLEAVED):
+        kvq.rope_quantize_scatter(a, q, k2, v, pos, turn, slots, layout=layout)
+        torch.cuda.synchronize()
+        scales = a.k_scales[slots].isnan().cpu()
+        bad = torch.zeros(T, H, dtype=torch.bool)
+        bad[12, 0] = bad[13, 1] = bad[14, 2] = True
+        assert torch.equal(scales, bad)
+
+
 def test_skipped_tokens_leave_everything_as_it_was():
     """Padding (slot -1, whatever its position), slots and positions out of range: flagged where
     out of range; their q_out, k_out and cache rows stay; the other tokens are stored."""
