@@ -3,7 +3,7 @@
 // buffer), before anything is read from the cache, on the 5th-generation
 // tensor cores.
 //
-//   out_i = sum_{j <= i} p_j v_j / sum_{j <= i} p_j,  p_j = 2^(c (q_i . k_j - m_i)),
+//   out_i = sum_{j <= i} p_j v_j / sum_{j <= i} p_j,  p_j = 2^(c (q_i . k_j - m_i) - 16),
 //   c = sm_scale log2(e), m_i a running reference within 16 / c of the row's maximum
 //
 //  * A unit of work is two 128-row tiles of one sequence and KV head.  The G
@@ -39,8 +39,11 @@
 //    warp spends on barriers, the other's MMAs fill (one warp for both left the
 //    tensor core idle for 60% of the time).
 //  * A row's reference m moves only when a score passes it by 2^16 in the
-//    exponent (P then stays below 2^16, and sums and outputs are fp32; with 2^8
-//    the rows of the ragged batch moved often enough to take 328 us, not 323); the
+//    exponent (with 2^8 the rows of the ragged batch moved often enough to take
+//    328 us, not 323).  The exponents are 16 lower for it, so that P, as in the
+//    formula under the maximum itself, is at most 1 and no sum passes
+//    sum_j |v_j|.  (At the other end, probabilities below 2^-110 are 0, and products
+//    with values below 2^-110 are subnormal, which the tensor cores keep.)  The
 //    thread that moves it rescales its O row, with no PV in flight on it since
 //    the QK^T that it waited for was issued after it.  P is rounded to bf16 for
 //    the product (2^-8 of each term at most, the tensor core's operand type) and
@@ -85,7 +88,7 @@ constexpr int kPtWarpEpi = 8, kPtWarpLoad = 12, kPtWarpMma = 13, kPtWarpClear = 
 constexpr int kPtThreads = 512;
 constexpr int kPtUnits = 4;                           // units ahead
 constexpr int kPtSeqs = 2048;                         // sequences whose units are summed
-constexpr float kPtLazy = 16.0f;                       // log2 of the largest unnormalised p
+constexpr float kPtLazy = 16.0f;                       // a row's maximum over its reference, log2
 
 // shared memory, offsets from a 1024-byte aligned base
 constexpr int kPtTileBytes = 128 * kHeadDim * 2;      // [2 halves of 64 dims][128 rows][128 B]
@@ -392,7 +395,7 @@ struct PtRow {
       }
     }
     if (move) m = top;
-    return m == -INFINITY ? 0.0f : -m * scale2;
+    return m == -INFINITY ? 0.0f : fmaf(-m, scale2, -kPtLazy);
   }
 };
 

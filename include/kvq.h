@@ -412,8 +412,9 @@ kvq_status kvq_paged_decode_codes(const kvq_cache *cache, int32_t code_format, c
  *     out_i = sum_{j <= i} p_j v_j / sum_{j <= i} p_j,
  *     p_j = exp(sm_scale (q_i . k_j - max_j q_i . k_j)),   j in its sequence.
  * fp32 scores and sums; the probabilities are rounded to bf16 for the product
- * with the values and not for the sum.  (The sums run under a reference that may
- * trail the maximum by 2^16, so values of 2^112 / length and more can overflow.)
+ * with the values and not for the sum.  (The sums are binary32: they overflow
+ * where sum_j p_j |v_j| does, at values of 2^128 / length and more.  A probability
+ * below 2^-110 may count as 0.)
  * Tokens a row does not see do not reach it, whatever they hold (infinities and
  * NaN included).
  *   q               device bf16, token t's row for query head h at element

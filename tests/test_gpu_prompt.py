@@ -325,6 +325,35 @@ def test_large_values(hq, H):
     assert_close(out, q, k, v, lens)
 
 
+@pytest.mark.parametrize("hq,H", [(4, 1), (64, 16)])
+def test_values_near_the_top_of_the_range(hq, H):
+    """Values of up to 2^119 under references that trail the rows' maxima by 2^15: the sums stay
+    below sum_j p_j |v_j| with p_j <= 1, 2^119 350 < 2^128."""
+    lens = [350, 40]
+    q, k, v = _inputs(390, hq, H, seed=29)
+    q.fill_(1.0)
+    k.mul_(1 / 64)
+    k[:128] += 15 / (128 * SCALE * float(np.log2(np.e)))     # the first sequence's oldest keys
+    v = (v.double().abs().clamp(0.25, 4.0) * 2.0 ** 117).to(torch.bfloat16)
+    out = kvq.prompt_attention(q, k, v, _cu(lens), 350, SCALE)
+    torch.cuda.synchronize()
+    assert_close(out, q, k, v, lens)
+
+
+@pytest.mark.parametrize("hq,H", [(4, 1), (64, 16)])
+@pytest.mark.parametrize("exponent", [-80, -110])
+def test_small_values(exponent, hq, H):
+    """Values around 2^-80 and 2^-110, under probabilities of 2^-16 for the reference's own score:
+    products of 2^-126 and less are subnormal, each off by at most 2^-149, 350 2^-149 2^16 of the
+    output in all, far below 2^-8 2^-110."""
+    lens = [350, 40]
+    q, k, v = _inputs(390, hq, H, seed=30)
+    v = (v.double() * 2.0 ** exponent).to(torch.bfloat16)
+    out = kvq.prompt_attention(q, k, v, _cu(lens), 350, SCALE)
+    torch.cuda.synchronize()
+    assert_close(out, q, k, v, lens)
+
+
 def test_calls_that_follow_one_another():
     """Calls in a row that read what the last one wrote (rotated in place and stored, attended over,
     the outputs the next queries), of few units and of many, give the bits that they give with a
