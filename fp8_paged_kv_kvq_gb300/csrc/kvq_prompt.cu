@@ -1184,8 +1184,12 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream) {
   // sequence, so long units start late).  152 SMs, not split against split: 1 x
   // 4,800 tokens, 300 units, 58 and 40 us; 1 x 640, 160 units, 13.9 and 11.5; 1 x
   // 900, 232 units, 16.9 and 18.4; 2 x 1,500, 188 units, 23.1 and 19.2; 3 x 1,000,
-  // 192 units, 18.0 and 19.4; 4 x 350, 176 units, 11.0 and 12.6.
-  const int64_t room = 8 * a.num_tokens / kPtKeys / a.num_seqs / a.num_seqs;
+  // 192 units, 18.0 and 19.4; 4 x 350, 176 units, 11.0 and 12.6.  (Padding behind
+  // the sequences is not theirs: 1 x 900 tokens in a buffer of 16,000, counted as
+  // 16,000 and split, took 18.4 us instead of 17.0.)
+  const int64_t tokens =
+      std::min(a.num_tokens, static_cast<int64_t>(a.num_seqs) * a.max_seqlen);
+  const int64_t room = 8 * tokens / kPtKeys / a.num_seqs / a.num_seqs;
   const bool split = prompt_units(a, 1) <= a.sms + std::min<int64_t>(a.sms, room);
   p.TU = (split ? 1 : 2) * p.TQ;
   const int64_t units = prompt_units(a, split ? 1 : 2);

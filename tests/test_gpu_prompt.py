@@ -354,6 +354,18 @@ def test_small_values(exponent, hq, H):
     assert_close(out, q, k, v, lens)
 
 
+@pytest.mark.parametrize("tail", [1, 2000, 15000])
+def test_padding_does_not_change_the_sequences_rows(tail):
+    """A sequence with padding behind it has the bits that it has alone: how its work is cut up
+    goes by the sequences' bounds, not by the buffer's length."""
+    L, hq, H = 900, 32, 8
+    q, k, v = _inputs(L + tail, hq, H, seed=32)
+    alone = kvq.prompt_attention(q[:L], k[:L], v[:L], _cu([L]), L, SCALE)
+    out = kvq.prompt_attention(q, k, v, _cu([L]), L, SCALE)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:L], alone)
+
+
 def test_calls_that_follow_one_another():
     """Calls in a row that read what the last one wrote (rotated in place and stored, attended over,
     the outputs the next queries), of few units and of many, give the bits that they give with a
