@@ -1133,7 +1133,8 @@ prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMa
   __syncthreads();
   if (warp == kPtWarpLoad) {
     tc_fence_after();
-    tmem_dealloc(tmem, kPtTmemCols);
+    // (read again: kept over the roles, the base spills)
+    tmem_dealloc(*tmem_slot, kPtTmemCols);
   }
 }
 
