@@ -51,8 +51,8 @@
 //  * 0 times an infinity is not 0, so zero probabilities do not hide unseen
 //    values.  Of the value tiles that some row of the unit does not see whole
 //    warp 15 clears the rows that none sees, and in the rows that some see every
-//    infinity and NaN; the epilogue adds those a row does see back (rare, one
-//    flag per unit).
+//    infinity and NaN; the epilogue adds those a row does see back, whatever
+//    their probability (rare, one flag per unit).
 //  * What bounds it: the tensor core, and on large calls the card's 1.4 kW
 //    (1.78-1.94 GHz in a loop): 16,381 tokens of 32 heads 1.33 ms, 1,650 TFLOP/s,
 //    86% of what a bf16 library product reaches in a burst; 4 x 8,192 tokens

@@ -416,7 +416,9 @@ kvq_status kvq_paged_decode_codes(const kvq_cache *cache, int32_t code_format, c
  * where sum_j p_j |v_j| does, at values of 2^128 / length and more.  A probability
  * below 2^-110 may count as 0.)
  * Tokens a row does not see do not reach it, whatever they hold (infinities and
- * NaN included).
+ * NaN included).  An infinite value that a row does see makes that element this
+ * infinity, or NaN with one of the other sign; where its probability counts as 0
+ * the element may be NaN (0 times it) for some rows and infinite for others.
  *   q               device bf16, token t's row for query head h at element
  *                   t*q_token_stride + h*head_dim (a view of a fused qkv tensor,
  *                   rotated); k and v the same with num_kv_heads heads

@@ -222,6 +222,32 @@ def test_seen_infinite_values(hq, H):
     assert bool((got[both] == want[both]).all())
 
 
+@pytest.mark.parametrize("L,hq,H", [(400, 8, 2), (400, 64, 16)])
+def test_seen_infinite_values_of_no_probability(L, hq, H):
+    """An infinite value whose probability underflows: a row that sees it has that infinity or NaN
+    (0 times it), never a finite value; every other element is the finite sum."""
+    q, k, v = _inputs(L, hq, H, seed=34)
+    q.fill_(1.0)
+    k.mul_(1 / 64)
+    spots = ((5, 3, float("inf")), (150, 4, float("-inf")), (390, 6, float("inf")))
+    clean = v.clone()
+    for tok, dim, x in spots:
+        k[tok] = -30.0                                  # a score some 490 powers of two below
+        v[tok, :, dim] = x
+        clean[tok, :, dim] = 0.0
+    out = kvq.prompt_attention(q, k, v, _cu([L]), L, SCALE)
+    torch.cuda.synchronize()
+    ref, mag, dot = plain.prompt_attention(q, k, clean, [L], SCALE)
+    seen = torch.zeros(L, hq, 128, dtype=torch.bool)
+    for tok, dim, x in spots:
+        seen[tok:, :, dim] = True
+    got = out.cpu().double()
+    assert bool(((got - ref).abs() <= bound(ref, mag, dot, [L]))[~seen].all())
+    for tok, dim, x in spots:
+        y = got[tok:, :, dim]
+        assert bool((y.isnan() | (y == x)).all())
+
+
 @pytest.mark.parametrize("cu,most", [
     ([0, 50, 40, 100], 64),           # decreasing
     ([0, 30, 60, 101], 64),           # past the buffer
