@@ -89,7 +89,8 @@ typedef enum kvq_status {
 #define KVQ_ERRF_CONTEXT_RANGE 4         /* context length < 0, > max_context_len or
                                             > max_blocks_per_req * block_size          */
 #define KVQ_ERRF_WAIT_TIMEOUT 8          /* a bounded in-kernel wait for an async copy
-                                            gave up; that CTA's outputs are not written */
+                                            gave up; that CTA's outputs are not written
+                                            (kvq_prompt_attention: any rows of out)     */
 #define KVQ_ERRF_POSITION_RANGE 16       /* token position outside the rotation table    */
 #define KVQ_ERRF_SEQUENCE_RANGE 32       /* a packed sequence's bounds decrease, leave the
                                             token buffer or pass max_seqlen               */
@@ -438,7 +439,9 @@ kvq_status kvq_paged_decode_codes(const kvq_cache *cache, int32_t code_format, c
  *   sm_scale        positive and finite, as are the scores times log2(e) sm_scale
  *   out             device bf16, rows like q with their own token stride; must
  *                   not overlap q, k or v
- *   err_flags       device int32, optional
+ *   err_flags       device int32, optional.  With KVQ_ERRF_WAIT_TIMEOUT the whole of
+ *                   out is unspecified, some rows written and others not (a CTA
+ *                   works on units of several blocks): the call has to be repeated
  * Needs no workspace. */
 kvq_status kvq_prompt_attention(const void *q, int64_t q_token_stride,
                                 const void *k, int64_t k_token_stride,
