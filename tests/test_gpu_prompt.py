@@ -110,6 +110,36 @@ def test_mixed_lengths(hq, H):
     _run(lens, hq, H, seed=31, tail=5, first=3)
 
 
+@pytest.mark.parametrize("lens,hq,H", [([700], 4, 1), ([1999], 8, 1), ([700, 300], 64, 16),
+                                       ([2000, 1, 129], 28, 4), ([517], 128, 1)])
+def test_each_key_counts_once(lens, hq, H):
+    """Equal scores (queries of zeros) and values that are 1 in dim d at one key of the sequence and
+    0 elsewhere: row i has 1 / (i + 1) there once it sees the key, and exactly 0 before.  A key
+    dropped or counted twice at a tile's seam, or a row that sees one too many, cannot hide: the
+    probabilities are all the same, so all that is left is the output's rounding (2^-8, and a few
+    2^-23 of the sum and its reciprocal)."""
+    q, k, v = _inputs(sum(lens), hq, H, seed=33)
+    q.zero_()
+    v.zero_()
+    seams = [x + d for x in range(0, max(lens) + 128, 128) for d in (-1, 0, 1)]
+    seams += list(range(31, max(lens), 32))[:30] + [x - 1 for x in lens] + [x - 2 for x in lens]
+    g = workloads.generator(33, sum(lens))
+    dims = torch.randperm(128, generator=g).tolist()
+    a, want = 0, torch.zeros(sum(lens), 128, dtype=torch.float64)
+    for L in lens:
+        keys = sorted({x for x in seams if 0 <= x < L})[:128]
+        for key, d in zip(keys, dims):
+            v[a + key, :, d] = 1.0
+            want[a + key:a + L, d] = 1.0 / torch.arange(key + 1, L + 1, dtype=torch.float64)
+        a += L
+    out = kvq.prompt_attention(q, k, v, _cu(lens), max(lens), SCALE)
+    torch.cuda.synchronize()
+    want = want[:, None, :].expand(-1, hq, -1)
+    got = out.cpu().double()
+    assert torch.equal(got == 0, want == 0)
+    assert bool(((got - want).abs() <= (2.0 ** -8 + 2.0 ** -20) * want).all())
+
+
 def test_longer_prompt():
     _run([2333, 130], 8, 2, seed=4)
 

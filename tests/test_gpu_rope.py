@@ -128,6 +128,38 @@ def test_rotation_in_place(r, interleaved):
     assert np.array_equal(_f32(v), vf)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("T", [700, 1301])
+@pytest.mark.parametrize("r,interleaved", [(128, False), (64, False), (32, False), (96, False),
+                                           (16, False), (128, True), (80, True)])
+def test_calls_of_many_tokens(r, interleaved, T, in_place):
+    """More tokens than SMs have warps for their rows: a token's rows one after the other on two
+    warps (700 tokens) or one, the next fetched ahead -- in place too, where a row fetched ahead
+    must be one that nobody has rotated."""
+    hq, H = 32, 8
+    _, q, k, v = _inputs(T, hq, H, seed=T + r)
+    qf, kf, vf = _f32(q), _f32(k), _f32(v)
+    table = plain.rope_table(2048, r)
+    g = workloads.generator(T, r)
+    pos = torch.randint(0, 2048, (T,), generator=g)
+    slots = torch.randperm(T + 5, generator=g)[:T]
+    slots[T // 2] = -1
+    cache = _cache(T + 5, H)
+    before = _planes(cache)
+    outs = dict(q_out=q, k_out=k) if in_place else \
+        dict(q_out=torch.full((T, hq, 128), 7.0, dtype=torch.bfloat16, device="cuda"),
+             k_out=torch.full((T, H, 128), 7.0, dtype=torch.bfloat16, device="cuda"))
+    kvq.rope_quantize_scatter(cache, q, k, v, pos.cuda(), table.cuda(), slots.cuda(),
+                              layout=int(interleaved), **outs)
+    torch.cuda.synchronize()
+    _check(cache, before, kf, vf, slots.numpy(), table.numpy(), pos.numpy(), interleaved,
+           outs["k_out"], qf, outs["q_out"])
+    for name, x in (("q_out", qf), ("k_out", kf)):       # the skipped token's rows
+        want = x[T // 2] if in_place else np.full_like(x[T // 2], 7.0)
+        assert np.array_equal(_f32(outs[name])[T // 2], want)
+    assert np.array_equal(_f32(v), vf)
+
+
 def test_rotation_zero_is_the_plain_store():
     """Position 0 (cosines 1, sines 0): codes and scales are kvq_quantize_scatter's of the same
     rows -- large and tiny rows, all-zero rows, negative zeros and rows of subnormals among them."""
