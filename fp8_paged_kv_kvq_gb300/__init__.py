@@ -166,10 +166,24 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _current_stream_handle(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _torch_call(name: str, public):
+    """torch's own call ``name`` without the checks and objects that ``public`` puts around
+    it (1 us each, of 11 for a rotary store), or ``public`` where torch has none."""
+    return getattr(torch._C, name, public)
+
+
+_get_device = _torch_call("_cuda_getDevice", torch.cuda.current_device)
+_get_raw_stream = _torch_call("_cuda_getCurrentRawStream", _current_stream_handle)
+
+
 def _raw_stream(stream, device: int) -> int:
     """The cudaStream_t of ``stream``, or of ``device``'s current one."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _get_raw_stream(device)
     if stream.device_index != device:
         raise ValueError(f"stream of device {stream.device_index}, not of the current one ({device})")
     return stream.cuda_stream
@@ -289,7 +303,7 @@ def _one_device(tensors) -> int:
     """The index of the current CUDA device, on which every tensor (None: not
     given) has to be: a pointer of the host or of another device would fault in
     the kernel."""
-    device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
+    device = _get_device() if torch.cuda.is_initialized() else None
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError(f"every tensor must be on the current CUDA device ({device}), "

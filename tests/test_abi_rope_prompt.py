@@ -1,6 +1,8 @@
 """Refusals of kvq_rope_quantize_scatter and kvq_prompt_attention: every call
 here is answered on the host, before anything could be launched."""
 import ctypes
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -125,3 +127,29 @@ def test_bindings_reject_bad_tensors():
             kvq.rope_quantize_scatter(cache, **{**good, **bad})
     with pytest.raises(ValueError, match="current CUDA device"):
         kvq.rope_quantize_scatter(cache, **good)
+
+
+def test_binding_without_private_torch_calls():
+    """The current stream and device come from public calls where torch lacks its private ones:
+    the package is imported by a torch without them, and the binding asks those."""
+    code = """
+import types, torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+torch.cuda.is_initialized = lambda: True
+torch.cuda.current_device = lambda: -1            # (a host tensor's)
+torch.cuda.current_stream = lambda d: types.SimpleNamespace(cuda_stream=0x1230 + d)
+import fp8_paged_kv_kvq_gb300 as kvq
+assert kvq._one_device([torch.zeros(1), None]) == -1
+assert kvq._raw_stream(None, 4) == 0x1234
+side = types.SimpleNamespace(device_index=4, cuda_stream=0x4000)
+assert kvq._raw_stream(side, 4) == 0x4000
+try:
+    kvq._raw_stream(side, 3)
+except ValueError:
+    print("refused")
+"""
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                         cwd=kbuild.ROOT)
+    assert res.returncode == 0 and "refused" in res.stdout, res.stderr
