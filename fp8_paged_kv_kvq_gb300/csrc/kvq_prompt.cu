@@ -54,14 +54,17 @@
 //    infinity and NaN; the epilogue adds those a row does see back, whatever
 //    their probability (rare, one flag per unit).
 //  * What bounds it: the tensor core, and on large calls the card's 1.4 kW
-//    (1.78-1.94 GHz in a loop): 16,381 tokens of 32 heads 1.33 ms, 1,650 TFLOP/s,
-//    86% of what a bf16 library product reaches in a burst; 4 x 8,192 tokens
-//    1.30-1.37 ms.  A step of two row tiles over a key tile takes about 2,700
-//    cycles: MMAs of 2,048, and at each of the two hand-overs some 300 of waiting
-//    for the turn and for the second half of P.  A change of units takes some 5,000
-//    more (queries from memory, a masked softmax, an epilogue of 2,500 a tile).
-//    Short prompts are bound by latency: 2 us to the first MMA, 1.5 us a step, 1 us
-//    for the rows.
+//    (1.78-1.94 GHz in a loop), so that a few calls are faster than a loop:
+//    16,381 tokens of 32 heads 1.32-1.36 ms and 1.36-1.40 (1,570-1,670 TFLOP/s, 82
+//    to 87% of what a bf16 library product reaches in a burst); 4 x 8,192 tokens
+//    1.33-1.38 and 1.40-1.44; the ragged batch of 64 heads 305 and 334 us (figures
+//    of it here are of a few calls).  A step of two row tiles over a key tile takes
+//    about 2,700 cycles: MMAs of 2,048, and at each of the two hand-overs some 300
+//    of waiting for the turn and for the second half of P.  A change of units takes
+//    some 5,000 more (queries from memory, a masked softmax, an epilogue of 2,500 a tile).
+//    Short prompts are bound by latency, 2 us to the first MMA, 1.5 us a step, 1 us
+//    for the rows (64 tokens 6.4 us in a graph; called from the binding, by its
+//    8.4).
 //  * Code that runs once a unit is kept in one copy (one search for units, one
 //    epilogue for both chains): the roles share an instruction cache, and with
 //    two copies 8 x 1,024 tokens take 86 us instead of 83, the short ragged batch

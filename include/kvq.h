@@ -433,7 +433,9 @@ kvq_status kvq_paged_decode_codes(const kvq_cache *cache, int32_t code_format, c
  *                   skipped and sets KVQ_ERRF_SEQUENCE_RANGE (the others'
  *                   outputs are then unspecified, but every access stays in
  *                   bounds)
- *   max_seqlen      host bound on every sequence's length
+ *   max_seqlen      host bound on every sequence's length; the launch is sized by it,
+ *                   num_seqs and num_tokens, so bounds far above the lengths (one
+ *                   graph for all sizes) cost time, never results
  *   num_q_heads     a multiple of num_kv_heads, at most 128 per KV head
  *   head_dim        128
  *   sm_scale        positive and finite, as are the scores times log2(e) sm_scale
