@@ -577,3 +577,30 @@ def test_workspace_needs_no_initialisation(R, Hq, H, bs, lens):
         graph.replay()
         torch.cuda.synchronize()
         assert_attention_close(out, ref, f"graph replay {rep}")
+
+
+@pytest.mark.parametrize("R,Hq,H,bs", [
+    (1, 32, 8, 16), (1, 8, 4, 256), (1, 32, 8, 4), (2, 32, 8, 16), (3, 12, 4, 32), (4, 64, 8, 64),
+    (4, 128, 8, 64), (16, 32, 8, 4),
+])
+@pytest.mark.parametrize("partition_tokens", [0, 128])
+def test_slots_that_no_row_sees_may_hold_nan(R, Hq, H, bs, partition_tokens):
+    """The stores keep a NaN (scale and codes) as NaN, so a page given back by one request may hold
+    some when the next request uses part of it: contexts that do not reach them give the same bits."""
+    w = workloads.scaled(workloads.WORKLOADS["verify"], num_requests=4, rows_per_request=R,
+                         num_q_heads=Hq, num_kv_heads=H, block_size=bs)
+    lens = np.array([R, 333, 520, 1000 + R], dtype=np.int32)
+    built = build_paged(w, lens)
+    q = _queries(w, 4, R, 2)
+    clean = gpu_decode(built, q, R, w.sm_scale, partition_tokens=partition_tokens)
+    seen = np.concatenate([workloads.token_slots(built["bt"], r, int(L), bs)
+                           for r, L in enumerate(lens)])
+    unseen = torch.ones(built["S"], dtype=torch.bool, device="cuda")
+    unseen[torch.from_numpy(seen).cuda()] = False
+    c = built["cache"]
+    c.k_codes[unseen], c.v_codes[unseen] = 0x7F, 0xFF
+    c.k_scales[unseen], c.v_scales[unseen] = float("nan"), float("nan")
+    out = gpu_decode(built, q, R, w.sm_scale, partition_tokens=partition_tokens)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(out).all())
+    assert torch.equal(out, clean)
