@@ -63,8 +63,8 @@
 //    of waiting for the turn and for the second half of P.  A change of units takes
 //    some 5,000 more (queries from memory, a masked softmax, an epilogue of 2,500 a tile).
 //    Short prompts are bound by latency, 2 us to the first MMA, 1.5 us a step, 1 us
-//    for the rows (64 tokens 6.4 us in a graph; called from the binding, by its
-//    8.4).
+//    for the rows (64 tokens take 6.4 us in a graph; calls one after the other from
+//    Python wait for the binding, 8.4 us each).
 //  * Code that runs once a unit is kept in one copy (one search for units, one
 //    epilogue for both chains): the roles share an instruction cache, and with
 //    two copies 8 x 1,024 tokens take 86 us instead of 83, the short ragged batch

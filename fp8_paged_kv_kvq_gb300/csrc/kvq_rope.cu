@@ -16,9 +16,10 @@
 // What bounds it: HBM from some 2,000 tokens on -- 32 + 8 + 8 heads, k_out
 // written: 16,384 tokens 71 us, 5.75 TB/s, 86% of a copy's rate; 65,536 tokens
 // 272 us, 91%.  Below, a launch and the chain slot, position, angles, rows: one
-// token 2.0 us, 1,021 tokens of 32 rows 3.8 us.  16,384 tokens take
-// 65 us in halves of 32 dims, 70 in neighbours; other halves, which read a row's partner pieces and
-// angles again, 70 us at 16 and 32 dims and 77 at 96 (80% of a copy's rate).
+// token 2.0 us, 1,021 tokens of 32 rows 3.8 us.  16,384 tokens take 65 us in halves
+// of 32 dims, 70 in neighbours; other halves, which read a row's partner pieces
+// and angles again, 70 us where 16 or 32 dims turn and 77 where 96 do (80% of a
+// copy's rate).
 #include <cuda_runtime.h>
 
 #include "kvq_device.cuh"
