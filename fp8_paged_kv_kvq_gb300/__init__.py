@@ -35,6 +35,9 @@ __all__ = [
     "paged_decode_codes_workspace_size",
     "ERRF_POSITION_RANGE", "ERRF_SEQUENCE_RANGE", "ROPE_HALVES", "ROPE_INTERLEAVED",
     "rope_quantize_scatter", "prompt_attention",
+    "paged_decode_window", "paged_decode_window_workspace_size", "paged_decode_tree",
+    "paged_decode_tree_workspace_size", "tree_commit", "PagePool", "pages_alloc", "pages_free",
+    "pages_fork", "ERRF_PATH_RANGE", "ERRF_NO_PAGES", "ERRF_PAGE_STATE",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -52,6 +55,9 @@ ERRF_BLOCK_RANGE = 2
 ERRF_CONTEXT_RANGE = 4
 ERRF_POSITION_RANGE = 16
 ERRF_SEQUENCE_RANGE = 32
+ERRF_PATH_RANGE = 64
+ERRF_NO_PAGES = 128
+ERRF_PAGE_STATE = 256
 
 ROPE_HALVES = 0
 ROPE_INTERLEAVED = 1
@@ -72,6 +78,12 @@ class _CacheStruct(ctypes.Structure):
                 ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
                 ("num_slots", ctypes.c_int64), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32)]
+
+
+class _PagePoolStruct(ctypes.Structure):
+    _fields_ = [("ref_counts", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("state", ctypes.c_void_p), ("marks", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32)]
 
 
 class _IndexCacheStruct(ctypes.Structure):
@@ -101,6 +113,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib = ctypes.CDLL(p)
         P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         CP = ctypes.POINTER(_CacheStruct)
+        PP = ctypes.POINTER(_PagePoolStruct)
         sigs = {
             "kvq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "kvq_abi_version": (i32, []),
@@ -126,6 +139,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "kvq_paged_decode_append": (ctypes.c_int, [CP, P, i64, P, i64, P, i32, i32, i32, P,
                                                        i32, P, i32, ctypes.c_float, i32, P, P,
                                                        sz, P, P]),
+            "kvq_paged_decode_window_workspace_size": (sz, [i32, i32, i32, i32, i32, i32, i32, i32,
+                                                            i32]),
+            "kvq_paged_decode_window": (ctypes.c_int, [CP, P, i32, i32, i32, P, i32, P, i32, i32,
+                                                       i32, ctypes.c_float, P, P, sz, P, P]),
+            "kvq_paged_decode_tree_workspace_size": (sz, [i32, i32, i32, i32, i32, i32, i32]),
+            "kvq_paged_decode_tree": (ctypes.c_int, [CP, P, P, i32, i32, i32, P, i32, P, i32,
+                                                     ctypes.c_float, P, P, sz, P, P]),
+            "kvq_tree_commit": (ctypes.c_int, [CP, P, P, i32, i32, P, i32, P, P, P, P]),
+            "kvq_pages_alloc": (ctypes.c_int, [PP, P, i32, i32, P, P, P, P]),
+            "kvq_pages_free": (ctypes.c_int, [PP, P, i32, i32, P, P, P, P]),
+            "kvq_pages_fork": (ctypes.c_int, [CP, PP, P, i32, P, i32, i32, P, P, P, P, P]),
             "kvq_dequant_rows": (ctypes.c_int, [CP, P, i64, i32, P, P, P, P]),
             "kvq_quantize_scatter_unscaled": (ctypes.c_int, [CP, i32, P, i64, P, i64, i64, P,
                                                              P, P]),
@@ -279,8 +303,8 @@ def quantize_scatter(cache: Cache, k: torch.Tensor, v: torch.Tensor, slot_ids: t
            "kvq_quantize_scatter")
 
 
-# The two operators below are called once per layer and step, on few tokens too,
-# so their checks keep to a few tensor attribute reads each.
+# The operators from here to pages_fork are called once per layer or step, on few
+# tokens too, so their checks keep to a few tensor attribute reads each.
 
 def _heads(x: torch.Tensor, name: str, T: int, heads: int, D: int) -> int:
     """Token stride (elements) of a bf16 view [T, heads, D] whose rows are
@@ -406,6 +430,248 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     if status:
         raise KvqError(status, "kvq_prompt_attention")
     return out
+
+
+def _masked_args(cache: Cache, q, block_tables, context_lens, R: int):
+    """Requests, query heads, KV heads and table width of a windowed or tree call."""
+    if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+        raise ValueError("q must be contiguous bfloat16 [num_requests * R, num_q_heads, head_dim]")
+    if block_tables.dtype is not torch.int32 or block_tables.dim() != 2 or \
+            not block_tables.is_contiguous():
+        raise ValueError("block_tables must be contiguous int32 [num_requests, max_blocks]")
+    n, width = block_tables.shape
+    rows, hq, d = q.shape
+    _, h, cd = cache.k_codes.shape
+    if R < 1 or rows != n * R or d != cd:
+        raise ValueError(f"q must have num_requests * R = {n} * {R} rows of {cd} dims")
+    _flat(context_lens, "context_lens", torch.int32, n)
+    return n, hq, h, width
+
+
+def _masked_out(q, out, workspace, size: int, stream):
+    """The output and the workspace (address and bytes) of a call; both are
+    allocated on the stream that writes them when not given."""
+    if out is None:
+        out = _rows_like(q, stream)
+    elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous bfloat16 of q's shape")
+    if workspace is None:
+        if stream is None:
+            workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return out, workspace
+
+
+def paged_decode_window_workspace_size(num_requests: int, rows_per_request: int, num_q_heads: int,
+                                       num_kv_heads: int, head_dim: int, block_size: int,
+                                       max_context_len: int, window: int,
+                                       num_sinks: int = 0) -> int:
+    return load().kvq_paged_decode_window_workspace_size(
+        num_requests, rows_per_request, num_q_heads, num_kv_heads, head_dim, block_size,
+        max_context_len, window, num_sinks)
+
+
+def paged_decode_window(cache: Cache, q: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, max_context_len: int, window: int,
+                        sm_scale: float, num_sinks: int = 0, rows_per_request: int = 1,
+                        out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        err_flags: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvq_paged_decode_window: paged_decode in which each row sees only the last
+    ``window`` tokens up to its own and the first ``num_sinks``; block-table
+    entries of tokens that no row of a request sees may hold anything.  Returns
+    ``out`` (bf16, shape of q); ``out`` and ``workspace`` (uint8, >=
+    paged_decode_window_workspace_size) are allocated here when not given."""
+    R = rows_per_request
+    n, hq, h, width = _masked_args(cache, q, block_tables, context_lens, R)
+    lib = load()
+    size = 0 if workspace is not None else lib.kvq_paged_decode_window_workspace_size(
+        n, R, hq, h, 128, cache.block_size, max_context_len, window, num_sinks)
+    out, workspace = _masked_out(q, out, workspace, size, stream)
+    _flags(err_flags)
+    device = _one_device((q, block_tables, context_lens, out, workspace, err_flags,
+                          cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales))
+    st = cache.struct()
+    status = lib.kvq_paged_decode_window(
+        ctypes.byref(st), q.data_ptr(), n, R, hq, block_tables.data_ptr(), width,
+        context_lens.data_ptr(), max_context_len, window, num_sinks, sm_scale, out.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _addr(err_flags), _raw_stream(stream, device))
+    if status:
+        raise KvqError(status, "kvq_paged_decode_window")
+    return out
+
+
+def paged_decode_tree_workspace_size(num_requests: int, rows_per_request: int, num_q_heads: int,
+                                     num_kv_heads: int, head_dim: int, block_size: int,
+                                     max_context_len: int) -> int:
+    return load().kvq_paged_decode_tree_workspace_size(
+        num_requests, rows_per_request, num_q_heads, num_kv_heads, head_dim, block_size,
+        max_context_len)
+
+
+def paged_decode_tree(cache: Cache, q: torch.Tensor, tree_mask: torch.Tensor,
+                      block_tables: torch.Tensor, context_lens: torch.Tensor,
+                      max_context_len: int, sm_scale: float, rows_per_request: int,
+                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      err_flags: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvq_paged_decode_tree: attention of ``rows_per_request`` drafted tokens, the
+    last cached ones of each request, over the context before them and the drafted
+    tokens whose bit ``tree_mask`` (int32 [num_requests, R, ceil(R / 32)], bit
+    b % 32 of word b / 32) sets for the row.  Returns ``out`` (bf16, shape of q);
+    ``out`` and ``workspace`` as for paged_decode_window."""
+    R = rows_per_request
+    n, hq, h, width = _masked_args(cache, q, block_tables, context_lens, R)
+    _flat(tree_mask, "tree_mask", torch.int32, n * R * ((R + 31) // 32))
+    lib = load()
+    size = 0 if workspace is not None else lib.kvq_paged_decode_tree_workspace_size(
+        n, R, hq, h, 128, cache.block_size, max_context_len)
+    out, workspace = _masked_out(q, out, workspace, size, stream)
+    _flags(err_flags)
+    device = _one_device((q, tree_mask, block_tables, context_lens, out, workspace, err_flags,
+                          cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales))
+    st = cache.struct()
+    status = lib.kvq_paged_decode_tree(
+        ctypes.byref(st), q.data_ptr(), tree_mask.data_ptr(), n, R, hq, block_tables.data_ptr(),
+        width, context_lens.data_ptr(), max_context_len, sm_scale, out.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _addr(err_flags), _raw_stream(stream, device))
+    if status:
+        raise KvqError(status, "kvq_paged_decode_tree")
+    return out
+
+
+def _table(x: torch.Tensor, name: str):
+    if x.dtype is not torch.int32 or x.dim() != 2 or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 [requests, max_blocks]")
+    return x.shape
+
+
+def tree_commit(cache: Cache, accepted: torch.Tensor, accepted_lens: torch.Tensor,
+                block_tables: torch.Tensor, context_lens: torch.Tensor,
+                new_lens: torch.Tensor | None = None, err_flags: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """kvq_tree_commit: the cache rows of the accepted drafted tokens (``accepted``
+    int32 [N, R], ``accepted_lens`` int32 [N]) moved together behind each request's
+    context.  Returns ``new_lens`` (int32 [N]: the context and the accepted tokens;
+    may be ``context_lens`` itself; allocated here when not given)."""
+    n, R = _table(accepted, "accepted")
+    tn, width = _table(block_tables, "block_tables")
+    if tn != n:
+        raise ValueError("accepted and block_tables must have a row per request")
+    _flat(accepted_lens, "accepted_lens", torch.int32, n)
+    _flat(context_lens, "context_lens", torch.int32, n)
+    if new_lens is None:
+        new_lens = _rows_like(context_lens, stream)
+    _flat(new_lens, "new_lens", torch.int32, n)
+    _flags(err_flags)
+    device = _one_device((accepted, accepted_lens, block_tables, context_lens, new_lens, err_flags,
+                          cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales))
+    st = cache.struct()
+    status = load().kvq_tree_commit(
+        ctypes.byref(st), accepted.data_ptr(), accepted_lens.data_ptr(), n, R,
+        block_tables.data_ptr(), width, context_lens.data_ptr(), new_lens.data_ptr(),
+        _addr(err_flags), _raw_stream(stream, device))
+    if status:
+        raise KvqError(status, "kvq_tree_commit")
+    return new_lens
+
+
+@dataclass
+class PagePool:
+    """Device tensors of a pool of pages (kvq_page_pool); int32 all.
+
+    ref_counts: [num_pages], block tables that hold each page
+    free_pages: [num_pages], a stack whose first state[0] entries are the free pages
+    state: [4], the free pages' number first
+    marks: [ceil(num_pages / 32)], zero between calls"""
+    ref_counts: torch.Tensor
+    free_pages: torch.Tensor
+    state: torch.Tensor
+    marks: torch.Tensor
+
+    @staticmethod
+    def empty(num_pages: int, device="cuda") -> "PagePool":
+        """A pool whose pages are all free; the top of its stack is the last page."""
+        def zeros(n):
+            return torch.zeros(n, dtype=torch.int32, device=device)
+        state = zeros(4)
+        state[0] = num_pages
+        return PagePool(zeros(num_pages), torch.arange(num_pages, dtype=torch.int32, device=device),
+                        state, zeros((num_pages + 31) // 32))
+
+    @property
+    def num_pages(self) -> int:
+        return self.ref_counts.shape[0]
+
+    def tensors(self):
+        return self.ref_counts, self.free_pages, self.state, self.marks
+
+    def struct(self) -> _PagePoolStruct:
+        refs, free, state, marks = self.tensors()
+        n = refs.numel()
+        _flat(refs, "ref_counts", torch.int32, n)
+        _flat(free, "free_pages", torch.int32, n)
+        _flat(state, "state", torch.int32, 4)
+        _flat(marks, "marks", torch.int32, (n + 31) // 32)
+        return _PagePoolStruct(refs.data_ptr(), free.data_ptr(), state.data_ptr(),
+                               marks.data_ptr(), n)
+
+
+def _page_ranges(name: str, pool: PagePool, block_tables, begin, end, err_flags, stream) -> None:
+    n, width = _table(block_tables, "block_tables")
+    _flat(begin, "begin", torch.int32, n)
+    _flat(end, "end", torch.int32, n)
+    _flags(err_flags)
+    st = pool.struct()
+    device = _one_device((*pool.tensors(), block_tables, begin, end, err_flags))
+    status = getattr(load(), name)(ctypes.byref(st), block_tables.data_ptr(), n, width,
+                                   begin.data_ptr(), end.data_ptr(), _addr(err_flags),
+                                   _raw_stream(stream, device))
+    if status:
+        raise KvqError(status, name)
+
+
+def pages_alloc(pool: PagePool, block_tables: torch.Tensor, begin: torch.Tensor,
+                end: torch.Tensor, err_flags: torch.Tensor | None = None, stream=None) -> None:
+    """kvq_pages_alloc: a page of the pool for each of the entries [begin[r], end[r])
+    (int32 [N]) of request r's block table."""
+    _page_ranges("kvq_pages_alloc", pool, block_tables, begin, end, err_flags, stream)
+
+
+def pages_free(pool: PagePool, block_tables: torch.Tensor, begin: torch.Tensor,
+               end: torch.Tensor, err_flags: torch.Tensor | None = None, stream=None) -> None:
+    """kvq_pages_free: one reference given back for each of the entries [begin[r],
+    end[r]) of request r's block table (entries < 0 are skipped)."""
+    _page_ranges("kvq_pages_free", pool, block_tables, begin, end, err_flags, stream)
+
+
+def pages_fork(cache: Cache, pool: PagePool, parents: torch.Tensor, block_tables: torch.Tensor,
+               context_lens: torch.Tensor, child_tables: torch.Tensor, child_lens: torch.Tensor,
+               err_flags: torch.Tensor | None = None, stream=None) -> None:
+    """kvq_pages_fork: child i continues the sequence of request ``parents[i]`` (int32
+    [M]): its row of ``child_tables`` [M, max_blocks] shares the parent's full pages
+    and gets a copy of a partly filled last one, ``child_lens[i]`` its length."""
+    num_parents, width = _table(block_tables, "block_tables")
+    m, child_width = _table(child_tables, "child_tables")
+    if child_width != width:
+        raise ValueError("child_tables must be as wide as block_tables")
+    _flat(parents, "parents", torch.int32, m)
+    _flat(context_lens, "context_lens", torch.int32, num_parents)
+    _flat(child_lens, "child_lens", torch.int32, m)
+    _flags(err_flags)
+    ps = pool.struct()
+    device = _one_device((*pool.tensors(), parents, block_tables, context_lens, child_tables,
+                          child_lens, err_flags, cache.k_codes, cache.v_codes, cache.k_scales,
+                          cache.v_scales))
+    st = cache.struct()
+    status = load().kvq_pages_fork(
+        ctypes.byref(st), ctypes.byref(ps), parents.data_ptr(), m, block_tables.data_ptr(),
+        num_parents, width, context_lens.data_ptr(), child_tables.data_ptr(),
+        child_lens.data_ptr(), _addr(err_flags), _raw_stream(stream, device))
+    if status:
+        raise KvqError(status, "kvq_pages_fork")
 
 
 def paged_decode_partition_tokens(num_requests: int, rows_per_request: int, num_q_heads: int,

@@ -592,6 +592,229 @@ kvq_status kvq_prompt_attention(const void *q, int64_t q_token_stride, const voi
   return from_cuda(kvq::launch_prompt_attention(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace {
+
+// The checks that the windowed and the tree attention share, and the launch.
+kvq_status masked_shape(const kvq_cache *cache, int32_t num_requests, int32_t rows_per_request,
+                        int32_t num_q_heads, int32_t max_blocks_per_req, int32_t max_context_len,
+                        int32_t window, int32_t num_sinks) {
+  const kvq_status st = check_cache(cache, true);
+  if (st != KVQ_OK) return st;
+  if (num_requests < 0 || rows_per_request < 1 || num_q_heads < 1 || max_blocks_per_req < 0 ||
+      max_context_len < 0 || window < 1 || num_sinks < 0 ||
+      num_q_heads % cache->num_kv_heads != 0)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  const int64_t M = static_cast<int64_t>(rows_per_request) * (num_q_heads / cache->num_kv_heads);
+  if (M > kvq::kRowsMaxRows || num_requests > 65535 || cache->block_size < 16 ||
+      cache->num_slots >= (int64_t(1) << 31))
+    return KVQ_ERR_UNSUPPORTED;
+  // 128-token pieces of one KV head are numbered in 31 bits
+  const int64_t tiles = (M + 127) / 128, chunks = static_cast<int64_t>(max_context_len) / 128 + 8;
+  if (static_cast<double>(num_requests) * cache->num_kv_heads * tiles * chunks >= 2147483647.0)
+    return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+kvq_status masked_call(const kvq_cache *cache, kvq::MaskedArgs a, size_t workspace_bytes,
+                       kvq_stream_t stream) {
+  if (!std::isfinite(a.sm_scale)) return KVQ_ERR_INVALID_ARGUMENT;
+  if (a.num_requests == 0) return KVQ_OK;
+  if (a.q == nullptr || a.out == nullptr || a.block_tables == nullptr || a.context_lens == nullptr)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.block_tables, 4) ||
+      !aligned(a.context_lens, 4) || !aligned(a.tree_mask, 4) || !aligned(a.workspace, 16) ||
+      !aligned(a.err_flags, 4))
+    return KVQ_ERR_MISALIGNED;
+  const size_t need = kvq::attn_masked_workspace_bytes(a, cache->num_kv_heads);
+  if (need > 0 && (a.workspace == nullptr || workspace_bytes < need))
+    return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  return from_cuda(kvq::launch_attn_masked(*cache, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t masked_workspace(int32_t num_requests, int32_t rows_per_request, int32_t num_q_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        int32_t max_context_len, int32_t window, int32_t num_sinks) {
+  kvq_cache c{};
+  c.num_kv_heads = num_kv_heads;
+  c.head_dim = head_dim;
+  c.block_size = block_size;
+  if (masked_shape(&c, num_requests, rows_per_request, num_q_heads, 1, max_context_len, window,
+                   num_sinks) != KVQ_OK)
+    return 0;
+  kvq::MaskedArgs a{};
+  a.num_requests = num_requests;
+  a.rows_per_request = rows_per_request;
+  a.num_q_heads = num_q_heads;
+  a.sms = current_sm_count();
+  return kvq::attn_masked_workspace_bytes(a, num_kv_heads);
+}
+
+kvq_status check_pool(const kvq_page_pool *pool) {
+  if (pool == nullptr || pool->num_pages < 0) return KVQ_ERR_INVALID_ARGUMENT;
+  if (pool->ref_counts == nullptr || pool->free_pages == nullptr || pool->state == nullptr ||
+      pool->marks == nullptr)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (!aligned(pool->ref_counts, 4) || !aligned(pool->free_pages, 4) || !aligned(pool->state, 4) ||
+      !aligned(pool->marks, 4))
+    return KVQ_ERR_MISALIGNED;
+  return KVQ_OK;
+}
+
+constexpr int32_t kMaxTableWidth = 1 << 20;   // pages of a request: 1,024 of them add up in 31 bits
+constexpr int32_t kMaxChildren = 4096;        // every block of a fork counts the children before its own
+
+kvq_status check_page_ranges(const kvq_page_pool *pool, const int32_t *block_tables,
+                             int32_t num_requests, int32_t max_blocks_per_req,
+                             const int32_t *begin, const int32_t *end, const int32_t *err_flags) {
+  const kvq_status st = check_pool(pool);
+  if (st != KVQ_OK) return st;
+  if (num_requests < 0 || max_blocks_per_req < 0) return KVQ_ERR_INVALID_ARGUMENT;
+  if (max_blocks_per_req > kMaxTableWidth) return KVQ_ERR_UNSUPPORTED;
+  if (num_requests == 0) return KVQ_OK;
+  if (block_tables == nullptr || begin == nullptr || end == nullptr)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (!aligned(block_tables, 4) || !aligned(begin, 4) || !aligned(end, 4) ||
+      !aligned(err_flags, 4))
+    return KVQ_ERR_MISALIGNED;
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kvq_paged_decode_window_workspace_size(int32_t num_requests, int32_t rows_per_request,
+                                              int32_t num_q_heads, int32_t num_kv_heads,
+                                              int32_t head_dim, int32_t block_size,
+                                              int32_t max_context_len, int32_t window,
+                                              int32_t num_sinks) {
+  return masked_workspace(num_requests, rows_per_request, num_q_heads, num_kv_heads, head_dim,
+                          block_size, max_context_len, window, num_sinks);
+}
+
+kvq_status kvq_paged_decode_window(const kvq_cache *cache, const void *q, int32_t num_requests,
+                                   int32_t rows_per_request, int32_t num_q_heads,
+                                   const int32_t *block_tables, int32_t max_blocks_per_req,
+                                   const int32_t *context_lens, int32_t max_context_len,
+                                   int32_t window, int32_t num_sinks, float sm_scale, void *out,
+                                   void *workspace, size_t workspace_bytes, int32_t *err_flags,
+                                   kvq_stream_t stream) {
+  const kvq_status st = masked_shape(cache, num_requests, rows_per_request, num_q_heads,
+                                     max_blocks_per_req, max_context_len, window, num_sinks);
+  if (st != KVQ_OK) return st;
+  const kvq::MaskedArgs a{q, num_requests, rows_per_request, num_q_heads, block_tables,
+                          max_blocks_per_req, log2_exact(cache->block_size), context_lens,
+                          max_context_len, window, num_sinks, nullptr, sm_scale, out, workspace,
+                          err_flags, current_sm_count()};
+  return masked_call(cache, a, workspace_bytes, stream);
+}
+
+size_t kvq_paged_decode_tree_workspace_size(int32_t num_requests, int32_t rows_per_request,
+                                            int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t block_size,
+                                            int32_t max_context_len) {
+  if (rows_per_request > kvq::kTreeMaxNodes) return 0;
+  return masked_workspace(num_requests, rows_per_request, num_q_heads, num_kv_heads, head_dim,
+                          block_size, max_context_len, 1, 0);
+}
+
+kvq_status kvq_paged_decode_tree(const kvq_cache *cache, const void *q, const int32_t *tree_mask,
+                                 int32_t num_requests, int32_t rows_per_request,
+                                 int32_t num_q_heads, const int32_t *block_tables,
+                                 int32_t max_blocks_per_req, const int32_t *context_lens,
+                                 int32_t max_context_len, float sm_scale, void *out,
+                                 void *workspace, size_t workspace_bytes, int32_t *err_flags,
+                                 kvq_stream_t stream) {
+  const kvq_status st = masked_shape(cache, num_requests, rows_per_request, num_q_heads,
+                                     max_blocks_per_req, max_context_len, 1, 0);
+  if (st != KVQ_OK) return st;
+  if (rows_per_request > kvq::kTreeMaxNodes) return KVQ_ERR_UNSUPPORTED;
+  if (num_requests > 0 && tree_mask == nullptr) return KVQ_ERR_INVALID_ARGUMENT;
+  const kvq::MaskedArgs a{q, num_requests, rows_per_request, num_q_heads, block_tables,
+                          max_blocks_per_req, log2_exact(cache->block_size), context_lens,
+                          max_context_len, 0, 0, tree_mask, sm_scale, out, workspace, err_flags,
+                          current_sm_count()};
+  return masked_call(cache, a, workspace_bytes, stream);
+}
+
+kvq_status kvq_tree_commit(const kvq_cache *cache, const int32_t *accepted,
+                           const int32_t *accepted_lens, int32_t num_requests,
+                           int32_t rows_per_request, const int32_t *block_tables,
+                           int32_t max_blocks_per_req, const int32_t *context_lens,
+                           int32_t *new_lens, int32_t *err_flags, kvq_stream_t stream) {
+  const kvq_status st = check_cache(cache, true);
+  if (st != KVQ_OK) return st;
+  if (num_requests < 0 || rows_per_request < 1 || max_blocks_per_req < 0)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (rows_per_request > kvq::kTreeMaxNodes || cache->num_kv_heads > (1 << 20))
+    return KVQ_ERR_UNSUPPORTED;
+  if (num_requests == 0) return KVQ_OK;
+  if (accepted == nullptr || accepted_lens == nullptr || block_tables == nullptr ||
+      context_lens == nullptr || new_lens == nullptr)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (!aligned(accepted, 4) || !aligned(accepted_lens, 4) || !aligned(block_tables, 4) ||
+      !aligned(context_lens, 4) || !aligned(new_lens, 4) || !aligned(err_flags, 4))
+    return KVQ_ERR_MISALIGNED;
+  return from_cuda(kvq::launch_tree_commit(*cache, accepted, accepted_lens, num_requests,
+                                           rows_per_request, block_tables, max_blocks_per_req,
+                                           log2_exact(cache->block_size), context_lens, new_lens,
+                                           err_flags, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_pages_alloc(const kvq_page_pool *pool, int32_t *block_tables, int32_t num_requests,
+                           int32_t max_blocks_per_req, const int32_t *begin, const int32_t *end,
+                           int32_t *err_flags, kvq_stream_t stream) {
+  const kvq_status st = check_page_ranges(pool, block_tables, num_requests, max_blocks_per_req,
+                                          begin, end, err_flags);
+  if (st != KVQ_OK || num_requests == 0) return st;
+  return from_cuda(kvq::launch_pages_alloc(*pool, block_tables, num_requests, max_blocks_per_req,
+                                           begin, end, err_flags,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_pages_free(const kvq_page_pool *pool, const int32_t *block_tables,
+                          int32_t num_requests, int32_t max_blocks_per_req, const int32_t *begin,
+                          const int32_t *end, int32_t *err_flags, kvq_stream_t stream) {
+  const kvq_status st = check_page_ranges(pool, block_tables, num_requests, max_blocks_per_req,
+                                          begin, end, err_flags);
+  if (st != KVQ_OK || num_requests == 0) return st;
+  return from_cuda(kvq::launch_pages_free(*pool, block_tables, num_requests, max_blocks_per_req,
+                                          begin, end, err_flags,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_pages_fork(const kvq_cache *cache, const kvq_page_pool *pool,
+                          const int32_t *parents, int32_t num_children,
+                          const int32_t *block_tables, int32_t num_parents,
+                          int32_t max_blocks_per_req, const int32_t *context_lens,
+                          int32_t *child_tables, int32_t *child_lens, int32_t *err_flags,
+                          kvq_stream_t stream) {
+  kvq_status st = check_cache(cache, true);
+  if (st != KVQ_OK) return st;
+  st = check_pool(pool);
+  if (st != KVQ_OK) return st;
+  if (num_children < 0 || num_parents < 0 || max_blocks_per_req < 0 ||
+      cache->num_slots / cache->block_size < pool->num_pages)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_children > kMaxChildren || max_blocks_per_req > kMaxTableWidth)
+    return KVQ_ERR_UNSUPPORTED;
+  if (num_children == 0) return KVQ_OK;
+  if (parents == nullptr || block_tables == nullptr || context_lens == nullptr ||
+      child_tables == nullptr || child_lens == nullptr || child_lens == context_lens ||
+      child_tables == block_tables)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (!aligned(parents, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+      !aligned(child_tables, 4) || !aligned(child_lens, 4) || !aligned(err_flags, 4))
+    return KVQ_ERR_MISALIGNED;
+  return from_cuda(kvq::launch_pages_fork(*cache, *pool, parents, num_children, block_tables,
+                                          num_parents, max_blocks_per_req, context_lens,
+                                          log2_exact(cache->block_size), child_tables, child_lens,
+                                          err_flags, current_sm_count(),
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
 kvq_status kvq_dequant_rows(const kvq_cache *cache, const int64_t *slot_ids, int64_t n,
                             int32_t out_dtype, void *out_k, void *out_v, int32_t *err_flags,
                             kvq_stream_t stream) {

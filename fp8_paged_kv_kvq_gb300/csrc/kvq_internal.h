@@ -243,6 +243,44 @@ constexpr int32_t kPromptMaxGroup = 128;     // query heads per KV head
 bool prompt_attention_supported(const PromptArgs &a);
 cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream);
 
+// Paged attention with a mask over the cached tokens: a sliding window with sinks
+// (tree_mask null) or a tree of drafted tokens.
+struct MaskedArgs {
+  const void *q;
+  int32_t num_requests, rows_per_request, num_q_heads;
+  const int32_t *block_tables;
+  int32_t max_blocks_per_req, log2_block;
+  const int32_t *context_lens;
+  int32_t max_context_len;
+  int32_t window, num_sinks;
+  const int32_t *tree_mask;                  // [requests][R][ceil(R / 32)]
+  float sm_scale;
+  void *out;
+  void *workspace;
+  int32_t *err_flags;
+  int32_t sms;
+};
+constexpr int32_t kTreeMaxNodes = 1024;      // drafted tokens of a request
+size_t attn_masked_workspace_bytes(const MaskedArgs &a, int32_t num_kv_heads);
+cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStream_t stream);
+
+// The page pool (kvq.h).
+cudaError_t launch_pages_alloc(const kvq_page_pool &pool, int32_t *tables, int32_t n, int32_t width,
+                               const int32_t *begin, const int32_t *end, int32_t *err_flags,
+                               cudaStream_t stream);
+cudaError_t launch_pages_free(const kvq_page_pool &pool, const int32_t *tables, int32_t n,
+                              int32_t width, const int32_t *begin, const int32_t *end,
+                              int32_t *err_flags, cudaStream_t stream);
+cudaError_t launch_pages_fork(const kvq_cache &c, const kvq_page_pool &pool, const int32_t *parents,
+                              int32_t children, const int32_t *tables, int32_t num_parents,
+                              int32_t width, const int32_t *lens, int32_t log2_block,
+                              int32_t *child_tables, int32_t *child_lens, int32_t *err_flags,
+                              int32_t sms, cudaStream_t stream);
+cudaError_t launch_tree_commit(const kvq_cache &c, const int32_t *paths, const int32_t *counts,
+                               int32_t n, int32_t R, const int32_t *tables, int32_t width,
+                               int32_t log2_block, const int32_t *lens, int32_t *new_lens,
+                               int32_t *err_flags, cudaStream_t stream);
+
 // The tcgen05 partials kernel for 9..32 stacked rows per KV head.
 bool attn_tc_supported(const kvq_cache &c, const AttnShape &s);
 cudaError_t launch_attn_partials_tc(const kvq_cache &c, const AttnShape &s, const void *q,

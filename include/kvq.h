@@ -94,6 +94,10 @@ typedef enum kvq_status {
 #define KVQ_ERRF_POSITION_RANGE 16       /* token position outside the rotation table    */
 #define KVQ_ERRF_SEQUENCE_RANGE 32       /* a packed sequence's bounds decrease, leave the
                                             token buffer or pass max_seqlen               */
+#define KVQ_ERRF_PATH_RANGE 64           /* an accepted path that is not one, or a parent
+                                            outside the batch                             */
+#define KVQ_ERRF_NO_PAGES 128            /* the page pool had too few free pages          */
+#define KVQ_ERRF_PAGE_STATE 256          /* a page given back that nobody held            */
 
 /* The cache: codes and scales always travel together (ATOM PR #2655,
  * "Motivation": a restore that drops the scale planes decodes rows under the
@@ -454,6 +458,165 @@ kvq_status kvq_prompt_attention(const void *q, int64_t q_token_stride,
                                 int32_t head_dim, float sm_scale, void *out,
                                 int64_t out_token_stride, int32_t *err_flags,
                                 kvq_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Sliding window with sinks.  kvq_paged_decode for models whose layers see only
+ * the last `window` tokens and the first `num_sinks` of a sequence: row i of
+ * request r, at position p = L_r - R + i, sees the cached tokens
+ *     j <= p  with  j < num_sinks  or  j > p - window,
+ * with the scores and weights of kvq_paged_decode; rows that see no token
+ * (p < 0) are zero.  One launch; only the tokens that some row of a request
+ * sees are read, so block-table entries of the others may hold anything (pages
+ * given back, -1).  Tokens that a row does not see do not reach it, whatever
+ * their slots hold; a NaN code in a value row that it does see makes that element
+ * of its output NaN, or all of them.
+ *   rows_per_request R >= 1, R * num_q_heads / num_kv_heads <= 8192: a decode or
+ *                   verify step, a chunk of a prompt
+ *   window          >= 1, the row's own token included
+ *   num_sinks       >= 0
+ *   workspace       device, >= kvq_paged_decode_window_workspace_size(...) bytes,
+ *                   16-byte aligned; needs no initialisation.  Calls that share
+ *                   one must not run concurrently (two captured graphs may, one
+ *                   after the other).
+ * Pages of at least 16 tokens, any number of KV heads, fewer than 2^31 slots, at
+ * most 65,535 requests and 2^31 - 1 units of 128 tokens of one KV head, else
+ * KVQ_ERR_UNSUPPORTED.  Other arguments and errors as for kvq_paged_decode. */
+size_t kvq_paged_decode_window_workspace_size(int32_t num_requests, int32_t rows_per_request,
+                                              int32_t num_q_heads, int32_t num_kv_heads,
+                                              int32_t head_dim, int32_t block_size,
+                                              int32_t max_context_len, int32_t window,
+                                              int32_t num_sinks);
+
+kvq_status kvq_paged_decode_window(const kvq_cache *cache, const void *q,
+                                   int32_t num_requests, int32_t rows_per_request,
+                                   int32_t num_q_heads, const int32_t *block_tables,
+                                   int32_t max_blocks_per_req, const int32_t *context_lens,
+                                   int32_t max_context_len, int32_t window, int32_t num_sinks,
+                                   float sm_scale, void *out, void *workspace,
+                                   size_t workspace_bytes, int32_t *err_flags,
+                                   kvq_stream_t stream);
+
+/* Attention of a tree of drafted tokens: the last R cached tokens of request r
+ * are the nodes of a tree (node b at position L_r - R + b), and row i, the query
+ * of node i, sees
+ *     every token j < L_r - R  and  the nodes b whose bit is set in its mask,
+ * with the scores and weights of kvq_paged_decode.  For a tree the mask holds a
+ * node's ancestors and the node itself, but any mask is allowed; rows that see
+ * no token are zero.  Nodes at negative positions (L_r < R) do not exist.  One
+ * launch.  Tokens that a row does not see do not reach it, whatever their slots
+ * hold.
+ *   tree_mask       device int32 [num_requests, R, ceil(R / 32)]: bit b % 32 of
+ *                   word b / 32 of row i is set where row i sees node b; bits of
+ *                   nodes >= R are ignored
+ *   rows_per_request R in [1, 1024], R * num_q_heads / num_kv_heads <= 8192
+ *   workspace       as for kvq_paged_decode_window
+ * Limits, other arguments and errors as for kvq_paged_decode_window. */
+size_t kvq_paged_decode_tree_workspace_size(int32_t num_requests, int32_t rows_per_request,
+                                            int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t block_size,
+                                            int32_t max_context_len);
+
+kvq_status kvq_paged_decode_tree(const kvq_cache *cache, const void *q, const int32_t *tree_mask,
+                                 int32_t num_requests, int32_t rows_per_request,
+                                 int32_t num_q_heads, const int32_t *block_tables,
+                                 int32_t max_blocks_per_req, const int32_t *context_lens,
+                                 int32_t max_context_len, float sm_scale, void *out,
+                                 void *workspace, size_t workspace_bytes, int32_t *err_flags,
+                                 kvq_stream_t stream);
+
+/* What follows the verification of a tree: the rows (codes and scales, K and V)
+ * of the accepted nodes moved together behind the context, node accepted[r][a]
+ * from position L_r - R + accepted[r][a] to L_r - R + a, and new_lens[r] = L_r -
+ * R + accepted_lens[r].  Rows behind the new length keep what they held.  One
+ * launch, capturable.
+ *   accepted        device int32 [num_requests, rows_per_request]: the path's
+ *                   nodes, ascending, in [0, R); entries from accepted_lens[r] on
+ *                   are not read
+ *   accepted_lens   device int32 [num_requests], in [0, R]
+ *   context_lens    device int32 [num_requests]: L_r, the R drafted tokens included
+ *   new_lens        device int32 [num_requests]; may be context_lens itself
+ * A request whose path is not ascending or leaves [0, R), whose count leaves
+ * [0, R] or whose length is below R or above max_blocks_per_req * block_size is
+ * left as it was (new_lens[r] = L_r) and sets KVQ_ERRF_PATH_RANGE (the length:
+ * KVQ_ERRF_CONTEXT_RANGE, unless it is idle, length and count 0); a moved row
+ * whose page lies outside the cache sets KVQ_ERRF_BLOCK_RANGE and is not moved.
+ * Requests must not share the pages of their drafted tokens.  R <= 1024. */
+kvq_status kvq_tree_commit(const kvq_cache *cache, const int32_t *accepted,
+                           const int32_t *accepted_lens, int32_t num_requests,
+                           int32_t rows_per_request, const int32_t *block_tables,
+                           int32_t max_blocks_per_req, const int32_t *context_lens,
+                           int32_t *new_lens, int32_t *err_flags, kvq_stream_t stream);
+
+/* A pool of pages on the device: who holds how many references to each page and
+ * which pages are free, so that sequences fork, grow and go without the host.
+ *   ref_counts   int32 [num_pages]: block tables that hold the page, 0 = free
+ *   free_pages   int32 [num_pages]: a stack; entries [0, state[0]) are the free pages
+ *   state        int32 [4]: state[0] the number of free pages, the others 0 between
+ *                calls
+ *   marks        int32 [ceil(num_pages / 32)]: 0 between calls
+ * A fresh pool: ref_counts 0, free_pages 0 .. num_pages - 1, state {num_pages, 0, 0,
+ * 0}, marks 0.  Calls on one pool must follow one another (one stream, or events). */
+typedef struct kvq_page_pool {
+    int32_t *ref_counts;
+    int32_t *free_pages;
+    int32_t *state;
+    int32_t *marks;
+    int32_t num_pages;
+} kvq_page_pool;
+
+/* Pages from the pool: the entries [begin[r], end[r]) of request r's block table
+ * get a page each with one reference, requests in order, entries in order, pages
+ * from the top of the stack.  One launch, capturable.
+ * A request whose pages and those of the requests before it are more than the
+ * pool has gets -1 in its entries and sets KVQ_ERRF_NO_PAGES; begin and end that
+ * leave [0, max_blocks_per_req] or cross set KVQ_ERRF_CONTEXT_RANGE, and the
+ * request gets nothing. */
+kvq_status kvq_pages_alloc(const kvq_page_pool *pool, int32_t *block_tables,
+                           int32_t num_requests, int32_t max_blocks_per_req,
+                           const int32_t *begin, const int32_t *end, int32_t *err_flags,
+                           kvq_stream_t stream);
+
+/* References given back: one for each of the entries [begin[r], end[r]) of each
+ * request's block table (a whole request that ends, pages that a window has
+ * left, the pages behind a shortened sequence); pages that nobody holds any more
+ * are pushed on the free stack in ascending order.  The tables are not changed.
+ * Entries < 0 are no pages and skipped.  One launch, capturable.
+ * Entries >= num_pages set KVQ_ERRF_BLOCK_RANGE, a page given back more often than
+ * it was held KVQ_ERRF_PAGE_STATE (each without effect), begin and end that leave
+ * [0, max_blocks_per_req] or cross KVQ_ERRF_CONTEXT_RANGE (nothing of that request
+ * is given back). */
+kvq_status kvq_pages_free(const kvq_page_pool *pool, const int32_t *block_tables,
+                          int32_t num_requests, int32_t max_blocks_per_req,
+                          const int32_t *begin, const int32_t *end, int32_t *err_flags,
+                          kvq_stream_t stream);
+
+/* Sequences that continue others (samples of one prompt, the beams that survive):
+ * child i takes over the L = context_lens[parents[i]] cached tokens of its parent.
+ * Its block table shares the parent's full pages (one reference more each); of a
+ * last page that is partly filled it gets a copy, the L % block_size rows of K and
+ * V codes and scales, in a page from the top of the pool's stack, children in
+ * order.  child_lens[i] = L.  Parents keep their pages.  One launch, capturable.
+ *   parents         device int32 [num_children]; < 0: no child (child_lens[i] = 0,
+ *                   nothing else is written)
+ *   block_tables, context_lens   of the parents, [num_parents, max_blocks_per_req]
+ *                   and [num_parents]
+ *   child_tables    device int32 [num_children, max_blocks_per_req], not
+ *                   overlapping block_tables; entries behind a child's pages are
+ *                   not written
+ *   child_lens      device int32 [num_children], not overlapping context_lens
+ * A child that needs a page when the pool has none left, or whose parent is >=
+ * num_parents or of a length outside [0, max_blocks_per_req * block_size], is no
+ * child, as above, and sets KVQ_ERRF_NO_PAGES, KVQ_ERRF_PATH_RANGE or
+ * KVQ_ERRF_CONTEXT_RANGE; a parent's page outside the pool sets
+ * KVQ_ERRF_BLOCK_RANGE, is passed on as it is and neither counted nor copied.
+ * The cache holds the pool's pages (num_slots >= num_pages * block_size).
+ * At most 4096 children. */
+kvq_status kvq_pages_fork(const kvq_cache *cache, const kvq_page_pool *pool,
+                          const int32_t *parents, int32_t num_children,
+                          const int32_t *block_tables, int32_t num_parents,
+                          int32_t max_blocks_per_req, const int32_t *context_lens,
+                          int32_t *child_tables, int32_t *child_lens, int32_t *err_flags,
+                          kvq_stream_t stream);
 
 /* Dequantise whole rows back to real values: out = fl32(e4m3(c) * scale), one
  * IEEE multiply, or that value rounded once more to bf16 (nearest-even).
