@@ -627,6 +627,7 @@ kvq_status masked_call(const kvq_cache *cache, kvq::MaskedArgs a, size_t workspa
       !aligned(a.context_lens, 4) || !aligned(a.tree_mask, 4) || !aligned(a.workspace, 16) ||
       !aligned(a.err_flags, 4))
     return KVQ_ERR_MISALIGNED;
+  if (cache->num_slots < cache->block_size) return KVQ_ERR_INVALID_ARGUMENT;   // no page
   const size_t need = kvq::attn_masked_workspace_bytes(a, cache->num_kv_heads);
   if (need > 0 && (a.workspace == nullptr || workspace_bytes < need))
     return KVQ_ERR_WORKSPACE_TOO_SMALL;
