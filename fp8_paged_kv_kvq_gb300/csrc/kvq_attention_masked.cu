@@ -39,17 +39,17 @@
 //    to 0 after the product with the scale (which may be NaN), and in chunks that
 //    some row of the unit does not see whole, value rows with a NaN code are cleared
 //    (0 times NaN is NaN) and noted; a row that does see one becomes NaN.
-//  * Roles, 640 threads: warps 0-3 and 4-7 the softmax of chain 0 and 1 (a thread owns
-//    a TMEM lane, a row), 8-11 the epilogue, 12-15 the value codes' conversion, 16 the
-//    units and the copies of codes, 17 and 18 the MMAs of chain 0 and 1, 19 the
-//    scales.  Every wait is bounded; a role that gives up raises a shared abort flag,
-//    copies and MMAs in flight complete, the block frees its tensor memory
-//    (KVQ_ERRF_WAIT_TIMEOUT).
+//  * Roles, 512 threads: warps 0-3 and 4-7 the softmax of chain 0 and 1 (a thread owns
+//    a TMEM lane, a row), 8-11 the value codes' conversion and the epilogue, 12 the
+//    units and all copies, 13 and 14 the MMAs of chain 0 and 1, 15 the scales.  Every
+//    wait is bounded; a role that gives up raises a shared abort flag, copies and MMAs
+//    in flight complete, the block frees its tensor memory (KVQ_ERRF_WAIT_TIMEOUT).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
@@ -59,8 +59,8 @@ namespace kvq {
 namespace {
 
 constexpr int kMkTok = 128;                           // tokens of a chunk
-constexpr int kMkWarpEpi = 8, kMkWarpConv = 12, kMkWarpLoad = 16, kMkWarpMma = 17, kMkWarpScale = 19;
-constexpr int kMkThreads = 640;
+constexpr int kMkWarpConv = 8, kMkWarpLoad = 12, kMkWarpMma = 13, kMkWarpScale = 15;
+constexpr int kMkThreads = 512;
 constexpr int kMkUnits = 8;                           // units announced ahead
 constexpr int kMkIdAhead = 4;                         // chunks whose page ids are in flight
 constexpr int kMkMaxBoxes = 8;                        // pages of a chunk (boxes of >= 16 tokens)
@@ -79,34 +79,31 @@ struct MkShape {
   static constexpr int kCopies = 128 / kRows;
   static constexpr int kQTiles = kPair ? 2 : 1;
   // shared memory, offsets from a 1024-byte aligned base
-  static constexpr int kKStages = kPair || kRows == 32 ? 3 : 4;
-  static constexpr int kVStages = kPair ? 2 : 3;
-  static constexpr int kCode = kMkTok * kHeadDim;            // a chunk's codes
+  static constexpr int kStages = kPair ? 2 : 3;
+  static constexpr int kStage = 2 * kMkTok * kHeadDim;       // a chunk's codes: 8 rows of K, 8 of V, ...
   static constexpr int kQPiece = 128 * kHeadDim;
   static constexpr int kOffQ = 0;                            // [tile][piece]
   static constexpr int kOffVf = kOffQ + kQTiles * 2 * kQPiece;   // f16 values, two chunks
-  static constexpr int kVfBytes = 2 * kCode;
-  static constexpr int kOffK = kOffVf + 2 * kVfBytes;
-  static constexpr int kOffV = kOffK + kKStages * kCode;
-  static constexpr int kOffSum = kOffV + kVStages * kCode;   // [chain][128] denominators
+  static constexpr int kVfBytes = kMkTok * kHeadDim * 2;
+  static constexpr int kOffKv = kOffVf + 2 * kVfBytes;
+  static constexpr int kOffSum = kOffKv + kStages * kStage;  // [chain][128] denominators
   static constexpr int kOffRef = kOffSum + 2 * 128 * 4;      // [chain][128] references
   static constexpr int kOffEg = kOffRef + 2 * 128 * 4;       // [chain]
-  static constexpr int kOffSc = kOffEg + 16;                 // [stage][K | V][128]
-  static constexpr int kOffMeta = kOffSc + kMkScales * 2 * kMkTok * 4;   // [stage] float4
+  static constexpr int kOffSc = kOffEg + 16;                 // [stage][K | V | log2 V][128]
+  static constexpr int kOffMeta = kOffSc + kMkScales * 3 * kMkTok * 4;   // [stage] float4
   static constexpr int kOffUnit = kOffMeta + kMkScales * 16;
   static constexpr int kOffIds = kOffUnit + kMkUnits * 64;
-  static constexpr int kOffBad = kOffIds + (kMkIdAhead + 1) * kMkMaxBoxes * 4;   // [Vf][4 words]
-  static constexpr int kOffMisc = kOffBad + 32;              // tmem base, abort, ticket
+  static constexpr int kOffBad = kOffIds + (kMkIdAhead + 1) * kMkMaxBoxes * 4;   // [Vf][4 words], [scales][4 words]
+  static constexpr int kOffMisc = kOffBad + 32 + kMkScales * 16;              // tmem base, abort, ticket
   static constexpr int kOffScan = kOffMisc + 16;             // a warp's sum each
   static constexpr int kOffPre = kOffScan + kMkThreads / 32 * 4;
   static constexpr int kOffBar = (kOffPre + (kMkMaxRequests + 1) * 4 + 7) / 8 * 8;
-  static constexpr int kKFull = 0;
-  static constexpr int kKEmpty = kKFull + kKStages;
-  static constexpr int kVcFull = kKEmpty + kKStages;
-  static constexpr int kVcEmpty = kVcFull + kVStages;
-  static constexpr int kVfFull = kVcEmpty + kVStages;
+  static constexpr int kKvFull = 0;
+  static constexpr int kKvEmpty = kKvFull + kStages;
+  static constexpr int kVfFull = kKvEmpty + kStages;
   static constexpr int kVfEmpty = kVfFull + 2;
-  static constexpr int kScFull = kVfEmpty + 2;
+  static constexpr int kScRaw = kVfEmpty + 2;
+  static constexpr int kScFull = kScRaw + kMkScales;
   static constexpr int kScEmpty = kScFull + kMkScales;
   static constexpr int kQFull = kScEmpty + kMkScales;        // per chain from here on
   static constexpr int kQEmpty = kQFull + 2;
@@ -123,37 +120,54 @@ struct MkShape {
   // at most 32 rows: the copies' outputs, 32 dims at a time
   static constexpr int kOffX = (kOffBar + 8 * kBars + 127) / 128 * 128;
   static constexpr int kSmem = kOffX + (kRows == 32 ? 4 * 32 * 32 * 4 : 0) + 1024;
-  static_assert(kOffK % 1024 == 0 && kOffVf % 1024 == 0 && kOffSc % 16 == 0 && kOffMeta % 16 == 0 &&
+  static_assert(kOffKv % 1024 == 0 && kOffVf % 1024 == 0 && kOffSc % 16 == 0 && kOffMeta % 16 == 0 &&
                     kOffUnit % 16 == 0 && kOffBad % 16 == 0 && kOffMisc % 16 == 0 && kOffBar % 8 == 0,
                 "alignment");
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kBars <= kMkThreads, "a thread initialises each barrier");
 };
 
-// TMEM: S of chain a at 128 a (its P'' over the first 64 columns), O at 256 + 128 a
+// TMEM: S of chain a at 128 a (P'' of each half of its tokens over the first 32 columns
+// of that half), O at 256 + 128 a
 constexpr uint32_t kMkTmemCols = 512;
 __device__ __forceinline__ uint32_t mk_s(int a) { return 128u * a; }
 __device__ __forceinline__ uint32_t mk_o(int a) { return 256u + 128u * a; }
 
 constexpr uint32_t kMkIdescQK = mma_idesc(128, kMkTok, false, false);        // e4m3
 constexpr uint32_t kMkIdescPV = mma_idesc(128, kHeadDim, false, true);       // f16, B MN-major
-// The operands' shared-memory descriptors (smem_desc: stride offset 1024, version 1,
-// 128-byte swizzle), upper words and the two leading offsets.
+// The operands' shared-memory descriptors (smem_desc: stride offset, version 1, 128-byte
+// swizzle), upper words and the two leading offsets.
 constexpr uint32_t kMkDescHi = (1024u >> 4) | (1u << 14) | (kSmemSwizzle128 << 29);
 constexpr uint32_t kMkKMajor = 1u << 16, kMkMnMajor = (16384u >> 4) << 16;
 
-__device__ __forceinline__ void mk_mma_qk(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t acc) {
+__device__ __forceinline__ void mk_mma_qk(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t b_hi,
+                                          uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n"
-      " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %6};\n"
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n"
-      :: "r"(d), "r"(a_lo), "r"(b_lo), "n"(kMkIdescQK), "r"(acc), "n"(kMkDescHi) : "memory");
+      :: "r"(d), "r"(a_lo), "r"(b_lo), "n"(kMkIdescQK), "r"(acc), "n"(kMkDescHi), "r"(b_hi)
+      : "memory");
 }
 __device__ __forceinline__ void mk_mma_pv(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n"
       :: "r"(d), "r"(a_tmem), "r"(b_lo), "n"(kMkIdescPV), "r"(acc), "n"(kMkDescHi) : "memory");
+}
+
+// One box of a copy: 8 rows of K, 8 of V, 8 of K, ... of a head, from group z of 8 slots on.
+__device__ __forceinline__ void mk_load_box(uint32_t dst, const void *tmap, int z, int head,
+                                            uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;\n"
+      :: "r"(dst), "l"(tmap), "r"(0), "r"(z), "r"(head), "r"(bar), "l"(policy) : "memory");
+}
+
+// This thread's cp.async so far arrive on `bar` when they have landed.
+__device__ __forceinline__ void mk_arrive_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" :: "r"(bar) : "memory");
 }
 
 // One lane of the (converged) warp.
@@ -172,10 +186,14 @@ struct MkParams {
   const float *k_scales, *v_scales;
   const int32_t *tree;                                 // mask words, null: a window
   int32_t N, R, Hq, H, G, M;
+  uint32_t inv_g;                                      // ceil(2^32 / G), G > 1
   int32_t T;                                           // units of a request and head
   int32_t width;                                       // max_blocks_per_req
   int32_t ctx_limit, num_blocks, log2_bs, box;
   int32_t window, sinks, words;
+  // a stage: groups of 8 rows every `group` bytes, K's and V's first (one map over both
+  // planes: K and V in turns; two maps: all of K, then all of V)
+  int32_t group, k_off, v_off, two_maps;
   float scale2;                                        // |sm_scale| log2(e)
   uint32_t flip;                                       // sign bits of a negative sm_scale
   float *o_part;                                       // [grid][2][rows of a unit][128]
@@ -183,7 +201,13 @@ struct MkParams {
   unsigned long long *tickets;                         // [N * H * T]
   uint32_t tag;
   int32_t *err_flags;
+  int32_t least;                                       // positions of a block's range
 };
+
+// m / G, m < 2^13: exact, since m (inv_g G - 2^32) < 2^26
+__device__ __forceinline__ int mk_query(const MkParams &p, int m) {
+  return p.G == 1 ? m : static_cast<int>(__umulhi(static_cast<uint32_t>(m), p.inv_g));
+}
 
 __device__ __forceinline__ float mk_ex2(float x) {
   float y;
@@ -215,18 +239,16 @@ __device__ __forceinline__ uint32_t mk_low(int n) {
   return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
-// Bounded wait that also gives up once another role raised the abort flag.
-__device__ __forceinline__ bool mk_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort) {
+// Bounded wait (about a second) that also gives up once another role raised the abort
+// flag.  One small loop: it is at every wait, and the roles share an instruction cache.
+__device__ __forceinline__ bool mk_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
 #pragma unroll 1
   for (int i = 0; i < (1 << 19); ++i) {
     if (mbar_try_wait_sleep(bar, parity, 2000u)) return true;
-    if ((i & 15) == 15 && *abort) return false;
+    if (*abort) return false;
   }
   *abort = 1;
   return false;
-}
-__device__ __forceinline__ bool mk_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-  return mbar_try_wait(bar, parity) || mk_wait_slow(bar, parity, abort);
 }
 // The whole warp's (every lane tries; one that gives up speaks for all).
 __device__ __forceinline__ bool mk_wait_all(uint32_t bar, uint32_t parity, volatile int *abort) {
@@ -245,7 +267,7 @@ template <int kTileRows>
 __device__ __forceinline__ MkSpan mk_span(const MkParams &p, int L, int t) {
   MkSpan s{L, 0, 0};
   if (p.tree != nullptr) return s;
-  const int first = t * kTileRows / p.G, last = (min(p.M, (t + 1) * kTileRows) - 1) / p.G;
+  const int first = mk_query(p, t * kTileRows), last = mk_query(p, min(p.M, (t + 1) * kTileRows) - 1);
   const int base = L - p.R;
   if (base + last < 0) return MkSpan{0, 0, 0};
   const int lo16 = max(0, base + first - p.window + 1) & ~15;
@@ -271,8 +293,6 @@ struct __align__(16) MkUnit {
   int c0, X, s16, shift;
   int base, direct, slot, b_first;
   int b_last, index, pad0, pad1;
-
-  __device__ __forceinline__ int pos(int x) const { return x < s16 ? x : x + shift; }
 };
 
 // What a query row sees, in a unit's token numbers: x < hi and (x < sinks or x >= lo),
@@ -296,7 +316,7 @@ struct MkSeen {
 };
 __device__ __forceinline__ MkSeen mk_seen(const MkParams &p, const MkUnit &u, int m) {
   MkSeen s;
-  const int i = min(m, p.M - 1) / p.G;                 // (rows past the last see what it sees)
+  const int i = mk_query(p, min(m, p.M - 1));          // (rows past the last see what it sees)
   const int own = u.base + i;
   s.hi = own + 1 - u.shift;
   s.lo = max(own - p.window + 1, u.s16 + u.shift) - u.shift;
@@ -304,11 +324,20 @@ __device__ __forceinline__ MkSeen mk_seen(const MkParams &p, const MkUnit &u, in
   s.words = p.tree + (static_cast<int64_t>(u.r) * p.R + i) * p.words;
   return s;
 }
-// Whether the rows between a first and a last one see all of the tokens [x0, x0 + n).
-__device__ __forceinline__ bool mk_whole(const MkParams &p, int hi_first, int lo_last, int base,
-                                         int x0, int n) {
-  if (p.tree != nullptr) return x0 + n <= base;
-  return x0 + n <= hi_first && (x0 + n <= p.sinks || x0 >= lo_last);
+// The chunks of a unit (numbered from its piece's first) that the rows from a first to a
+// last one see whole: those below `hi` that are below `sink` or not below `lo`.
+struct MkWhole {
+  int hi, sink, lo;
+  __device__ __forceinline__ bool at(int k) const { return k < hi && (k < sink || k >= lo); }
+};
+__device__ __forceinline__ MkWhole mk_whole(const MkParams &p, const MkUnit &u, int hi_first,
+                                            int lo_last) {
+  if (p.tree != nullptr) return MkWhole{(u.base >> 7) - u.c0, 0, 0};
+  return MkWhole{(hi_first >> 7) - u.c0, (p.sinks >> 7) - u.c0, ((lo_last + kMkTok - 1) >> 7) - u.c0};
+}
+template <int kTileRows>
+__device__ __forceinline__ MkWhole mk_unit_whole(const MkParams &p, const MkUnit &u) {
+  return mk_whole(p, u, mk_seen(p, u, u.row0).hi, mk_seen(p, u, u.row0 + kTileRows - 1).lo);
 }
 
 // ---------------------------------------------------------------------------
@@ -320,34 +349,46 @@ struct MkRow {
   int eg = 0;                                          // value scales are held over 2^eg
 };
 
-// max_j (u_j + log2 of the value scale) over the seen of 32 tokens.
-__device__ __forceinline__ float mk_top32(const float (&x)[32], const float *ks, const float *vs,
-                                          float rowf, uint32_t bits, float top) {
+// max_j (u_j + log2 of the value scale) over 32 tokens, those of `bits` (kMasked).
+template <bool kMasked>
+__device__ __forceinline__ float mk_top32(const uint32_t (&x)[32], const float *ks, const float *lg,
+                                          uint64_t rowf, uint32_t bits, float top) {
+  float m[2] = {top, -INFINITY};
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     const float4 k4 = reinterpret_cast<const float4 *>(ks)[q];
-    const float4 v4 = reinterpret_cast<const float4 *>(vs)[q];
-    const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, vv[4] = {v4.x, v4.y, v4.z, v4.w};
+    const float4 l4 = reinterpret_cast<const float4 *>(lg)[q];
+    const uint64_t kk[2] = {pack_f32x2(k4.x, k4.y), pack_f32x2(k4.z, k4.w)};
+    const uint64_t ll[2] = {pack_f32x2(l4.x, l4.y), pack_f32x2(l4.z, l4.w)};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float w = x[4 * q + i] * kk[i] * rowf +
-                      fmaxf(static_cast<float>(mk_ceil_log2(vv[i])), kMkFloor);
-      if ((bits >> (4 * q + i)) & 1u) top = fmaxf(top, w);
+    for (int i = 0; i < 2; ++i) {
+      const int e = 4 * q + 2 * i;
+      float a, b;
+      unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                       kk[i]), rowf, ll[i]), a, b);
+      if (kMasked) {
+        a = (bits >> e) & 1u ? a : -INFINITY;
+        b = (bits >> (e + 1)) & 1u ? b : -INFINITY;
+      }
+      m[i] = mk_max3(m[i], a, b);
     }
   }
-  return top;
+  return fmaxf(m[0], m[1]);
 }
 
 // The reference moved where `top` is far above it, the denominator and (unless the
-// chain has no earlier chunk of the unit) the O row brought under the new one; `de`:
-// by how much 2^Eg grew, which the O rows are brought under as well.
+// chain has no earlier chunk of the unit) the O row brought under the new one.  de: by
+// how much 2^Eg grew; weights stay as large as they were under a reference that is
+// lower by as much (as long as the denominator stays below 2^100).
 __device__ __forceinline__ void mk_meet(MkRow &row, float top, int de, bool fresh, uint32_t ocol) {
   const bool unset = row.m == -INFINITY;
-  const bool move = unset ? top > -INFINITY : top - row.m > kMkLazy;
-  const float f = (move && !unset) ? mk_ex2(row.m - top) : 1.0f;
-  if (!fresh && __any_sync(0xFFFFFFFFu, (move && !unset) || de != 0)) {
-    const float fo = f * mk_pow2_down(-de);
-    row.sum *= f;
+  const float keep = row.m - static_cast<float>(de == 0 ? 0 : min(de, 100 - mk_ceil_log2(row.sum)));
+  const bool move = unset ? top > -INFINITY : top - keep > kMkLazy;
+  const float next = move ? top : keep;
+  const float f = unset ? 1.0f : mk_ex2(row.m - next), fo = f * mk_pow2_down(-de);
+  row.m = next;
+  row.sum *= f;
+  if (!fresh && __any_sync(0xFFFFFFFFu, fo != 1.0f && !unset)) {
 #pragma unroll 1
     for (int c = 0; c < kHeadDim; c += 16) {
       float o[16];
@@ -358,10 +399,10 @@ __device__ __forceinline__ void mk_meet(MkRow &row, float top, int de, bool fres
     }
     tmem_wait_st();
   }
-  if (move) row.m = top;
 }
 
-// P'' of 32 scores as f16 in w, the sum of the p added to `sum`.
+// P'' of 32 scores as f16 in w, the sum of the p added to `sum`; tokens that are not in
+// `bits` (kMasked) have p = 0.
 template <bool kMasked>
 __device__ __forceinline__ void mk_part(const uint32_t (&x)[32], const float *ks, const float *vs,
                                         uint64_t rowf, uint64_t shift, uint32_t bits,
@@ -375,21 +416,17 @@ __device__ __forceinline__ void mk_part(const uint32_t (&x)[32], const float *ks
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int e = 4 * q + 2 * i;
-      const uint64_t s = pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-      float a, b, wa, wb;
-      unpack_f32x2(fma_f32x2(mul_f32x2(s, kk[i]), rowf, shift), a, b);
+      float a, b;
+      unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                       kk[i]), rowf, shift), a, b);
       if (kMasked) {
         a = (bits >> e) & 1u ? a : -INFINITY;
         b = (bits >> (e + 1)) & 1u ? b : -INFINITY;
       }
       const uint64_t p = pack_f32x2(mk_ex2(a), mk_ex2(b));
       sum[i] = mk_add2(sum[i], p);
-      unpack_f32x2(mul_f32x2(p, vv[i]), wa, wb);
-      if (kMasked) {
-        wa = (bits >> e) & 1u ? wa : 0.0f;
-        wb = (bits >> (e + 1)) & 1u ? wb : 0.0f;
-      }
-      w[2 * q + i] = pack_f16x2(wa, wb);
+      unpack_f32x2(mul_f32x2(p, vv[i]), a, b);
+      w[2 * q + i] = pack_f16x2(a, b);
     }
   }
 }
@@ -402,58 +439,57 @@ __device__ __forceinline__ void mk_announce(uint32_t bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// One chunk of one row: S from TMEM, the row's statistics brought up to date, P'' over
-// S's columns, its halves announced one after the other.  ks, vs: the chunk's scales;
-// meta: the largest key scale, the log2 of the largest value scale, Eg.  bits: what the
-// row sees of the four groups of 32 tokens (kMasked).
-template <bool kMasked>
+// One chunk of one row whose warp sees all of it: S from TMEM, the row's statistics
+// brought up to date, P'' over S's columns (tokens 64 h .. in the columns from 64 h on),
+// its halves announced one after the other.  ks: the chunk's key scales, value scales
+// and their log2; meta: the largest key scale, the log2 of the largest value scale, Eg.
 __device__ __forceinline__ void mk_softmax128(uint32_t scol, uint32_t ocol, const float *ks,
-                                              const float *vs, const float4 meta, float rowf,
-                                              const uint32_t (&bits)[4], bool fresh,
+                                              const float4 meta, float rowf, bool fresh,
                                               uint32_t ready, int lane, MkRow &row) {
   const int eg = __float_as_int(meta.z);
   const int de = fresh ? 0 : eg - row.eg;
   row.eg = eg;
-  bool search = true;
-  if (!kMasked) {
-    float mx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float *vs = ks + kMkTok, *lg = vs + kMkTok;
+  const uint64_t rf = pack_f32x2(rowf, rowf);
+  // the largest a score can be under the chunk's largest scales
+  float mx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 64) {
-      float x[64];
-      tmem_ld64(scol + c, x);
+  for (int c = 0; c < 128; c += 64) {
+    float x[64];
+    tmem_ld64(scol + c, x);
 #pragma unroll
-      for (int i = 0; i < 64; i += 8)
+    for (int i = 0; i < 64; i += 8)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = mk_max3(mx[q], x[i + q], x[i + q + 4]);
-    }
-    const float most = fmaxf(mk_max3(mx[0], mx[1], mx[2]), mx[3]) * meta.x * rowf + meta.y;
-    search = __any_sync(0xFFFFFFFFu, !(most - row.m <= kMkLazy));
+      for (int q = 0; q < 4; ++q) mx[q] = mk_max3(mx[q], x[i + q], x[i + q + 4]);
   }
-  if (search || de != 0) {
+  const float most = fmaxf(mk_max3(mx[0], mx[1], mx[2]), mx[3]) * meta.x * rowf + meta.y;
+  if (de != 0 || __any_sync(0xFFFFFFFFu, !(most - row.m <= kMkLazy))) {
     float top = -INFINITY;
 #pragma unroll 1
     for (int g = 0; g < 4; ++g) {
-      float x[32];
-      tmem_ld32(scol + 32 * g, x);
-      const uint32_t b = !kMasked ? 0xFFFFFFFFu : (g == 0 ? bits[0] : g == 1 ? bits[1] : g == 2 ? bits[2] : bits[3]);
-      top = mk_top32(x, ks + 32 * g, vs + 32 * g, rowf, b, top);
+      uint32_t x[32];
+      tmem_ld32_start(scol + 32 * g, x);
+      tmem_ld32_done(x);
+      top = mk_top32<false>(x, ks + 32 * g, lg + 32 * g, rf, 0u, top);
     }
     mk_meet(row, top, de, fresh, ocol);
   }
   const float sh = row.m == -INFINITY ? 0.0f : -row.m;
-  const uint64_t rf = pack_f32x2(rowf, rowf), s2 = pack_f32x2(sh, sh);
+  const uint64_t s2 = pack_f32x2(sh, sh);
   uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
+  uint32_t x0[32], x1[32], w[16];
+  tmem_ld32_start(scol, x0);
+  tmem_ld32_done(x0);
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
-    uint32_t x0[32], x1[32], w[16];
-    tmem_ld32_start(scol + 64 * h, x0);
-    tmem_ld32_done(x0);
     tmem_ld32_start(scol + 64 * h + 32, x1);
-    mk_part<kMasked>(x0, ks + 64 * h, vs + 64 * h, rf, s2, h == 0 ? bits[0] : bits[2], sum, w);
+    mk_part<false>(x0, ks + 64 * h, vs + 64 * h, rf, s2, 0u, sum, w);
     tmem_ld32_done(x1);
-    tmem_st16u(scol + 32 * h, w);
-    mk_part<kMasked>(x1, ks + 64 * h + 32, vs + 64 * h + 32, rf, s2, h == 0 ? bits[1] : bits[3], sum, w);
-    tmem_st16u(scol + 32 * h + 16, w);
+    tmem_st16u(scol + 64 * h, w);
+    if (h == 0) tmem_ld32_start(scol + 64, x0);
+    mk_part<false>(x1, ks + 64 * h + 32, vs + 64 * h + 32, rf, s2, 0u, sum, w);
+    if (h == 0) tmem_ld32_done(x0);
+    tmem_st16u(scol + 64 * h + 16, w);
     mk_announce(ready + 8 * h, lane);
   }
   float a, b;
@@ -461,32 +497,91 @@ __device__ __forceinline__ void mk_softmax128(uint32_t scol, uint32_t ocol, cons
   row.sum += a + b;
 }
 
-// The same for a row of which each of four copies takes 32 tokens of the chunk: this
-// thread's are those of `copy`; the other copies' columns are 0.
-__device__ __forceinline__ void mk_softmax32(uint32_t scol, uint32_t ocol, const float *ks,
-                                             const float *vs, const float4 meta, float rowf,
-                                             uint32_t bits, int copy, bool fresh, uint32_t ready,
-                                             int lane, MkRow &row) {
+// The same where some of the warp's rows do not see some of the tokens [x0, x0 + 128):
+// seldom, so small rather than fast (the roles share an instruction cache).  bad: tokens
+// whose value was cleared; returns whether the row sees one of them.
+__device__ __forceinline__ bool mk_softmax128_masked(const MkParams &p, const MkSeen &seen, int x0,
+                                                     int X, const uint32_t (&bad)[4], uint32_t scol,
+                                                     uint32_t ocol, const float *ks,
+                                                     const float4 meta, float rowf, bool fresh,
+                                                     uint32_t ready, int lane, MkRow &row) {
   const int eg = __float_as_int(meta.z);
   const int de = fresh ? 0 : eg - row.eg;
   row.eg = eg;
-  float x[32];
-  tmem_ld32(scol + 32 * copy, x);
-  const float *kc = ks + 32 * copy, *vc = vs + 32 * copy;
-  mk_meet(row, mk_top32(x, kc, vc, rowf, bits, -INFINITY), de, fresh, ocol);
+  const float *vs = ks + kMkTok, *lg = vs + kMkTok;
+  const uint64_t rf = pack_f32x2(rowf, rowf);
+  float top = -INFINITY;
+  uint32_t b0 = 0u, b1 = 0u, b2 = 0u, b3 = 0u, hit = 0u, x[32];
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t bits = seen.bits(p, x0 + 32 * g, X);
+    if (g == 0) b0 = bits;
+    else if (g == 1) b1 = bits;
+    else if (g == 2) b2 = bits;
+    else b3 = bits;
+    hit |= bits & (g < 2 ? (g == 0 ? bad[0] : bad[1]) : (g == 2 ? bad[2] : bad[3]));
+    tmem_ld32_start(scol + 32 * g, x);
+    tmem_ld32_done(x);
+    top = mk_top32<true>(x, ks + 32 * g, lg + 32 * g, rf, bits, top);
+  }
+  mk_meet(row, top, de, fresh, ocol);
   const float sh = row.m == -INFINITY ? 0.0f : -row.m;
   uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
-  uint32_t xu[32], w[16], z[16];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) xu[i] = __float_as_uint(x[i]);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] = 0u;
-  mk_part<true>(xu, kc, vc, pack_f32x2(rowf, rowf), pack_f32x2(sh, sh), bits, sum, w);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (c == copy) tmem_st16u(scol + 16 * c, w);
-    else tmem_st16u(scol + 16 * c, z);
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    uint32_t w[16];
+    tmem_ld32_start(scol + 32 * g, x);
+    tmem_ld32_done(x);
+    mk_part<true>(x, ks + 32 * g, vs + 32 * g, rf, pack_f32x2(sh, sh),
+                  g < 2 ? (g == 0 ? b0 : b1) : (g == 2 ? b2 : b3), sum, w);
+    tmem_st16u(scol + 64 * (g >> 1) + 16 * (g & 1), w);
+    if (g & 1) mk_announce(ready + 8 * (g >> 1), lane);
   }
+  float a, b;
+  unpack_f32x2(mk_add2(sum[0], sum[1]), a, b);
+  row.sum += a + b;
+  return hit != 0u;
+}
+
+// The same for a row of which each of four copies takes 32 tokens of the chunk: this
+// thread's are those of `copy` (bits[0]); the other copies' P'' is 0.
+template <bool kMasked>
+__device__ __forceinline__ void mk_softmax32(uint32_t scol, uint32_t ocol, const float *ks,
+                                             const float4 meta, float rowf, uint32_t bits, int copy,
+                                             bool fresh, uint32_t ready, int lane, MkRow &row) {
+  const int eg = __float_as_int(meta.z);
+  const int de = fresh ? 0 : eg - row.eg;
+  row.eg = eg;
+  const float *kc = ks + 32 * copy, *vc = kc + kMkTok, *lg = vc + kMkTok;
+  const uint64_t rf = pack_f32x2(rowf, rowf);
+  uint32_t x[32], w[16];
+  tmem_ld32_start(scol + 32 * copy, x);
+  tmem_ld32_done(x);
+  bool search = true;
+  if (!kMasked) {
+    float mx[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 32; i += 4)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        mx[q] = mk_max3(mx[q], __uint_as_float(x[i + q]), __uint_as_float(x[i + q + 2]));
+    const float most = fmaxf(mx[0], mx[1]) * meta.x * rowf + meta.y;
+    search = __any_sync(0xFFFFFFFFu, !(most - row.m <= kMkLazy));
+  }
+  if (search || de != 0) mk_meet(row, mk_top32<kMasked>(x, kc, lg, rf, bits, -INFINITY), de, fresh, ocol);
+  const float sh = row.m == -INFINITY ? 0.0f : -row.m;
+  uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
+  mk_part<kMasked>(x, kc, vc, rf, pack_f32x2(sh, sh), bits, sum, w);
+  float a, b;
+  unpack_f32x2(mk_add2(sum[0], sum[1]), a, b);
+  row.sum += a + b;
+  // (P'' of the tokens 32 c .. in the columns 64 (c / 2) + 16 (c % 2) ..)
+  tmem_st16u(scol + 64 * (copy >> 1) + 16 * (copy & 1), w);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = 0u;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c)
+    if (c != copy) tmem_st16u(scol + 64 * (c >> 1) + 16 * (c & 1), w);
   tmem_wait_st();
   tc_fence_before();
   __syncwarp();
@@ -494,57 +589,59 @@ __device__ __forceinline__ void mk_softmax32(uint32_t scol, uint32_t ocol, const
     mbar_arrive(ready);
     mbar_arrive(ready + 8);
   }
-  float a, b;
-  unpack_f32x2(mk_add2(sum[0], sum[1]), a, b);
-  row.sum += a + b;
 }
 
-// A query row as two e4m3 pieces into its place in a K-major, 128-byte swizzled tile;
-// returns 2^e |sm_scale| log2(e), which takes its scores to log2 units.
-__device__ __forceinline__ float mk_query_row(const uint4 (&v)[16], float scale2, uint32_t flip,
+// A query row (null: zeros) as two e4m3 pieces into its place in a K-major, 128-byte
+// swizzled tile; returns 2^e |sm_scale| log2(e), which takes its scores to log2 units.
+// The row waits for its largest magnitude in the pieces' own place: of 16 dims, the first
+// 8 where the first piece goes, the others where the second goes.
+__device__ __forceinline__ float mk_query_row(const uint4 *src, float scale2, uint32_t flip,
                                               uint8_t *tile, int row, bool store) {
-  uint32_t mg = 0u;                                    // largest magnitude, as bf16 bits
+  uint4 v[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    mg = __vmaxu2(mg, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
-    mg = __vmaxu2(mg, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+  for (int k = 0; k < 16; ++k) v[k] = src != nullptr ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t mg = 0u;                                    // largest magnitude, as bf16 bits
+  uint8_t *at = tile + row * kHeadDim;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    mg = __vmaxu2(mg, __vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu));
+    mg = __vmaxu2(mg, __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu));
+    if (store)
+      *reinterpret_cast<uint4 *>(at + (k & 1) * 128 * kHeadDim + (((k >> 1) ^ (row & 7)) << 4)) = v[k];
   }
   const uint32_t top = max(mg & 0xFFFFu, mg >> 16);
   const int ex = static_cast<int>(top >> 7);
   int e = ex == 0 ? -126 : ex - 127 - 7;
   e = e < -126 ? -126 : e;
-  // (a row with an infinity or a NaN has no scores)
-  const float back = ex == 255 ? __uint_as_float(0x7FC00000u) : mk_pow2(e) * scale2;
   if (store) {
     const float inv = top == 0u ? 0.0f : mk_pow2(-e);
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 8; ++c) {
+      uint4 *to1 = reinterpret_cast<uint4 *>(at + (c << 4)), *to2 = to1 + 8 * kHeadDim;
+      const uint4 y[2] = {*to1, *to2};
       uint32_t p1[4], p2[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint4 &y = v[2 * c + (j >> 1)];
-        const uint32_t w0 = (j & 1) ? y.z : y.x, w1 = (j & 1) ? y.w : y.y;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w0 = (i & 1) ? y[i >> 1].z : y[i >> 1].x, w1 = (i & 1) ? y[i >> 1].w : y[i >> 1].y;
         const float xs[4] = {bf16_lo(w0) * inv, bf16_hi(w0) * inv, bf16_lo(w1) * inv, bf16_hi(w1) * inv};
-        e4m3_pieces4(xs, p1[j], p2[j]);
-        p1[j] ^= flip;
-        p2[j] ^= flip;
+        e4m3_pieces4(xs, p1[i], p2[i]);
       }
-      const int off = row * kHeadDim + ((c ^ (row & 7)) << 4);
-      *reinterpret_cast<uint4 *>(tile + off) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-      *reinterpret_cast<uint4 *>(tile + 128 * kHeadDim + off) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+      *to1 = make_uint4(p1[0] ^ flip, p1[1] ^ flip, p1[2] ^ flip, p1[3] ^ flip);
+      *to2 = make_uint4(p2[0] ^ flip, p2[1] ^ flip, p2[2] ^ flip, p2[3] ^ flip);
     }
   }
-  return back;
+  // (a row with an infinity or a NaN has no scores)
+  return ex == 255 ? __uint_as_float(0x7FC00000u) : mk_pow2(e) * scale2;
 }
 
 template <bool kPair, int kRows>
 __global__ void __launch_bounds__(kMkThreads, 1)
-attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
+attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
                    const __grid_constant__ CUtensorMap tm_v) {
   using S = MkShape<kPair, kRows>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // (an offset from the array, not a rounded address: the compiler keeps to shared memory)
+  uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t bar0 = smem_addr(smem + S::kOffBar);
   auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -555,23 +652,24 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
   volatile float *sum_s = reinterpret_cast<volatile float *>(smem + S::kOffSum);
   volatile float *ref_s = reinterpret_cast<volatile float *>(smem + S::kOffRef);
   volatile int *eg_s = reinterpret_cast<volatile int *>(smem + S::kOffEg);
-  volatile uint32_t *bad_s = reinterpret_cast<volatile uint32_t *>(smem + S::kOffBad);
+  uint32_t *bad_s = reinterpret_cast<uint32_t *>(smem + S::kOffBad);
   int *pre = reinterpret_cast<int *>(smem + S::kOffPre);
 
   allow_dependents_launch();
   if (tid < S::kBars) {
     uint32_t count = 1;
     const int i = tid;
-    if ((i >= S::kKEmpty && i < S::kKEmpty + S::kKStages) || (i >= S::kVfEmpty && i < S::kVfEmpty + 2))
+    if (i >= S::kVfEmpty && i < S::kVfEmpty + 2)
       count = kPair ? 2 : 1;                           // a commit of each chain that reads it
-    if ((i >= S::kVcEmpty && i < S::kVcEmpty + S::kVStages) || (i >= S::kVfFull && i < S::kVfFull + 2))
-      count = 4;                                       // the converting warps
+    if (i >= S::kVfFull && i < S::kVfFull + 2) count = 4;   // the converting warps
+    if (i >= S::kKvEmpty && i < S::kKvEmpty + S::kStages) count = 4 + (kPair ? 2 : 1);
+    if (i >= S::kScRaw && i < S::kScRaw + kMkScales) count = 32;     // the copying warp's lanes
     if (i >= S::kScEmpty && i < S::kScEmpty + kMkScales) count = kPair ? 8 : 4;
     if ((i >= S::kQFull && i < S::kQFull + 2) || (i >= S::kPReady && i < S::kPReady + 4) ||
         (i >= S::kOEmpty && i < S::kOEmpty + 2) || (i >= S::kSumFull && i < S::kSumFull + 2))
       count = 4;                                       // a chain's softmax or the epilogue
     if (i >= S::kUnitEmpty && i < S::kUnitEmpty + kMkUnits)
-      count = 8 + 4 + 4 + 2 + 1;                       // softmax, epilogue, conversion, MMAs, scales
+      count = 8 + 4 + 2 + 1;                           // softmax, conversion, MMAs, scales
     mbar_init(BAR(i), count);
     fence_mbarrier_init();
   }
@@ -589,6 +687,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
       atomicOr(p.err_flags, KVQ_ERRF_CONTEXT_RANGE);
     const int Lc = L < 0 ? 0 : min(L, p.ctx_limit);
     int w = 0;
+#pragma unroll 1
     for (int t = 0; t < p.T; ++t) w += mk_positions(mk_span<S::kTileRows>(p, Lc, t).X);
     return w * p.H;
   };
@@ -619,21 +718,16 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int total = carry;
-  const int B = max(1, static_cast<int>((static_cast<int64_t>(total) + gridDim.x - 1) / gridDim.x));
+  const int B = max(p.least, static_cast<int>((static_cast<int64_t>(total) + gridDim.x - 1) / gridDim.x));
 
-  // Unit t of this block; the caller's warp (converged) releases its entry.
-  auto take_unit = [&](int t, MkUnit &u) -> bool {
-    const int e = t % kMkUnits;
-    if (!mk_wait_all(BAR(S::kUnitFull + e), (t / kMkUnits) & 1, abort_s)) return false;
-    const int4 *src = reinterpret_cast<const int4 *>(unit_s + e);
-    int4 *dst = reinterpret_cast<int4 *>(&u);
-    dst[0] = src[0];
-    dst[1] = src[1];
-    dst[2] = src[2];
-    dst[3] = src[3];
+  // Unit t of this block is announced (unit_s[t % kMkUnits], read where it is needed:
+  // registers are few); each warp of the other roles releases it once.
+  auto wait_unit = [&](int t) -> bool {
+    return mk_wait_all(BAR(S::kUnitFull + t % kMkUnits), (t / kMkUnits) & 1, abort_s);
+  };
+  auto release_unit = [&](int t) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(BAR(S::kUnitEmpty + e));
-    return true;
+    if (lane == 0) mbar_arrive(BAR(S::kUnitEmpty + t % kMkUnits));
   };
   // chunks of chain a in a unit, and whether it has any
   auto chain_chunks = [&](const MkUnit &u, int a) -> int {
@@ -642,35 +736,34 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
   };
   bool gave_up = false;
 
-  if (warp < kMkWarpEpi) {
+  if (warp < kMkWarpConv) {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
     const int a = warp >> 2, q4 = warp & 3;
     const int lane_row = 32 * q4 + lane;               // TMEM lane
     const int copy = kRows == 32 ? q4 : 0;
     const int trow = (kPair ? 128 * a : 0) + (kRows == 32 ? lane : lane_row);   // of the unit
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     uint32_t steps = 0, done = 0, seq = 0;             // chunks and units of this chain, chunks of all
+    uint32_t sc = 0, sc_par = 0;                       // place in the scales' ring
     uint32_t q_units = 0, q_units1 = 0;                // units with rows of chain a (split: 0 and 1)
     for (int t = 0;; ++t) {
-      MkUnit u;
-      if (!take_unit(t, u)) {
+      if (!wait_unit(t)) {
         gave_up = true;
         break;
       }
-      if (u.n == 0) break;
-      const int n = chain_chunks(u, a);
+      const MkUnit &u = unit_s[t % kMkUnits];
+      const int un = u.n, n = chain_chunks(u, a);
+      if (un == 0) break;
       float rowf = 0.0f;
       if (n > 0) {
         // the row's query; the tile's space is free once the last unit's products
         // with it are done.  (Where the chains share a tile, chain 0 stores it.)
         const int m = u.row0 + trow;
-        uint4 v[16];
-        const int i = m / p.G;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + ((static_cast<int64_t>(u.r) * p.R + i) * p.Hq + u.h * p.G + (m - i * p.G)) * kHeadDim);
-#pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = m < p.M ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        const int i = mk_query(p, m);
+        const uint4 *src = m < p.M ? reinterpret_cast<const uint4 *>(
+            p.q + ((static_cast<int64_t>(u.r) * p.R + i) * p.Hq + u.h * p.G + (m - i * p.G)) * kHeadDim)
+            : nullptr;
         const bool store = kPair || a == 0;
         bool ok = true;
         if (kPair && q_units > 0) ok = mk_wait_all(BAR(S::kQEmpty + a), (q_units - 1) & 1, abort_s);
@@ -682,7 +775,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
           gave_up = true;
           break;
         }
-        rowf = mk_query_row(v, p.scale2, p.flip, smem + S::kOffQ + (kPair ? a : 0) * 2 * S::kQPiece,
+        rowf = mk_query_row(src, p.scale2, p.flip, smem + S::kOffQ + (kPair ? a : 0) * 2 * S::kQPiece,
                             kRows == 32 ? 32 * copy + lane : lane_row, store);
         if (store) {
           fence_proxy_async_smem();
@@ -691,17 +784,18 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
         }
       }
       q_units += kPair ? n > 0 : 1;
-      q_units1 += u.n >= 2;
+      q_units1 += un >= 2;
       const MkSeen seen = mk_seen(p, u, u.row0 + trow);
       // the warp's first and last row
-      const int hi0 = __shfl_sync(0xFFFFFFFFu, seen.hi, 0), lo31 = __shfl_sync(0xFFFFFFFFu, seen.lo, 31);
-      const int hi_first = mk_seen(p, u, u.row0).hi, lo_last = mk_seen(p, u, u.row0 + S::kTileRows - 1).lo;
+      const MkWhole whole = mk_whole(p, u, __shfl_sync(0xFFFFFFFFu, seen.hi, 0),
+                                     __shfl_sync(0xFFFFFFFFu, seen.lo, 31));
+      const MkWhole all_whole = mk_unit_whole<S::kTileRows>(p, u);
       MkRow row;
       bool nan_row = false, fresh = true;
-      for (int k = 0; k < u.n; ++k, ++seq) {
+#pragma unroll 1
+      for (int k = 0; k < un; ++k, ++seq, sc_par ^= sc == kMkScales - 1, sc = sc == kMkScales - 1 ? 0 : sc + 1) {
         if (!kPair && (k & 1) != a) continue;
-        const uint32_t sb = seq % kMkScales;
-        bool ok = mk_wait_all(BAR(S::kScFull + sb), (seq / kMkScales) & 1, abort_s);
+        bool ok = mk_wait_all(BAR(S::kScFull + sc), sc_par, abort_s);
         if (ok && n > 0) ok = mk_wait_all(BAR(S::kSFull + a), steps & 1, abort_s);
         if (!ok) {
           gave_up = true;
@@ -709,53 +803,48 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
         }
         if (n > 0) {
           tc_fence_after();
+          const float *ks = reinterpret_cast<const float *>(smem + S::kOffSc) + sc * 3 * kMkTok;
+          const float4 meta = reinterpret_cast<const float4 *>(smem + S::kOffMeta)[sc];
+          const uint32_t ready = BAR(S::kPReady + 2 * a);
+          const uint32_t scol = tl + mk_s(a), ocol = tl + mk_o(a);
           const int x0 = (u.c0 + k) * kMkTok;
-          const float *ks = reinterpret_cast<const float *>(smem + S::kOffSc) + sb * 2 * kMkTok;
-          const float *vs = ks + kMkTok;
-          const float4 meta = reinterpret_cast<const float4 *>(smem + S::kOffMeta)[sb];
-          uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-          // (edge: some row of the unit does not see all of the chunk)
-          const bool edge = !mk_whole(p, hi_first, lo_last, u.base, x0, kMkTok);
-          const bool whole = mk_whole(p, hi0, lo31, u.base, x0, kMkTok);
-          if (!whole) {
-            if (kRows == 32) {
-              bits[0] = seen.bits(p, x0 + 32 * copy, u.X);
-            } else {
-#pragma unroll
-              for (int g = 0; g < 4; ++g) bits[g] = seen.bits(p, x0 + 32 * g, u.X);
-            }
-          }
-          if (edge) {
-            // value rows with a NaN code, which the conversion has cleared
+          uint32_t bad[4] = {0u, 0u, 0u, 0u};
+          if (!all_whole.at(k)) {
+            // some row of the unit does not see all of the chunk: value rows with a NaN code
+            // or such a scale have been cleared
             if (!mk_wait_all(BAR(S::kVfFull + (seq & 1)), (seq >> 1) & 1, abort_s)) {
               gave_up = true;
               break;
             }
-            const volatile uint32_t *bad = bad_s + 4 * (seq & 1);
-            if (kRows == 32) {
-              nan_row |= (bad[copy] & bits[0]) != 0u;
-            } else {
+            const uint32_t *codes = bad_s + 4 * (seq & 1), *scales = bad_s + 8 + 4 * sc;
+            const bool some = meta.w != 0.0f;
 #pragma unroll
-              for (int g = 0; g < 4; ++g) nan_row |= (bad[g] & bits[g]) != 0u;
-            }
+            for (int g = 0; g < 4; ++g) bad[g] = codes[g] | (some ? scales[g] : 0u);
           }
-          const uint32_t ready = BAR(S::kPReady + 2 * a);
-          if (kRows == 32)
-            mk_softmax32(tl + mk_s(a), tl + mk_o(a), ks, vs, meta, rowf, bits[0], copy, fresh, ready,
-                         lane, row);
-          else if (whole)
-            mk_softmax128<false>(tl + mk_s(a), tl + mk_o(a), ks, vs, meta, rowf, bits, fresh, ready,
-                                 lane, row);
-          else
-            mk_softmax128<true>(tl + mk_s(a), tl + mk_o(a), ks, vs, meta, rowf, bits, fresh, ready,
-                                lane, row);
+          const bool see_all = whole.at(k);
+          if (kRows == 32) {
+            const uint32_t bits = see_all ? 0xFFFFFFFFu : seen.bits(p, x0 + 32 * copy, u.X);
+            const uint32_t mine = copy < 2 ? (copy == 0 ? bad[0] : bad[1]) : (copy == 2 ? bad[2] : bad[3]);
+            nan_row |= (mine & bits) != 0u;
+            if (see_all)
+              mk_softmax32<false>(scol, ocol, ks, meta, rowf, bits, copy, fresh, ready, lane, row);
+            else
+              mk_softmax32<true>(scol, ocol, ks, meta, rowf, bits, copy, fresh, ready, lane, row);
+          } else if (see_all) {
+            nan_row |= (bad[0] | bad[1] | bad[2] | bad[3]) != 0u;
+            mk_softmax128(scol, ocol, ks, meta, rowf, fresh, ready, lane, row);
+          } else {
+            nan_row |= mk_softmax128_masked(p, seen, x0, u.X, bad, scol, ocol, ks, meta, rowf, fresh,
+                                            ready, lane, row);
+          }
           fresh = false;
           ++steps;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(S::kScEmpty + sb));
+        if (lane == 0) mbar_arrive(BAR(S::kScEmpty + sc));
       }
       if (gave_up) break;
+      release_unit(t);
       if (n == 0) continue;
       // the row's statistics, once the epilogue has read the last unit's
       if (done > 0 && !mk_wait_all(BAR(S::kOEmpty + a), (done - 1) & 1, abort_s)) {
@@ -769,24 +858,19 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
       if (lane == 0) mbar_arrive(BAR(S::kSumFull + a));
       ++done;
     }
-  } else if (warp < kMkWarpConv) {
-    // ------------------------------------------------------------ epilogue
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+  } else if (warp < kMkWarpLoad) {
+    // ------------------------- value codes to f16 values, and the epilogue
+    // A unit's epilogue comes after the conversion of the next one's first chunk.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
     const int q4 = warp & 3;
     const int lane_row = 32 * q4 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     uint32_t par = 0;                                  // barrier parities, bit a
-    auto out_row = [&](const MkUnit &u, int m) -> uint16_t * {
-      const int i = m / p.G;
-      return p.out + ((static_cast<int64_t>(u.r) * p.R + i) * p.Hq + u.h * p.G + (m - i * p.G)) * kHeadDim;
+    auto out_row = [&](int r, int h, int m) -> uint16_t * {
+      const int i = mk_query(p, m);
+      return p.out + ((static_cast<int64_t>(r) * p.R + i) * p.Hq + h * p.G + (m - i * p.G)) * kHeadDim;
     };
-    for (int t = 0;; ++t) {
-      MkUnit u;
-      if (!take_unit(t, u)) {
-        gave_up = true;
-        break;
-      }
-      if (u.n == 0) break;
+    auto epilogue = [&](const MkUnit &u) -> bool {
       const int64_t piece = static_cast<int64_t>(u.slot) * S::kTileRows;
 #pragma unroll 1
       for (int a = 0; a < (kPair ? 2 : 1); ++a) {
@@ -798,8 +882,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
           got = got && mk_wait_all(BAR(S::kSumFull + 1), par >> 1, abort_s) &&
                 mk_wait_all(BAR(S::kOFull + 1), par >> 1, abort_s);
         if (!got) {
-          gave_up = true;
-          break;
+          return false;
         }
         tc_fence_after();
         par ^= 1u << a;
@@ -854,7 +937,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
             }
           }
         };
-        uint16_t *dst = out_row(u, mine ? m : 0);
+        uint16_t *dst = out_row(u.r, u.h, mine ? m : 0);
         const int64_t prow = piece + (kPair ? 128 * a : 0) + row;
         if (kRows == 32) {
           float *xs = reinterpret_cast<float *>(smem + S::kOffX);   // [copy][32 dims][32 rows]
@@ -914,8 +997,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
           if (both) mbar_arrive(BAR(S::kOEmpty + 1));
         }
       }
-      if (gave_up) break;
-      if (u.direct) continue;
+      if (u.direct) return true;
       // the block whose piece comes last joins the unit's pieces
       __threadfence();
       named_barrier(1, 128);
@@ -929,103 +1011,143 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
       }
       named_barrier(1, 128);
       if (*ticket_s) {
-        const int rows = min(S::kTileRows, p.M - u.row0);
+        // a warp per row: a lane per piece for the weights, then four dims a lane over the
+        // pieces, eight loads under way
+        const int rows = min(S::kTileRows, p.M - u.row0), b_first = u.b_first, pieces = u.b_last - b_first + 1;
+        auto place = [&](int b, int r) -> int64_t {
+          return static_cast<int64_t>(2 * (b_first + b) + (b == 0 ? 1 : 0)) * S::kTileRows + r;
+        };
+#pragma unroll 1
         for (int r = q4; r < rows; r += 4) {
           float top = -INFINITY, all = 0.0f;
           float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-          for (int b = u.b_first; b <= u.b_last; ++b) {
-            const int64_t at = static_cast<int64_t>(2 * b + (b == u.b_first ? 1 : 0)) * S::kTileRows + r;
-            const float2 ml = __ldcg(p.ml_part + at);
-            const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.o_part + at * kHeadDim) + lane);
-            const float next = fmaxf(top, ml.x);
-            const float f = top == -INFINITY ? 0.0f : mk_ex2(top - next);
+#pragma unroll 1
+          for (int b0 = 0; b0 < pieces; b0 += 32) {
             // (a part that saw nothing has no reference and a sum of 0, or NaN)
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (b0 + lane < pieces) ml = __ldcg(p.ml_part + place(b0 + lane, r));
+            float next = fmaxf(top, ml.x);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+              next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, off));
             const float w = ml.x == -INFINITY ? ml.y : mk_ex2(ml.x - next) * ml.y;
-            all = all * f + w;
-            y.x = y.x * f + o.x * w;
-            y.y = y.y * f + o.y * w;
-            y.z = y.z * f + o.z * w;
-            y.w = y.w * f + o.w * w;
+            const float f = top == -INFINITY ? 0.0f : mk_ex2(top - next);
+            float sum = w;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+            all = all * f + sum;
+            y.x *= f;
+            y.y *= f;
+            y.z *= f;
+            y.w *= f;
             top = next;
+            const int n = min(32, pieces - b0);
+#pragma unroll 1
+            for (int b = 0; b < n; b += 8) {
+              float4 o[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                o[i] = b + i < n ? __ldcg(reinterpret_cast<const float4 *>(
+                                              p.o_part + place(b0 + b + i, r) * kHeadDim) + lane)
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float wi = __shfl_sync(0xFFFFFFFFu, w, (b + i) & 31);
+                y.x = fmaf(o[i].x, wi, y.x);
+                y.y = fmaf(o[i].y, wi, y.y);
+                y.z = fmaf(o[i].z, wi, y.z);
+                y.w = fmaf(o[i].w, wi, y.w);
+              }
+            }
           }
           const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-          *reinterpret_cast<uint2 *>(out_row(u, u.row0 + r) + 4 * lane) =
+          *reinterpret_cast<uint2 *>(out_row(u.r, u.h, u.row0 + r) + 4 * lane) =
               make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
         }
       }
-    }
-    // units whose rows see no token: zero rows, spread over the grid
-    if (!gave_up) {
-      const int units = p.N * p.H * p.T;
-      for (int x = blockIdx.x * 4 + q4; x < units; x += gridDim.x * 4) {
-        const int t = x % p.T, rh = x / p.T, h = rh % p.H, r = rh / p.H;
-        if (mk_span<S::kTileRows>(p, mk_len(p, r), t).X > 0) continue;
-        MkUnit u;
-        u.r = r;
-        u.h = h;
-        for (int m = t * S::kTileRows; m < min(p.M, (t + 1) * S::kTileRows); ++m)
-          *reinterpret_cast<uint2 *>(out_row(u, m) + 4 * lane) = make_uint2(0u, 0u);
+      return true;
+    };
+    // chunk k of a unit, the seq-th of all: thread j converts token j: dims 64 b + 8 c .. in
+    // block b, MN-major and 128-byte swizzled; tokens past the unit's are cleared
+    const int j = lane_row;
+    auto convert = [&](const MkUnit &u, int k, uint32_t seq, bool whole) -> bool {
+      const uint32_t b = seq % S::kStages;
+      bool ok = mk_wait_all(BAR(S::kKvFull + b), (seq / S::kStages) & 1, abort_s);
+      if (ok && seq >= 2) ok = mk_wait_all(BAR(S::kVfEmpty + (seq & 1)), ((seq >> 1) - 1) & 1, abort_s);
+      if (!ok) return false;
+      const int x0 = (u.c0 + k) * kMkTok;
+      const uint8_t *src = smem + S::kOffKv + b * S::kStage + p.v_off + (j >> 3) * p.group + (j & 7) * 128;
+      uint8_t *dst = smem + S::kOffVf + (seq & 1) * S::kVfBytes + j * 128;
+      bool keep = x0 + j < u.X;
+      if (!whole) {
+        bool bad = false;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(src + ((c ^ (j & 7)) << 4));
+          bad |= (__vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                  __vcmpeq4(w.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0u;
+        }
+        const uint32_t word = __ballot_sync(0xFFFFFFFFu, keep && bad);
+        if (lane == 0) bad_s[4 * (seq & 1) + q4] = word;
+        keep = keep && !bad;
       }
-    }
-  } else if (warp < kMkWarpLoad) {
-    // ------------------------------------------- value codes to f16 values
-    // Thread j converts token j: dims 64 b + 8 c .. in block b, MN-major and 128-byte
-    // swizzled.  Tokens past the unit's are cleared.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
-    const int q4 = warp & 3, j = 32 * q4 + lane;
+#pragma unroll 4
+      for (int c = 0; c < 8; ++c) {
+        uint4 w = *reinterpret_cast<const uint4 *>(src + ((c ^ (j & 7)) << 4));
+        if (!keep) w = make_uint4(0u, 0u, 0u, 0u);
+        const uint4 lo = make_uint4(e4m3x2_to_f16x2(w.x & 0xFFFFu), e4m3x2_to_f16x2(w.x >> 16),
+                                    e4m3x2_to_f16x2(w.y & 0xFFFFu), e4m3x2_to_f16x2(w.y >> 16));
+        const uint4 hi = make_uint4(e4m3x2_to_f16x2(w.z & 0xFFFFu), e4m3x2_to_f16x2(w.z >> 16),
+                                    e4m3x2_to_f16x2(w.w & 0xFFFFu), e4m3x2_to_f16x2(w.w >> 16));
+        uint8_t *blk = dst + (c >> 2) * (S::kVfBytes / 2);
+        const int c0 = (2 * c) & 7;
+        *reinterpret_cast<uint4 *>(blk + ((c0 ^ (j & 7)) << 4)) = lo;
+        *reinterpret_cast<uint4 *>(blk + (((c0 + 1) ^ (j & 7)) << 4)) = hi;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(BAR(S::kKvEmpty + b));
+        mbar_arrive(BAR(S::kVfFull + (seq & 1)));
+      }
+      return true;
+    };
     uint32_t seq = 0;
-    for (int t = 0; !gave_up; ++t) {
-      MkUnit u;
-      if (!take_unit(t, u)) {
+    int last = -1;                                     // the unit whose epilogue is to come
+    for (int t = 0;; ++t) {
+      if (!wait_unit(t)) {
         gave_up = true;
         break;
       }
-      if (u.n == 0) break;
-      const int hi_first = mk_seen(p, u, u.row0).hi, lo_last = mk_seen(p, u, u.row0 + S::kTileRows - 1).lo;
-      for (int k = 0; k < u.n; ++k, ++seq) {
-        const uint32_t b = seq % S::kVStages;
-        bool ok = mk_wait_all(BAR(S::kVcFull + b), (seq / S::kVStages) & 1, abort_s);
-        if (ok && seq >= 2) ok = mk_wait_all(BAR(S::kVfEmpty + (seq & 1)), ((seq >> 1) - 1) & 1, abort_s);
-        if (!ok) {
-          gave_up = true;
-          break;
+      const MkUnit &u = unit_s[t % kMkUnits];
+      const int un = u.n;
+      const MkWhole all_whole = mk_unit_whole<S::kTileRows>(p, u);
+#pragma unroll 1
+      for (int k = 0; k < max(un, 1) && !gave_up; ++k) {
+        if (un != 0) {
+          gave_up = !convert(u, k, seq, all_whole.at(k));
+          ++seq;
         }
-        const int x0 = (u.c0 + k) * kMkTok;
-        const uint8_t *src = smem + S::kOffV + b * S::kCode + j * kHeadDim;
-        uint8_t *dst = smem + S::kOffVf + (seq & 1) * S::kVfBytes + j * 128;
-        bool keep = x0 + j < u.X;
-        if (!mk_whole(p, hi_first, lo_last, u.base, x0, kMkTok)) {
-          bool bad = false;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(src + ((c ^ (j & 7)) << 4));
-            bad |= (__vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                    __vcmpeq4(w.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0u;
-          }
-          const uint32_t word = __ballot_sync(0xFFFFFFFFu, keep && bad);
-          if (lane == 0) bad_s[4 * (seq & 1) + q4] = word;
-          keep = keep && !bad;
+        if (k == 0 && last >= 0 && !gave_up) {
+          gave_up = !epilogue(unit_s[last % kMkUnits]);
+          release_unit(last);
         }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint4 w = *reinterpret_cast<const uint4 *>(src + ((c ^ (j & 7)) << 4));
-          if (!keep) w = make_uint4(0u, 0u, 0u, 0u);
-          const uint4 lo = make_uint4(e4m3x2_to_f16x2(w.x & 0xFFFFu), e4m3x2_to_f16x2(w.x >> 16),
-                                      e4m3x2_to_f16x2(w.y & 0xFFFFu), e4m3x2_to_f16x2(w.y >> 16));
-          const uint4 hi = make_uint4(e4m3x2_to_f16x2(w.z & 0xFFFFu), e4m3x2_to_f16x2(w.z >> 16),
-                                      e4m3x2_to_f16x2(w.w & 0xFFFFu), e4m3x2_to_f16x2(w.w >> 16));
-          uint8_t *blk = dst + (c >> 2) * (S::kVfBytes / 2);
-          const int c0 = (2 * c) & 7;
-          *reinterpret_cast<uint4 *>(blk + ((c0 ^ (j & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4 *>(blk + (((c0 + 1) ^ (j & 7)) << 4)) = hi;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(BAR(S::kVcEmpty + b));
-          mbar_arrive(BAR(S::kVfFull + (seq & 1)));
-        }
+      }
+      if (gave_up || un == 0) break;
+      last = t;
+    }
+    // units whose rows see no token: zero rows, a request per block
+#pragma unroll 1
+    for (int r = blockIdx.x; r < p.N && !gave_up; r += gridDim.x) {
+      const int L = mk_len(p, r);
+#pragma unroll 1
+      for (int t = 0; t < p.T; ++t) {
+        if (mk_span<S::kTileRows>(p, L, t).X > 0) break;           // (later rows see no less)
+#pragma unroll 1
+        for (int m = t * S::kTileRows + q4; m < min(p.M, (t + 1) * S::kTileRows); m += 4)
+#pragma unroll 1
+          for (int h = 0; h < p.H; ++h)
+            *reinterpret_cast<uint2 *>(out_row(r, h, m) + 4 * lane) = make_uint2(0u, 0u);
       }
     }
   } else {
@@ -1034,256 +1156,260 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
       // --------------------------------------------- units, copies of codes
       int x = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * B, static_cast<int64_t>(total)));
       const int x_end = static_cast<int>(min(static_cast<int64_t>(x) + B, static_cast<int64_t>(total)));
-      // the next piece of the block's range with chunks (n = 0: none left)
-      auto next_unit = [&]() -> MkUnit {
-        MkUnit u;
-        u.n = 0;
+      // the unit that position x is in or in front of: request, head, tile, where it starts
+      int lo = 0, h = 0, t = 0, at = 0, L = 0;
+      if (x < x_end) {
+        int hi = p.N - 1;                              // the last request with pre[r] <= x
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (pre[mid] <= x) lo = mid;
+          else hi = mid - 1;
+        }
+        L = mk_len(p, lo);
+        const unsigned W = static_cast<unsigned>(pre[lo + 1] - pre[lo]) / static_cast<unsigned>(p.H);
+        h = static_cast<int>(static_cast<unsigned>(x - pre[lo]) / W);
+        at = pre[lo] + h * static_cast<int>(W);
+      }
+      // the next piece of the block's range with chunks, into the announcements' entry u;
+      // returns its chunks (0: none left)
+      auto next_unit = [&](MkUnit &u) -> int {
+        int n = 0;
+#pragma unroll 1
         while (x < x_end) {
-          int lo = 0, hi = p.N - 1;                    // the last request with pre[r] <= x
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (pre[mid] <= x) lo = mid;
-            else hi = mid - 1;
-          }
-          const int L = mk_len(p, lo), W = (pre[lo + 1] - pre[lo]) / p.H;
-          const int h = (x - pre[lo]) / W;
-          int at = pre[lo] + h * W;                    // where unit t starts
-          MkSpan s{0, 0, 0};
-          int t = 0, V = 0;
-          for (;; ++t) {
-            s = mk_span<S::kTileRows>(p, L, t);
-            V = mk_positions(s.X);
-            if (x < at + V || t == p.T - 1) break;
+          const MkSpan s = mk_span<S::kTileRows>(p, L, t);
+          const int V = mk_positions(s.X), ut = t, uh = h, ur = lo, ua = at, uL = L;
+          if (x >= at + V || at + V <= x_end) {        // (nothing of it is left after this)
             at += V;
-          }
-          const int first = at + kMkCharge, end = min(at + V, x_end), from = max(x, first);
-          x = max(end, x + 1);
-          if (from >= end) continue;
-          u.r = lo;
-          u.h = h;
-          u.row0 = t * S::kTileRows;
-          u.c0 = from - first;
-          u.n = end - from;
-          u.X = s.X;
-          u.s16 = s.s16;
-          u.shift = s.shift;
-          u.base = L - p.R;
-          u.direct = u.n == V - kMkCharge;
-          u.b_first = first / B;
-          u.b_last = (at + V - 1) / B;
-          u.slot = 2 * static_cast<int>(blockIdx.x) + (static_cast<int>(blockIdx.x) == u.b_first ? 1 : 0);
-          u.index = (lo * p.H + h) * p.T + t;
-          break;
-        }
-        return u;
-      };
-      bool ok = true;
-      int published = 0;
-      auto publish = [&](const MkUnit &u) {
-        const int e = published % kMkUnits;
-        if (published >= kMkUnits &&
-            !mk_wait_all(BAR(S::kUnitEmpty + e), (published / kMkUnits - 1) & 1, abort_s)) {
-          ok = false;
-          return;
-        }
-        if (lane == 0) {
-          unit_s[e] = u;
-          mbar_arrive(BAR(S::kUnitFull + e));
-        }
-        __syncwarp();
-        ++published;
-      };
-      int32_t *ids = reinterpret_cast<int32_t *>(smem + S::kOffIds);
-      const int boxes = kMkTok / p.box;
-      MkUnit f = next_unit(), u = f;                   // of the page ids, of the copies
-      publish(f);
-      int fk = 0;
-      // page ids of the next chunk of f (a commit group in any case)
-      auto fetch = [&](uint32_t slot) {
-        if (f.n != 0 && ok) {
-          const int xt = (f.c0 + fk) * kMkTok + lane * p.box;
-          if (lane < boxes) {
-            const bool need = xt < f.X;
-            const int32_t *src = p.tables + static_cast<int64_t>(f.r) * p.width +
-                                 (need ? f.pos(xt) >> p.log2_bs : 0);
-            cp_async_4(ids + slot * kMkMaxBoxes + lane, src, need ? 4u : 0u);
-          }
-          if (++fk == f.n) {
-            f = next_unit();
-            publish(f);
-            fk = 0;
-          }
-        }
-        cp_async_commit();
-      };
-#pragma unroll 1
-      for (uint32_t i = 0; i < kMkIdAhead; ++i) fetch(i);
-      const uint64_t pol = l2_policy_evict_normal();
-      const int mask = (1 << p.log2_bs) - 1;
-      uint32_t seq = 0, k_issued = 0, v_issued = 0;
-      bool bad = false;
-      int unit_no = 0;
-      while (u.n != 0 && ok) {
-        for (int k = 0; k < u.n && ok; ++k, ++seq) {
-          fetch((seq + kMkIdAhead) % (kMkIdAhead + 1));
-          cp_async_wait<kMkIdAhead>();
-          __syncwarp();
-          if (lane == 0) {
-            const int32_t *cid = ids + (seq % (kMkIdAhead + 1)) * kMkMaxBoxes;
-            const int x0 = (u.c0 + k) * kMkTok;
-#pragma unroll 1
-            for (int kv = 0; kv < 2 && ok; ++kv) {
-              const uint32_t ring = kv == 0 ? S::kKStages : S::kVStages;
-              const uint32_t b = seq % ring, round = seq / ring;
-              const uint32_t full = BAR((kv == 0 ? S::kKFull : S::kVcFull) + b);
-              if (round > 0)
-                ok = mk_wait(BAR((kv == 0 ? S::kKEmpty : S::kVcEmpty) + b), (round - 1) & 1, abort_s);
-              if (!ok) break;
-              const uint32_t dst = smem_addr(smem + (kv == 0 ? S::kOffK : S::kOffV) + b * S::kCode);
-              uint32_t bytes = 0;
-#pragma unroll 1
-              for (int i = 0; i < boxes; ++i) {
-                const int xt = x0 + i * p.box;
-                if (xt >= u.X) break;
-                const uint32_t page = static_cast<uint32_t>(cid[i]);
-                if (page >= static_cast<uint32_t>(p.num_blocks)) {
-                  bad = true;
-                  continue;
-                }
-                const int slot = static_cast<int>((page << p.log2_bs) | (u.pos(xt) & mask));
-                tma_load_3d_hint(dst + i * p.box * kHeadDim, kv == 0 ? &tm_k : &tm_v, 0, u.h, slot, full, pol);
-                bytes += p.box * kHeadDim;
+            if (++t == p.T) {
+              t = 0;
+              if (++h == p.H) {
+                h = 0;
+                do ++lo;
+                while (lo < p.N && pre[lo + 1] <= at);
+                if (lo < p.N) L = mk_len(p, lo);
               }
-              mbar_arrive_expect_tx(full, bytes);
-              if (kv == 0) ++k_issued;
-              else ++v_issued;
             }
           }
-          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (x >= ua + V) continue;
+          const int first = ua + kMkCharge, end = min(ua + V, x_end), from = max(x, first);
+          x = end;
+          if (from >= end) continue;
+          n = end - from;
+          if (lane == 0) {
+            u.r = ur;
+            u.h = uh;
+            u.row0 = ut * S::kTileRows;
+            u.c0 = from - first;
+            u.X = s.X;
+            u.s16 = s.s16;
+            u.shift = s.shift;
+            u.base = uL - p.R;
+            u.direct = n == V - kMkCharge;
+            const int b_first = static_cast<int>(static_cast<unsigned>(first) / static_cast<unsigned>(B));
+            u.b_first = b_first;
+            u.b_last = static_cast<int>(static_cast<unsigned>(ua + V - 1) / static_cast<unsigned>(B));
+            u.slot = 2 * static_cast<int>(blockIdx.x) + (static_cast<int>(blockIdx.x) == b_first ? 1 : 0);
+            u.index = (ur * p.H + uh) * p.T + ut;
+          }
+          break;
         }
-        // the next unit, announced by now
-        ++unit_no;
-        if (ok && unit_no < published) {
-          const int4 *src = reinterpret_cast<const int4 *>(unit_s + unit_no % kMkUnits);
-          int4 *dst = reinterpret_cast<int4 *>(&u);
-          dst[0] = src[0];
-          dst[1] = src[1];
-          dst[2] = src[2];
-          dst[3] = src[3];
-        } else {
-          u.n = 0;
+        if (lane == 0) u.n = n;
+        __syncwarp();
+        return n;
+      };
+      int32_t *ids = reinterpret_cast<int32_t *>(smem + S::kOffIds);
+      const int boxes = kMkTok / p.box, log2_box = 31 - __clz(p.box), mask = (1 << p.log2_bs) - 1;
+      const uint64_t pol = l2_policy_evict_normal();
+      // What is kept of the unit whose page ids are asked for (f) and of the one whose
+      // chunks are copied.
+      int fn = 0, fk = 0, fx = 0, fX = 0, fs16 = 0, fshift = 0;
+      const int32_t *ftable = p.tables;
+      int un = 0, k = 0, x0 = 0, uX = 0, us16 = 0, ushift = 0, uh = 0;
+      int published = 0, taken = 0;
+      bool ok = true, more = true, bad = false;
+      uint32_t issued = 0;
+#pragma unroll 1
+      for (int seq = -kMkIdAhead;; ++seq) {
+        // page ids of the chunk kMkIdAhead ahead (a commit group in any case); its unit is
+        // announced when its first chunk's are asked for
+        if (more && fk == fn) {
+          const int e = published % kMkUnits;
+          if (published >= kMkUnits)
+            ok = mk_wait_all(BAR(S::kUnitEmpty + e), (published / kMkUnits - 1) & 1, abort_s);
+          if (!ok) break;
+          fn = next_unit(unit_s[e]);
+          fk = 0;
+          more = fn != 0;
+          if (lane == 0) mbar_arrive(BAR(S::kUnitFull + e));
+          const MkUnit &f = unit_s[e];
+          fx = f.c0 * kMkTok + lane * p.box;
+          fX = f.X;
+          fs16 = f.s16;
+          fshift = f.shift;
+          if (more) ftable = p.tables + static_cast<int64_t>(f.r) * p.width;
+          ++published;
         }
+        if (more) {
+          if (lane < boxes) {
+            const bool need = fx < fX;
+            const int pos = fx < fs16 ? fx : fx + fshift;
+            cp_async_4(ids + ((seq + kMkIdAhead) % (kMkIdAhead + 1)) * kMkMaxBoxes + lane,
+                       ftable + (need ? pos >> p.log2_bs : 0), need ? 4u : 0u);
+          }
+          fx += kMkTok;
+          ++fk;
+        }
+        cp_async_commit();
+        if (seq < 0) continue;
+        if (k == un) {                                 // the next unit (announced by now)
+          const MkUnit &u = unit_s[taken % kMkUnits];
+          un = u.n;
+          x0 = u.c0 * kMkTok;
+          uX = u.X;
+          us16 = u.s16;
+          ushift = u.shift;
+          uh = u.h;
+          ++taken;
+          k = 0;
+          if (un == 0) break;
+        }
+        cp_async_wait<kMkIdAhead>();
+        __syncwarp();
+        // lane i: the first slot of the chunk's box i (-1: none)
+        int slot = -1;
+        {
+          const int xt = x0 + lane * p.box;
+          if (lane < boxes && xt < uX) {
+            const uint32_t page = static_cast<uint32_t>(ids[(seq % (kMkIdAhead + 1)) * kMkMaxBoxes + lane]);
+            const int pos = xt < us16 ? xt : xt + ushift;
+            if (page < static_cast<uint32_t>(p.num_blocks))
+              slot = static_cast<int>((page << p.log2_bs) | (pos & mask));
+            else
+              bad = true;
+          }
+        }
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+        const uint32_t n = seq, b = n % S::kStages, bs = n % kMkScales;
+        if (n >= S::kStages)
+          ok = mk_wait_all(BAR(S::kKvEmpty + b), (n / S::kStages - 1) & 1, abort_s);
+        if (ok && n >= kMkScales)
+          ok = mk_wait_all(BAR(S::kScEmpty + bs), (n / kMkScales - 1) & 1, abort_s);
+        if (!ok) break;
+        int z[kMkMaxBoxes];                            // in groups of 8 slots
+#pragma unroll
+        for (int i = 0; i < kMkMaxBoxes; ++i) z[i] = __shfl_sync(0xFFFFFFFFu, slot >> 3, i);
+        if (mk_elect()) {
+          const uint32_t dst = smem_addr(smem + S::kOffKv) + b * S::kStage;
+          const uint32_t full = BAR(S::kKvFull + b), step = p.box / 8 * p.group;
+          mbar_arrive_expect_tx(full, __popc(have) * 2 * p.box * kHeadDim);
+#pragma unroll 1
+          for (int plane = 0; plane <= p.two_maps; ++plane) {
+            const CUtensorMap *map = plane == 0 ? &tm : &tm_v;
+#pragma unroll
+            for (int i = 0; i < kMkMaxBoxes; ++i)
+              if ((have >> i) & 1u)
+                mk_load_box(dst + plane * p.v_off + i * step, map, z[i], uh, full, pol);
+          }
+        }
+        __syncwarp();
+        {
+          // the scales of the tokens 4 lane .. 4 lane + 3 (of one box)
+          const int first = __shfl_sync(0xFFFFFFFFu, slot, 4 * lane >> log2_box);
+          const int left = first < 0 ? 0 : uX - x0 - 4 * lane;
+          const int64_t at = left > 0 ? (static_cast<int64_t>(first) + (4 * lane & (p.box - 1))) * p.H + uh : 0;
+          const float *kp = p.k_scales + at, *vp = p.v_scales + at;
+          float *ks = reinterpret_cast<float *>(smem + S::kOffSc) + bs * 3 * kMkTok + 4 * lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t size = i < left ? 4u : 0u;
+            const int of = i < left ? i * p.H : 0;
+            cp_async_4(ks + i, kp + of, size);
+            cp_async_4(ks + kMkTok + i, vp + of, size);
+          }
+          mk_arrive_copies(BAR(S::kScRaw + bs));
+        }
+        x0 += kMkTok;
+        ++k;
+        ++issued;
       }
       cp_async_wait<0>();
       gave_up = !ok;
+      bad = __any_sync(0xFFFFFFFFu, bad);
       if (lane == 0) {
         if (bad && p.err_flags) atomicOr(p.err_flags, KVQ_ERRF_BLOCK_RANGE);
         // copies in flight land before the block leaves
-        for (uint32_t v = k_issued > S::kKStages ? k_issued - S::kKStages : 0; v < k_issued; ++v)
-          mbar_wait_sleep_bounded(BAR(S::kKFull + v % S::kKStages), (v / S::kKStages) & 1);
-        for (uint32_t v = v_issued > S::kVStages ? v_issued - S::kVStages : 0; v < v_issued; ++v)
-          mbar_wait_sleep_bounded(BAR(S::kVcFull + v % S::kVStages), (v / S::kVStages) & 1);
+        for (uint32_t v = issued > S::kStages ? issued - S::kStages : 0; v < issued; ++v)
+          mbar_wait_sleep_bounded(BAR(S::kKvFull + v % S::kStages), (v / S::kStages) & 1);
       }
     } else if (warp == kMkWarpScale) {
       // -------------------------------------------------------------- scales
-      // Lane l has the tokens 4 l .. 4 l + 3 of a chunk.  Page ids are read two chunks
-      // ahead and scales one.
-      struct Walk {
-        MkUnit u;
-        int t = -1, k = 0;
-        bool end = false;
-      };
-      bool ok = true;
-      auto advance = [&](Walk &w) {                    // to the next chunk
-        if (w.end || !ok) return;
-        if (w.t >= 0 && ++w.k < w.u.n) return;
-        ++w.t;
-        w.k = 0;
-        const int e = w.t % kMkUnits;
-        ok = mk_wait_all(BAR(S::kUnitFull + e), (w.t / kMkUnits) & 1, abort_s);
-        if (!ok) return;
-        const int4 *src = reinterpret_cast<const int4 *>(unit_s + e);
-        int4 *dst = reinterpret_cast<int4 *>(&w.u);
-        dst[0] = src[0];
-        dst[1] = src[1];
-        w.end = w.u.n == 0;
-      };
-      auto read_id = [&](const Walk &w) -> int {
-        const int x = (w.u.c0 + w.k) * kMkTok + 4 * lane;
-        if (w.end || !ok || x >= w.u.X) return -1;
-        return __ldg(p.tables + static_cast<int64_t>(w.u.r) * p.width + (w.u.pos(x) >> p.log2_bs));
-      };
-      auto read_scales = [&](const Walk &w, int page, float (&kk)[4], float (&vv)[4]) {
-        const int x = (w.u.c0 + w.k) * kMkTok + 4 * lane;
-        const bool in = !w.end && ok && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_blocks);
-        const int64_t slot = (static_cast<int64_t>(page) << p.log2_bs) + (w.u.pos(x) & ((1 << p.log2_bs) - 1));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool get = in && x + i < w.u.X;
-          kk[i] = get ? __ldg(p.k_scales + (slot + i) * p.H + w.u.h) : 0.0f;
-          vv[i] = get ? __ldg(p.v_scales + (slot + i) * p.H + w.u.h) : 0.0f;
-        }
-      };
-      Walk wi, ws;                                     // of the ids, of the scales
-      advance(wi);
-      int id = read_id(wi);
-      ws = wi;
-      float kn[4], vn[4];
-      read_scales(ws, id, kn, vn);
-      advance(wi);
-      id = read_id(wi);
+      // Value scales brought over 2^Eg, the chunk's largest scales found; lane l has the
+      // tokens 4 l .. 4 l + 3.
       uint32_t seq = 0;
-      int eg = 0;
-      while (ok && !ws.end) {
-        float kk[4], vv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          kk[i] = kn[i];
-          vv[i] = vn[i];
-        }
-        const bool first = ws.k == 0, last = ws.k == ws.u.n - 1;
-        const int t = ws.t;
-        advance(ws);
-        read_scales(ws, id, kn, vn);
-        advance(wi);
-        id = read_id(wi);
-        if (!ok) break;
-        const uint32_t b = seq % kMkScales;
-        if (seq >= kMkScales &&
-            !mk_wait_all(BAR(S::kScEmpty + b), (seq / kMkScales - 1) & 1, abort_s)) {
-          ok = false;
+      for (int t = 0; !gave_up; ++t) {
+        if (!wait_unit(t)) {
+          gave_up = true;
           break;
         }
-        // the largest scales (of non-negative numbers, as unsigned words; NaN aside)
-        uint32_t km = 0u, vm = 0u;
+        const MkUnit &u = unit_s[t % kMkUnits];
+        const int un = u.n;
+        if (un == 0) break;
+        const MkWhole all_whole = mk_unit_whole<S::kTileRows>(p, u);
+        release_unit(t);
+        int eg = 0;
+#pragma unroll 1
+        for (int k = 0; k < un; ++k, ++seq) {
+          const uint32_t b = seq % kMkScales;
+          if (!mk_wait_all(BAR(S::kScRaw + b), (seq / kMkScales) & 1, abort_s)) {
+            gave_up = true;
+            break;
+          }
+          float4 *ks = reinterpret_cast<float4 *>(smem + S::kOffSc + b * 3 * kMkTok * 4) + lane;
+          const float4 kk = ks[0];
+          const float4 v4 = ks[kMkTok / 4];
+          float vv[4] = {v4.x, v4.y, v4.z, v4.w}, lg[4];
+          uint32_t bad = 0u;
+          if (!all_whole.at(k)) {
+            // scales that are not finite reach nobody by a product; rows that see them
+            // become NaN
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (kk[i] == kk[i]) km = max(km, __float_as_uint(fabsf(kk[i])));
-          if (vv[i] == vv[i]) vm = max(vm, __float_as_uint(fabsf(vv[i])));
+            for (int i = 0; i < 4; ++i)
+              if (!(vv[i] - vv[i] == 0.0f)) {
+                vv[i] = 0.0f;
+                bad |= 1u << i;
+              }
+            if (__any_sync(0xFFFFFFFFu, bad != 0u)) {
+              if (lane < 4) bad_s[8 + 4 * b + lane] = 0u;
+              __syncwarp();
+              if (bad != 0u)
+                atomicOr(bad_s + 8 + 4 * b + (lane >> 3), bad << (4 * (lane & 7)));
+            }
+          }
+          const float flagged = __any_sync(0xFFFFFFFFu, bad != 0u) ? 1.0f : 0.0f;
+          // (fmaxf leaves NaN out)
+          const float km4 = fmaxf(fmaxf(kk.x, kk.y), fmaxf(kk.z, kk.w));
+          const float vm4 = fmaxf(fmaxf(vv[0], vv[1]), fmaxf(vv[2], vv[3]));
+          const uint32_t km = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(km4, 0.0f)));
+          const uint32_t vm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(vm4, 0.0f)));
+          const int ev = min(mk_ceil_log2(__uint_as_float(vm)), 126);
+          if (k == 0) eg = min(ev, kMkMaxEg);
+          else if (ev > eg) eg = min(ev + 2, kMkMaxEg);
+          const float down = mk_pow2(-eg);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            vv[i] *= down;
+            lg[i] = fmaxf(static_cast<float>(mk_ceil_log2(vv[i])), kMkFloor);
+          }
+          ks[kMkTok / 4] = make_float4(vv[0], vv[1], vv[2], vv[3]);
+          ks[kMkTok / 2] = make_float4(lg[0], lg[1], lg[2], lg[3]);
+          if (lane == 0)
+            reinterpret_cast<float4 *>(smem + S::kOffMeta)[b] =
+                make_float4(__uint_as_float(km), fmaxf(static_cast<float>(ev - eg), kMkFloor),
+                            __int_as_float(eg), flagged);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(S::kScFull + b));
         }
-        km = __reduce_max_sync(0xFFFFFFFFu, km);
-        vm = __reduce_max_sync(0xFFFFFFFFu, vm);
-        const int ev = min(mk_ceil_log2(__uint_as_float(vm)), 126);
-        if (first) eg = min(ev, kMkMaxEg);
-        else if (ev > eg) eg = min(ev + 2, kMkMaxEg);
-        const float down = mk_pow2(-eg);
-        float *ks = reinterpret_cast<float *>(smem + S::kOffSc) + b * 2 * kMkTok;
-        reinterpret_cast<float4 *>(ks)[lane] = make_float4(kk[0], kk[1], kk[2], kk[3]);
-        reinterpret_cast<float4 *>(ks + kMkTok)[lane] =
-            make_float4(vv[0] * down, vv[1] * down, vv[2] * down, vv[3] * down);
-        if (lane == 0)
-          reinterpret_cast<float4 *>(smem + S::kOffMeta)[b] =
-              make_float4(__uint_as_float(km), fmaxf(static_cast<float>(ev - eg), kMkFloor),
-                          __int_as_float(eg), 0.0f);
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(BAR(S::kScFull + b));
-          // (held to here: the walks have read the unit)
-          if (last) mbar_arrive(BAR(S::kUnitEmpty + t % kMkUnits));
-        }
-        ++seq;
       }
-      gave_up = !ok;
     } else {
       // ---------------------------------------------------- MMAs of a chain
       // Each turn: PV of one of the chain's chunks and QK^T of its next, chain 0's and
@@ -1292,28 +1418,31 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
       const int a = warp - kMkWarpMma;
       const uint32_t q1 = (smem_addr(smem + S::kOffQ + (kPair ? a : 0) * 2 * S::kQPiece) >> 4) | kMkKMajor;
       const uint32_t q2 = q1 + (S::kQPiece >> 4);
-      const uint32_t k0 = (smem_addr(smem + S::kOffK) >> 4) | kMkKMajor;
+      const uint32_t k0 = (smem_addr(smem + S::kOffKv + p.k_off) >> 4) | kMkKMajor;
+      const uint32_t k_hi = (static_cast<uint32_t>(p.group) >> 4) | (1u << 14) | (kSmemSwizzle128 << 29);
       const uint32_t v0 = (smem_addr(smem + S::kOffVf) >> 4) | kMkMnMajor;
       const uint32_t s_col = tmem + mk_s(a), o_col = tmem + mk_o(a);
       uint32_t base = 0;                               // chunks of earlier units
       uint32_t par_q = 0, par_p = 0, par_o = 1, par_turn = a ^ 1;
       bool ok = true;
       for (int t = 0; ok; ++t) {
-        MkUnit u;
-        ok = take_unit(t, u);
-        if (!ok || u.n == 0) break;
-        const int mine = chain_chunks(u, a);           // chunks with products of this chain
-        const int steps = kPair ? u.n : (u.n + 1) / 2;
+        ok = wait_unit(t);
+        if (!ok) break;
+        const MkUnit &u = unit_s[t % kMkUnits];
+        const int un = u.n;
+        if (un == 0) break;
+        const int steps = kPair ? un : (un + 1) / 2;
         const bool turns = chain_chunks(u, 1) > 0;     // (a lone chain 0 need not pass them)
-        const bool live = mine > 0;
+        const bool live = chain_chunks(u, a) > 0;      // (the chain has products)
+        release_unit(t);
         for (int j = 0; j <= steps; ++j) {
           const int cv = kPair ? j - 1 : 2 * (j - 1) + a, cq = kPair ? j : 2 * j + a;
-          const bool use_v = j > 0 && cv < u.n, use_k = cq < u.n;
+          const bool use_v = j > 0 && cv < un, use_k = cq < un;
           const bool pv = use_v && live, qk = use_k && live;
           const uint32_t sv = base + cv, sq = base + cq;
-          const uint32_t bk = sq % S::kKStages, bv = sv & 1;
+          const uint32_t bk = sq % S::kStages, bv = sv & 1;
           if (use_v) ok = mk_wait_all(BAR(S::kVfFull + bv), (sv >> 1) & 1, abort_s);
-          if (ok && use_k) ok = mk_wait_all(BAR(S::kKFull + bk), (sq / S::kKStages) & 1, abort_s);
+          if (ok && use_k) ok = mk_wait_all(BAR(S::kKvFull + bk), (sq / S::kStages) & 1, abort_s);
           if (ok && qk && j == 0) ok = mk_wait_all(BAR(S::kQFull + (kPair ? a : 0)), kPair ? par_q : t & 1, abort_s);
           if (ok && pv) {
             if (j == 1) {
@@ -1342,32 +1471,32 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
             if (mk_elect()) {
 #pragma unroll
               for (int kk = 4; kk < 8; ++kk)
-                mk_mma_pv(o_col, s_col + 8 * kk, v_lo + (2048 >> 4) * kk, 1u);
+                mk_mma_pv(o_col, s_col + 32 + 8 * kk, v_lo + (2048 >> 4) * kk, 1u);
             }
           }
           if (qk) {
-            const uint32_t k_lo = k0 + bk * (S::kCode >> 4);
+            const uint32_t k_lo = k0 + bk * (S::kStage >> 4);
             tc_fence_after();
             if (mk_elect()) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mk_mma_qk(s_col, q1 + 2 * kk, k_lo + 2 * kk, kk != 0);
+              for (int kk = 0; kk < 4; ++kk) mk_mma_qk(s_col, q1 + 2 * kk, k_lo + 2 * kk, k_hi, kk != 0);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mk_mma_qk(s_col, q2 + 2 * kk, k_lo + 2 * kk, 1u);
+              for (int kk = 0; kk < 4; ++kk) mk_mma_qk(s_col, q2 + 2 * kk, k_lo + 2 * kk, k_hi, 1u);
               tc_commit(BAR(S::kSFull + a));
             }
           }
           __syncwarp();
           if (mk_elect()) {
             if (turns) mbar_arrive(BAR(S::kTurn + (a ^ 1)));
-            if (pv && (kPair ? cv == u.n - 1 : cv + 2 >= u.n)) tc_commit(BAR(S::kOFull + a));
-            if (qk && (kPair ? cq == u.n - 1 : cq + 2 >= u.n)) tc_commit(BAR(S::kQEmpty + a));
+            if (pv && (kPair ? cv == un - 1 : cv + 2 >= un)) tc_commit(BAR(S::kOFull + a));
+            if (qk && (kPair ? cq == un - 1 : cq + 2 >= un)) tc_commit(BAR(S::kQEmpty + a));
             if (use_v) tc_commit(BAR(S::kVfEmpty + bv));
-            if (use_k) tc_commit(BAR(S::kKEmpty + bk));
+            if (use_k) tc_commit(BAR(S::kKvEmpty + bk));
           }
           __syncwarp();
         }
         if (live) par_q ^= 1u;
-        base += u.n;
+        base += un;
       }
       gave_up = !ok;
       // every MMA issued has completed before the tensor memory is freed
@@ -1392,7 +1521,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm_k,
 int mk_tile_rows(int M) { return M <= 32 ? 32 : (M <= 128 ? 128 : 256); }
 
 template <bool kPair, int kRows>
-cudaError_t mk_launch(const MkParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int grid,
+cudaError_t mk_launch(const MkParams &p, const CUtensorMap &map, const CUtensorMap &map_v, int grid,
                       cudaStream_t stream) {
   constexpr int kSmem = MkShape<kPair, kRows>::kSmem;
   const auto kernel = attn_masked_kernel<kPair, kRows>;
@@ -1407,7 +1536,7 @@ cudaError_t mk_launch(const MkParams &p, const CUtensorMap &mk, const CUtensorMa
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
   return launch_overlapped(kernel, dim3(static_cast<unsigned>(grid)), dim3(kMkThreads), kSmem, stream,
-                           p, mk, mv);
+                           p, map, map_v);
 }
 
 size_t mk_round(size_t n) { return (n + 255) / 256 * 256; }
@@ -1433,6 +1562,7 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
   p.H = H;
   p.G = a.num_q_heads / H;
   p.M = p.R * p.G;
+  p.inv_g = static_cast<uint32_t>(((uint64_t(1) << 32) + p.G - 1) / p.G);
   const int rows = mk_tile_rows(p.M);
   p.T = (p.M + rows - 1) / rows;
   p.width = a.max_blocks_per_req;
@@ -1446,13 +1576,36 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
   p.words = (p.R + 31) / 32;
   p.scale2 = (a.sm_scale < 0.0f ? -a.sm_scale : a.sm_scale) * 1.4426950408889634f;
   p.flip = a.sm_scale < 0.0f ? 0x80808080u : 0u;
+  // A cut unit costs its last block some 8 cycles a row and 200 for each piece, a chunk takes
+  // it 2,000: pieces of at least sqrt(chunks (8 rows + 200) / 2000) chunks.
+  const int64_t reach = a.tree_mask != nullptr ? a.max_context_len
+                                               : std::min<int64_t>(a.max_context_len, int64_t(p.window) + p.sinks + p.R);
+  const double chunks = static_cast<double>((reach + kMkTok - 1) / kMkTok + 1);
+  p.least = std::max(1, static_cast<int>(std::sqrt(chunks * (8 * std::min(p.M, rows) + 200) / 2000) + 0.5));
   p.k_scales = c.k_scales;
   p.v_scales = c.v_scales;
   p.err_flags = a.err_flags;
-  CUtensorMap mk, mv;
-  if (!encode_code_tensor_map(&mk, c.k_codes, c.num_slots, H, p.box) ||
-      !encode_code_tensor_map(&mv, c.v_codes, c.num_slots, H, p.box))
-    return cudaErrorInvalidValue;
+  // one map over both planes, whichever comes first in memory; planes that are too far
+  // apart for a map's stride have one each
+  const uint8_t *low = std::min(c.k_codes, c.v_codes), *high = std::max(c.k_codes, c.v_codes);
+  const int64_t slots = static_cast<int64_t>(p.num_blocks) << a.log2_block;
+  CUtensorMap map, map_v;
+  p.two_maps = high - low < 128 || high - low >= (int64_t(1) << 40);
+  bool ok;
+  if (p.two_maps) {
+    ok = encode_plane_tensor_map(&map, c.k_codes, 0, slots, H, p.box) &&
+         encode_plane_tensor_map(&map_v, c.v_codes, 0, slots, H, p.box);
+    p.group = 1024;
+    p.k_off = 0;
+    p.v_off = kMkTok * kHeadDim;
+  } else {
+    ok = encode_plane_tensor_map(&map, low, high - low, slots, H, p.box);
+    map_v = map;
+    p.group = 2048;
+    p.k_off = low == c.k_codes ? 0 : 1024;
+    p.v_off = 1024 - p.k_off;
+  }
+  if (!ok) return cudaErrorInvalidValue;
   const int grid = a.sms;
   for (int r0 = 0; r0 < a.num_requests; r0 += kMkMaxRequests) {
     p.N = std::min(a.num_requests - r0, kMkMaxRequests);
@@ -1470,9 +1623,9 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
     ws += mk_round(slots * kHeadDim * sizeof(float));
     p.ml_part = reinterpret_cast<float2 *>(ws);
     p.tag = next_call_tag();
-    const cudaError_t e = rows == 32    ? mk_launch<false, 32>(p, mk, mv, grid, stream)
-                          : rows == 128 ? mk_launch<false, 128>(p, mk, mv, grid, stream)
-                                        : mk_launch<true, 128>(p, mk, mv, grid, stream);
+    const cudaError_t e = rows == 32    ? mk_launch<false, 32>(p, map, map_v, grid, stream)
+                          : rows == 128 ? mk_launch<false, 128>(p, map, map_v, grid, stream)
+                                        : mk_launch<true, 128>(p, map, map_v, grid, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
