@@ -982,7 +982,7 @@ bool encode_code_tensor_map_strided(CUtensorMap *map, const uint8_t *codes, int6
 }
 
 bool encode_plane_tensor_map(CUtensorMap *map, const uint8_t *codes, int64_t distance,
-                             int64_t num_slots, int H, int rows) {
+                             int64_t num_slots, int H, int rows, int heads) {
   EncodeTiledFn f = encode_tiled_fn();
   if (f == nullptr) return false;
   const cuuint64_t row = static_cast<cuuint64_t>(H) * kHeadDim;
@@ -992,7 +992,7 @@ bool encode_plane_tensor_map(CUtensorMap *map, const uint8_t *codes, int64_t dis
   const cuuint64_t strides[4] = {row, distance > 0 ? static_cast<cuuint64_t>(distance) : row, 8 * row,
                                  static_cast<cuuint64_t>(kHeadDim)};
   const cuuint32_t box[5] = {static_cast<cuuint32_t>(kHeadDim), 8u, planes,
-                             static_cast<cuuint32_t>(rows / 8), 1u};
+                             static_cast<cuuint32_t>(rows / 8), static_cast<cuuint32_t>(heads)};
   const cuuint32_t estride[5] = {1u, 1u, 1u, 1u, 1u};
   return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t *>(codes), dims, strides, box,
            estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

@@ -49,6 +49,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 
 #include "kvq_device.cuh"
@@ -58,12 +59,10 @@ namespace kvq {
 
 namespace {
 
-constexpr int kMkTok = 128;                           // tokens of a chunk
+constexpr int kMkTok = 128;                           // keys of a chunk: (token, KV head) pairs
 constexpr int kMkWarpConv = 8, kMkWarpLoad = 12, kMkWarpMma = 13, kMkWarpScale = 15;
 constexpr int kMkThreads = 512;
 constexpr int kMkUnits = 8;                           // units announced ahead
-constexpr int kMkIdAhead = 4;                         // chunks whose page ids are in flight
-constexpr int kMkMaxBoxes = 8;                        // pages of a chunk (boxes of >= 16 tokens)
 constexpr int kMkScales = 6;                          // chunks of scales in the ring
 constexpr int kMkMaxRequests = 1024;                  // of a launch
 constexpr int kMkCharge = 2;                          // chunks that a unit's start counts for
@@ -71,12 +70,15 @@ constexpr float kMkLazy = 14.0f;                      // log2 of the largest P''
 constexpr float kMkFloor = -90.0f;                    // log2 of the smallest value scale, over 2^Eg
 constexpr int kMkMaxEg = 30;                          // Eg at most
 
-// Shapes: kPair (two row tiles, one per chain) or one row tile of kRows rows whose
-// chunks the chains share.
+// Shapes: kPair (two row tiles of one head, one per chain), or one tile of kRows rows of
+// each of 128 / kRows heads, whose chunks the chains share.
 template <bool kPair, int kRows>
 struct MkShape {
-  static constexpr int kTileRows = kPair ? 256 : kRows;      // rows of a unit
-  static constexpr int kCopies = 128 / kRows;
+  static constexpr int kTileRows = kPair ? 256 : kRows;      // rows of a unit, per head
+  static constexpr int kLanes = kPair ? 256 : 128;           // of all its heads
+  static constexpr int kHeads = 128 / kRows;
+  static constexpr int kTok = kMkTok / kHeads;               // tokens of a chunk
+  static constexpr int kTokLog2 = kRows == 32 ? 5 : (kRows == 64 ? 6 : 7);
   static constexpr int kQTiles = kPair ? 2 : 1;
   // shared memory, offsets from a 1024-byte aligned base
   static constexpr int kStages = kPair ? 2 : 3;
@@ -92,8 +94,7 @@ struct MkShape {
   static constexpr int kOffSc = kOffEg + 16;                 // [stage][K | V | log2 V][128]
   static constexpr int kOffMeta = kOffSc + kMkScales * 3 * kMkTok * 4;   // [stage] float4
   static constexpr int kOffUnit = kOffMeta + kMkScales * 16;
-  static constexpr int kOffIds = kOffUnit + kMkUnits * 64;
-  static constexpr int kOffBad = kOffIds + (kMkIdAhead + 1) * kMkMaxBoxes * 4;   // [Vf][4 words], [scales][4 words]
+  static constexpr int kOffBad = kOffUnit + kMkUnits * 64;   // [Vf][4 words], [scales][4 words]
   static constexpr int kOffMisc = kOffBad + 32 + kMkScales * 16;              // tmem base, abort, ticket
   static constexpr int kOffScan = kOffMisc + 16;             // a warp's sum each
   static constexpr int kOffPre = kOffScan + kMkThreads / 32 * 4;
@@ -102,8 +103,7 @@ struct MkShape {
   static constexpr int kKvEmpty = kKvFull + kStages;
   static constexpr int kVfFull = kKvEmpty + kStages;
   static constexpr int kVfEmpty = kVfFull + 2;
-  static constexpr int kScRaw = kVfEmpty + 2;
-  static constexpr int kScFull = kScRaw + kMkScales;
+  static constexpr int kScFull = kVfEmpty + 2;
   static constexpr int kScEmpty = kScFull + kMkScales;
   static constexpr int kQFull = kScEmpty + kMkScales;        // per chain from here on
   static constexpr int kQEmpty = kQFull + 2;
@@ -117,9 +117,7 @@ struct MkShape {
   static constexpr int kUnitFull = kDrain + 2;
   static constexpr int kUnitEmpty = kUnitFull + kMkUnits;
   static constexpr int kBars = kUnitEmpty + kMkUnits;
-  // at most 32 rows: the copies' outputs, 32 dims at a time
-  static constexpr int kOffX = (kOffBar + 8 * kBars + 127) / 128 * 128;
-  static constexpr int kSmem = kOffX + (kRows == 32 ? 4 * 32 * 32 * 4 : 0) + 1024;
+  static constexpr int kSmem = kOffBar + 8 * kBars + 1024;
   static_assert(kOffKv % 1024 == 0 && kOffVf % 1024 == 0 && kOffSc % 16 == 0 && kOffMeta % 16 == 0 &&
                     kOffUnit % 16 == 0 && kOffBad % 16 == 0 && kOffMisc % 16 == 0 && kOffBar % 8 == 0,
                 "alignment");
@@ -165,11 +163,6 @@ __device__ __forceinline__ void mk_load_box(uint32_t dst, const void *tmap, int 
       :: "r"(dst), "l"(tmap), "r"(0), "r"(z), "r"(head), "r"(bar), "l"(policy) : "memory");
 }
 
-// This thread's cp.async so far arrive on `bar` when they have landed.
-__device__ __forceinline__ void mk_arrive_copies(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" :: "r"(bar) : "memory");
-}
-
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool mk_elect() {
   uint32_t r;
@@ -187,7 +180,7 @@ struct MkParams {
   const int32_t *tree;                                 // mask words, null: a window
   int32_t N, R, Hq, H, G, M;
   uint32_t inv_g;                                      // ceil(2^32 / G), G > 1
-  int32_t T;                                           // units of a request and head
+  int32_t T, HG;                                       // units of a request and group of heads, groups
   int32_t width;                                       // max_blocks_per_req
   int32_t ctx_limit, num_blocks, log2_bs, box;
   int32_t window, sinks, words;
@@ -196,9 +189,9 @@ struct MkParams {
   int32_t group, k_off, v_off, two_maps;
   float scale2;                                        // |sm_scale| log2(e)
   uint32_t flip;                                       // sign bits of a negative sm_scale
-  float *o_part;                                       // [grid][2][rows of a unit][128]
-  float2 *ml_part;                                     // [grid][2][rows of a unit]
-  unsigned long long *tickets;                         // [N * H * T]
+  float *o_part;                                       // [grid][2][lanes of a unit][128]
+  float2 *ml_part;                                     // [grid][2][lanes of a unit]
+  unsigned long long *tickets;                         // [N * HG * T]
   uint32_t tag;
   int32_t *err_flags;
   int32_t least;                                       // positions of a block's range
@@ -282,8 +275,9 @@ __device__ __forceinline__ int mk_len(const MkParams &p, int r) {
   return L < 0 ? 0 : min(L, p.ctx_limit);
 }
 
+template <typename S>
 __device__ __forceinline__ int mk_positions(int X) {   // of a unit in the work sequence
-  return X > 0 ? (X + kMkTok - 1) / kMkTok + kMkCharge : 0;
+  return X > 0 ? ((X + S::kTok - 1) >> S::kTokLog2) + kMkCharge : 0;
 }
 
 // A unit as the loading warp announces it: the chunks [c0, c0 + n) of a unit, which is
@@ -330,14 +324,17 @@ struct MkWhole {
   int hi, sink, lo;
   __device__ __forceinline__ bool at(int k) const { return k < hi && (k < sink || k >= lo); }
 };
+template <typename S>
 __device__ __forceinline__ MkWhole mk_whole(const MkParams &p, const MkUnit &u, int hi_first,
                                             int lo_last) {
-  if (p.tree != nullptr) return MkWhole{(u.base >> 7) - u.c0, 0, 0};
-  return MkWhole{(hi_first >> 7) - u.c0, (p.sinks >> 7) - u.c0, ((lo_last + kMkTok - 1) >> 7) - u.c0};
+  constexpr int kLog2 = S::kTokLog2;
+  if (p.tree != nullptr) return MkWhole{(u.base >> kLog2) - u.c0, 0, 0};
+  return MkWhole{(hi_first >> kLog2) - u.c0, (p.sinks >> kLog2) - u.c0,
+                 ((lo_last + S::kTok - 1) >> kLog2) - u.c0};
 }
-template <int kTileRows>
+template <typename S>
 __device__ __forceinline__ MkWhole mk_unit_whole(const MkParams &p, const MkUnit &u) {
-  return mk_whole(p, u, mk_seen(p, u, u.row0).hi, mk_seen(p, u, u.row0 + kTileRows - 1).lo);
+  return mk_whole<S>(p, u, mk_seen(p, u, u.row0).hi, mk_seen(p, u, u.row0 + S::kTileRows - 1).lo);
 }
 
 // ---------------------------------------------------------------------------
@@ -349,13 +346,12 @@ struct MkRow {
   int eg = 0;                                          // value scales are held over 2^eg
 };
 
-// max_j (u_j + log2 of the value scale) over 32 tokens, those of `bits` (kMasked).
-template <bool kMasked>
-__device__ __forceinline__ float mk_top32(const uint32_t (&x)[32], const float *ks, const float *lg,
+// max_j (u_j + log2 of the value scale) over 16 tokens, those of `bits`.
+__device__ __forceinline__ float mk_top16(const float (&x)[16], const float *ks, const float *lg,
                                           uint64_t rowf, uint32_t bits, float top) {
   float m[2] = {top, -INFINITY};
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
+  for (int q = 0; q < 4; ++q) {
     const float4 k4 = reinterpret_cast<const float4 *>(ks)[q];
     const float4 l4 = reinterpret_cast<const float4 *>(lg)[q];
     const uint64_t kk[2] = {pack_f32x2(k4.x, k4.y), pack_f32x2(k4.z, k4.w)};
@@ -364,12 +360,9 @@ __device__ __forceinline__ float mk_top32(const uint32_t (&x)[32], const float *
     for (int i = 0; i < 2; ++i) {
       const int e = 4 * q + 2 * i;
       float a, b;
-      unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                                       kk[i]), rowf, ll[i]), a, b);
-      if (kMasked) {
-        a = (bits >> e) & 1u ? a : -INFINITY;
-        b = (bits >> (e + 1)) & 1u ? b : -INFINITY;
-      }
+      unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(x[e], x[e + 1]), kk[i]), rowf, ll[i]), a, b);
+      a = (bits >> e) & 1u ? a : -INFINITY;
+      b = (bits >> (e + 1)) & 1u ? b : -INFINITY;
       m[i] = mk_max3(m[i], a, b);
     }
   }
@@ -401,14 +394,14 @@ __device__ __forceinline__ void mk_meet(MkRow &row, float top, int de, bool fres
   }
 }
 
-// P'' of 32 scores as f16 in w, the sum of the p added to `sum`; tokens that are not in
+// P'' of 16 scores as f16 in w, the sum of the p added to `sum`; tokens that are not in
 // `bits` (kMasked) have p = 0.
 template <bool kMasked>
-__device__ __forceinline__ void mk_part(const uint32_t (&x)[32], const float *ks, const float *vs,
-                                        uint64_t rowf, uint64_t shift, uint32_t bits,
-                                        uint64_t (&sum)[2], uint32_t (&w)[16]) {
+__device__ __forceinline__ void mk_part16(const float (&x)[16], const float *ks, const float *vs,
+                                          uint64_t rowf, uint64_t shift, uint32_t bits,
+                                          uint64_t (&sum)[2], uint32_t (&w)[8]) {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
+  for (int q = 0; q < 4; ++q) {
     const float4 k4 = reinterpret_cast<const float4 *>(ks)[q];
     const float4 v4 = reinterpret_cast<const float4 *>(vs)[q];
     const uint64_t kk[2] = {pack_f32x2(k4.x, k4.y), pack_f32x2(k4.z, k4.w)};
@@ -417,8 +410,7 @@ __device__ __forceinline__ void mk_part(const uint32_t (&x)[32], const float *ks
     for (int i = 0; i < 2; ++i) {
       const int e = 4 * q + 2 * i;
       float a, b;
-      unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                                       kk[i]), rowf, shift), a, b);
+      unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(x[e], x[e + 1]), kk[i]), rowf, shift), a, b);
       if (kMasked) {
         a = (bits >> e) & 1u ? a : -INFINITY;
         b = (bits >> (e + 1)) & 1u ? b : -INFINITY;
@@ -439,156 +431,171 @@ __device__ __forceinline__ void mk_announce(uint32_t bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
+// A row's keys of a chunk: groups of 16 tokens, group g at the scores' (and the scales')
+// column 16 (kHeads g + its head), its P'' at column mk_pcol of that (the halves of the 128
+// keys each start at their own scores' place).
+template <int kHeads>
+__device__ __forceinline__ int mk_col(int g, int hu) {
+  return 16 * (kHeads * g + hu);
+}
+__device__ __forceinline__ int mk_pcol(int col) { return (col & 64) + ((col & 63) >> 1); }
+
+// The other heads' P'' columns of half h are 0.
+template <int kHeads>
+__device__ __forceinline__ void mk_zero(uint32_t scol, int h, int hu) {
+  if (kHeads == 1) return;
+  const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c % kHeads != hu) tmem_st8u(scol + 64 * h + 8 * c, z);
+}
+
 // One chunk of one row whose warp sees all of it: S from TMEM, the row's statistics
-// brought up to date, P'' over S's columns (tokens 64 h .. in the columns from 64 h on),
-// its halves announced one after the other.  ks: the chunk's key scales, value scales
-// and their log2; meta: the largest key scale, the log2 of the largest value scale, Eg.
-__device__ __forceinline__ void mk_softmax128(uint32_t scol, uint32_t ocol, const float *ks,
-                                              const float4 meta, float rowf, bool fresh,
-                                              uint32_t ready, int lane, MkRow &row) {
+// brought up to date, P'' over S's columns, its halves announced one after the other.
+// ks: the chunk's key scales, value scales and their log2; meta: the largest key scale,
+// the log2 of the largest value scale, Eg.
+template <int kHeads>
+__device__ __forceinline__ void mk_softmax(uint32_t scol, uint32_t ocol, const float *ks,
+                                           const float4 meta, float rowf, int hu, bool fresh,
+                                           uint32_t ready, int lane, MkRow &row) {
+  constexpr int kGroups = 8 / kHeads, kHalf = kGroups / 2;
   const int eg = __float_as_int(meta.z);
   const int de = fresh ? 0 : eg - row.eg;
   row.eg = eg;
   const float *vs = ks + kMkTok, *lg = vs + kMkTok;
   const uint64_t rf = pack_f32x2(rowf, rowf);
   // the largest a score can be under the chunk's largest scales
-  float mx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float mx[2] = {0.0f, 0.0f};
+  if (kHeads == 1) {
 #pragma unroll 1
-  for (int c = 0; c < 128; c += 64) {
-    float x[64];
-    tmem_ld64(scol + c, x);
+    for (int c = 0; c < 128; c += 64) {
+      float x[64];
+      tmem_ld64(scol + c, x);
 #pragma unroll
-    for (int i = 0; i < 64; i += 8)
+      for (int i = 0; i < 64; i += 4)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) mx[q] = mk_max3(mx[q], x[i + q], x[i + q + 4]);
+        for (int q = 0; q < 2; ++q) mx[q] = mk_max3(mx[q], x[i + q], x[i + q + 2]);
+    }
+  } else {
+#pragma unroll 1
+    for (int g = 0; g < kGroups; g += 2) {
+      float x[16], y[16];
+      tmem_ld16(scol + mk_col<kHeads>(g, hu), x);
+      tmem_ld16(scol + mk_col<kHeads>(g + 1, hu), y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx[i & 1] = mk_max3(mx[i & 1], x[i], y[i]);
+    }
   }
-  const float most = fmaxf(mk_max3(mx[0], mx[1], mx[2]), mx[3]) * meta.x * rowf + meta.y;
+  const float most = fmaxf(mx[0], mx[1]) * meta.x * rowf + meta.y;
   if (de != 0 || __any_sync(0xFFFFFFFFu, !(most - row.m <= kMkLazy))) {
     float top = -INFINITY;
 #pragma unroll 1
-    for (int g = 0; g < 4; ++g) {
-      uint32_t x[32];
-      tmem_ld32_start(scol + 32 * g, x);
-      tmem_ld32_done(x);
-      top = mk_top32<false>(x, ks + 32 * g, lg + 32 * g, rf, 0u, top);
+    for (int g = 0; g < kGroups; ++g) {
+      float x[16];
+      const int col = mk_col<kHeads>(g, hu);
+      tmem_ld16(scol + col, x);
+      top = mk_top16(x, ks + col, lg + col, rf, 0xFFFFu, top);
     }
     mk_meet(row, top, de, fresh, ocol);
   }
   const float sh = row.m == -INFINITY ? 0.0f : -row.m;
   const uint64_t s2 = pack_f32x2(sh, sh);
   uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
-  uint32_t x0[32], x1[32], w[16];
-  tmem_ld32_start(scol, x0);
-  tmem_ld32_done(x0);
+  if (kHeads == 4) {
+    // (a half's P'' lies over the other's scores of other heads only)
+    float x0[16], x1[16];
+    uint32_t w[8];
+    tmem_ld16(scol + mk_col<kHeads>(0, hu), x0);
+    tmem_ld16(scol + mk_col<kHeads>(1, hu), x1);
+    int col = mk_col<kHeads>(0, hu);
+    mk_part16<false>(x0, ks + col, vs + col, rf, s2, 0u, sum, w);
+    tmem_st8u(scol + mk_pcol(col), w);
+    mk_zero<kHeads>(scol, 0, hu);
+    mk_announce(ready, lane);
+    col = mk_col<kHeads>(1, hu);
+    mk_part16<false>(x1, ks + col, vs + col, rf, s2, 0u, sum, w);
+    tmem_st8u(scol + mk_pcol(col), w);
+    mk_zero<kHeads>(scol, 1, hu);
+    mk_announce(ready + 8, lane);
+  } else {
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    tmem_ld32_start(scol + 64 * h + 32, x1);
-    mk_part<false>(x0, ks + 64 * h, vs + 64 * h, rf, s2, 0u, sum, w);
-    tmem_ld32_done(x1);
-    tmem_st16u(scol + 64 * h, w);
-    if (h == 0) tmem_ld32_start(scol + 64, x0);
-    mk_part<false>(x1, ks + 64 * h + 32, vs + 64 * h + 32, rf, s2, 0u, sum, w);
-    if (h == 0) tmem_ld32_done(x0);
-    tmem_st16u(scol + 64 * h + 16, w);
-    mk_announce(ready + 8 * h, lane);
+    for (int g = 0; g < kGroups; g += 2) {
+      float x0[16], x1[16];
+      uint32_t w[8];
+      const int c0 = mk_col<kHeads>(g, hu), c1 = mk_col<kHeads>(g + 1, hu);
+      tmem_ld16(scol + c0, x0);
+      tmem_ld16(scol + c1, x1);
+      mk_part16<false>(x0, ks + c0, vs + c0, rf, s2, 0u, sum, w);
+      tmem_st8u(scol + mk_pcol(c0), w);
+      mk_part16<false>(x1, ks + c1, vs + c1, rf, s2, 0u, sum, w);
+      tmem_st8u(scol + mk_pcol(c1), w);
+      if ((g + 2) % kHalf == 0) {
+        const int h = g / kHalf;
+        mk_zero<kHeads>(scol, h, hu);
+        mk_announce(ready + 8 * h, lane);
+      }
+    }
   }
   float a, b;
   unpack_f32x2(mk_add2(sum[0], sum[1]), a, b);
   row.sum += a + b;
 }
 
-// The same where some of the warp's rows do not see some of the tokens [x0, x0 + 128):
-// seldom, so small rather than fast (the roles share an instruction cache).  bad: tokens
-// whose value was cleared; returns whether the row sees one of them.
-__device__ __forceinline__ bool mk_softmax128_masked(const MkParams &p, const MkSeen &seen, int x0,
-                                                     int X, const uint32_t (&bad)[4], uint32_t scol,
-                                                     uint32_t ocol, const float *ks,
-                                                     const float4 meta, float rowf, bool fresh,
-                                                     uint32_t ready, int lane, MkRow &row) {
+// The same where some of the warp's rows do not see some of the chunk's tokens, from x0
+// on: seldom, so small rather than fast (the roles share an instruction cache).  bad:
+// keys whose value was cleared, 16 a word; returns whether the row sees one of them.
+template <int kHeads>
+__device__ __forceinline__ bool mk_softmax_masked(const MkParams &p, const MkSeen &seen, int x0,
+                                                  int X, const uint16_t *bad, const uint16_t *bad_sc,
+                                                  uint32_t scol, uint32_t ocol, const float *ks,
+                                                  const float4 meta, float rowf, int hu, bool fresh,
+                                                  uint32_t ready, int lane, MkRow &row) {
+  constexpr int kGroups = 8 / kHeads, kHalf = kGroups / 2;
   const int eg = __float_as_int(meta.z);
   const int de = fresh ? 0 : eg - row.eg;
   row.eg = eg;
   const float *vs = ks + kMkTok, *lg = vs + kMkTok;
   const uint64_t rf = pack_f32x2(rowf, rowf);
   float top = -INFINITY;
-  uint32_t b0 = 0u, b1 = 0u, b2 = 0u, b3 = 0u, hit = 0u, x[32];
+  uint64_t lo = 0u, hi = 0u;                           // what the row sees, 16 bits a group
+  uint32_t hit = 0u, word = 0u;
 #pragma unroll 1
-  for (int g = 0; g < 4; ++g) {
-    const uint32_t bits = seen.bits(p, x0 + 32 * g, X);
-    if (g == 0) b0 = bits;
-    else if (g == 1) b1 = bits;
-    else if (g == 2) b2 = bits;
-    else b3 = bits;
-    hit |= bits & (g < 2 ? (g == 0 ? bad[0] : bad[1]) : (g == 2 ? bad[2] : bad[3]));
-    tmem_ld32_start(scol + 32 * g, x);
-    tmem_ld32_done(x);
-    top = mk_top32<true>(x, ks + 32 * g, lg + 32 * g, rf, bits, top);
+  for (int g = 0; g < kGroups; ++g) {
+    float x[16];
+    const int col = mk_col<kHeads>(g, hu);
+    word = (g & 1) == 0 ? seen.bits(p, x0 + 16 * g, X) : word >> 16;
+    const uint32_t bits = word & 0xFFFFu;
+    hi = (hi >> 16) | (lo << 48);
+    lo = (lo >> 16) | (static_cast<uint64_t>(bits) << 48);
+    hit |= bits & (bad[col >> 4] | (meta.w != 0.0f ? bad_sc[col >> 4] : 0u));
+    tmem_ld16(scol + col, x);
+    top = mk_top16(x, ks + col, lg + col, rf, bits, top);
   }
   mk_meet(row, top, de, fresh, ocol);
   const float sh = row.m == -INFINITY ? 0.0f : -row.m;
   uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
+  // (the groups' bits: the first are the lowest 16 of hi, or of what of lo is in use)
+  uint64_t bits = kGroups == 8 ? hi : (kGroups == 4 ? lo : lo >> 32);
 #pragma unroll 1
-  for (int g = 0; g < 4; ++g) {
-    uint32_t w[16];
-    tmem_ld32_start(scol + 32 * g, x);
-    tmem_ld32_done(x);
-    mk_part<true>(x, ks + 32 * g, vs + 32 * g, rf, pack_f32x2(sh, sh),
-                  g < 2 ? (g == 0 ? b0 : b1) : (g == 2 ? b2 : b3), sum, w);
-    tmem_st16u(scol + 64 * (g >> 1) + 16 * (g & 1), w);
-    if (g & 1) mk_announce(ready + 8 * (g >> 1), lane);
+  for (int g = 0; g < kGroups; ++g) {
+    float x[16];
+    uint32_t w[8];
+    const int col = mk_col<kHeads>(g, hu);
+    tmem_ld16(scol + col, x);
+    mk_part16<true>(x, ks + col, vs + col, rf, pack_f32x2(sh, sh), static_cast<uint32_t>(bits) & 0xFFFFu,
+                    sum, w);
+    bits >>= 16;
+    if (kGroups == 8 && g == 3) bits = lo;
+    tmem_st8u(scol + mk_pcol(col), w);
+    if ((g + 1) % kHalf == 0) {
+      mk_zero<kHeads>(scol, g / kHalf, hu);
+      mk_announce(ready + 8 * (g / kHalf), lane);
+    }
   }
   float a, b;
   unpack_f32x2(mk_add2(sum[0], sum[1]), a, b);
   row.sum += a + b;
   return hit != 0u;
-}
-
-// The same for a row of which each of four copies takes 32 tokens of the chunk: this
-// thread's are those of `copy` (bits[0]); the other copies' P'' is 0.
-template <bool kMasked>
-__device__ __forceinline__ void mk_softmax32(uint32_t scol, uint32_t ocol, const float *ks,
-                                             const float4 meta, float rowf, uint32_t bits, int copy,
-                                             bool fresh, uint32_t ready, int lane, MkRow &row) {
-  const int eg = __float_as_int(meta.z);
-  const int de = fresh ? 0 : eg - row.eg;
-  row.eg = eg;
-  const float *kc = ks + 32 * copy, *vc = kc + kMkTok, *lg = vc + kMkTok;
-  const uint64_t rf = pack_f32x2(rowf, rowf);
-  uint32_t x[32], w[16];
-  tmem_ld32_start(scol + 32 * copy, x);
-  tmem_ld32_done(x);
-  bool search = true;
-  if (!kMasked) {
-    float mx[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 32; i += 4)
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        mx[q] = mk_max3(mx[q], __uint_as_float(x[i + q]), __uint_as_float(x[i + q + 2]));
-    const float most = fmaxf(mx[0], mx[1]) * meta.x * rowf + meta.y;
-    search = __any_sync(0xFFFFFFFFu, !(most - row.m <= kMkLazy));
-  }
-  if (search || de != 0) mk_meet(row, mk_top32<kMasked>(x, kc, lg, rf, bits, -INFINITY), de, fresh, ocol);
-  const float sh = row.m == -INFINITY ? 0.0f : -row.m;
-  uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
-  mk_part<kMasked>(x, kc, vc, rf, pack_f32x2(sh, sh), bits, sum, w);
-  float a, b;
-  unpack_f32x2(mk_add2(sum[0], sum[1]), a, b);
-  row.sum += a + b;
-  // (P'' of the tokens 32 c .. in the columns 64 (c / 2) + 16 (c % 2) ..)
-  tmem_st16u(scol + 64 * (copy >> 1) + 16 * (copy & 1), w);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] = 0u;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c)
-    if (c != copy) tmem_st16u(scol + 64 * (c >> 1) + 16 * (c & 1), w);
-  tmem_wait_st();
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) {
-    mbar_arrive(ready);
-    mbar_arrive(ready + 8);
-  }
 }
 
 // A query row (null: zeros) as two e4m3 pieces into its place in a K-major, 128-byte
@@ -663,7 +670,6 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       count = kPair ? 2 : 1;                           // a commit of each chain that reads it
     if (i >= S::kVfFull && i < S::kVfFull + 2) count = 4;   // the converting warps
     if (i >= S::kKvEmpty && i < S::kKvEmpty + S::kStages) count = 4 + (kPair ? 2 : 1);
-    if (i >= S::kScRaw && i < S::kScRaw + kMkScales) count = 32;     // the copying warp's lanes
     if (i >= S::kScEmpty && i < S::kScEmpty + kMkScales) count = kPair ? 8 : 4;
     if ((i >= S::kQFull && i < S::kQFull + 2) || (i >= S::kPReady && i < S::kPReady + 4) ||
         (i >= S::kOEmpty && i < S::kOEmpty + 2) || (i >= S::kSumFull && i < S::kSumFull + 2))
@@ -688,8 +694,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
     const int Lc = L < 0 ? 0 : min(L, p.ctx_limit);
     int w = 0;
 #pragma unroll 1
-    for (int t = 0; t < p.T; ++t) w += mk_positions(mk_span<S::kTileRows>(p, Lc, t).X);
-    return w * p.H;
+    for (int t = 0; t < p.T; ++t) w += mk_positions<S>(mk_span<S::kTileRows>(p, Lc, t).X);
+    return w * p.HG;
   };
   int *warp_sum = reinterpret_cast<int *>(smem + S::kOffScan);
   int carry = 0;
@@ -741,8 +747,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
     const int a = warp >> 2, q4 = warp & 3;
     const int lane_row = 32 * q4 + lane;               // TMEM lane
-    const int copy = kRows == 32 ? q4 : 0;
-    const int trow = (kPair ? 128 * a : 0) + (kRows == 32 ? lane : lane_row);   // of the unit
+    const int hu = kPair ? 0 : lane_row / kRows;       // its head and its row, of the unit's
+    const int trow = kPair ? 128 * a + lane_row : lane_row % kRows;
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     uint32_t steps = 0, done = 0, seq = 0;             // chunks and units of this chain, chunks of all
     uint32_t sc = 0, sc_par = 0;                       // place in the scales' ring
@@ -759,10 +765,10 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       if (n > 0) {
         // the row's query; the tile's space is free once the last unit's products
         // with it are done.  (Where the chains share a tile, chain 0 stores it.)
-        const int m = u.row0 + trow;
+        const int m = u.row0 + trow, head = u.h + hu;
         const int i = mk_query(p, m);
-        const uint4 *src = m < p.M ? reinterpret_cast<const uint4 *>(
-            p.q + ((static_cast<int64_t>(u.r) * p.R + i) * p.Hq + u.h * p.G + (m - i * p.G)) * kHeadDim)
+        const uint4 *src = m < p.M && head < p.H ? reinterpret_cast<const uint4 *>(
+            p.q + ((static_cast<int64_t>(u.r) * p.R + i) * p.Hq + head * p.G + (m - i * p.G)) * kHeadDim)
             : nullptr;
         const bool store = kPair || a == 0;
         bool ok = true;
@@ -776,7 +782,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           break;
         }
         rowf = mk_query_row(src, p.scale2, p.flip, smem + S::kOffQ + (kPair ? a : 0) * 2 * S::kQPiece,
-                            kRows == 32 ? 32 * copy + lane : lane_row, store);
+                            lane_row, store);
         if (store) {
           fence_proxy_async_smem();
           __syncwarp();
@@ -787,9 +793,9 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       q_units1 += un >= 2;
       const MkSeen seen = mk_seen(p, u, u.row0 + trow);
       // the warp's first and last row
-      const MkWhole whole = mk_whole(p, u, __shfl_sync(0xFFFFFFFFu, seen.hi, 0),
+      const MkWhole whole = mk_whole<S>(p, u, __shfl_sync(0xFFFFFFFFu, seen.hi, 0),
                                      __shfl_sync(0xFFFFFFFFu, seen.lo, 31));
-      const MkWhole all_whole = mk_unit_whole<S::kTileRows>(p, u);
+      const MkWhole all_whole = mk_unit_whole<S>(p, u);
       MkRow row;
       bool nan_row = false, fresh = true;
 #pragma unroll 1
@@ -807,35 +813,27 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           const float4 meta = reinterpret_cast<const float4 *>(smem + S::kOffMeta)[sc];
           const uint32_t ready = BAR(S::kPReady + 2 * a);
           const uint32_t scol = tl + mk_s(a), ocol = tl + mk_o(a);
-          const int x0 = (u.c0 + k) * kMkTok;
-          uint32_t bad[4] = {0u, 0u, 0u, 0u};
-          if (!all_whole.at(k)) {
-            // some row of the unit does not see all of the chunk: value rows with a NaN code
-            // or such a scale have been cleared
-            if (!mk_wait_all(BAR(S::kVfFull + (seq & 1)), (seq >> 1) & 1, abort_s)) {
-              gave_up = true;
-              break;
-            }
-            const uint32_t *codes = bad_s + 4 * (seq & 1), *scales = bad_s + 8 + 4 * sc;
-            const bool some = meta.w != 0.0f;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) bad[g] = codes[g] | (some ? scales[g] : 0u);
+          const uint16_t *bad = reinterpret_cast<const uint16_t *>(bad_s + 4 * (seq & 1));
+          const uint16_t *bad_sc = reinterpret_cast<const uint16_t *>(bad_s + 8 + 4 * sc);
+          const bool see_all = whole.at(k), edge = !all_whole.at(k);
+          // where some row of the unit does not see all of the chunk, value rows with a NaN
+          // code or such a scale have been cleared
+          if (edge && !mk_wait_all(BAR(S::kVfFull + (seq & 1)), (seq >> 1) & 1, abort_s)) {
+            gave_up = true;
+            break;
           }
-          const bool see_all = whole.at(k);
-          if (kRows == 32) {
-            const uint32_t bits = see_all ? 0xFFFFFFFFu : seen.bits(p, x0 + 32 * copy, u.X);
-            const uint32_t mine = copy < 2 ? (copy == 0 ? bad[0] : bad[1]) : (copy == 2 ? bad[2] : bad[3]);
-            nan_row |= (mine & bits) != 0u;
-            if (see_all)
-              mk_softmax32<false>(scol, ocol, ks, meta, rowf, bits, copy, fresh, ready, lane, row);
-            else
-              mk_softmax32<true>(scol, ocol, ks, meta, rowf, bits, copy, fresh, ready, lane, row);
-          } else if (see_all) {
-            nan_row |= (bad[0] | bad[1] | bad[2] | bad[3]) != 0u;
-            mk_softmax128(scol, ocol, ks, meta, rowf, fresh, ready, lane, row);
+          if (see_all) {
+            if (edge) {
+#pragma unroll 1
+              for (int g = 0; g < 8 / S::kHeads; ++g) {
+                const int c = mk_col<S::kHeads>(g, hu) >> 4;
+                nan_row |= (bad[c] | (meta.w != 0.0f ? bad_sc[c] : 0)) != 0;
+              }
+            }
+            mk_softmax<S::kHeads>(scol, ocol, ks, meta, rowf, hu, fresh, ready, lane, row);
           } else {
-            nan_row |= mk_softmax128_masked(p, seen, x0, u.X, bad, scol, ocol, ks, meta, rowf, fresh,
-                                            ready, lane, row);
+            nan_row |= mk_softmax_masked<S::kHeads>(p, seen, (u.c0 + k) * S::kTok, u.X, bad, bad_sc, scol,
+                                                    ocol, ks, meta, rowf, hu, fresh, ready, lane, row);
           }
           fresh = false;
           ++steps;
@@ -871,125 +869,63 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       return p.out + ((static_cast<int64_t>(r) * p.R + i) * p.Hq + h * p.G + (m - i * p.G)) * kHeadDim;
     };
     auto epilogue = [&](const MkUnit &u) -> bool {
-      const int64_t piece = static_cast<int64_t>(u.slot) * S::kTileRows;
+      const int64_t piece = static_cast<int64_t>(u.slot) * S::kLanes;
+      const bool both = !kPair && u.n >= 2;
 #pragma unroll 1
       for (int a = 0; a < (kPair ? 2 : 1); ++a) {
         if (chain_chunks(u, a) == 0) continue;
-        const bool both = !kPair && u.n >= 2;
         bool got = mk_wait_all(BAR(S::kSumFull + a), (par >> a) & 1, abort_s) &&
                    mk_wait_all(BAR(S::kOFull + a), (par >> a) & 1, abort_s);
         if (both)
           got = got && mk_wait_all(BAR(S::kSumFull + 1), par >> 1, abort_s) &&
                 mk_wait_all(BAR(S::kOFull + 1), par >> 1, abort_s);
-        if (!got) {
-          return false;
-        }
+        if (!got) return false;
         tc_fence_after();
         par ^= 1u << a;
         if (both) par ^= 2u;
-        // the row's parts (chains, copies) under their largest reference
-        const int row = kRows == 32 ? lane : lane_row;
-        float top = -INFINITY, all = 0.0f;
-        if (kPair) {
-          top = ref_s[128 * a + lane_row];
-          all = sum_s[128 * a + lane_row];
-        } else {
-#pragma unroll
-          for (int c = 0; c < S::kCopies; ++c) {
-            top = fmaxf(top, ref_s[32 * c + row]);
-            if (both) top = fmaxf(top, ref_s[128 + 32 * c + row]);
-          }
-#pragma unroll
-          for (int c = 0; c < S::kCopies; ++c) {
-            const float m0 = ref_s[32 * c + row];
-            if (m0 != -INFINITY) all += mk_ex2(m0 - top) * sum_s[32 * c + row];
-            else all += sum_s[32 * c + row];           // (0, or NaN)
-            if (both) {
-              const float m1 = ref_s[128 + 32 * c + row];
-              if (m1 != -INFINITY) all += mk_ex2(m1 - top) * sum_s[128 + 32 * c + row];
-              else all += sum_s[128 + 32 * c + row];
-            }
-          }
-        }
+        // the row's parts under their larger reference (one that saw nothing has no
+        // reference and a sum of 0, or NaN)
+        const float m0 = ref_s[128 * a + lane_row], m1 = both ? ref_s[128 + lane_row] : -INFINITY;
+        const float top = fmaxf(m0, m1);
+        const float w0 = m0 == -INFINITY ? 0.0f : mk_ex2(m0 - top), w1 = m1 == -INFINITY ? 0.0f : mk_ex2(m1 - top);
+        float all = m0 == -INFINITY ? sum_s[128 * a + lane_row] : w0 * sum_s[128 * a + lane_row];
+        if (both) all += m1 == -INFINITY ? sum_s[128 + lane_row] : w1 * sum_s[128 + lane_row];
         const bool none = all == 0.0f;                 // (the row has seen nothing)
-        auto factor = [&](int chain) -> float {
-          const float m = ref_s[128 * chain + lane_row];
-          if (none) return 0.0f;
-          const float f = m == -INFINITY ? 0.0f : mk_ex2(m - top);
-          return f / all * mk_pow2(eg_s[chain]);
-        };
-        const float f0 = factor(kPair ? a : 0), f1 = both ? factor(1) : 0.0f;
-        const int m = u.row0 + (kPair ? 128 * a : 0) + row;
-        const bool mine = m < p.M;
-        // 32 dims of this lane's part of its row
-        auto dims = [&](int c, float (&o)[32]) {
-          tmem_ld32(tl + mk_o(kPair ? a : 0) + c, o);
+        const float f0 = w0 / all * mk_pow2(eg_s[a]), f1 = both ? w1 / all * mk_pow2(eg_s[1]) : 0.0f;
+        const int head = u.h + (kPair ? 0 : lane_row / kRows);
+        const int m = u.row0 + (kPair ? 128 * a + lane_row : lane_row % kRows);
+        const bool mine = m < p.M && head < p.H;
+        uint16_t *dst = out_row(u.r, mine ? head : 0, mine ? m : 0);
+        const int64_t prow = piece + (kPair ? 128 * a : 0) + lane_row;
+        const bool direct = u.direct != 0;
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim; c += 16) {
+          float o[16];
+          tmem_ld16(tl + mk_o(a) + c, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = none ? 0.0f : o[i] * f0;
+          for (int i = 0; i < 16; ++i) o[i] = none ? 0.0f : o[i] * f0;
           if (both) {
+            float o1[16];
+            tmem_ld16(tl + mk_o(1) + c, o1);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float o1[16];
-              tmem_ld16(tl + mk_o(1) + c + 16 * h, o1);
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                o[16 * h + i] = none ? 0.0f : fmaf(o1[i], f1, o[16 * h + i]);
-            }
+            for (int i = 0; i < 16; ++i) o[i] = none ? 0.0f : fmaf(o1[i], f1, o[i]);
           }
-        };
-        uint16_t *dst = out_row(u.r, u.h, mine ? m : 0);
-        const int64_t prow = piece + (kPair ? 128 * a : 0) + row;
-        if (kRows == 32) {
-          float *xs = reinterpret_cast<float *>(smem + S::kOffX);   // [copy][32 dims][32 rows]
-#pragma unroll 1
-          for (int c = 0; c < kHeadDim; c += 32) {
-            float o[32];
-            dims(c, o);
+          if (mine) {
+            if (direct) {
+              uint4 *to = reinterpret_cast<uint4 *>(dst + c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) xs[(32 * q4 + i) * 32 + lane] = o[i];
-            named_barrier(1, 128);
-            float y[8];                                // dims c + 8 q4 .. + 7 of the row
+              for (int i = 0; i < 2; ++i)
+                to[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                   pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+            } else {
+              float4 *to = reinterpret_cast<float4 *>(p.o_part + prow * kHeadDim + c);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              y[j] = 0.0f;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) y[j] += xs[(32 * k + 8 * q4 + j) * 32 + lane];
-            }
-            if (mine) {
-              if (u.direct) {
-                *reinterpret_cast<uint4 *>(dst + c + 8 * q4) =
-                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                               pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-              } else {
-                float4 *to = reinterpret_cast<float4 *>(p.o_part + prow * kHeadDim + c + 8 * q4);
-                to[0] = make_float4(y[0], y[1], y[2], y[3]);
-                to[1] = make_float4(y[4], y[5], y[6], y[7]);
-              }
-            }
-            named_barrier(1, 128);
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < kHeadDim; c += 32) {
-            float o[32];
-            dims(c, o);
-            if (mine) {
-              if (u.direct) {
-                uint4 *to = reinterpret_cast<uint4 *>(dst + c);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  to[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                     pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-              } else {
-                float4 *to = reinterpret_cast<float4 *>(p.o_part + prow * kHeadDim + c);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-              }
+              for (int i = 0; i < 4; ++i)
+                to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
           }
         }
-        if (!u.direct && mine && (kRows != 32 || q4 == 0)) p.ml_part[prow] = make_float2(top, all);
+        if (!direct && mine) p.ml_part[prow] = make_float2(top, all);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -1013,12 +949,14 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       if (*ticket_s) {
         // a warp per row: a lane per piece for the weights, then four dims a lane over the
         // pieces, eight loads under way
-        const int rows = min(S::kTileRows, p.M - u.row0), b_first = u.b_first, pieces = u.b_last - b_first + 1;
+        const int b_first = u.b_first, pieces = u.b_last - b_first + 1;
         auto place = [&](int b, int r) -> int64_t {
-          return static_cast<int64_t>(2 * (b_first + b) + (b == 0 ? 1 : 0)) * S::kTileRows + r;
+          return static_cast<int64_t>(2 * (b_first + b) + (b == 0 ? 1 : 0)) * S::kLanes + r;
         };
 #pragma unroll 1
-        for (int r = q4; r < rows; r += 4) {
+        for (int r = q4; r < S::kLanes; r += 4) {
+          const int head = u.h + (kPair ? 0 : r / kRows), m = u.row0 + (kPair ? r : r % kRows);
+          if (m >= p.M || head >= p.H) continue;
           float top = -INFINITY, all = 0.0f;
           float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
@@ -1061,7 +999,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             }
           }
           const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-          *reinterpret_cast<uint2 *>(out_row(u.r, u.h, u.row0 + r) + 4 * lane) =
+          *reinterpret_cast<uint2 *>(out_row(u.r, head, m) + 4 * lane) =
               make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
         }
       }
@@ -1075,10 +1013,11 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       bool ok = mk_wait_all(BAR(S::kKvFull + b), (seq / S::kStages) & 1, abort_s);
       if (ok && seq >= 2) ok = mk_wait_all(BAR(S::kVfEmpty + (seq & 1)), ((seq >> 1) - 1) & 1, abort_s);
       if (!ok) return false;
-      const int x0 = (u.c0 + k) * kMkTok;
+      // (key j: box of 16 tokens and all heads, head, token)
+      const int x = (u.c0 + k) * S::kTok + (S::kHeads == 1 ? j : 16 * (j / (16 * S::kHeads)) + (j & 15));
       const uint8_t *src = smem + S::kOffKv + b * S::kStage + p.v_off + (j >> 3) * p.group + (j & 7) * 128;
       uint8_t *dst = smem + S::kOffVf + (seq & 1) * S::kVfBytes + j * 128;
-      bool keep = x0 + j < u.X;
+      bool keep = x < u.X;
       if (!whole) {
         bool bad = false;
 #pragma unroll 1
@@ -1121,7 +1060,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       }
       const MkUnit &u = unit_s[t % kMkUnits];
       const int un = u.n;
-      const MkWhole all_whole = mk_unit_whole<S::kTileRows>(p, u);
+      const MkWhole all_whole = mk_unit_whole<S>(p, u);
 #pragma unroll 1
       for (int k = 0; k < max(un, 1) && !gave_up; ++k) {
         if (un != 0) {
@@ -1152,6 +1091,28 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    // Pages are looked up for 32 boxes at a time, a lane each: `per` chunks.
+    const int log2_box = 31 - __clz(p.box), boxes = S::kTok >> log2_box, per = 32 >> (S::kTokLog2 - log2_box);
+    auto box_pos = [&](const MkUnit &u, int kb, int *pos) -> bool {
+      const int x = (u.c0 + kb) * S::kTok + lane * p.box;
+      *pos = x < u.s16 ? x : x + u.shift;
+      return x < u.X && (lane >> (S::kTokLog2 - log2_box)) < u.n - kb;
+    };
+    auto read_page = [&](const MkUnit &u, int kb) -> int {
+      int pos;
+      if (!box_pos(u, kb, &pos)) return -1;
+      return __ldg(p.tables + static_cast<int64_t>(u.r) * p.width + (pos >> p.log2_bs));
+    };
+    // a box's first slot, -1 if it has none (bad: a page outside the cache)
+    auto to_slot = [&](const MkUnit &u, int kb, int page, bool &bad) -> int {
+      int pos;
+      if (!box_pos(u, kb, &pos)) return -1;
+      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_blocks)) {
+        bad = true;
+        return -1;
+      }
+      return static_cast<int>((static_cast<uint32_t>(page) << p.log2_bs) | (pos & ((1 << p.log2_bs) - 1)));
+    };
     if (warp == kMkWarpLoad) {
       // --------------------------------------------- units, copies of codes
       int x = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * B, static_cast<int64_t>(total)));
@@ -1166,7 +1127,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           else hi = mid - 1;
         }
         L = mk_len(p, lo);
-        const unsigned W = static_cast<unsigned>(pre[lo + 1] - pre[lo]) / static_cast<unsigned>(p.H);
+        const unsigned W = static_cast<unsigned>(pre[lo + 1] - pre[lo]) / static_cast<unsigned>(p.HG);
         h = static_cast<int>(static_cast<unsigned>(x - pre[lo]) / W);
         at = pre[lo] + h * static_cast<int>(W);
       }
@@ -1177,12 +1138,12 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
 #pragma unroll 1
         while (x < x_end) {
           const MkSpan s = mk_span<S::kTileRows>(p, L, t);
-          const int V = mk_positions(s.X), ut = t, uh = h, ur = lo, ua = at, uL = L;
+          const int V = mk_positions<S>(s.X), ut = t, uh = h, ur = lo, ua = at, uL = L;
           if (x >= at + V || at + V <= x_end) {        // (nothing of it is left after this)
             at += V;
             if (++t == p.T) {
               t = 0;
-              if (++h == p.H) {
+              if (++h == p.HG) {
                 h = 0;
                 do ++lo;
                 while (lo < p.N && pre[lo + 1] <= at);
@@ -1197,7 +1158,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           n = end - from;
           if (lane == 0) {
             u.r = ur;
-            u.h = uh;
+            u.h = uh * S::kHeads;
             u.row0 = ut * S::kTileRows;
             u.c0 = from - first;
             u.X = s.X;
@@ -1209,7 +1170,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             u.b_first = b_first;
             u.b_last = static_cast<int>(static_cast<unsigned>(ua + V - 1) / static_cast<unsigned>(B));
             u.slot = 2 * static_cast<int>(blockIdx.x) + (static_cast<int>(blockIdx.x) == b_first ? 1 : 0);
-            u.index = (ur * p.H + uh) * p.T + ut;
+            u.index = (ur * p.HG + uh) * p.T + ut;
           }
           break;
         }
@@ -1217,199 +1178,201 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         __syncwarp();
         return n;
       };
-      int32_t *ids = reinterpret_cast<int32_t *>(smem + S::kOffIds);
-      const int boxes = kMkTok / p.box, log2_box = 31 - __clz(p.box), mask = (1 << p.log2_bs) - 1;
       const uint64_t pol = l2_policy_evict_normal();
-      // What is kept of the unit whose page ids are asked for (f) and of the one whose
-      // chunks are copied.
-      int fn = 0, fk = 0, fx = 0, fX = 0, fs16 = 0, fshift = 0;
-      const int32_t *ftable = p.tables;
-      int un = 0, k = 0, x0 = 0, uX = 0, us16 = 0, ushift = 0, uh = 0;
-      int published = 0, taken = 0;
-      bool ok = true, more = true, bad = false;
-      uint32_t issued = 0;
+      // A batch: the pages of 32 boxes, one a lane, read while the batch before is copied.
+      int t_cur = 0, un = next_unit(unit_s[0]);
+      if (lane == 0) mbar_arrive(BAR(S::kUnitFull));
+      int kb = -1, j = 0, id = un != 0 ? read_page(unit_s[0], 0) : -1;
+      int next_un = un, next_kb = 0, next_t = 0;       // of the batch that `id` belongs to
+      int slot = -1, uh = 0;
+      uint32_t have = 0u, n = 0u;
+      bool ok = true, bad = false;
 #pragma unroll 1
-      for (int seq = -kMkIdAhead;; ++seq) {
-        // page ids of the chunk kMkIdAhead ahead (a commit group in any case); its unit is
-        // announced when its first chunk's are asked for
-        if (more && fk == fn) {
-          const int e = published % kMkUnits;
-          if (published >= kMkUnits)
-            ok = mk_wait_all(BAR(S::kUnitEmpty + e), (published / kMkUnits - 1) & 1, abort_s);
-          if (!ok) break;
-          fn = next_unit(unit_s[e]);
-          fk = 0;
-          more = fn != 0;
-          if (lane == 0) mbar_arrive(BAR(S::kUnitFull + e));
-          const MkUnit &f = unit_s[e];
-          fx = f.c0 * kMkTok + lane * p.box;
-          fX = f.X;
-          fs16 = f.s16;
-          fshift = f.shift;
-          if (more) ftable = p.tables + static_cast<int64_t>(f.r) * p.width;
-          ++published;
-        }
-        if (more) {
-          if (lane < boxes) {
-            const bool need = fx < fX;
-            const int pos = fx < fs16 ? fx : fx + fshift;
-            cp_async_4(ids + ((seq + kMkIdAhead) % (kMkIdAhead + 1)) * kMkMaxBoxes + lane,
-                       ftable + (need ? pos >> p.log2_bs : 0), need ? 4u : 0u);
-          }
-          fx += kMkTok;
-          ++fk;
-        }
-        cp_async_commit();
-        if (seq < 0) continue;
-        if (k == un) {                                 // the next unit (announced by now)
-          const MkUnit &u = unit_s[taken % kMkUnits];
-          un = u.n;
-          x0 = u.c0 * kMkTok;
-          uX = u.X;
-          us16 = u.s16;
-          ushift = u.shift;
-          uh = u.h;
-          ++taken;
-          k = 0;
+      for (;;) {
+        if (kb < 0 || j == per || kb + j == un) {
+          // the next batch
+          un = next_un;
+          kb = next_kb;
+          t_cur = next_t;
+          j = 0;
           if (un == 0) break;
-        }
-        cp_async_wait<kMkIdAhead>();
-        __syncwarp();
-        // lane i: the first slot of the chunk's box i (-1: none)
-        int slot = -1;
-        {
-          const int xt = x0 + lane * p.box;
-          if (lane < boxes && xt < uX) {
-            const uint32_t page = static_cast<uint32_t>(ids[(seq % (kMkIdAhead + 1)) * kMkMaxBoxes + lane]);
-            const int pos = xt < us16 ? xt : xt + ushift;
-            if (page < static_cast<uint32_t>(p.num_blocks))
-              slot = static_cast<int>((page << p.log2_bs) | (pos & mask));
-            else
-              bad = true;
+          const MkUnit &u = unit_s[t_cur % kMkUnits];
+          slot = to_slot(u, kb, id, bad);
+          uh = u.h;
+          have = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+          next_kb = kb + per;
+          if (next_kb >= un) {
+            // the next unit, announced
+            next_kb = 0;
+            ++next_t;
+            const int e = next_t % kMkUnits;
+            if (next_t >= kMkUnits)
+              ok = mk_wait_all(BAR(S::kUnitEmpty + e), (next_t / kMkUnits - 1) & 1, abort_s);
+            if (!ok) break;
+            next_un = next_unit(unit_s[e]);
+            if (lane == 0) mbar_arrive(BAR(S::kUnitFull + e));
           }
+          id = next_un != 0 ? read_page(unit_s[next_t % kMkUnits], next_kb) : -1;
         }
-        const uint32_t have = __ballot_sync(0xFFFFFFFFu, slot >= 0);
-        const uint32_t n = seq, b = n % S::kStages, bs = n % kMkScales;
+        const uint32_t b = n % S::kStages;
+        constexpr int kBoxes = 8 / S::kHeads;          // at most
+        int z[kBoxes];                                 // in groups of 8 slots
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i) z[i] = __shfl_sync(0xFFFFFFFFu, slot >> 3, j * boxes + i);
+        const uint32_t now = (have >> (j * boxes)) & ((1u << boxes) - 1u);
         if (n >= S::kStages)
           ok = mk_wait_all(BAR(S::kKvEmpty + b), (n / S::kStages - 1) & 1, abort_s);
-        if (ok && n >= kMkScales)
-          ok = mk_wait_all(BAR(S::kScEmpty + bs), (n / kMkScales - 1) & 1, abort_s);
         if (!ok) break;
-        int z[kMkMaxBoxes];                            // in groups of 8 slots
-#pragma unroll
-        for (int i = 0; i < kMkMaxBoxes; ++i) z[i] = __shfl_sync(0xFFFFFFFFu, slot >> 3, i);
         if (mk_elect()) {
           const uint32_t dst = smem_addr(smem + S::kOffKv) + b * S::kStage;
-          const uint32_t full = BAR(S::kKvFull + b), step = p.box / 8 * p.group;
-          mbar_arrive_expect_tx(full, __popc(have) * 2 * p.box * kHeadDim);
+          const uint32_t full = BAR(S::kKvFull + b), step = p.box * S::kHeads / 8 * p.group;
+          mbar_arrive_expect_tx(full, __popc(now) * 2 * p.box * S::kHeads * kHeadDim);
 #pragma unroll 1
           for (int plane = 0; plane <= p.two_maps; ++plane) {
             const CUtensorMap *map = plane == 0 ? &tm : &tm_v;
 #pragma unroll
-            for (int i = 0; i < kMkMaxBoxes; ++i)
-              if ((have >> i) & 1u)
+            for (int i = 0; i < kBoxes; ++i)
+              if ((now >> i) & 1u)
                 mk_load_box(dst + plane * p.v_off + i * step, map, z[i], uh, full, pol);
           }
         }
         __syncwarp();
-        {
-          // the scales of the tokens 4 lane .. 4 lane + 3 (of one box)
-          const int first = __shfl_sync(0xFFFFFFFFu, slot, 4 * lane >> log2_box);
-          const int left = first < 0 ? 0 : uX - x0 - 4 * lane;
-          const int64_t at = left > 0 ? (static_cast<int64_t>(first) + (4 * lane & (p.box - 1))) * p.H + uh : 0;
-          const float *kp = p.k_scales + at, *vp = p.v_scales + at;
-          float *ks = reinterpret_cast<float *>(smem + S::kOffSc) + bs * 3 * kMkTok + 4 * lane;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t size = i < left ? 4u : 0u;
-            const int of = i < left ? i * p.H : 0;
-            cp_async_4(ks + i, kp + of, size);
-            cp_async_4(ks + kMkTok + i, vp + of, size);
-          }
-          mk_arrive_copies(BAR(S::kScRaw + bs));
-        }
-        x0 += kMkTok;
-        ++k;
-        ++issued;
+        ++j;
+        ++n;
       }
-      cp_async_wait<0>();
       gave_up = !ok;
       bad = __any_sync(0xFFFFFFFFu, bad);
       if (lane == 0) {
         if (bad && p.err_flags) atomicOr(p.err_flags, KVQ_ERRF_BLOCK_RANGE);
         // copies in flight land before the block leaves
-        for (uint32_t v = issued > S::kStages ? issued - S::kStages : 0; v < issued; ++v)
+        for (uint32_t v = n > S::kStages ? n - S::kStages : 0; v < n; ++v)
           mbar_wait_sleep_bounded(BAR(S::kKvFull + v % S::kStages), (v / S::kStages) & 1);
       }
     } else if (warp == kMkWarpScale) {
       // -------------------------------------------------------------- scales
-      // Value scales brought over 2^Eg, the chunk's largest scales found; lane l has the
-      // tokens 4 l .. 4 l + 3.
-      uint32_t seq = 0;
-      for (int t = 0; !gave_up; ++t) {
-        if (!wait_unit(t)) {
-          gave_up = true;
-          break;
-        }
-        const MkUnit &u = unit_s[t % kMkUnits];
-        const int un = u.n;
-        if (un == 0) break;
-        const MkWhole all_whole = mk_unit_whole<S::kTileRows>(p, u);
-        release_unit(t);
-        int eg = 0;
+      // Copied two chunks ahead; value scales brought over 2^Eg, the chunk's largest scales
+      // found.  Lane l has the tokens 4 l .. 4 l + 3.
+      constexpr int kAhead = 2;
+      const int box_of = 4 * lane / (p.box * S::kHeads), tok_of = 4 * lane & (p.box - 1);
+      const int head_of = (4 * lane >> log2_box) & (S::kHeads - 1);
+      bool ok = wait_unit(0), bad_page = false;
+      int un = ok ? unit_s[0].n : 0;
+      int t_cur = 0, kb = -1, j = 0, next_un = un, next_kb = 0, next_t = 0;
+      int id = un != 0 ? read_page(unit_s[0], 0) : -1;
+      int slot = -1, eg = 0;
+      const float *kp = p.k_scales, *vp = p.v_scales;
+      int left = 0;                                    // tokens of the unit from the lane's first on
+      MkWhole all_whole{0, 0, 0};
+      uint32_t n = 0u, done = 0u, hist = 0u;           // hist: 2 bits a chunk: a unit's first, edge
+      bool more = ok;
 #pragma unroll 1
-        for (int k = 0; k < un; ++k, ++seq) {
-          const uint32_t b = seq % kMkScales;
-          if (!mk_wait_all(BAR(S::kScRaw + b), (seq / kMkScales) & 1, abort_s)) {
-            gave_up = true;
-            break;
-          }
-          float4 *ks = reinterpret_cast<float4 *>(smem + S::kOffSc + b * 3 * kMkTok * 4) + lane;
-          const float4 kk = ks[0];
-          const float4 v4 = ks[kMkTok / 4];
-          float vv[4] = {v4.x, v4.y, v4.z, v4.w}, lg[4];
-          uint32_t bad = 0u;
-          if (!all_whole.at(k)) {
-            // scales that are not finite reach nobody by a product; rows that see them
-            // become NaN
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (!(vv[i] - vv[i] == 0.0f)) {
-                vv[i] = 0.0f;
-                bad |= 1u << i;
-              }
-            if (__any_sync(0xFFFFFFFFu, bad != 0u)) {
-              if (lane < 4) bad_s[8 + 4 * b + lane] = 0u;
-              __syncwarp();
-              if (bad != 0u)
-                atomicOr(bad_s + 8 + 4 * b + (lane >> 3), bad << (4 * (lane & 7)));
+      for (;;) {
+        if (more && (kb < 0 || j == per || kb + j == un)) {
+          // the next batch
+          if (kb >= 0 && next_t != t_cur) release_unit(t_cur);
+          un = next_un;
+          kb = next_kb;
+          t_cur = next_t;
+          j = 0;
+          more = un != 0;
+          if (more) {
+            const MkUnit &u = unit_s[t_cur % kMkUnits];
+            slot = to_slot(u, kb, id, bad_page);
+            kp = p.k_scales + u.h + head_of;
+            vp = p.v_scales + u.h + head_of;
+            // (keys 4 lane ..: box, head, tokens from `tok` of the box on)
+            left = head_of < p.H - u.h ? u.X - (u.c0 + kb) * S::kTok - box_of * p.box - tok_of : INT_MIN;
+            if (kb == 0) all_whole = mk_unit_whole<S>(p, u);
+            next_kb = kb + per;
+            if (next_kb >= un) {
+              next_kb = 0;
+              ++next_t;
+              ok = wait_unit(next_t);
+              if (!ok) break;
+              next_un = unit_s[next_t % kMkUnits].n;
             }
+            id = next_un != 0 ? read_page(unit_s[next_t % kMkUnits], next_kb) : -1;
           }
-          const float flagged = __any_sync(0xFFFFFFFFu, bad != 0u) ? 1.0f : 0.0f;
-          // (fmaxf leaves NaN out)
-          const float km4 = fmaxf(fmaxf(kk.x, kk.y), fmaxf(kk.z, kk.w));
-          const float vm4 = fmaxf(fmaxf(vv[0], vv[1]), fmaxf(vv[2], vv[3]));
-          const uint32_t km = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(km4, 0.0f)));
-          const uint32_t vm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(vm4, 0.0f)));
-          const int ev = min(mk_ceil_log2(__uint_as_float(vm)), 126);
-          if (k == 0) eg = min(ev, kMkMaxEg);
-          else if (ev > eg) eg = min(ev + 2, kMkMaxEg);
-          const float down = mk_pow2(-eg);
+        }
+        if (more) {
+          const uint32_t b = n % kMkScales;
+          if (n >= kMkScales)
+            ok = mk_wait_all(BAR(S::kScEmpty + b), (n / kMkScales - 1) & 1, abort_s);
+          if (!ok) break;
+          const int first = __shfl_sync(0xFFFFFFFFu, slot, j * boxes + box_of);
+          const int len = first < 0 ? 0 : left;
+          const int64_t at = len > 0 ? (static_cast<int64_t>(first) + tok_of) * p.H : 0;
+          float *ks = reinterpret_cast<float *>(smem + S::kOffSc) + b * 3 * kMkTok + 4 * lane;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            vv[i] *= down;
-            lg[i] = fmaxf(static_cast<float>(mk_ceil_log2(vv[i])), kMkFloor);
+            const uint32_t size = i < len ? 4u : 0u;
+            const int of = i < len ? i * p.H : 0;
+            cp_async_4(ks + i, kp + at + of, size);
+            cp_async_4(ks + kMkTok + i, vp + at + of, size);
           }
-          ks[kMkTok / 4] = make_float4(vv[0], vv[1], vv[2], vv[3]);
-          ks[kMkTok / 2] = make_float4(lg[0], lg[1], lg[2], lg[3]);
-          if (lane == 0)
-            reinterpret_cast<float4 *>(smem + S::kOffMeta)[b] =
-                make_float4(__uint_as_float(km), fmaxf(static_cast<float>(ev - eg), kMkFloor),
-                            __int_as_float(eg), flagged);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(S::kScFull + b));
+          const int k = kb + j;
+          hist = (hist << 2) | (k == 0 ? 1u : 0u) | (all_whole.at(k) ? 0u : 2u);
+          if (left > INT_MIN / 2) left -= S::kTok;
+          ++j;
+          ++n;
         }
+        cp_async_commit();
+        if (!more && done == n) break;
+        if (more && n - done <= kAhead) continue;
+        // chunk `done`, copied kAhead chunks ago
+        if (more) cp_async_wait<kAhead>();
+        else cp_async_wait<0>();
+        __syncwarp();
+        const uint32_t b = done % kMkScales;
+        float4 *ks = reinterpret_cast<float4 *>(smem + S::kOffSc + b * 3 * kMkTok * 4) + lane;
+        const float4 kk = ks[0];
+        const float4 v4 = ks[kMkTok / 4];
+        float vv[4] = {v4.x, v4.y, v4.z, v4.w}, lg[4];
+        const uint32_t what = hist >> (2 * (n - 1 - done));
+        float flagged = 0.0f;
+        if (what & 2u) {
+          // scales that are not finite reach nobody by a product; rows that see them become
+          // NaN
+          uint32_t bad = 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(vv[i] - vv[i] == 0.0f)) {
+              vv[i] = 0.0f;
+              bad |= 1u << i;
+            }
+          if (__any_sync(0xFFFFFFFFu, bad != 0u)) {
+            flagged = 1.0f;
+            if (lane < 4) bad_s[8 + 4 * b + lane] = 0u;
+            __syncwarp();
+            if (bad != 0u) atomicOr(bad_s + 8 + 4 * b + (lane >> 3), bad << (4 * (lane & 7)));
+          }
+        }
+        // (fmaxf leaves NaN out)
+        const float km4 = fmaxf(fmaxf(kk.x, kk.y), fmaxf(kk.z, kk.w));
+        const float vm4 = fmaxf(fmaxf(vv[0], vv[1]), fmaxf(vv[2], vv[3]));
+        const uint32_t km = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(km4, 0.0f)));
+        const uint32_t vm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(vm4, 0.0f)));
+        const int ev = min(mk_ceil_log2(__uint_as_float(vm)), 126);
+        if (what & 1u) eg = min(ev, kMkMaxEg);
+        else if (ev > eg) eg = min(ev + 2, kMkMaxEg);
+        const float down = mk_pow2(-eg);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vv[i] *= down;
+          lg[i] = fmaxf(static_cast<float>(mk_ceil_log2(vv[i])), kMkFloor);
+        }
+        ks[kMkTok / 4] = make_float4(vv[0], vv[1], vv[2], vv[3]);
+        ks[kMkTok / 2] = make_float4(lg[0], lg[1], lg[2], lg[3]);
+        if (lane == 0)
+          reinterpret_cast<float4 *>(smem + S::kOffMeta)[b] =
+              make_float4(__uint_as_float(km), fmaxf(static_cast<float>(ev - eg), kMkFloor),
+                          __int_as_float(eg), flagged);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(S::kScFull + b));
+        ++done;
       }
+      cp_async_wait<0>();
+      gave_up = !ok;
     } else {
       // ---------------------------------------------------- MMAs of a chain
       // Each turn: PV of one of the chain's chunks and QK^T of its next, chain 0's and
@@ -1518,7 +1481,13 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
   }
 }
 
-int mk_tile_rows(int M) { return M <= 32 ? 32 : (M <= 128 ? 128 : 256); }
+// Rows of a unit and head, and its heads.
+int mk_tile_rows(int M) { return M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256)); }
+int mk_heads(int rows) { return rows >= 128 ? 1 : 128 / rows; }
+int64_t mk_units(int n, int H, int M) {
+  const int rows = mk_tile_rows(M), heads = mk_heads(rows);
+  return static_cast<int64_t>(n) * ((H + heads - 1) / heads) * ((M + rows - 1) / rows);
+}
 
 template <bool kPair, int kRows>
 cudaError_t mk_launch(const MkParams &p, const CUtensorMap &map, const CUtensorMap &map_v, int grid,
@@ -1545,10 +1514,10 @@ size_t mk_round(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t attn_masked_workspace_bytes(const MaskedArgs &a, int32_t num_kv_heads) {
   const int64_t M = static_cast<int64_t>(a.rows_per_request) * (a.num_q_heads / num_kv_heads);
-  const int64_t rows = mk_tile_rows(static_cast<int>(M)), T = (M + rows - 1) / rows;
-  const int64_t n = std::min(a.num_requests, kMkMaxRequests);
-  const size_t slots = static_cast<size_t>(a.sms) * 2 * rows;
-  return mk_round(static_cast<size_t>(n * num_kv_heads * T) * 8) +
+  const int rows = mk_tile_rows(static_cast<int>(M));
+  const size_t slots = static_cast<size_t>(a.sms) * 2 * std::max(rows, 128);
+  return mk_round(static_cast<size_t>(mk_units(std::min(a.num_requests, kMkMaxRequests), num_kv_heads,
+                                               static_cast<int>(M))) * 8) +
          mk_round(slots * kHeadDim * sizeof(float)) + mk_round(slots * sizeof(float2));
 }
 
@@ -1564,12 +1533,15 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
   p.M = p.R * p.G;
   p.inv_g = static_cast<uint32_t>(((uint64_t(1) << 32) + p.G - 1) / p.G);
   const int rows = mk_tile_rows(p.M);
+  const int heads = mk_heads(rows), tokens = kMkTok / heads;
   p.T = (p.M + rows - 1) / rows;
+  p.HG = (H + heads - 1) / heads;
   p.width = a.max_blocks_per_req;
   p.num_blocks = static_cast<int32_t>(c.num_slots >> a.log2_block);
   p.log2_bs = a.log2_block;
-  // boxes of a copy: a window and its sinks start on any 16 tokens of a page
-  p.box = a.tree_mask != nullptr ? std::min(1 << a.log2_block, kMkTok) : 16;
+  // tokens of a box: a window and its sinks start on any 16 of a page, and of several heads
+  // a chunk has no more
+  p.box = a.tree_mask != nullptr && heads == 1 ? std::min(1 << a.log2_block, kMkTok) : 16;
   // (beyond the longest context neither bound means anything)
   p.window = std::min(a.window, a.max_context_len + p.R);
   p.sinks = std::min(a.num_sinks, a.max_context_len);
@@ -1580,8 +1552,8 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
   // it 2,000: pieces of at least sqrt(chunks (8 rows + 200) / 2000) chunks.
   const int64_t reach = a.tree_mask != nullptr ? a.max_context_len
                                                : std::min<int64_t>(a.max_context_len, int64_t(p.window) + p.sinks + p.R);
-  const double chunks = static_cast<double>((reach + kMkTok - 1) / kMkTok + 1);
-  p.least = std::max(1, static_cast<int>(std::sqrt(chunks * (8 * std::min(p.M, rows) + 200) / 2000) + 0.5));
+  const double chunks = static_cast<double>((reach + tokens - 1) / tokens + 1);
+  p.least = std::max(1, static_cast<int>(std::sqrt(chunks * (8 * std::min(p.M, rows) * heads + 200) / 2000) + 0.5));
   p.k_scales = c.k_scales;
   p.v_scales = c.v_scales;
   p.err_flags = a.err_flags;
@@ -1593,13 +1565,13 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
   p.two_maps = high - low < 128 || high - low >= (int64_t(1) << 40);
   bool ok;
   if (p.two_maps) {
-    ok = encode_plane_tensor_map(&map, c.k_codes, 0, slots, H, p.box) &&
-         encode_plane_tensor_map(&map_v, c.v_codes, 0, slots, H, p.box);
+    ok = encode_plane_tensor_map(&map, c.k_codes, 0, slots, H, p.box, heads) &&
+         encode_plane_tensor_map(&map_v, c.v_codes, 0, slots, H, p.box, heads);
     p.group = 1024;
     p.k_off = 0;
     p.v_off = kMkTok * kHeadDim;
   } else {
-    ok = encode_plane_tensor_map(&map, low, high - low, slots, H, p.box);
+    ok = encode_plane_tensor_map(&map, low, high - low, slots, H, p.box, heads);
     map_v = map;
     p.group = 2048;
     p.k_off = low == c.k_codes ? 0 : 1024;
@@ -1616,14 +1588,15 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
     p.lens = a.context_lens + r0;
     p.tree = a.tree_mask != nullptr ? a.tree_mask + row * p.words : nullptr;
     char *ws = static_cast<char *>(a.workspace);
-    const size_t slots = static_cast<size_t>(grid) * 2 * rows;
+    const size_t slots_ws = static_cast<size_t>(grid) * 2 * std::max(rows, 128);
     p.tickets = reinterpret_cast<unsigned long long *>(ws);
-    ws += mk_round(static_cast<size_t>(std::min(a.num_requests, kMkMaxRequests)) * H * p.T * 8);
+    ws += mk_round(static_cast<size_t>(mk_units(std::min(a.num_requests, kMkMaxRequests), H, p.M)) * 8);
     p.o_part = reinterpret_cast<float *>(ws);
-    ws += mk_round(slots * kHeadDim * sizeof(float));
+    ws += mk_round(slots_ws * kHeadDim * sizeof(float));
     p.ml_part = reinterpret_cast<float2 *>(ws);
     p.tag = next_call_tag();
     const cudaError_t e = rows == 32    ? mk_launch<false, 32>(p, map, map_v, grid, stream)
+                          : rows == 64  ? mk_launch<false, 64>(p, map, map_v, grid, stream)
                           : rows == 128 ? mk_launch<false, 128>(p, map, map_v, grid, stream)
                                         : mk_launch<true, 128>(p, map, map_v, grid, stream);
     if (e != cudaSuccess) return e;
