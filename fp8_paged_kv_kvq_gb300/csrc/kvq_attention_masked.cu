@@ -41,9 +41,9 @@
 //    (0 times NaN is NaN) and noted; a row that does see one becomes NaN.
 //  * Roles, 512 threads: warps 0-3 and 4-7 the softmax of chain 0 and 1 (a thread owns
 //    a TMEM lane, a row), 8-11 the value codes' conversion and the epilogue, 12 the
-//    units and all copies, 13 and 14 the MMAs of chain 0 and 1, 15 the scales.  Every
-//    wait is bounded; a role that gives up raises a shared abort flag, copies and MMAs
-//    in flight complete, the block frees its tensor memory (KVQ_ERRF_WAIT_TIMEOUT).
+//    units and the copies of codes, 13 and 14 the MMAs of chain 0 and 1, 15 the scales.
+//    Every wait is bounded; a role that gives up raises a shared abort flag, copies and
+//    MMAs in flight complete, the block frees its tensor memory (KVQ_ERRF_WAIT_TIMEOUT).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -81,28 +81,32 @@ struct MkShape {
   static constexpr int kTokLog2 = kRows == 32 ? 5 : (kRows == 64 ? 6 : 7);
   static constexpr int kQTiles = kPair ? 2 : 1;
   // shared memory, offsets from a 1024-byte aligned base
-  static constexpr int kStages = kPair ? 2 : 3;
-  static constexpr int kStage = 2 * kMkTok * kHeadDim;       // a chunk's codes: 8 rows of K, 8 of V, ...
+  // Code stages of a chunk (8 rows of K, 8 of V, ...).  kPair: values are converted into two
+  // buffers of their own.  Else in place, over the chunk's key codes (which S has been made
+  // of) and its value codes, so that five chunks are on their way or at work.
+  static constexpr int kStages = kPair ? 2 : 5;
+  static constexpr int kVfs = kPair ? 2 : kStages;
+  static constexpr int kStage = 2 * kMkTok * kHeadDim;
   static constexpr int kQPiece = 128 * kHeadDim;
   static constexpr int kOffQ = 0;                            // [tile][piece]
-  static constexpr int kOffVf = kOffQ + kQTiles * 2 * kQPiece;   // f16 values, two chunks
-  static constexpr int kVfBytes = kMkTok * kHeadDim * 2;
-  static constexpr int kOffKv = kOffVf + 2 * kVfBytes;
-  static constexpr int kOffSum = kOffKv + kStages * kStage;  // [chain][128] denominators
+  static constexpr int kVfBytes = kMkTok * kHeadDim * 2;     // f16 values of a chunk
+  static constexpr int kOffKv = kOffQ + kQTiles * 2 * kQPiece;
+  static constexpr int kOffVf = kPair ? kOffKv + kStages * kStage : kOffKv;
+  static constexpr int kOffSum = kOffKv + kStages * kStage + (kPair ? 2 * kVfBytes : 0);   // [chain][128] denominators
   static constexpr int kOffRef = kOffSum + 2 * 128 * 4;      // [chain][128] references
   static constexpr int kOffEg = kOffRef + 2 * 128 * 4;       // [chain]
   static constexpr int kOffSc = kOffEg + 16;                 // [stage][K | V | log2 V][128]
   static constexpr int kOffMeta = kOffSc + kMkScales * 3 * kMkTok * 4;   // [stage] float4
   static constexpr int kOffUnit = kOffMeta + kMkScales * 16;
   static constexpr int kOffBad = kOffUnit + kMkUnits * 64;   // [Vf][4 words], [scales][4 words]
-  static constexpr int kOffMisc = kOffBad + 32 + kMkScales * 16;              // tmem base, abort, ticket
+  static constexpr int kOffMisc = kOffBad + (kVfs + kMkScales) * 16;              // tmem base, abort, ticket
   static constexpr int kOffScan = kOffMisc + 16;             // a warp's sum each
   static constexpr int kOffPre = kOffScan + kMkThreads / 32 * 4;
   static constexpr int kOffBar = (kOffPre + (kMkMaxRequests + 1) * 4 + 7) / 8 * 8;
   static constexpr int kKvFull = 0;
   static constexpr int kKvEmpty = kKvFull + kStages;
   static constexpr int kVfFull = kKvEmpty + kStages;
-  static constexpr int kVfEmpty = kVfFull + 2;
+  static constexpr int kVfEmpty = kVfFull + kVfs;
   static constexpr int kScFull = kVfEmpty + 2;
   static constexpr int kScEmpty = kScFull + kMkScales;
   static constexpr int kQFull = kScEmpty + kMkScales;        // per chain from here on
@@ -118,7 +122,7 @@ struct MkShape {
   static constexpr int kUnitEmpty = kUnitFull + kMkUnits;
   static constexpr int kBars = kUnitEmpty + kMkUnits;
   static constexpr int kSmem = kOffBar + 8 * kBars + 1024;
-  static_assert(kOffKv % 1024 == 0 && kOffVf % 1024 == 0 && kOffSc % 16 == 0 && kOffMeta % 16 == 0 &&
+  static_assert(kStage == kVfBytes && kOffKv % 1024 == 0 && kOffVf % 1024 == 0 && kOffSc % 16 == 0 && kOffMeta % 16 == 0 &&
                     kOffUnit % 16 == 0 && kOffBad % 16 == 0 && kOffMisc % 16 == 0 && kOffBar % 8 == 0,
                 "alignment");
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -136,7 +140,7 @@ constexpr uint32_t kMkIdescPV = mma_idesc(128, kHeadDim, false, true);       // 
 // The operands' shared-memory descriptors (smem_desc: stride offset, version 1, 128-byte
 // swizzle), upper words and the two leading offsets.
 constexpr uint32_t kMkDescHi = (1024u >> 4) | (1u << 14) | (kSmemSwizzle128 << 29);
-constexpr uint32_t kMkKMajor = 1u << 16, kMkMnMajor = (16384u >> 4) << 16;
+constexpr uint32_t kMkKMajor = 1u << 16;
 
 __device__ __forceinline__ void mk_mma_qk(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t b_hi,
                                           uint32_t acc) {
@@ -147,11 +151,12 @@ __device__ __forceinline__ void mk_mma_qk(uint32_t d, uint32_t a_lo, uint32_t b_
       :: "r"(d), "r"(a_lo), "r"(b_lo), "n"(kMkIdescQK), "r"(acc), "n"(kMkDescHi), "r"(b_hi)
       : "memory");
 }
-__device__ __forceinline__ void mk_mma_pv(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t acc) {
+__device__ __forceinline__ void mk_mma_pv(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+                                          uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n"
-      :: "r"(d), "r"(a_tmem), "r"(b_lo), "n"(kMkIdescPV), "r"(acc), "n"(kMkDescHi) : "memory");
+      :: "r"(d), "r"(a_tmem), "r"(b_lo), "n"(kMkIdescPV), "r"(acc), "r"(b_hi) : "memory");
 }
 
 // One box of a copy: 8 rows of K, 8 of V, 8 of K, ... of a head, from group z of 8 slots on.
@@ -666,10 +671,10 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
   if (tid < S::kBars) {
     uint32_t count = 1;
     const int i = tid;
-    if (i >= S::kVfEmpty && i < S::kVfEmpty + 2)
-      count = kPair ? 2 : 1;                           // a commit of each chain that reads it
-    if (i >= S::kVfFull && i < S::kVfFull + 2) count = 4;   // the converting warps
-    if (i >= S::kKvEmpty && i < S::kKvEmpty + S::kStages) count = 4 + (kPair ? 2 : 1);
+    // commits of the chains that read it, and arrivals of the converting warps
+    if (i >= S::kVfEmpty && i < S::kVfEmpty + 2) count = 2;
+    if (i >= S::kVfFull && i < S::kVfFull + S::kVfs) count = 4;
+    if (i >= S::kKvEmpty && i < S::kKvEmpty + S::kStages) count = kPair ? 4 + 2 : 1;
     if (i >= S::kScEmpty && i < S::kScEmpty + kMkScales) count = kPair ? 8 : 4;
     if ((i >= S::kQFull && i < S::kQFull + 2) || (i >= S::kPReady && i < S::kPReady + 4) ||
         (i >= S::kOEmpty && i < S::kOEmpty + 2) || (i >= S::kSumFull && i < S::kSumFull + 2))
@@ -744,7 +749,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
 
   if (warp < kMkWarpConv) {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
     const int a = warp >> 2, q4 = warp & 3;
     const int lane_row = 32 * q4 + lane;               // TMEM lane
     const int hu = kPair ? 0 : lane_row / kRows;       // its head and its row, of the unit's
@@ -813,12 +818,12 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           const float4 meta = reinterpret_cast<const float4 *>(smem + S::kOffMeta)[sc];
           const uint32_t ready = BAR(S::kPReady + 2 * a);
           const uint32_t scol = tl + mk_s(a), ocol = tl + mk_o(a);
-          const uint16_t *bad = reinterpret_cast<const uint16_t *>(bad_s + 4 * (seq & 1));
-          const uint16_t *bad_sc = reinterpret_cast<const uint16_t *>(bad_s + 8 + 4 * sc);
+          const uint16_t *bad = reinterpret_cast<const uint16_t *>(bad_s + 4 * (seq % S::kVfs));
+          const uint16_t *bad_sc = reinterpret_cast<const uint16_t *>(bad_s + 4 * (S::kVfs + sc));
           const bool see_all = whole.at(k), edge = !all_whole.at(k);
           // where some row of the unit does not see all of the chunk, value rows with a NaN
           // code or such a scale have been cleared
-          if (edge && !mk_wait_all(BAR(S::kVfFull + (seq & 1)), (seq >> 1) & 1, abort_s)) {
+          if (edge && !mk_wait_all(BAR(S::kVfFull + seq % S::kVfs), (seq / S::kVfs) & 1, abort_s)) {
             gave_up = true;
             break;
           }
@@ -947,107 +952,132 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       }
       named_barrier(1, 128);
       if (*ticket_s) {
-        // a warp per row: a lane per piece for the weights, then four dims a lane over the
-        // pieces, eight loads under way
-        const int b_first = u.b_first, pieces = u.b_last - b_first + 1;
+        // half a warp per row: a lane per piece for the weights, then eight dims a lane over
+        // the pieces, eight loads under way
+        const int b_first = u.b_first, pieces = u.b_last - b_first + 1, l16 = lane & 15;
         auto place = [&](int b, int r) -> int64_t {
           return static_cast<int64_t>(2 * (b_first + b) + (b == 0 ? 1 : 0)) * S::kLanes + r;
         };
 #pragma unroll 1
-        for (int r = q4; r < S::kLanes; r += 4) {
+        for (int r0 = 2 * q4; r0 < S::kLanes; r0 += 8) {
+          const int r = r0 + (lane >> 4);
           const int head = u.h + (kPair ? 0 : r / kRows), m = u.row0 + (kPair ? r : r % kRows);
-          if (m >= p.M || head >= p.H) continue;
-          float top = -INFINITY, all = 0.0f;
-          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          const bool mine = m < p.M && head < p.H;
+          if (__any_sync(0xFFFFFFFFu, mine) == 0) continue;
+          float top = -INFINITY, all = 0.0f, y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = 0.0f;
 #pragma unroll 1
-          for (int b0 = 0; b0 < pieces; b0 += 32) {
+          for (int b0 = 0; b0 < pieces; b0 += 16) {
             // (a part that saw nothing has no reference and a sum of 0, or NaN)
             float2 ml = make_float2(-INFINITY, 0.0f);
-            if (b0 + lane < pieces) ml = __ldcg(p.ml_part + place(b0 + lane, r));
+            if (mine && b0 + l16 < pieces) ml = __ldcg(p.ml_part + place(b0 + l16, r));
             float next = fmaxf(top, ml.x);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
+            for (int off = 8; off > 0; off >>= 1)
               next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, off));
             const float w = ml.x == -INFINITY ? ml.y : mk_ex2(ml.x - next) * ml.y;
             const float f = top == -INFINITY ? 0.0f : mk_ex2(top - next);
             float sum = w;
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+            for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
             all = all * f + sum;
-            y.x *= f;
-            y.y *= f;
-            y.z *= f;
-            y.w *= f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] *= f;
             top = next;
-            const int n = min(32, pieces - b0);
+            const int n = min(16, pieces - b0);
 #pragma unroll 1
-            for (int b = 0; b < n; b += 8) {
-              float4 o[8];
+            for (int b = 0; b < n; b += 4) {
+              float4 o[4][2];
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                o[i] = b + i < n ? __ldcg(reinterpret_cast<const float4 *>(
-                                              p.o_part + place(b0 + b + i, r) * kHeadDim) + lane)
-                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              for (int i = 0; i < 4; ++i) {
+                const float4 *src = reinterpret_cast<const float4 *>(p.o_part + place(b0 + b + i, r) * kHeadDim) + 2 * l16;
+                const bool get = mine && b + i < n;
+                o[i][0] = get ? __ldcg(src) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                o[i][1] = get ? __ldcg(src + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float wi = __shfl_sync(0xFFFFFFFFu, w, (b + i) & 31);
-                y.x = fmaf(o[i].x, wi, y.x);
-                y.y = fmaf(o[i].y, wi, y.y);
-                y.z = fmaf(o[i].z, wi, y.z);
-                y.w = fmaf(o[i].w, wi, y.w);
+              for (int i = 0; i < 4; ++i) {
+                const float wi = __shfl_sync(0xFFFFFFFFu, w, (lane & 16) | ((b + i) & 15));
+                y[0] = fmaf(o[i][0].x, wi, y[0]);
+                y[1] = fmaf(o[i][0].y, wi, y[1]);
+                y[2] = fmaf(o[i][0].z, wi, y[2]);
+                y[3] = fmaf(o[i][0].w, wi, y[3]);
+                y[4] = fmaf(o[i][1].x, wi, y[4]);
+                y[5] = fmaf(o[i][1].y, wi, y[5]);
+                y[6] = fmaf(o[i][1].z, wi, y[6]);
+                y[7] = fmaf(o[i][1].w, wi, y[7]);
               }
             }
           }
           const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-          *reinterpret_cast<uint2 *>(out_row(u.r, head, m) + 4 * lane) =
-              make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+          if (mine)
+            *reinterpret_cast<uint4 *>(out_row(u.r, head, m) + 8 * l16) =
+                make_uint4(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv),
+                           pack_bf16x2(y[4] * inv, y[5] * inv), pack_bf16x2(y[6] * inv, y[7] * inv));
         }
       }
       return true;
     };
-    // chunk k of a unit, the seq-th of all: thread j converts token j: dims 64 b + 8 c .. in
-    // block b, MN-major and 128-byte swizzled; tokens past the unit's are cleared
+    // chunk k of a unit, the seq-th of all: thread j converts key j, MN-major and 128-byte
+    // swizzled, dims 0-63 and 64-127 in a block each; tokens past the unit's are cleared,
+    // and where some row does not see all of the chunk, values with a NaN code.  In place
+    // the blocks are the key's and the value's own codes, which one thread reads before it
+    // writes.
     const int j = lane_row;
+    uint32_t chain_seq = 0;                            // chunks of chain 0, and of chain 1 in the upper half
     auto convert = [&](const MkUnit &u, int k, uint32_t seq, bool whole) -> bool {
-      const uint32_t b = seq % S::kStages;
-      bool ok = mk_wait_all(BAR(S::kKvFull + b), (seq / S::kStages) & 1, abort_s);
-      if (ok && seq >= 2) ok = mk_wait_all(BAR(S::kVfEmpty + (seq & 1)), ((seq >> 1) - 1) & 1, abort_s);
+      const uint32_t b = seq % S::kStages, v = seq % S::kVfs;
+      bool ok;
+      if (kPair) {
+        ok = mk_wait_all(BAR(S::kKvFull + b), (seq / S::kStages) & 1, abort_s);
+        if (ok && seq >= 2) ok = mk_wait_all(BAR(S::kVfEmpty + v), ((seq >> 1) - 1) & 1, abort_s);
+      } else {
+        const int a = k & 1;                           // its scores are made
+        ok = mk_wait_all(BAR(S::kSFull + a), (chain_seq >> (16 * a)) & 1, abort_s);
+        chain_seq += a == 0 ? 1u : 0x10000u;
+        tc_fence_after();
+      }
       if (!ok) return false;
       // (key j: box of 16 tokens and all heads, head, token)
       const int x = (u.c0 + k) * S::kTok + (S::kHeads == 1 ? j : 16 * (j / (16 * S::kHeads)) + (j & 15));
-      const uint8_t *src = smem + S::kOffKv + b * S::kStage + p.v_off + (j >> 3) * p.group + (j & 7) * 128;
-      uint8_t *dst = smem + S::kOffVf + (seq & 1) * S::kVfBytes + j * 128;
+      uint8_t *stage = smem + S::kOffKv + b * S::kStage + (j >> 3) * p.group + (j & 7) * 128;
+      const uint8_t *src = stage + p.v_off;
+      uint8_t *dst = kPair ? smem + S::kOffVf + v * S::kVfBytes + j * 128 : stage;
+      const int block = kPair || p.two_maps != 0 ? S::kVfBytes / 2 : 1024;
+      uint4 w[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + ((c ^ (j & 7)) << 4));
       bool keep = x < u.X;
       if (!whole) {
-        bool bad = false;
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          const uint4 w = *reinterpret_cast<const uint4 *>(src + ((c ^ (j & 7)) << 4));
-          bad |= (__vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                  __vcmpeq4(w.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0u;
-        }
-        const uint32_t word = __ballot_sync(0xFFFFFFFFu, keep && bad);
-        if (lane == 0) bad_s[4 * (seq & 1) + q4] = word;
-        keep = keep && !bad;
+        uint32_t bad = 0u;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          bad |= __vcmpeq4(w[c].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w[c].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                 __vcmpeq4(w[c].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w[c].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        const uint32_t word = __ballot_sync(0xFFFFFFFFu, keep && bad != 0u);
+        if (lane == 0) bad_s[4 * v + q4] = word;
+        keep = keep && bad == 0u;
       }
-#pragma unroll 4
+      if (!keep) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
       for (int c = 0; c < 8; ++c) {
-        uint4 w = *reinterpret_cast<const uint4 *>(src + ((c ^ (j & 7)) << 4));
-        if (!keep) w = make_uint4(0u, 0u, 0u, 0u);
-        const uint4 lo = make_uint4(e4m3x2_to_f16x2(w.x & 0xFFFFu), e4m3x2_to_f16x2(w.x >> 16),
-                                    e4m3x2_to_f16x2(w.y & 0xFFFFu), e4m3x2_to_f16x2(w.y >> 16));
-        const uint4 hi = make_uint4(e4m3x2_to_f16x2(w.z & 0xFFFFu), e4m3x2_to_f16x2(w.z >> 16),
-                                    e4m3x2_to_f16x2(w.w & 0xFFFFu), e4m3x2_to_f16x2(w.w >> 16));
-        uint8_t *blk = dst + (c >> 2) * (S::kVfBytes / 2);
-        const int c0 = (2 * c) & 7;
-        *reinterpret_cast<uint4 *>(blk + ((c0 ^ (j & 7)) << 4)) = lo;
-        *reinterpret_cast<uint4 *>(blk + (((c0 + 1) ^ (j & 7)) << 4)) = hi;
+        const uint4 lo = make_uint4(e4m3x2_to_f16x2(w[c].x & 0xFFFFu), e4m3x2_to_f16x2(w[c].x >> 16),
+                                    e4m3x2_to_f16x2(w[c].y & 0xFFFFu), e4m3x2_to_f16x2(w[c].y >> 16));
+        const uint4 hi = make_uint4(e4m3x2_to_f16x2(w[c].z & 0xFFFFu), e4m3x2_to_f16x2(w[c].z >> 16),
+                                    e4m3x2_to_f16x2(w[c].w & 0xFFFFu), e4m3x2_to_f16x2(w[c].w >> 16));
+        uint8_t *to = dst + (c >> 2) * block;
+        *reinterpret_cast<uint4 *>(to + (((2 * (c & 3)) ^ (j & 7)) << 4)) = lo;
+        *reinterpret_cast<uint4 *>(to + (((2 * (c & 3) + 1) ^ (j & 7)) << 4)) = hi;
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(BAR(S::kKvEmpty + b));
-        mbar_arrive(BAR(S::kVfFull + (seq & 1)));
+        if (kPair) mbar_arrive(BAR(S::kKvEmpty + b));
+        mbar_arrive(BAR(S::kVfFull + v));
       }
       return true;
     };
@@ -1090,7 +1120,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
     // Pages are looked up for 32 boxes at a time, a lane each: `per` chunks.
     const int log2_box = 31 - __clz(p.box), boxes = S::kTok >> log2_box, per = 32 >> (S::kTokLog2 - log2_box);
     auto box_pos = [&](const MkUnit &u, int kb, int *pos) -> bool {
@@ -1342,9 +1372,9 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             }
           if (__any_sync(0xFFFFFFFFu, bad != 0u)) {
             flagged = 1.0f;
-            if (lane < 4) bad_s[8 + 4 * b + lane] = 0u;
+            if (lane < 4) bad_s[4 * (S::kVfs + b) + lane] = 0u;
             __syncwarp();
-            if (bad != 0u) atomicOr(bad_s + 8 + 4 * b + (lane >> 3), bad << (4 * (lane & 7)));
+            if (bad != 0u) atomicOr(bad_s + 4 * (S::kVfs + b) + (lane >> 3), bad << (4 * (lane & 7)));
           }
         }
         // (fmaxf leaves NaN out)
@@ -1383,7 +1413,11 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       const uint32_t q2 = q1 + (S::kQPiece >> 4);
       const uint32_t k0 = (smem_addr(smem + S::kOffKv + p.k_off) >> 4) | kMkKMajor;
       const uint32_t k_hi = (static_cast<uint32_t>(p.group) >> 4) | (1u << 14) | (kSmemSwizzle128 << 29);
-      const uint32_t v0 = (smem_addr(smem + S::kOffVf) >> 4) | kMkMnMajor;
+      // (values: blocks of 64 dims, groups of 8 keys, by bytes)
+      const uint32_t v_group = kPair ? 1024u : static_cast<uint32_t>(p.group);
+      const uint32_t v_block = kPair || p.two_maps != 0 ? S::kVfBytes / 2 : 1024u;
+      const uint32_t v_hi = (v_group >> 4) | (1u << 14) | (kSmemSwizzle128 << 29), v_step = 2 * v_group >> 4;
+      const uint32_t v0 = (smem_addr(smem + S::kOffVf) >> 4) | (v_block >> 4) << 16;
       const uint32_t s_col = tmem + mk_s(a), o_col = tmem + mk_o(a);
       uint32_t base = 0;                               // chunks of earlier units
       uint32_t par_q = 0, par_p = 0, par_o = 1, par_turn = a ^ 1;
@@ -1403,8 +1437,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           const bool use_v = j > 0 && cv < un, use_k = cq < un;
           const bool pv = use_v && live, qk = use_k && live;
           const uint32_t sv = base + cv, sq = base + cq;
-          const uint32_t bk = sq % S::kStages, bv = sv & 1;
-          if (use_v) ok = mk_wait_all(BAR(S::kVfFull + bv), (sv >> 1) & 1, abort_s);
+          const uint32_t bk = sq % S::kStages, bv = sv % S::kVfs;
+          if (use_v) ok = mk_wait_all(BAR(S::kVfFull + bv), (sv / S::kVfs) & 1, abort_s);
           if (ok && use_k) ok = mk_wait_all(BAR(S::kKvFull + bk), (sq / S::kStages) & 1, abort_s);
           if (ok && qk && j == 0) ok = mk_wait_all(BAR(S::kQFull + (kPair ? a : 0)), kPair ? par_q : t & 1, abort_s);
           if (ok && pv) {
@@ -1425,7 +1459,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             if (mk_elect()) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mk_mma_pv(o_col, s_col + 8 * kk, v_lo + (2048 >> 4) * kk, (j == 1 && kk == 0) ? 0u : 1u);
+                mk_mma_pv(o_col, s_col + 8 * kk, v_lo + v_step * kk, v_hi, (j == 1 && kk == 0) ? 0u : 1u);
             }
             ok = mk_wait_all(BAR(S::kPReady + 2 * a + 1), par_p, abort_s);
             if (!ok) break;
@@ -1434,7 +1468,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             if (mk_elect()) {
 #pragma unroll
               for (int kk = 4; kk < 8; ++kk)
-                mk_mma_pv(o_col, s_col + 32 + 8 * kk, v_lo + (2048 >> 4) * kk, 1u);
+                mk_mma_pv(o_col, s_col + 32 + 8 * kk, v_lo + v_step * kk, v_hi, 1u);
             }
           }
           if (qk) {
@@ -1453,8 +1487,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             if (turns) mbar_arrive(BAR(S::kTurn + (a ^ 1)));
             if (pv && (kPair ? cv == un - 1 : cv + 2 >= un)) tc_commit(BAR(S::kOFull + a));
             if (qk && (kPair ? cq == un - 1 : cq + 2 >= un)) tc_commit(BAR(S::kQEmpty + a));
-            if (use_v) tc_commit(BAR(S::kVfEmpty + bv));
-            if (use_k) tc_commit(BAR(S::kKvEmpty + bk));
+            if (use_v) tc_commit(BAR(kPair ? S::kVfEmpty + bv : S::kKvEmpty + bv));
+            if (kPair && use_k) tc_commit(BAR(S::kKvEmpty + bk));
           }
           __syncwarp();
         }
@@ -1548,12 +1582,12 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
   p.words = (p.R + 31) / 32;
   p.scale2 = (a.sm_scale < 0.0f ? -a.sm_scale : a.sm_scale) * 1.4426950408889634f;
   p.flip = a.sm_scale < 0.0f ? 0x80808080u : 0u;
-  // A cut unit costs its last block some 8 cycles a row and 200 for each piece, a chunk takes
-  // it 2,000: pieces of at least sqrt(chunks (8 rows + 200) / 2000) chunks.
+  // A cut unit costs the block that joins it, for every 8 rows, some 1,000 cycles and 200 a
+  // piece, a chunk takes it 2,400: pieces of at least sqrt(chunks 200 (rows / 8) / 2400) chunks.
   const int64_t reach = a.tree_mask != nullptr ? a.max_context_len
                                                : std::min<int64_t>(a.max_context_len, int64_t(p.window) + p.sinks + p.R);
   const double chunks = static_cast<double>((reach + tokens - 1) / tokens + 1);
-  p.least = std::max(1, static_cast<int>(std::sqrt(chunks * (8 * std::min(p.M, rows) * heads + 200) / 2000) + 0.5));
+  p.least = std::max(1, static_cast<int>(std::sqrt(chunks * 200 * ((std::min(p.M, rows) * heads + 7) / 8) / 2400) + 0.5));
   p.k_scales = c.k_scales;
   p.v_scales = c.v_scales;
   p.err_flags = a.err_flags;
