@@ -19,8 +19,9 @@
 //    multiple of 16 tokens), so that a few sinks cost no chunk of their own.
 //  * Split.  The chunks of all units, in order, with a charge for each unit's start,
 //    are cut into one equal range per SM; a unit that is cut leaves a piece per range
-//    (normalised output, reference, denominator) in the workspace, and the block
-//    whose piece comes last joins them (a counter per unit, tagged with the call).
+//    (normalised output, reference, denominator) in the workspace, which a second
+//    launch joins, with all SMs (joined by the block whose piece came last, 175 rows in
+//    7 pieces took it 34 us).
 //  * S = Q K^T: 128 x 128 x 128, kind::f8f6f4, the query as two e4m3 pieces (q = 2^e
 //    (p1 + p2), exact for elements >= 2^-9 of the row's largest) on the key codes as
 //    they are.  O += P V: kind::f16, P'' = p v_scale in f16 from tensor memory, the
@@ -50,7 +51,6 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
-#include <cmath>
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
@@ -69,6 +69,16 @@ constexpr int kMkCharge = 2;                          // chunks that a unit's st
 constexpr float kMkLazy = 14.0f;                      // log2 of the largest P''
 constexpr float kMkFloor = -90.0f;                    // log2 of the smallest value scale, over 2^Eg
 constexpr int kMkMaxEg = 30;                          // Eg at most
+
+// A unit as the loading warp announces it: the chunks [c0, c0 + n) of the rows from row0
+// on of the heads from h on of request r, of X tokens (x < s16 is position x, others x +
+// shift); all of them (direct) or a piece, for workspace slot `slot`.  base: the position
+// of query row 0.  n = 0 ends the work.
+struct __align__(16) MkUnit {
+  int r, h, row0, n;
+  int c0, X, s16, shift;
+  int base, direct, slot, pad;
+};
 
 // Shapes: kPair (two row tiles of one head, one per chain), or one tile of kRows rows of
 // each of 128 / kRows heads, whose chunks the chains share.
@@ -98,8 +108,8 @@ struct MkShape {
   static constexpr int kOffSc = kOffEg + 16;                 // [stage][K | V | log2 V][128]
   static constexpr int kOffMeta = kOffSc + kMkScales * 3 * kMkTok * 4;   // [stage] float4
   static constexpr int kOffUnit = kOffMeta + kMkScales * 16;
-  static constexpr int kOffBad = kOffUnit + kMkUnits * 64;   // [Vf][4 words], [scales][4 words]
-  static constexpr int kOffMisc = kOffBad + (kVfs + kMkScales) * 16;              // tmem base, abort, ticket
+  static constexpr int kOffBad = kOffUnit + kMkUnits * static_cast<int>(sizeof(MkUnit));   // [Vf][4 words], [scales][4 words]
+  static constexpr int kOffMisc = kOffBad + (kVfs + kMkScales) * 16;              // tmem base, abort
   static constexpr int kOffScan = kOffMisc + 16;             // a warp's sum each
   static constexpr int kOffPre = kOffScan + kMkThreads / 32 * 4;
   static constexpr int kOffBar = (kOffPre + (kMkMaxRequests + 1) * 4 + 7) / 8 * 8;
@@ -196,8 +206,7 @@ struct MkParams {
   uint32_t flip;                                       // sign bits of a negative sm_scale
   float *o_part;                                       // [grid][2][lanes of a unit][128]
   float2 *ml_part;                                     // [grid][2][lanes of a unit]
-  unsigned long long *tickets;                         // [N * HG * T]
-  uint32_t tag;
+  int4 *cuts;                                          // [grid]: the unit that block b is the first of several to work on
   int32_t *err_flags;
   int32_t least;                                       // positions of a block's range
 };
@@ -284,15 +293,6 @@ template <typename S>
 __device__ __forceinline__ int mk_positions(int X) {   // of a unit in the work sequence
   return X > 0 ? ((X + S::kTok - 1) >> S::kTokLog2) + kMkCharge : 0;
 }
-
-// A unit as the loading warp announces it: the chunks [c0, c0 + n) of a unit, which is
-// whole (direct) or one of the pieces of the blocks [b_first, b_last].  n = 0 ends the work.
-struct __align__(16) MkUnit {
-  int r, h, row0, n;
-  int c0, X, s16, shift;
-  int base, direct, slot, b_first;
-  int b_last, index, pad0, pad1;
-};
 
 // What a query row sees, in a unit's token numbers: x < hi and (x < sinks or x >= lo),
 // or x < base and the nodes of its mask row.
@@ -659,7 +659,6 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
   auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
   volatile int *abort_s = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
-  volatile int *ticket_s = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 8);
   MkUnit *unit_s = reinterpret_cast<MkUnit *>(smem + S::kOffUnit);
   volatile float *sum_s = reinterpret_cast<volatile float *>(smem + S::kOffSum);
   volatile float *ref_s = reinterpret_cast<volatile float *>(smem + S::kOffRef);
@@ -938,85 +937,6 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           if (both) mbar_arrive(BAR(S::kOEmpty + 1));
         }
       }
-      if (u.direct) return true;
-      // the block whose piece comes last joins the unit's pieces
-      __threadfence();
-      named_barrier(1, 128);
-      if (q4 == 0 && lane == 0) {
-        const uint32_t landed = ticket_take(p.tickets + u.index, p.tag);
-        const bool last = landed == static_cast<uint32_t>(u.b_last - u.b_first + 1);
-        if (last) p.tickets[u.index] = 0ull;
-        if (landed == 0u && p.err_flags) atomicOr(p.err_flags, KVQ_ERRF_WAIT_TIMEOUT);
-        *ticket_s = last ? 1 : 0;
-        __threadfence();
-      }
-      named_barrier(1, 128);
-      if (*ticket_s) {
-        // half a warp per row: a lane per piece for the weights, then eight dims a lane over
-        // the pieces, eight loads under way
-        const int b_first = u.b_first, pieces = u.b_last - b_first + 1, l16 = lane & 15;
-        auto place = [&](int b, int r) -> int64_t {
-          return static_cast<int64_t>(2 * (b_first + b) + (b == 0 ? 1 : 0)) * S::kLanes + r;
-        };
-#pragma unroll 1
-        for (int r0 = 2 * q4; r0 < S::kLanes; r0 += 8) {
-          const int r = r0 + (lane >> 4);
-          const int head = u.h + (kPair ? 0 : r / kRows), m = u.row0 + (kPair ? r : r % kRows);
-          const bool mine = m < p.M && head < p.H;
-          if (__any_sync(0xFFFFFFFFu, mine) == 0) continue;
-          float top = -INFINITY, all = 0.0f, y[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-#pragma unroll 1
-          for (int b0 = 0; b0 < pieces; b0 += 16) {
-            // (a part that saw nothing has no reference and a sum of 0, or NaN)
-            float2 ml = make_float2(-INFINITY, 0.0f);
-            if (mine && b0 + l16 < pieces) ml = __ldcg(p.ml_part + place(b0 + l16, r));
-            float next = fmaxf(top, ml.x);
-#pragma unroll
-            for (int off = 8; off > 0; off >>= 1)
-              next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, off));
-            const float w = ml.x == -INFINITY ? ml.y : mk_ex2(ml.x - next) * ml.y;
-            const float f = top == -INFINITY ? 0.0f : mk_ex2(top - next);
-            float sum = w;
-#pragma unroll
-            for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-            all = all * f + sum;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= f;
-            top = next;
-            const int n = min(16, pieces - b0);
-#pragma unroll 1
-            for (int b = 0; b < n; b += 4) {
-              float4 o[4][2];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 *src = reinterpret_cast<const float4 *>(p.o_part + place(b0 + b + i, r) * kHeadDim) + 2 * l16;
-                const bool get = mine && b + i < n;
-                o[i][0] = get ? __ldcg(src) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                o[i][1] = get ? __ldcg(src + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float wi = __shfl_sync(0xFFFFFFFFu, w, (lane & 16) | ((b + i) & 15));
-                y[0] = fmaf(o[i][0].x, wi, y[0]);
-                y[1] = fmaf(o[i][0].y, wi, y[1]);
-                y[2] = fmaf(o[i][0].z, wi, y[2]);
-                y[3] = fmaf(o[i][0].w, wi, y[3]);
-                y[4] = fmaf(o[i][1].x, wi, y[4]);
-                y[5] = fmaf(o[i][1].y, wi, y[5]);
-                y[6] = fmaf(o[i][1].z, wi, y[6]);
-                y[7] = fmaf(o[i][1].w, wi, y[7]);
-              }
-            }
-          }
-          const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-          if (mine)
-            *reinterpret_cast<uint4 *>(out_row(u.r, head, m) + 8 * l16) =
-                make_uint4(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv),
-                           pack_bf16x2(y[4] * inv, y[5] * inv), pack_bf16x2(y[6] * inv, y[7] * inv));
-        }
-      }
       return true;
     };
     // chunk k of a unit, the seq-th of all: thread j converts key j, MN-major and 128-byte
@@ -1161,6 +1081,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         h = static_cast<int>(static_cast<unsigned>(x - pre[lo]) / W);
         at = pre[lo] + h * static_cast<int>(W);
       }
+      int4 cut = make_int4(-1, 0, 0, 0);               // (lane 0's)
       // the next piece of the block's range with chunks, into the announcements' entry u;
       // returns its chunks (0: none left)
       auto next_unit = [&](MkUnit &u) -> int {
@@ -1197,10 +1118,11 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             u.base = uL - p.R;
             u.direct = n == V - kMkCharge;
             const int b_first = static_cast<int>(static_cast<unsigned>(first) / static_cast<unsigned>(B));
-            u.b_first = b_first;
-            u.b_last = static_cast<int>(static_cast<unsigned>(ua + V - 1) / static_cast<unsigned>(B));
-            u.slot = 2 * static_cast<int>(blockIdx.x) + (static_cast<int>(blockIdx.x) == b_first ? 1 : 0);
-            u.index = (ur * p.HG + uh) * p.T + ut;
+            const bool starts = static_cast<int>(blockIdx.x) == b_first;
+            u.slot = 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
+            if (starts && n != V - kMkCharge)
+              cut = make_int4(ur, uh * S::kHeads, ut * S::kTileRows,
+                              static_cast<int>(static_cast<unsigned>(ua + V - 1) / static_cast<unsigned>(B)));
           }
           break;
         }
@@ -1273,6 +1195,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       gave_up = !ok;
       bad = __any_sync(0xFFFFFFFFu, bad);
       if (lane == 0) {
+        p.cuts[blockIdx.x] = cut;
         if (bad && p.err_flags) atomicOr(p.err_flags, KVQ_ERRF_BLOCK_RANGE);
         // copies in flight land before the block leaves
         for (uint32_t v = n > S::kStages ? n - S::kStages : 0; v < n; ++v)
@@ -1515,13 +1438,71 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
   }
 }
 
+// The pieces of the units that are cut, joined: kMkJoinParts blocks for each block of the
+// first launch that was the first of several to work on a unit, a warp per row at a time,
+// four dims a lane.
+constexpr int kMkJoinParts = 8, kMkJoinWarps = 4;
+
+__global__ void __launch_bounds__(32 * kMkJoinWarps)
+attn_masked_join_kernel(const MkParams p, int lanes, int rows_of_head) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b_first = static_cast<int>(blockIdx.x) / kMkJoinParts, part = static_cast<int>(blockIdx.x) % kMkJoinParts;
+  allow_dependents_launch();
+  grid_dependency_wait();
+  const int4 cut = p.cuts[b_first];                    // request, first head, first row, last block
+  if (cut.x < 0) return;
+  const int pieces = cut.w - b_first + 1, step = kMkJoinParts * kMkJoinWarps;
+  auto place = [&](int b, int r) -> int64_t {
+    return static_cast<int64_t>(2 * (b_first + b) + (b == 0 ? 1 : 0)) * lanes + r;
+  };
+  for (int r = part * kMkJoinWarps + warp; r < lanes; r += step) {
+    const int head = cut.y + r / rows_of_head, m = cut.z + r % rows_of_head;
+    if (head >= p.H || m >= p.M) continue;
+    float top = -INFINITY, all = 0.0f;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int b0 = 0; b0 < pieces; b0 += 8) {
+      float2 ml[8];
+      float4 o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t at = place(b0 + i, r);
+        const bool get = b0 + i < pieces;
+        ml[i] = get ? __ldcg(p.ml_part + at) : make_float2(-INFINITY, 0.0f);
+        o[i] = get ? __ldcg(reinterpret_cast<const float4 *>(p.o_part + at * kHeadDim) + lane)
+                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      float next = top;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) next = fmaxf(next, ml[i].x);
+      const float f = top == -INFINITY ? 0.0f : mk_ex2(top - next);
+      all *= top == -INFINITY ? 1.0f : f;              // (NaN stays)
+      y.x *= f;
+      y.y *= f;
+      y.z *= f;
+      y.w *= f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // (a part that saw nothing has no reference and a sum of 0, or NaN)
+        const float w = ml[i].x == -INFINITY ? ml[i].y : mk_ex2(ml[i].x - next) * ml[i].y;
+        all += w;
+        y.x = fmaf(o[i].x, w, y.x);
+        y.y = fmaf(o[i].y, w, y.y);
+        y.z = fmaf(o[i].z, w, y.z);
+        y.w = fmaf(o[i].w, w, y.w);
+      }
+      top = next;
+    }
+    const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+    const int i = mk_query(p, m);
+    uint16_t *dst = p.out + ((static_cast<int64_t>(cut.x) * p.R + i) * p.Hq + head * p.G + (m - i * p.G)) * kHeadDim;
+    *reinterpret_cast<uint2 *>(dst + 4 * lane) =
+        make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+  }
+}
+
 // Rows of a unit and head, and its heads.
 int mk_tile_rows(int M) { return M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256)); }
 int mk_heads(int rows) { return rows >= 128 ? 1 : 128 / rows; }
-int64_t mk_units(int n, int H, int M) {
-  const int rows = mk_tile_rows(M), heads = mk_heads(rows);
-  return static_cast<int64_t>(n) * ((H + heads - 1) / heads) * ((M + rows - 1) / rows);
-}
 
 template <bool kPair, int kRows>
 cudaError_t mk_launch(const MkParams &p, const CUtensorMap &map, const CUtensorMap &map_v, int grid,
@@ -1538,8 +1519,12 @@ cudaError_t mk_launch(const MkParams &p, const CUtensorMap &map, const CUtensorM
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  return launch_overlapped(kernel, dim3(static_cast<unsigned>(grid)), dim3(kMkThreads), kSmem, stream,
-                           p, map, map_v);
+  e = launch_overlapped(kernel, dim3(static_cast<unsigned>(grid)), dim3(kMkThreads), kSmem, stream, p,
+                        map, map_v);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(attn_masked_join_kernel, dim3(static_cast<unsigned>(grid * kMkJoinParts)),
+                           dim3(32 * kMkJoinWarps), 0, stream, p, MkShape<kPair, kRows>::kLanes,
+                           MkShape<kPair, kRows>::kTileRows);
 }
 
 size_t mk_round(size_t n) { return (n + 255) / 256 * 256; }
@@ -1550,9 +1535,8 @@ size_t attn_masked_workspace_bytes(const MaskedArgs &a, int32_t num_kv_heads) {
   const int64_t M = static_cast<int64_t>(a.rows_per_request) * (a.num_q_heads / num_kv_heads);
   const int rows = mk_tile_rows(static_cast<int>(M));
   const size_t slots = static_cast<size_t>(a.sms) * 2 * std::max(rows, 128);
-  return mk_round(static_cast<size_t>(mk_units(std::min(a.num_requests, kMkMaxRequests), num_kv_heads,
-                                               static_cast<int>(M))) * 8) +
-         mk_round(slots * kHeadDim * sizeof(float)) + mk_round(slots * sizeof(float2));
+  return mk_round(a.sms * sizeof(int4)) + mk_round(slots * kHeadDim * sizeof(float)) +
+         mk_round(slots * sizeof(float2));
 }
 
 cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStream_t stream) {
@@ -1582,12 +1566,10 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
   p.words = (p.R + 31) / 32;
   p.scale2 = (a.sm_scale < 0.0f ? -a.sm_scale : a.sm_scale) * 1.4426950408889634f;
   p.flip = a.sm_scale < 0.0f ? 0x80808080u : 0u;
-  // A cut unit costs the block that joins it, for every 8 rows, some 1,000 cycles and 200 a
-  // piece, a chunk takes it 2,400: pieces of at least sqrt(chunks 200 (rows / 8) / 2400) chunks.
-  const int64_t reach = a.tree_mask != nullptr ? a.max_context_len
-                                               : std::min<int64_t>(a.max_context_len, int64_t(p.window) + p.sinks + p.R);
-  const double chunks = static_cast<double>((reach + tokens - 1) / tokens + 1);
-  p.least = std::max(1, static_cast<int>(std::sqrt(chunks * 200 * ((std::min(p.M, rows) * heads + 7) / 8) / 2400) + 0.5));
+  // Ranges of at least 128 tokens and a unit's start: shorter ones are joined from more
+  // pieces than they save (one row, 1,028 tokens: 32 us with ranges of one chunk of 32
+  // tokens, 20 with five; 16 rows, 2,000 tokens: 36 with one of 64, 27 to 30 with 2 to 5).
+  p.least = kMkTok / tokens + 1;
   p.k_scales = c.k_scales;
   p.v_scales = c.v_scales;
   p.err_flags = a.err_flags;
@@ -1623,12 +1605,11 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
     p.tree = a.tree_mask != nullptr ? a.tree_mask + row * p.words : nullptr;
     char *ws = static_cast<char *>(a.workspace);
     const size_t slots_ws = static_cast<size_t>(grid) * 2 * std::max(rows, 128);
-    p.tickets = reinterpret_cast<unsigned long long *>(ws);
-    ws += mk_round(static_cast<size_t>(mk_units(std::min(a.num_requests, kMkMaxRequests), H, p.M)) * 8);
+    p.cuts = reinterpret_cast<int4 *>(ws);
+    ws += mk_round(grid * sizeof(int4));
     p.o_part = reinterpret_cast<float *>(ws);
     ws += mk_round(slots_ws * kHeadDim * sizeof(float));
     p.ml_part = reinterpret_cast<float2 *>(ws);
-    p.tag = next_call_tag();
     const cudaError_t e = rows == 32    ? mk_launch<false, 32>(p, map, map_v, grid, stream)
                           : rows == 64  ? mk_launch<false, 64>(p, map, map_v, grid, stream)
                           : rows == 128 ? mk_launch<false, 128>(p, map, map_v, grid, stream)
