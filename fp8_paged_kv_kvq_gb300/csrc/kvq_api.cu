@@ -610,9 +610,13 @@ kvq_status masked_shape(const kvq_cache *cache, int32_t num_requests, int32_t ro
   if (M > kvq::kRowsMaxRows || num_requests > 65535 || cache->block_size < 16 ||
       cache->num_slots >= (int64_t(1) << 31))
     return KVQ_ERR_UNSUPPORTED;
-  // 128-token pieces of one KV head are numbered in 31 bits
-  const int64_t tiles = (M + 127) / 128, chunks = static_cast<int64_t>(max_context_len) / 128 + 8;
-  if (static_cast<double>(num_requests) * cache->num_kv_heads * tiles * chunks >= 2147483647.0)
+  // (positions and chunks are numbered in 31 bits)
+  kvq::MaskedArgs a{};
+  a.num_requests = num_requests;
+  a.rows_per_request = rows_per_request;
+  a.num_q_heads = num_q_heads;
+  a.max_context_len = max_context_len;
+  if (max_context_len > (1 << 30) || kvq::attn_masked_too_long(a, cache->num_kv_heads))
     return KVQ_ERR_UNSUPPORTED;
   return KVQ_OK;
 }

@@ -945,7 +945,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
     // the blocks are the key's and the value's own codes, which one thread reads before it
     // writes.
     const int j = lane_row;
-    uint32_t chain_seq = 0;                            // chunks of chain 0, and of chain 1 in the upper half
+    uint32_t chain_par = 0;                            // parity of chain a's chunks, bit a
     auto convert = [&](const MkUnit &u, int k, uint32_t seq, bool whole) -> bool {
       const uint32_t b = seq % S::kStages, v = seq % S::kVfs;
       bool ok;
@@ -954,8 +954,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         if (ok && seq >= 2) ok = mk_wait_all(BAR(S::kVfEmpty + v), ((seq >> 1) - 1) & 1, abort_s);
       } else {
         const int a = k & 1;                           // its scores are made
-        ok = mk_wait_all(BAR(S::kSFull + a), (chain_seq >> (16 * a)) & 1, abort_s);
-        chain_seq += a == 0 ? 1u : 0x10000u;
+        ok = mk_wait_all(BAR(S::kSFull + a), (chain_par >> a) & 1, abort_s);
+        chain_par ^= 1u << a;
         tc_fence_after();
       }
       if (!ok) return false;
@@ -1530,6 +1530,15 @@ cudaError_t mk_launch(const MkParams &p, const CUtensorMap &map, const CUtensorM
 size_t mk_round(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
+
+// Positions in the work sequence of a launch, at most; 2^31 are too many to number.
+bool attn_masked_too_long(const MaskedArgs &a, int32_t num_kv_heads) {
+  const int M = a.rows_per_request * (a.num_q_heads / num_kv_heads);
+  const int rows = mk_tile_rows(M), heads = mk_heads(rows), tokens = kMkTok / heads;
+  const double units = static_cast<double>(std::min(a.num_requests, kMkMaxRequests)) *
+                       ((num_kv_heads + heads - 1) / heads) * ((M + rows - 1) / rows);
+  return units * (a.max_context_len / tokens + 1 + kMkCharge) >= 2147483648.0;
+}
 
 size_t attn_masked_workspace_bytes(const MaskedArgs &a, int32_t num_kv_heads) {
   const int64_t M = static_cast<int64_t>(a.rows_per_request) * (a.num_q_heads / num_kv_heads);

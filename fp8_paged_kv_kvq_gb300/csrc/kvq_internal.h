@@ -268,6 +268,7 @@ struct MaskedArgs {
   int32_t sms;
 };
 constexpr int32_t kTreeMaxNodes = 1024;      // drafted tokens of a request
+bool attn_masked_too_long(const MaskedArgs &a, int32_t num_kv_heads);
 size_t attn_masked_workspace_bytes(const MaskedArgs &a, int32_t num_kv_heads);
 cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStream_t stream);
 

@@ -479,7 +479,9 @@ kvq_status kvq_prompt_attention(const void *q, int64_t q_token_stride,
  *                   one must not run concurrently (two captured graphs may, one
  *                   after the other).
  * Pages of at least 16 tokens, any number of KV heads, fewer than 2^31 slots, at
- * most 65,535 requests and 2^31 - 1 units of 128 tokens of one KV head, else
+ * most 65,535 requests and contexts of 2^30 tokens, and fewer than 2^31 chunks (of
+ * 128 tokens of a KV head; where R * num_q_heads / num_kv_heads is at most 64, 64
+ * tokens of two heads, at most 32, 32 of four) for 1,024 requests, else
  * KVQ_ERR_UNSUPPORTED.  Other arguments and errors as for kvq_paged_decode. */
 size_t kvq_paged_decode_window_workspace_size(int32_t num_requests, int32_t rows_per_request,
                                               int32_t num_q_heads, int32_t num_kv_heads,

@@ -59,6 +59,15 @@ def test_attention_refusals(lib, call, changes, status):
     assert call(lib, **changes) == status
 
 
+@pytest.mark.parametrize("call", [_window, _tree])
+def test_attention_refuses_more_than_31_bits_number(lib, call):
+    # chunks of 32 tokens of four heads (R G <= 32), 1,024 requests a launch
+    assert call(lib, cache=_cache(H=1), N=1024, R=1, hq=1, most=1 << 26) == UNSUPPORTED
+    assert call(lib, cache=_cache(H=4), N=2048, R=1, hq=4, most=1 << 26) == UNSUPPORTED
+    assert call(lib, N=1, R=4, most=(1 << 30) + 1) == UNSUPPORTED
+    assert call(lib, N=1, R=4, most=(1 << 31) - 1) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("changes,status", [
     (dict(window=0), INVALID), (dict(window=-5), INVALID), (dict(sinks=-1), INVALID)])
 def test_window_refusals(lib, changes, status):

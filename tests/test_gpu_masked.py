@@ -467,3 +467,20 @@ def test_no_requests():
     out = kvq.paged_decode_window(on_gpu(c), q.cuda(), tables[:0].cuda(),
                                   torch.zeros(0, dtype=torch.int32, device="cuda"), 50, 20, SCALE)
     assert out.shape == (0, 8, 128)
+
+
+def test_more_chunks_than_16_bits_count():
+    # 1,024 requests of 2^20 tokens over the same 64 pages: over 100,000 chunks a block and chain.
+    # Keys of score 0 and integers as values: weights of 1 and all sums (below 2^24) are exact, so
+    # that only the division, the pieces' joining (under 32 roundings) and bf16 round.
+    n, most, bs, pages = 1024, 1 << 20, 64, 64
+    g = torch.Generator().manual_seed(3)
+    v = torch.randint(0, 8, (pages * bs, 1, 128), generator=g).float()
+    c = dict(block_size=bs, v_codes=v.to(F8).view(torch.uint8), v_scales=torch.ones(pages * bs, 1),
+             k_codes=torch.randn(pages * bs, 1, 128, generator=g).to(F8).view(torch.uint8),
+             k_scales=torch.ones(pages * bs, 1))
+    order = torch.randperm(pages, generator=g).to(torch.int32)
+    tables = order.repeat(most // bs // pages)[None].cuda().expand(n, -1).contiguous()
+    got = window(on_gpu(c), torch.zeros(n, 1, 128, dtype=torch.bfloat16), tables, [most] * n, most, 0, 1)
+    want = v.double().mean(0)
+    assert bool(((got.cpu().double() - want).abs() <= (2.0 ** -8 + 2.0 ** -19) * want).all())
