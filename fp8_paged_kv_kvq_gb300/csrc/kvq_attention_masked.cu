@@ -128,7 +128,8 @@ struct MkShape {
   static constexpr int kSumFull = kOEmpty + 2;
   static constexpr int kTurn = kSumFull + 2;
   static constexpr int kDrain = kTurn + 2;
-  static constexpr int kUnitFull = kDrain + 2;
+  static constexpr int kQRows = kDrain + 2;                  // (of a shared tile, per 32 rows)
+  static constexpr int kUnitFull = kQRows + 4;
   static constexpr int kUnitEmpty = kUnitFull + kMkUnits;
   static constexpr int kBars = kUnitEmpty + kMkUnits;
   static constexpr int kSmem = kOffBar + 8 * kBars + 1024;
@@ -176,6 +177,10 @@ __device__ __forceinline__ void mk_load_box(uint32_t dst, const void *tmap, int 
       "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;\n"
       :: "r"(dst), "l"(tmap), "r"(0), "r"(z), "r"(head), "r"(bar), "l"(policy) : "memory");
+}
+
+__device__ __forceinline__ void mk_prefetch_map(const void *tmap) {
+  asm volatile("prefetch.tensormap [%0];\n" :: "l"(tmap) : "memory");
 }
 
 // One lane of the (converged) warp.
@@ -603,44 +608,54 @@ __device__ __forceinline__ bool mk_softmax_masked(const MkParams &p, const MkSee
   return hit != 0u;
 }
 
-// A query row (null: zeros) as two e4m3 pieces into its place in a K-major, 128-byte
-// swizzled tile; returns 2^e |sm_scale| log2(e), which takes its scores to log2 units.
-// The row waits for its largest magnitude in the pieces' own place: of 16 dims, the first
-// 8 where the first piece goes, the others where the second goes.
-__device__ __forceinline__ float mk_query_row(const uint4 *src, float scale2, uint32_t flip,
-                                              uint8_t *tile, int row, bool store) {
-  uint4 v[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = src != nullptr ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-  uint32_t mg = 0u;                                    // largest magnitude, as bf16 bits
-  uint8_t *at = tile + row * kHeadDim;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    mg = __vmaxu2(mg, __vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu));
-    mg = __vmaxu2(mg, __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu));
-    if (store)
-      *reinterpret_cast<uint4 *>(at + (k & 1) * 128 * kHeadDim + (((k >> 1) ^ (row & 7)) << 4)) = v[k];
+// Query rows wait for their largest magnitude in their pieces' own place in a K-major,
+// 128-byte swizzled tile (two pieces of 128 bytes a row): of 16 dims, the first 8 where the
+// first piece goes, the others where the second goes.
+__device__ __forceinline__ uint8_t *mk_query_place(uint8_t *tile, int row, int c) {   // dims 8 c ..
+  return tile + (c & 1) * 128 * kHeadDim + row * kHeadDim + (((c >> 1) ^ (row & 7)) << 4);
+}
+// The row's largest magnitude, as bf16 bits.
+__device__ __forceinline__ uint32_t mk_query_top(uint8_t *tile, int row) {
+  uint32_t mg = 0u;
+#pragma unroll 4
+  for (int c = 0; c < 16; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(mk_query_place(tile, row, c));
+    mg = __vmaxu2(mg, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
+    mg = __vmaxu2(mg, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
   }
-  const uint32_t top = max(mg & 0xFFFFu, mg >> 16);
+  return max(mg & 0xFFFFu, mg >> 16);
+}
+// e4m3 pieces of two elements that f16 holds: p1 = e4m3(x), p2 = e4m3(x - p1).
+__device__ __forceinline__ void mk_pieces2(uint32_t x, uint32_t &p1, uint32_t &p2) {
+  asm("{\n .reg .b16 a, b;\n .reg .b32 y, z;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\n cvt.rn.f16x2.e4m3x2 y, a;\n sub.rn.f16x2 z, %2, y;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 b, z;\n cvt.u32.u16 %0, a;\n cvt.u32.u16 %1, b;\n}\n"
+      : "=r"(p1), "=r"(p2) : "r"(x));
+}
+// Dims [16 c0, 16 c1) of the row, largest magnitude `top`, as two e4m3 pieces (x = 2^e (p1
+// + p2); elements below 2^-14 of 2^e in f16 are 2^-32 of the largest); returns 2^e |sm_scale|
+// log2(e), which takes the row's scores to log2 units.
+__device__ __forceinline__ float mk_query_pieces(uint8_t *tile, int row, int c0, int c1,
+                                                 uint32_t top, float scale2, uint32_t flip) {
   const int ex = static_cast<int>(top >> 7);
   int e = ex == 0 ? -126 : ex - 127 - 7;
   e = e < -126 ? -126 : e;
-  if (store) {
-    const float inv = top == 0u ? 0.0f : mk_pow2(-e);
+  const float inv = top == 0u ? 0.0f : mk_pow2(-e);
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
-      uint4 *to1 = reinterpret_cast<uint4 *>(at + (c << 4)), *to2 = to1 + 8 * kHeadDim;
-      const uint4 y[2] = {*to1, *to2};
-      uint32_t p1[4], p2[4];
+  for (int c = c0; c < c1; ++c) {
+    uint4 *to1 = reinterpret_cast<uint4 *>(mk_query_place(tile, row, 2 * c)), *to2 = to1 + 8 * kHeadDim;
+    const uint4 y[2] = {*to1, *to2};
+    uint32_t p1[8], p2[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w0 = (i & 1) ? y[i >> 1].z : y[i >> 1].x, w1 = (i & 1) ? y[i >> 1].w : y[i >> 1].y;
-        const float xs[4] = {bf16_lo(w0) * inv, bf16_hi(w0) * inv, bf16_lo(w1) * inv, bf16_hi(w1) * inv};
-        e4m3_pieces4(xs, p1[i], p2[i]);
-      }
-      *to1 = make_uint4(p1[0] ^ flip, p1[1] ^ flip, p1[2] ^ flip, p1[3] ^ flip);
-      *to2 = make_uint4(p2[0] ^ flip, p2[1] ^ flip, p2[2] ^ flip, p2[3] ^ flip);
+    for (int i = 0; i < 8; ++i) {
+      const uint4 &q = y[i >> 2];
+      const uint32_t w = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+      mk_pieces2(pack_f16x2(bf16_lo(w) * inv, bf16_hi(w) * inv), p1[i], p2[i]);
     }
+    *to1 = make_uint4((p1[0] | p1[1] << 16) ^ flip, (p1[2] | p1[3] << 16) ^ flip,
+                      (p1[4] | p1[5] << 16) ^ flip, (p1[6] | p1[7] << 16) ^ flip);
+    *to2 = make_uint4((p2[0] | p2[1] << 16) ^ flip, (p2[2] | p2[3] << 16) ^ flip,
+                      (p2[4] | p2[5] << 16) ^ flip, (p2[6] | p2[7] << 16) ^ flip);
   }
   // (a row with an infinity or a NaN has no scores)
   return ex == 255 ? __uint_as_float(0x7FC00000u) : mk_pow2(e) * scale2;
@@ -675,7 +690,9 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
     if (i >= S::kVfFull && i < S::kVfFull + S::kVfs) count = 4;
     if (i >= S::kKvEmpty && i < S::kKvEmpty + S::kStages) count = kPair ? 4 + 2 : 1;
     if (i >= S::kScEmpty && i < S::kScEmpty + kMkScales) count = kPair ? 8 : 4;
-    if ((i >= S::kQFull && i < S::kQFull + 2) || (i >= S::kPReady && i < S::kPReady + 4) ||
+    if (i >= S::kQFull && i < S::kQFull + 2) count = kPair ? 4 : 8;
+    if (i >= S::kQRows && i < S::kQRows + 4) count = 2;  // the chains' warps of those rows
+    if ((i >= S::kPReady && i < S::kPReady + 4) ||
         (i >= S::kOEmpty && i < S::kOEmpty + 2) || (i >= S::kSumFull && i < S::kSumFull + 2))
       count = 4;                                       // a chain's softmax or the epilogue
     if (i >= S::kUnitEmpty && i < S::kUnitEmpty + kMkUnits)
@@ -684,6 +701,10 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
     fence_mbarrier_init();
   }
   if (tid == 0) *abort_s = 0;
+  if (tid == 32) {
+    mk_prefetch_map(&tm);
+    if (p.two_maps) mk_prefetch_map(&tm_v);
+  }
   if (warp == kMkWarpLoad) {
     tmem_alloc(smem_addr(tmem_slot), kMkTmemCols);
     tmem_relinquish();
@@ -766,32 +787,44 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       const int un = u.n, n = chain_chunks(u, a);
       if (un == 0) break;
       float rowf = 0.0f;
-      if (n > 0) {
-        // the row's query; the tile's space is free once the last unit's products
-        // with it are done.  (Where the chains share a tile, chain 0 stores it.)
-        const int m = u.row0 + trow, head = u.h + hu;
-        const int i = mk_query(p, m);
-        const uint4 *src = m < p.M && head < p.H ? reinterpret_cast<const uint4 *>(
-            p.q + ((static_cast<int64_t>(u.r) * p.R + i) * p.Hq + head * p.G + (m - i * p.G)) * kHeadDim)
-            : nullptr;
-        const bool store = kPair || a == 0;
+      if (!kPair || n > 0) {
+        // the warp's queries; the tile's space is free once the last unit's products with it
+        // are done.  (Where the chains share a tile, a warp of each has half of its rows to
+        // load and half of their dims to convert.)
         bool ok = true;
-        if (kPair && q_units > 0) ok = mk_wait_all(BAR(S::kQEmpty + a), (q_units - 1) & 1, abort_s);
-        if (!kPair && store) {
+        if (kPair) {
+          if (q_units > 0) ok = mk_wait_all(BAR(S::kQEmpty + a), (q_units - 1) & 1, abort_s);
+        } else {
           if (q_units > 0) ok = mk_wait_all(BAR(S::kQEmpty), (q_units - 1) & 1, abort_s);
           if (ok && q_units1 > 0) ok = mk_wait_all(BAR(S::kQEmpty + 1), (q_units1 - 1) & 1, abort_s);
         }
-        if (!ok) {
-          gave_up = true;
-          break;
+        if (!ok) gave_up = true;
+        uint8_t *tile = smem + S::kOffQ + (kPair ? a : 0) * 2 * S::kQPiece;
+        const int r0 = kPair ? 0 : 16 * a;
+#pragma unroll 1
+        for (int r = r0 + (lane >> 4); r < r0 + (kPair ? 32 : 16); r += 2) {
+          const int row = 32 * q4 + r, m = u.row0 + (kPair ? 128 * a + row : row % kRows);
+          const int head = u.h + (kPair ? 0 : row / kRows), i = mk_query(p, m), c = lane & 15;
+          const bool have = m < p.M && head < p.H;
+          const int64_t at = (static_cast<int64_t>(u.r) * p.R + i) * p.Hq + head * p.G + (m - i * p.G);
+          cp_async_16(mk_query_place(tile, row, c), p.q + (have ? at * kHeadDim + 8 * c : 0), have ? 16u : 0u);
         }
-        rowf = mk_query_row(src, p.scale2, p.flip, smem + S::kOffQ + (kPair ? a : 0) * 2 * S::kQPiece,
-                            lane_row, store);
-        if (store) {
-          fence_proxy_async_smem();
+        cp_async_commit();
+        cp_async_wait<0>();
+        auto both = [&](uint32_t parity) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(S::kQFull + (kPair ? a : 0)));
-        }
+          if (kPair) return;
+          if (lane == 0) mbar_arrive(BAR(S::kQRows + q4));
+          if (!mk_wait_all(BAR(S::kQRows + q4), parity, abort_s)) gave_up = true;
+        };
+        both(0);
+        const uint32_t top = mk_query_top(tile, lane_row);
+        both(1);
+        rowf = mk_query_pieces(tile, lane_row, kPair ? 0 : 4 * a, kPair ? 8 : 4 * a + 4, top, p.scale2, p.flip);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(S::kQFull + (kPair ? a : 0)));
+        if (gave_up) break;
       }
       q_units += kPair ? n > 0 : 1;
       q_units1 += un >= 2;
@@ -903,28 +936,31 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         const int64_t prow = piece + (kPair ? 128 * a : 0) + lane_row;
         const bool direct = u.direct != 0;
 #pragma unroll 1
-        for (int c = 0; c < kHeadDim; c += 16) {
-          float o[16];
-          tmem_ld16(tl + mk_o(a) + c, o);
+        for (int c = 0; c < kHeadDim; c += 32) {
+          float o[32];
+          tmem_ld32(tl + mk_o(a) + c, o);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = none ? 0.0f : o[i] * f0;
+          for (int i = 0; i < 32; ++i) o[i] = none ? 0.0f : o[i] * f0;
           if (both) {
-            float o1[16];
-            tmem_ld16(tl + mk_o(1) + c, o1);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = none ? 0.0f : fmaf(o1[i], f1, o[i]);
+            for (int h = 0; h < 32; h += 16) {
+              float o1[16];
+              tmem_ld16(tl + mk_o(1) + c + h, o1);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[h + i] = none ? 0.0f : fmaf(o1[i], f1, o[h + i]);
+            }
           }
           if (mine) {
             if (direct) {
               uint4 *to = reinterpret_cast<uint4 *>(dst + c);
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
+              for (int i = 0; i < 4; ++i)
                 to[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
                                    pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
             } else {
               float4 *to = reinterpret_cast<float4 *>(p.o_part + prow * kHeadDim + c);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 8; ++i)
                 to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
           }
