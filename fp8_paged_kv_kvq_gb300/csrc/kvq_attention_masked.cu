@@ -356,6 +356,18 @@ struct MkRow {
   int eg = 0;                                          // value scales are held over 2^eg
 };
 
+// 16 columns of this thread's TMEM lane, not waited for; done: after tmem_wait_ld, before
+// any use.
+__device__ __forceinline__ void mk_ld16_start(uint32_t taddr, float *x) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+               "%11, %12, %13, %14, %15}, [%16];\n"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+               : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void mk_ld16_done(float *x) {
+  asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]), "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]) :: "memory");
+}
+
 // max_j (u_j + log2 of the value scale) over 16 tokens, those of `bits`.
 __device__ __forceinline__ float mk_top16(const float (&x)[16], const float *ks, const float *lg,
                                           uint64_t rowf, uint32_t bits, float top) {
@@ -407,7 +419,7 @@ __device__ __forceinline__ void mk_meet(MkRow &row, float top, int de, bool fres
 // P'' of 16 scores as f16 in w, the sum of the p added to `sum`; tokens that are not in
 // `bits` (kMasked) have p = 0.
 template <bool kMasked>
-__device__ __forceinline__ void mk_part16(const float (&x)[16], const float *ks, const float *vs,
+__device__ __forceinline__ void mk_part16(const float *x, const float *ks, const float *vs,
                                           uint64_t rowf, uint64_t shift, uint32_t bits,
                                           uint64_t (&sum)[2], uint32_t (&w)[8]) {
 #pragma unroll
@@ -474,75 +486,60 @@ __device__ __forceinline__ void mk_softmax(uint32_t scol, uint32_t ocol, const f
   row.eg = eg;
   const float *vs = ks + kMkTok, *lg = vs + kMkTok;
   const uint64_t rf = pack_f32x2(rowf, rowf);
+  // Scores in registers: of one head, 64 of the 128 at a time.
+  constexpr int kRegs = kGroups > 4 ? 4 : kGroups;     // groups
+  float x[16 * kRegs];
+  auto load = [&](int h) {
+    if (kHeads == 1) {
+      tmem_ld64(scol + 64 * h, x);
+    } else {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+        mk_ld16_start(scol + mk_col<kHeads>(g, hu), x + 16 * g % (16 * kRegs));
+      tmem_wait_ld();
+#pragma unroll
+      for (int g = 0; g < kRegs; ++g) mk_ld16_done(x + 16 * g);
+    }
+  };
   // the largest a score can be under the chunk's largest scales
   float mx[2] = {0.0f, 0.0f};
-  if (kHeads == 1) {
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 64) {
-      float x[64];
-      tmem_ld64(scol + c, x);
+  for (int h = kHeads == 1 ? 1 : 0; h >= 0; --h) {
+    load(h);
 #pragma unroll
-      for (int i = 0; i < 64; i += 4)
+    for (int i = 0; i < 16 * kRegs; i += 4)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) mx[q] = mk_max3(mx[q], x[i + q], x[i + q + 2]);
-    }
-  } else {
-#pragma unroll 1
-    for (int g = 0; g < kGroups; g += 2) {
-      float x[16], y[16];
-      tmem_ld16(scol + mk_col<kHeads>(g, hu), x);
-      tmem_ld16(scol + mk_col<kHeads>(g + 1, hu), y);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) mx[i & 1] = mk_max3(mx[i & 1], x[i], y[i]);
-    }
+      for (int q = 0; q < 2; ++q) mx[q] = mk_max3(mx[q], x[i + q], x[i + q + 2]);
   }
   const float most = fmaxf(mx[0], mx[1]) * meta.x * rowf + meta.y;
   if (de != 0 || __any_sync(0xFFFFFFFFu, !(most - row.m <= kMkLazy))) {
     float top = -INFINITY;
 #pragma unroll 1
     for (int g = 0; g < kGroups; ++g) {
-      float x[16];
+      float y[16];
       const int col = mk_col<kHeads>(g, hu);
-      tmem_ld16(scol + col, x);
-      top = mk_top16(x, ks + col, lg + col, rf, 0xFFFFu, top);
+      tmem_ld16(scol + col, y);
+      top = mk_top16(y, ks + col, lg + col, rf, 0xFFFFu, top);
     }
     mk_meet(row, top, de, fresh, ocol);
   }
   const float sh = row.m == -INFINITY ? 0.0f : -row.m;
   const uint64_t s2 = pack_f32x2(sh, sh);
   uint64_t sum[2] = {pack_f32x2(0.0f, 0.0f), pack_f32x2(0.0f, 0.0f)};
-  if (kHeads == 4) {
-    // (a half's P'' lies over the other's scores of other heads only)
-    float x0[16], x1[16];
-    uint32_t w[8];
-    tmem_ld16(scol + mk_col<kHeads>(0, hu), x0);
-    tmem_ld16(scol + mk_col<kHeads>(1, hu), x1);
-    int col = mk_col<kHeads>(0, hu);
-    mk_part16<false>(x0, ks + col, vs + col, rf, s2, 0u, sum, w);
-    tmem_st8u(scol + mk_pcol(col), w);
-    mk_zero<kHeads>(scol, 0, hu);
-    mk_announce(ready, lane);
-    col = mk_col<kHeads>(1, hu);
-    mk_part16<false>(x1, ks + col, vs + col, rf, s2, 0u, sum, w);
-    tmem_st8u(scol + mk_pcol(col), w);
-    mk_zero<kHeads>(scol, 1, hu);
-    mk_announce(ready + 8, lane);
-  } else {
+  // (a half's P'' lies over its own scores, or of several heads over others')
 #pragma unroll 1
-    for (int g = 0; g < kGroups; g += 2) {
-      float x0[16], x1[16];
+  for (int h = 0; h < (kHeads == 1 ? 2 : 1); ++h) {
+    if (h == 1) load(1);
+#pragma unroll
+    for (int g = 0; g < kRegs; ++g) {
       uint32_t w[8];
-      const int c0 = mk_col<kHeads>(g, hu), c1 = mk_col<kHeads>(g + 1, hu);
-      tmem_ld16(scol + c0, x0);
-      tmem_ld16(scol + c1, x1);
-      mk_part16<false>(x0, ks + c0, vs + c0, rf, s2, 0u, sum, w);
-      tmem_st8u(scol + mk_pcol(c0), w);
-      mk_part16<false>(x1, ks + c1, vs + c1, rf, s2, 0u, sum, w);
-      tmem_st8u(scol + mk_pcol(c1), w);
-      if ((g + 2) % kHalf == 0) {
-        const int h = g / kHalf;
-        mk_zero<kHeads>(scol, h, hu);
-        mk_announce(ready + 8 * h, lane);
+      const int col = mk_col<kHeads>(kHeads == 1 ? 4 * h + g : g, hu);
+      mk_part16<false>(x + 16 * g, ks + col, vs + col, rf, s2, 0u, sum, w);
+      tmem_st8u(scol + mk_pcol(col), w);
+      if ((g + 1) % kHalf == 0) {
+        const int half = kHeads == 1 ? h : g / kHalf;
+        mk_zero<kHeads>(scol, half, hu);
+        mk_announce(ready + 8 * half, lane);
       }
     }
   }
