@@ -1471,26 +1471,27 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
   }
 }
 
-// The pieces of the units that are cut, joined: kMkJoinParts blocks for each block of the
-// first launch that was the first of several to work on a unit, a warp per row at a time,
-// four dims a lane.
-constexpr int kMkJoinParts = 8, kMkJoinWarps = 4;
+// The pieces of the units that are cut, joined: `parts` blocks for each block of the first
+// launch that was the first of several to work on a unit, a warp per row at a time, four
+// dims a lane.
+constexpr int kMkJoinParts = 32, kMkJoinWarps = 4;     // (parts at most)
 
 __global__ void __launch_bounds__(32 * kMkJoinWarps)
-attn_masked_join_kernel(const MkParams p, int lanes, int rows_of_head) {
+attn_masked_join_kernel(const MkParams p, int parts, int lanes, int heads) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b_first = static_cast<int>(blockIdx.x) / kMkJoinParts, part = static_cast<int>(blockIdx.x) % kMkJoinParts;
+  const int b_first = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) % parts;
   allow_dependents_launch();
   grid_dependency_wait();
-  const int4 cut = p.cuts[b_first];                    // request, first head, first row, last block
+  const int4 cut = __ldcg(p.cuts + b_first);           // request, first head, first row, last block
   if (cut.x < 0) return;
-  const int pieces = cut.w - b_first + 1, step = kMkJoinParts * kMkJoinWarps;
+  const int pieces = cut.w - b_first + 1, step = parts * kMkJoinWarps;
+  const int head_lanes = lanes / heads, rows = min(head_lanes, p.M - cut.z);
   auto place = [&](int b, int r) -> int64_t {
     return static_cast<int64_t>(2 * (b_first + b) + (b == 0 ? 1 : 0)) * lanes + r;
   };
-  for (int r = part * kMkJoinWarps + warp; r < lanes; r += step) {
-    const int head = cut.y + r / rows_of_head, m = cut.z + r % rows_of_head;
-    if (head >= p.H || m >= p.M) continue;
+  for (int n = part * kMkJoinWarps + warp; n < rows * min(heads, p.H - cut.y); n += step) {
+    const int of = n / rows, head = cut.y + of, m = cut.z + n - of * rows;
+    const int r = of * head_lanes + n - of * rows;
     float top = -INFINITY, all = 0.0f;
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int b0 = 0; b0 < pieces; b0 += 8) {
@@ -1555,9 +1556,11 @@ cudaError_t mk_launch(const MkParams &p, const CUtensorMap &map, const CUtensorM
   e = launch_overlapped(kernel, dim3(static_cast<unsigned>(grid)), dim3(kMkThreads), kSmem, stream, p,
                         map, map_v);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(attn_masked_join_kernel, dim3(static_cast<unsigned>(grid * kMkJoinParts)),
-                           dim3(32 * kMkJoinWarps), 0, stream, p, MkShape<kPair, kRows>::kLanes,
-                           MkShape<kPair, kRows>::kTileRows);
+  using S = MkShape<kPair, kRows>;
+  const int rows = S::kHeads * std::min(p.M, S::kTileRows);
+  const int parts = std::min((rows + kMkJoinWarps - 1) / kMkJoinWarps, kMkJoinParts);
+  return launch_overlapped(attn_masked_join_kernel, dim3(static_cast<unsigned>(grid * parts)),
+                           dim3(32 * kMkJoinWarps), 0, stream, p, parts, S::kLanes, S::kHeads);
 }
 
 size_t mk_round(size_t n) { return (n + 255) / 256 * 256; }
