@@ -774,7 +774,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     uint32_t steps = 0, done = 0, seq = 0;             // chunks and units of this chain, chunks of all
     uint32_t sc = 0, sc_par = 0;                       // place in the scales' ring
-    uint32_t q_units = 0, q_units1 = 0;                // units with rows of chain a (split: 0 and 1)
+    uint32_t q_units = 0;                              // units with rows of chain a
     for (int t = 0;; ++t) {
       if (!wait_unit(t)) {
         gave_up = true;
@@ -792,8 +792,9 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         if (kPair) {
           if (q_units > 0) ok = mk_wait_all(BAR(S::kQEmpty + a), (q_units - 1) & 1, abort_s);
         } else {
-          if (q_units > 0) ok = mk_wait_all(BAR(S::kQEmpty), (q_units - 1) & 1, abort_s);
-          if (ok && q_units1 > 0) ok = mk_wait_all(BAR(S::kQEmpty + 1), (q_units1 - 1) & 1, abort_s);
+          if (q_units > 0)
+            ok = mk_wait_all(BAR(S::kQEmpty), (q_units - 1) & 1, abort_s) &&
+                 mk_wait_all(BAR(S::kQEmpty + 1), (q_units - 1) & 1, abort_s);
         }
         if (!ok) gave_up = true;
         uint8_t *tile = smem + S::kOffQ + (kPair ? a : 0) * 2 * S::kQPiece;
@@ -824,7 +825,6 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         if (gave_up) break;
       }
       q_units += kPair ? n > 0 : 1;
-      q_units1 += un >= 2;
       const MkSeen seen = mk_seen(p, u, u.row0 + trow);
       // the warp's first and last row
       const MkWhole whole = mk_whole<S>(p, u, __shfl_sync(0xFFFFFFFFu, seen.hi, 0),
@@ -1361,9 +1361,11 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       gave_up = !ok;
     } else {
       // ---------------------------------------------------- MMAs of a chain
-      // Each turn: PV of one of the chain's chunks and QK^T of its next, chain 0's and
-      // chain 1's bursts one after the other; everything but P'' is waited for before
-      // the turn.
+      // Each step: PV of one of the chain's chunks and QK^T of its next.  kPair: chain 0's
+      // and chain 1's steps one after the other, all but the second half of P'' waited for
+      // before the turn (without turns the chunks of prompts took 638 us, with them 586).
+      // Chains that share a tile have half the softmax work and take no turns (window of 64
+      // requests: 107 us with turns, 100 without).
       const int a = warp - kMkWarpMma;
       const uint32_t q1 = (smem_addr(smem + S::kOffQ + (kPair ? a : 0) * 2 * S::kQPiece) >> 4) | kMkKMajor;
       const uint32_t q2 = q1 + (S::kQPiece >> 4);
@@ -1385,7 +1387,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         const int un = u.n;
         if (un == 0) break;
         const int steps = kPair ? un : (un + 1) / 2;
-        const bool turns = chain_chunks(u, 1) > 0;     // (a lone chain 0 need not pass them)
+        const bool turns = kPair && chain_chunks(u, 1) > 0;    // (a lone chain 0 need not take them)
         const bool live = chain_chunks(u, a) > 0;      // (the chain has products)
         release_unit(t);
         for (int j = 0; j <= steps; ++j) {
@@ -1396,7 +1398,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           const uint32_t bk = sq % S::kStages, bv = sv % S::kVfs;
           if (use_v) ok = mk_wait_all(BAR(S::kVfFull + bv), (sv / S::kVfs) & 1, abort_s);
           if (ok && use_k) ok = mk_wait_all(BAR(S::kKvFull + bk), (sq / S::kStages) & 1, abort_s);
-          if (ok && qk && j == 0) ok = mk_wait_all(BAR(S::kQFull + (kPair ? a : 0)), kPair ? par_q : t & 1, abort_s);
+          if (ok && j == 0 && (qk || !kPair))
+            ok = mk_wait_all(BAR(S::kQFull + (kPair ? a : 0)), kPair ? par_q : t & 1, abort_s);
           if (ok && pv) {
             if (j == 1) {
               ok = mk_wait_all(BAR(S::kOEmpty + a), par_o, abort_s);
@@ -1443,6 +1446,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             if (turns) mbar_arrive(BAR(S::kTurn + (a ^ 1)));
             if (pv && (kPair ? cv == un - 1 : cv + 2 >= un)) tc_commit(BAR(S::kOFull + a));
             if (qk && (kPair ? cq == un - 1 : cq + 2 >= un)) tc_commit(BAR(S::kQEmpty + a));
+            if (!kPair && !live && j == 0) mbar_arrive(BAR(S::kQEmpty + a));   // (each unit's queries)
             if (use_v) tc_commit(BAR(kPair ? S::kVfEmpty + bv : S::kKvEmpty + bv));
             if (kPair && use_k) tc_commit(BAR(S::kKvEmpty + bk));
           }
