@@ -63,7 +63,6 @@ constexpr int kMkTok = 128;                           // keys of a chunk: (token
 constexpr int kMkWarpConv = 8, kMkWarpLoad = 12, kMkWarpMma = 13, kMkWarpScale = 15;
 constexpr int kMkThreads = 512;
 constexpr int kMkUnits = 8;                           // units announced ahead
-constexpr int kMkScales = 6;                          // chunks of scales in the ring
 constexpr int kMkMaxRequests = 1024;                  // of a launch
 constexpr int kMkCharge = 2;                          // chunks that a unit's start counts for
 constexpr float kMkLazy = 14.0f;                      // log2 of the largest P''
@@ -96,6 +95,7 @@ struct MkShape {
   // of) and its value codes, so that five chunks are on their way or at work.
   static constexpr int kStages = kPair ? 2 : 5;
   static constexpr int kVfs = kPair ? 2 : kStages;
+  static constexpr int kScales = kPair ? 6 : kStages;        // chunks of scales in their ring
   static constexpr int kStage = 2 * kMkTok * kHeadDim;
   static constexpr int kQPiece = 128 * kHeadDim;
   static constexpr int kOffQ = 0;                            // [tile][piece]
@@ -106,20 +106,20 @@ struct MkShape {
   static constexpr int kOffRef = kOffSum + 2 * 128 * 4;      // [chain][128] references
   static constexpr int kOffEg = kOffRef + 2 * 128 * 4;       // [chain]
   static constexpr int kOffSc = kOffEg + 16;                 // [stage][K | V | log2 V][128]
-  static constexpr int kOffMeta = kOffSc + kMkScales * 3 * kMkTok * 4;   // [stage] float4
-  static constexpr int kOffUnit = kOffMeta + kMkScales * 16;
+  static constexpr int kOffMeta = kOffSc + kScales * 3 * kMkTok * 4;   // [stage] float4
+  static constexpr int kOffUnit = kOffMeta + kScales * 16;
   static constexpr int kOffBad = kOffUnit + kMkUnits * static_cast<int>(sizeof(MkUnit));   // [Vf][4 words], [scales][4 words]
-  static constexpr int kOffMisc = kOffBad + (kVfs + kMkScales) * 16;              // tmem base, abort
+  static constexpr int kOffMisc = kOffBad + (kVfs + kScales) * 16;              // tmem base, abort
   static constexpr int kOffScan = kOffMisc + 16;             // a warp's sum each
   static constexpr int kOffPre = kOffScan + kMkThreads / 32 * 4;
   static constexpr int kOffBar = (kOffPre + (kMkMaxRequests + 1) * 4 + 7) / 8 * 8;
   static constexpr int kKvFull = 0;
   static constexpr int kKvEmpty = kKvFull + kStages;
   static constexpr int kVfFull = kKvEmpty + kStages;
-  static constexpr int kVfEmpty = kVfFull + kVfs;
+  static constexpr int kVfEmpty = kVfFull + 2;               // (kPair; else kVfFull: cleared values noted, per chain)
   static constexpr int kScFull = kVfEmpty + 2;
-  static constexpr int kScEmpty = kScFull + kMkScales;
-  static constexpr int kQFull = kScEmpty + kMkScales;        // per chain from here on
+  static constexpr int kScEmpty = kScFull + kScales;
+  static constexpr int kQFull = kScEmpty + kScales;        // per chain from here on
   static constexpr int kQEmpty = kQFull + 2;
   static constexpr int kSFull = kQEmpty + 2;
   static constexpr int kPReady = kSFull + 2;                 // (per chain and half of the chunk)
@@ -476,7 +476,7 @@ __device__ __forceinline__ void mk_zero(uint32_t scol, int h, int hu) {
 // brought up to date, P'' over S's columns, its halves announced one after the other.
 // ks: the chunk's key scales, value scales and their log2; meta: the largest key scale,
 // the log2 of the largest value scale, Eg.
-template <int kHeads>
+template <int kHeads, bool kHalves>
 __device__ __forceinline__ void mk_softmax(uint32_t scol, uint32_t ocol, const float *ks,
                                            const float4 meta, float rowf, int hu, bool fresh,
                                            uint32_t ready, int lane, MkRow &row) {
@@ -539,7 +539,7 @@ __device__ __forceinline__ void mk_softmax(uint32_t scol, uint32_t ocol, const f
       if ((g + 1) % kHalf == 0) {
         const int half = kHeads == 1 ? h : g / kHalf;
         mk_zero<kHeads>(scol, half, hu);
-        mk_announce(ready + 8 * half, lane);
+        if (kHalves || half == 1) mk_announce(ready + (kHalves ? 8 * half : 0), lane);
       }
     }
   }
@@ -551,7 +551,7 @@ __device__ __forceinline__ void mk_softmax(uint32_t scol, uint32_t ocol, const f
 // The same where some of the warp's rows do not see some of the chunk's tokens, from x0
 // on: seldom, so small rather than fast (the roles share an instruction cache).  bad:
 // keys whose value was cleared, 16 a word; returns whether the row sees one of them.
-template <int kHeads>
+template <int kHeads, bool kHalves>
 __device__ __forceinline__ bool mk_softmax_masked(const MkParams &p, const MkSeen &seen, int x0,
                                                   int X, const uint16_t *bad, const uint16_t *bad_sc,
                                                   uint32_t scol, uint32_t ocol, const float *ks,
@@ -596,7 +596,7 @@ __device__ __forceinline__ bool mk_softmax_masked(const MkParams &p, const MkSee
     tmem_st8u(scol + mk_pcol(col), w);
     if ((g + 1) % kHalf == 0) {
       mk_zero<kHeads>(scol, g / kHalf, hu);
-      mk_announce(ready + 8 * (g / kHalf), lane);
+      if (kHalves || g / kHalf == 1) mk_announce(ready + (kHalves ? 8 * (g / kHalf) : 0), lane);
     }
   }
   float a, b;
@@ -684,13 +684,14 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
     const int i = tid;
     // commits of the chains that read it, and arrivals of the converting warps
     if (i >= S::kVfEmpty && i < S::kVfEmpty + 2) count = 2;
-    if (i >= S::kVfFull && i < S::kVfFull + S::kVfs) count = 4;
+    if (i >= S::kVfFull && i < S::kVfFull + 2) count = 4;
+    if (i >= S::kKvFull && i < S::kKvFull + S::kStages) count = kPair ? 1 : 2;   // copies, scales
     if (i >= S::kKvEmpty && i < S::kKvEmpty + S::kStages) count = kPair ? 4 + 2 : 1;
-    if (i >= S::kScEmpty && i < S::kScEmpty + kMkScales) count = kPair ? 8 : 4;
+    if (i >= S::kScEmpty && i < S::kScEmpty + S::kScales) count = 8;
     if (i >= S::kQFull && i < S::kQFull + 2) count = kPair ? 4 : 8;
     if (i >= S::kQRows && i < S::kQRows + 4) count = 2;  // the chains' warps of those rows
-    if ((i >= S::kPReady && i < S::kPReady + 4) ||
-        (i >= S::kOEmpty && i < S::kOEmpty + 2) || (i >= S::kSumFull && i < S::kSumFull + 2))
+    if (i >= S::kPReady && i < S::kPReady + 4) count = kPair ? 4 : 8;   // a chain's softmax; values
+    if ((i >= S::kOEmpty && i < S::kOEmpty + 2) || (i >= S::kSumFull && i < S::kSumFull + 2))
       count = 4;                                       // a chain's softmax or the epilogue
     if (i >= S::kUnitEmpty && i < S::kUnitEmpty + kMkUnits)
       count = 8 + 4 + 2 + 1;                           // softmax, conversion, MMAs, scales
@@ -774,6 +775,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     uint32_t steps = 0, done = 0, seq = 0;             // chunks and units of this chain, chunks of all
     uint32_t sc = 0, sc_par = 0;                       // place in the scales' ring
+    uint32_t edge_par = 0;
     uint32_t q_units = 0;                              // units with rows of chain a
     for (int t = 0;; ++t) {
       if (!wait_unit(t)) {
@@ -833,9 +835,9 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       MkRow row;
       bool nan_row = false, fresh = true;
 #pragma unroll 1
-      for (int k = 0; k < un; ++k, ++seq, sc_par ^= sc == kMkScales - 1, sc = sc == kMkScales - 1 ? 0 : sc + 1) {
+      for (int k = 0; k < un; ++k, ++seq, sc_par ^= sc == S::kScales - 1, sc = sc == S::kScales - 1 ? 0 : sc + 1) {
         if (!kPair && (k & 1) != a) continue;
-        bool ok = mk_wait_all(BAR(S::kScFull + sc), sc_par, abort_s);
+        bool ok = !kPair || mk_wait_all(BAR(S::kScFull + sc), sc_par, abort_s);
         if (ok && n > 0) ok = mk_wait_all(BAR(S::kSFull + a), steps & 1, abort_s);
         if (!ok) {
           gave_up = true;
@@ -852,9 +854,14 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           const bool see_all = whole.at(k), edge = !all_whole.at(k);
           // where some row of the unit does not see all of the chunk, value rows with a NaN
           // code or such a scale have been cleared
-          if (edge && !mk_wait_all(BAR(S::kVfFull + seq % S::kVfs), (seq / S::kVfs) & 1, abort_s)) {
-            gave_up = true;
-            break;
+          if (edge) {
+            ok = kPair ? mk_wait_all(BAR(S::kVfFull + seq % S::kVfs), (seq / S::kVfs) & 1, abort_s)
+                       : mk_wait_all(BAR(S::kVfFull + a), edge_par, abort_s);
+            edge_par ^= 1u;
+            if (!ok) {
+              gave_up = true;
+              break;
+            }
           }
           if (see_all) {
             if (edge) {
@@ -864,16 +871,18 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
                 nan_row |= (bad[c] | (meta.w != 0.0f ? bad_sc[c] : 0)) != 0;
               }
             }
-            mk_softmax<S::kHeads>(scol, ocol, ks, meta, rowf, hu, fresh, ready, lane, row);
+            mk_softmax<S::kHeads, kPair>(scol, ocol, ks, meta, rowf, hu, fresh, ready, lane, row);
           } else {
-            nan_row |= mk_softmax_masked<S::kHeads>(p, seen, (u.c0 + k) * S::kTok, u.X, bad, bad_sc, scol,
+            nan_row |= mk_softmax_masked<S::kHeads, kPair>(p, seen, (u.c0 + k) * S::kTok, u.X, bad, bad_sc, scol,
                                                     ocol, ks, meta, rowf, hu, fresh, ready, lane, row);
           }
           fresh = false;
           ++steps;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(S::kScEmpty + sc));
+        if (kPair) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(S::kScEmpty + sc));
+        }
       }
       if (gave_up) break;
       release_unit(t);
@@ -1009,7 +1018,10 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           bad |= __vcmpeq4(w[c].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w[c].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
                  __vcmpeq4(w[c].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w[c].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         const uint32_t word = __ballot_sync(0xFFFFFFFFu, keep && bad != 0u);
-        if (lane == 0) bad_s[4 * v + q4] = word;
+        if (lane == 0) {
+          bad_s[4 * v + q4] = word;
+          if (!kPair) mbar_arrive(BAR(S::kVfFull + (k & 1)));
+        }
         keep = keep && bad == 0u;
       }
       if (!keep) {
@@ -1030,7 +1042,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       __syncwarp();
       if (lane == 0) {
         if (kPair) mbar_arrive(BAR(S::kKvEmpty + b));
-        mbar_arrive(BAR(S::kVfFull + v));
+        mbar_arrive(kPair ? BAR(S::kVfFull + v) : BAR(S::kPReady + 2 * (k & 1)));
       }
       return true;
     };
@@ -1281,9 +1293,9 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           }
         }
         if (more) {
-          const uint32_t b = n % kMkScales;
-          if (n >= kMkScales)
-            ok = mk_wait_all(BAR(S::kScEmpty + b), (n / kMkScales - 1) & 1, abort_s);
+          const uint32_t b = n % S::kScales;
+          if (n >= S::kScales)
+            ok = mk_wait_all(BAR(kPair ? S::kScEmpty + b : S::kKvEmpty + b), (n / S::kScales - 1) & 1, abort_s);
           if (!ok) break;
           const int first = __shfl_sync(0xFFFFFFFFu, slot, j * boxes + box_of);
           const int len = first < 0 ? 0 : left;
@@ -1309,7 +1321,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         if (more) cp_async_wait<kAhead>();
         else cp_async_wait<0>();
         __syncwarp();
-        const uint32_t b = done % kMkScales;
+        const uint32_t b = done % S::kScales;
         float4 *ks = reinterpret_cast<float4 *>(smem + S::kOffSc + b * 3 * kMkTok * 4) + lane;
         const float4 kk = ks[0];
         const float4 v4 = ks[kMkTok / 4];
@@ -1354,7 +1366,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
               make_float4(__uint_as_float(km), fmaxf(static_cast<float>(ev - eg), kMkFloor),
                           __int_as_float(eg), flagged);
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(S::kScFull + b));
+        if (lane == 0) mbar_arrive(BAR(kPair ? S::kScFull + b : S::kKvFull + b));
         ++done;
       }
       cp_async_wait<0>();
@@ -1396,8 +1408,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
           const bool pv = use_v && live, qk = use_k && live;
           const uint32_t sv = base + cv, sq = base + cq;
           const uint32_t bk = sq % S::kStages, bv = sv % S::kVfs;
-          if (use_v) ok = mk_wait_all(BAR(S::kVfFull + bv), (sv / S::kVfs) & 1, abort_s);
-          if (ok && use_k) ok = mk_wait_all(BAR(S::kKvFull + bk), (sq / S::kStages) & 1, abort_s);
+          if (kPair && use_v) ok = mk_wait_all(BAR(S::kVfFull + bv), (sv / S::kVfs) & 1, abort_s);
+          if (kPair && ok && use_k) ok = mk_wait_all(BAR(S::kKvFull + bk), (sq / S::kStages) & 1, abort_s);
           if (ok && j == 0 && (qk || !kPair))
             ok = mk_wait_all(BAR(S::kQFull + (kPair ? a : 0)), kPair ? par_q : t & 1, abort_s);
           if (ok && pv) {
@@ -1420,7 +1432,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
               for (int kk = 0; kk < 4; ++kk)
                 mk_mma_pv(o_col, s_col + 8 * kk, v_lo + v_step * kk, v_hi, (j == 1 && kk == 0) ? 0u : 1u);
             }
-            ok = mk_wait_all(BAR(S::kPReady + 2 * a + 1), par_p, abort_s);
+            if (kPair) ok = mk_wait_all(BAR(S::kPReady + 2 * a + 1), par_p, abort_s);
             if (!ok) break;
             par_p ^= 1u;
             tc_fence_after();
@@ -1428,7 +1440,12 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
 #pragma unroll
               for (int kk = 4; kk < 8; ++kk)
                 mk_mma_pv(o_col, s_col + 32 + 8 * kk, v_lo + v_step * kk, v_hi, 1u);
+              if (!kPair) tc_commit(BAR(S::kKvEmpty + bv));
             }
+          }
+          if (!kPair && use_k) {
+            ok = mk_wait_all(BAR(S::kKvFull + bk), (sq / S::kStages) & 1, abort_s);
+            if (!ok) break;
           }
           if (qk) {
             const uint32_t k_lo = k0 + bk * (S::kStage >> 4);
@@ -1447,7 +1464,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             if (pv && (kPair ? cv == un - 1 : cv + 2 >= un)) tc_commit(BAR(S::kOFull + a));
             if (qk && (kPair ? cq == un - 1 : cq + 2 >= un)) tc_commit(BAR(S::kQEmpty + a));
             if (!kPair && !live && j == 0) mbar_arrive(BAR(S::kQEmpty + a));   // (each unit's queries)
-            if (use_v) tc_commit(BAR(kPair ? S::kVfEmpty + bv : S::kKvEmpty + bv));
+            if (kPair && use_v) tc_commit(BAR(S::kVfEmpty + bv));
             if (kPair && use_k) tc_commit(BAR(S::kKvEmpty + bk));
           }
           __syncwarp();
