@@ -64,7 +64,6 @@ constexpr int kMkWarpConv = 8, kMkWarpLoad = 12, kMkWarpMma = 13, kMkWarpScale =
 constexpr int kMkThreads = 512;
 constexpr int kMkUnits = 8;                           // units announced ahead
 constexpr int kMkMaxRequests = 1024;                  // of a launch
-constexpr int kMkCharge = 2;                          // chunks that a unit's start counts for
 constexpr float kMkLazy = 14.0f;                      // log2 of the largest P''
 constexpr float kMkFloor = -90.0f;                    // log2 of the smallest value scale, over 2^Eg
 constexpr int kMkMaxEg = 30;                          // Eg at most
@@ -87,6 +86,11 @@ struct MkShape {
   static constexpr int kLanes = kPair ? 256 : 128;           // of all its heads
   static constexpr int kHeads = 128 / kRows;
   static constexpr int kTok = kMkTok / kHeads;               // tokens of a chunk
+  // Chunks that a unit's start counts for: its queries are read and converted and the chains
+  // run empty.  (Window of 64 requests: 98 us with 2, 89 with 6 and with 8, 91 with 13; tree
+  // batch 198, 185, 184, 187.  Chunks of prompts: 589 with 1, 586 with 2, 584 with 3; 5 trees
+  // of 25 nodes 44, 40, 42.)
+  static constexpr int kCharge = kPair ? 2 : 8;
   static constexpr int kTokLog2 = kRows == 32 ? 5 : (kRows == 64 ? 6 : 7);
   static constexpr int kQTiles = kPair ? 2 : 1;
   // shared memory, offsets from a 1024-byte aligned base
@@ -296,7 +300,7 @@ __device__ __forceinline__ int mk_len(const MkParams &p, int r) {
 
 template <typename S>
 __device__ __forceinline__ int mk_positions(int X) {   // of a unit in the work sequence
-  return X > 0 ? ((X + S::kTok - 1) >> S::kTokLog2) + kMkCharge : 0;
+  return X > 0 ? ((X + S::kTok - 1) >> S::kTokLog2) + S::kCharge : 0;
 }
 
 // What a query row sees, in a unit's token numbers: x < hi and (x < sinks or x >= lo),
@@ -1148,7 +1152,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             }
           }
           if (x >= ua + V) continue;
-          const int first = ua + kMkCharge, end = min(ua + V, x_end), from = max(x, first);
+          const int first = ua + S::kCharge, end = min(ua + V, x_end), from = max(x, first);
           x = end;
           if (from >= end) continue;
           n = end - from;
@@ -1161,11 +1165,11 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
             u.s16 = s.s16;
             u.shift = s.shift;
             u.base = uL - p.R;
-            u.direct = n == V - kMkCharge;
+            u.direct = n == V - S::kCharge;
             const int b_first = static_cast<int>(static_cast<unsigned>(first) / static_cast<unsigned>(B));
             const bool starts = static_cast<int>(blockIdx.x) == b_first;
             u.slot = 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
-            if (starts && n != V - kMkCharge)
+            if (starts && n != V - S::kCharge)
               cut = make_int4(ur, uh * S::kHeads, ut * S::kTileRows,
                               static_cast<int>(static_cast<unsigned>(ua + V - 1) / static_cast<unsigned>(B)));
           }
@@ -1175,7 +1179,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         __syncwarp();
         return n;
       };
-      const uint64_t pol = l2_policy_evict_normal();
+      // (pages that only one unit reads need not stay: tree batch 200 -> 194 us)
+      const uint64_t pol = p.T == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
       // A batch: the pages of 32 boxes, one a lane, read while the batch before is copied.
       int t_cur = 0, un = next_unit(unit_s[0]);
       if (lane == 0) mbar_arrive(BAR(S::kUnitFull));
@@ -1557,6 +1562,7 @@ attn_masked_join_kernel(const MkParams p, int parts, int lanes, int heads) {
 
 // Rows of a unit and head, and its heads.
 int mk_tile_rows(int M) { return M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256)); }
+int mk_charge(int rows) { return rows > 128 ? MkShape<true, 128>::kCharge : MkShape<false, 32>::kCharge; }
 int mk_heads(int rows) { return rows >= 128 ? 1 : 128 / rows; }
 
 template <bool kPair, int kRows>
@@ -1594,7 +1600,7 @@ bool attn_masked_too_long(const MaskedArgs &a, int32_t num_kv_heads) {
   const int rows = mk_tile_rows(M), heads = mk_heads(rows), tokens = kMkTok / heads;
   const double units = static_cast<double>(std::min(a.num_requests, kMkMaxRequests)) *
                        ((num_kv_heads + heads - 1) / heads) * ((M + rows - 1) / rows);
-  return units * (a.max_context_len / tokens + 1 + kMkCharge) >= 2147483648.0;
+  return units * (a.max_context_len / tokens + 1 + mk_charge(rows)) >= 2147483648.0;
 }
 
 size_t attn_masked_workspace_bytes(const MaskedArgs &a, int32_t num_kv_heads) {
@@ -1632,9 +1638,9 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
   p.words = (p.R + 31) / 32;
   p.scale2 = (a.sm_scale < 0.0f ? -a.sm_scale : a.sm_scale) * 1.4426950408889634f;
   p.flip = a.sm_scale < 0.0f ? 0x80808080u : 0u;
-  // Ranges of at least 128 tokens and a unit's start: shorter ones are joined from more
-  // pieces than they save (one row, 1,028 tokens: 32 us with ranges of one chunk of 32
-  // tokens, 20 with five; 16 rows, 2,000 tokens: 36 with one of 64, 27 to 30 with 2 to 5).
+  // Ranges of at least 128 tokens (and a chunk): shorter ones are joined from more pieces
+  // than they save (one row, 1,028 tokens: 21 us with ranges of three chunks of 32 tokens, 19
+  // with five or six, 21 with seven).
   p.least = kMkTok / tokens + 1;
   p.k_scales = c.k_scales;
   p.v_scales = c.v_scales;
