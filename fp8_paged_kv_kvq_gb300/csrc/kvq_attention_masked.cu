@@ -8,12 +8,14 @@
 //  * Rows.  The R query rows of a request that share a KV head are stacked with
 //    their G query heads: row m is query row m / G, head m % G.  A unit of work is
 //    one (request, KV head, row tile) over the tokens that some row of the tile
-//    sees, in chunks of 128.  Two chains (QK^T -> softmax -> PV) work on a unit: of
-//    more than 128 rows each has a 128-row tile of its own over all chunks (kPair),
-//    of fewer they take turns at the chunks, and their sums and outputs are joined
-//    at the end.  Of at most 32 rows the tile is repeated four times on the tensor
-//    core's 128 rows and copy c takes the tokens [32 c, 32 c + 32) of a chunk, so
-//    that all four warps of a chain's softmax have work.
+//    sees, in chunks.  Two chains (QK^T -> softmax -> PV) work on a unit: of more
+//    than 128 rows each has a 128-row tile of its own over all chunks (kPair), of
+//    fewer they share a tile, take the chunks in turn, and their sums and outputs are
+//    joined at the end.  Of at most 32 (64) rows a unit is four (two) KV heads side by
+//    side, 32 (64) of the tensor core's 128 rows each; its chunk is 32 (64) tokens of
+//    each head, and a row's weights are 0 at the other heads' keys.  All four warps of
+//    a softmax have work so, and one copy brings a page's tokens of four heads
+//    (window of 64 requests, a unit per head: 172 us, per four heads 125).
 //  * Tokens.  A unit's tokens are numbered without the gap between sinks and
 //    window: x < S16 is position x, the others x + shift (both parts start on a
 //    multiple of 16 tokens), so that a few sinks cost no chunk of their own.
@@ -22,6 +24,12 @@
 //    (normalised output, reference, denominator) in the workspace, which a second
 //    launch joins, with all SMs (joined by the block whose piece came last, 175 rows in
 //    7 pieces took it 34 us).
+//  * Stages.  A chunk's K and V codes are copied by TMA, 8 rows of K and 8 of V in
+//    turns, 16 tokens (a tree's whole page) a copy.  kPair: two stages, values converted
+//    into two f16 buffers of their own.  Else five stages, values converted in place,
+//    over the chunk's own keys (once its scores are made) and codes: the copies in flight
+//    are what bounds a step's time with few rows (with separate buffers and three stages
+//    the window of 64 requests took 125 us, in place 115).
 //  * S = Q K^T: 128 x 128 x 128, kind::f8f6f4, the query as two e4m3 pieces (q = 2^e
 //    (p1 + p2), exact for elements >= 2^-9 of the row's largest) on the key codes as
 //    they are.  O += P V: kind::f16, P'' = p v_scale in f16 from tensor memory, the
@@ -45,6 +53,20 @@
 //    units and the copies of codes, 13 and 14 the MMAs of chain 0 and 1, 15 the scales.
 //    Every wait is bounded; a role that gives up raises a shared abort flag, copies and
 //    MMAs in flight complete, the block frees its tensor memory (KVQ_ERRF_WAIT_TIMEOUT).
+//  * What bounds it.  Few rows: memory, once the batch is large; a chunk of 32 KB costs
+//    1,094 tensor cycles (two pieces of the query, all 128 rows), 1,460 at the measured
+//    copy rate, and takes 1,900: two chains in flight, whose score, softmax, product and
+//    their hand-overs follow one another, and five stages.  Window of 4,096 over 64 requests
+//    (421 MB): 89 us in a graph, 70% of the measured copy rate; trees of 8 nodes over 128
+//    requests (891 MB) 184 us, 71%.  kPair: a step of both chains costs 2,190 tensor cycles
+//    and takes 4,950; the softmax of a chain, 2,900 cycles of dependent instructions in one
+//    warp per scheduler, is as long as its products and the other chain's together, and no
+//    single part of it is the limit (without loading scales 554 us instead of 582, without
+//    exponentials 584, without the search for the largest 569, with a quarter of the
+//    conversion's stores 571).  4 x 2,048 rows of 32 / 8 heads, window 4,096: 586 us, half
+//    the measured bf16 product rate.  Small calls are latency: one row over 1,028 tokens 16 us:
+//    set-up 1, unit 2.4, pages 3.3, keys 4.2, queries 5.3, then three chunks, epilogue, and 4
+//    us of the join.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

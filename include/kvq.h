@@ -90,7 +90,8 @@ typedef enum kvq_status {
                                             > max_blocks_per_req * block_size          */
 #define KVQ_ERRF_WAIT_TIMEOUT 8          /* a bounded in-kernel wait for an async copy
                                             gave up; that CTA's outputs are not written
-                                            (kvq_prompt_attention: any rows of out)     */
+                                            (kvq_prompt_attention, _decode_window and
+                                            _decode_tree: any rows of out)              */
 #define KVQ_ERRF_POSITION_RANGE 16       /* token position outside the rotation table    */
 #define KVQ_ERRF_SEQUENCE_RANGE 32       /* a packed sequence's bounds decrease, leave the
                                             token buffer or pass max_seqlen               */
@@ -465,8 +466,9 @@ kvq_status kvq_prompt_attention(const void *q, int64_t q_token_stride,
  * request r, at position p = L_r - R + i, sees the cached tokens
  *     j <= p  with  j < num_sinks  or  j > p - window,
  * with the scores and weights of kvq_paged_decode; rows that see no token
- * (p < 0) are zero.  One launch; only the tokens that some row of a request
- * sees are read, so block-table entries of the others may hold anything (pages
+ * (p < 0) are zero.  Two launches (the second joins the rows whose tokens SMs have
+ * shared), for more than 1,024 requests two for every 1,024; capturable.  Only the
+ * tokens that some row of a request sees are read, so block-table entries of the others may hold anything (pages
  * given back, -1).  Tokens that a row does not see do not reach it, whatever
  * their slots hold; a NaN code in a value row that it does see makes that element
  * of its output NaN, or all of them.
@@ -504,8 +506,8 @@ kvq_status kvq_paged_decode_window(const kvq_cache *cache, const void *q,
  *     every token j < L_r - R  and  the nodes b whose bit is set in its mask,
  * with the scores and weights of kvq_paged_decode.  For a tree the mask holds a
  * node's ancestors and the node itself, but any mask is allowed; rows that see
- * no token are zero.  Nodes at negative positions (L_r < R) do not exist.  One
- * launch.  Tokens that a row does not see do not reach it, whatever their slots
+ * no token are zero.  Nodes at negative positions (L_r < R) do not exist.
+ * Launches as for kvq_paged_decode_window.  Tokens that a row does not see do not reach it, whatever their slots
  * hold.
  *   tree_mask       device int32 [num_requests, R, ceil(R / 32)]: bit b % 32 of
  *                   word b / 32 of row i is set where row i sees node b; bits of
