@@ -981,20 +981,18 @@ bool encode_code_tensor_map_strided(CUtensorMap *map, const uint8_t *codes, int6
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_plane_tensor_map(CUtensorMap *map, const uint8_t *codes, int64_t distance,
-                             int64_t num_slots, int H, int rows, int heads) {
+bool encode_plane_tensor_map(CUtensorMap *map, const uint8_t *codes, int64_t num_slots, int H,
+                             int rows, int heads) {
   EncodeTiledFn f = encode_tiled_fn();
-  if (f == nullptr) return false;
+  if (f == nullptr || heads > H || rows > num_slots) return false;
   const cuuint64_t row = static_cast<cuuint64_t>(H) * kHeadDim;
-  const cuuint32_t planes = distance > 0 ? 2u : 1u;
-  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(kHeadDim), 8u, planes,
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), 8u,
                               static_cast<cuuint64_t>(num_slots / 8), static_cast<cuuint64_t>(H)};
-  const cuuint64_t strides[4] = {row, distance > 0 ? static_cast<cuuint64_t>(distance) : row, 8 * row,
-                                 static_cast<cuuint64_t>(kHeadDim)};
-  const cuuint32_t box[5] = {static_cast<cuuint32_t>(kHeadDim), 8u, planes,
-                             static_cast<cuuint32_t>(rows / 8), static_cast<cuuint32_t>(heads)};
-  const cuuint32_t estride[5] = {1u, 1u, 1u, 1u, 1u};
-  return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t *>(codes), dims, strides, box,
+  const cuuint64_t strides[3] = {row, 8 * row, static_cast<cuuint64_t>(kHeadDim)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(kHeadDim), 8u, static_cast<cuuint32_t>(rows / 8),
+                             static_cast<cuuint32_t>(heads)};
+  const cuuint32_t estride[4] = {1u, 1u, 1u, 1u};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(codes), dims, strides, box,
            estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -116,13 +116,15 @@ struct MkShape {
   static constexpr int kTokLog2 = kRows == 32 ? 5 : (kRows == 64 ? 6 : 7);
   static constexpr int kQTiles = kPair ? 2 : 1;
   // shared memory, offsets from a 1024-byte aligned base
-  // Code stages of a chunk (8 rows of K, 8 of V, ...).  kPair: values are converted into two
+  // Code stages of a chunk.  kPair: values are converted into two
   // buffers of their own.  Else in place, over the chunk's key codes (which S has been made
   // of) and its value codes, so that five chunks are on their way or at work.
   static constexpr int kStages = kPair ? 2 : 5;
   static constexpr int kVfs = kPair ? 2 : kStages;
   static constexpr int kScales = kPair ? 6 : kStages;        // chunks of scales in their ring
-  static constexpr int kStage = 2 * kMkTok * kHeadDim;
+  static constexpr int kStage = 2 * kMkTok * kHeadDim;       // the chunk's K codes, then its V codes
+  static constexpr int kVOff = kMkTok * kHeadDim;
+  static constexpr int kGroup = 8 * kHeadDim;                // 8 rows
   static constexpr int kQPiece = 128 * kHeadDim;
   static constexpr int kOffQ = 0;                            // [tile][piece]
   static constexpr int kVfBytes = kMkTok * kHeadDim * 2;     // f16 values of a chunk
@@ -196,17 +198,13 @@ __device__ __forceinline__ void mk_mma_pv(uint32_t d, uint32_t a_tmem, uint32_t 
       :: "r"(d), "r"(a_tmem), "r"(b_lo), "n"(kMkIdescPV), "r"(acc), "r"(b_hi) : "memory");
 }
 
-// One box of a copy: 8 rows of K, 8 of V, 8 of K, ... of a head, from group z of 8 slots on.
+// One box of a copy: a plane's codes of some heads, from group z of 8 slots on.
 __device__ __forceinline__ void mk_load_box(uint32_t dst, const void *tmap, int z, int head,
                                             uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;\n"
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %2, %3, %4}], [%5], %6;\n"
       :: "r"(dst), "l"(tmap), "r"(0), "r"(z), "r"(head), "r"(bar), "l"(policy) : "memory");
-}
-
-__device__ __forceinline__ void mk_prefetch_map(const void *tmap) {
-  asm volatile("prefetch.tensormap [%0];\n" :: "l"(tmap) : "memory");
 }
 
 // One lane of the (converged) warp.
@@ -229,10 +227,8 @@ struct MkParams {
   int32_t T, HG;                                       // units of a request and group of heads, groups
   int32_t width;                                       // max_blocks_per_req
   int32_t ctx_limit, num_blocks, log2_bs, box;
+  int32_t box_heads;                                   // heads of a copy
   int32_t window, sinks, words;
-  // a stage: groups of 8 rows every `group` bytes, K's and V's first (one map over both
-  // planes: K and V in turns; two maps: all of K, then all of V)
-  int32_t group, k_off, v_off, two_maps;
   float scale2;                                        // |sm_scale| log2(e)
   uint32_t flip;                                       // sign bits of a negative sm_scale
   float *o_part;                                       // [grid][2][lanes of a unit][128]
@@ -725,10 +721,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
     fence_mbarrier_init();
   }
   if (tid == 0) *abort_s = 0;
-  if (tid == 32) {
-    mk_prefetch_map(&tm);
-    if (p.two_maps) mk_prefetch_map(&tm_v);
-  }
+  // (the maps are not prefetched: nothing can wait for that, and a block without work would
+  // leave it behind, a read of the launch's parameters that may outlive the launch)
   if (warp == kMkWarpLoad) {
     tmem_alloc(smem_addr(tmem_slot), kMkTmemCols);
     tmem_relinquish();
@@ -1029,14 +1023,14 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       if (!ok) return false;
       // (key j: box of 16 tokens and all heads, head, token)
       const int x = (u.c0 + k) * S::kTok + (S::kHeads == 1 ? j : 16 * (j / (16 * S::kHeads)) + (j & 15));
-      uint8_t *stage = smem + S::kOffKv + b * S::kStage + (j >> 3) * p.group + (j & 7) * 128;
-      const uint8_t *src = stage + p.v_off;
+      uint8_t *stage = smem + S::kOffKv + b * S::kStage + (j >> 3) * S::kGroup + (j & 7) * 128;
+      const uint8_t *src = stage + S::kVOff;
       uint8_t *dst = kPair ? smem + S::kOffVf + v * S::kVfBytes + j * 128 : stage;
-      const int block = kPair || p.two_maps != 0 ? S::kVfBytes / 2 : 1024;
+      constexpr int block = S::kVfBytes / 2;
       uint4 w[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + ((c ^ (j & 7)) << 4));
-      bool keep = x < u.X;
+      bool keep = x < u.X && (S::kHeads == 1 || (j >> 4) % S::kHeads < p.H - u.h);
       if (!whole) {
         uint32_t bad = 0u;
 #pragma unroll
@@ -1249,15 +1243,15 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         if (!ok) break;
         if (mk_elect()) {
           const uint32_t dst = smem_addr(smem + S::kOffKv) + b * S::kStage;
-          const uint32_t full = BAR(S::kKvFull + b), step = p.box * S::kHeads / 8 * p.group;
-          mbar_arrive_expect_tx(full, __popc(now) * 2 * p.box * S::kHeads * kHeadDim);
+          const uint32_t full = BAR(S::kKvFull + b), step = p.box * S::kHeads / 8 * S::kGroup;
+          mbar_arrive_expect_tx(full, __popc(now) * 2 * p.box * p.box_heads * kHeadDim);
 #pragma unroll 1
-          for (int plane = 0; plane <= p.two_maps; ++plane) {
+          for (int plane = 0; plane < 2; ++plane) {
             const CUtensorMap *map = plane == 0 ? &tm : &tm_v;
 #pragma unroll
             for (int i = 0; i < kBoxes; ++i)
               if ((now >> i) & 1u)
-                mk_load_box(dst + plane * p.v_off + i * step, map, z[i], uh, full, pol);
+                mk_load_box(dst + plane * S::kVOff + i * step, map, z[i], uh, full, pol);
           }
         }
         __syncwarp();
@@ -1408,11 +1402,11 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
       const int a = warp - kMkWarpMma;
       const uint32_t q1 = (smem_addr(smem + S::kOffQ + (kPair ? a : 0) * 2 * S::kQPiece) >> 4) | kMkKMajor;
       const uint32_t q2 = q1 + (S::kQPiece >> 4);
-      const uint32_t k0 = (smem_addr(smem + S::kOffKv + p.k_off) >> 4) | kMkKMajor;
-      const uint32_t k_hi = (static_cast<uint32_t>(p.group) >> 4) | (1u << 14) | (kSmemSwizzle128 << 29);
+      const uint32_t k0 = (smem_addr(smem + S::kOffKv) >> 4) | kMkKMajor;
+      const uint32_t k_hi = (static_cast<uint32_t>(S::kGroup) >> 4) | (1u << 14) | (kSmemSwizzle128 << 29);
       // (values: blocks of 64 dims, groups of 8 keys, by bytes)
-      const uint32_t v_group = kPair ? 1024u : static_cast<uint32_t>(p.group);
-      const uint32_t v_block = kPair || p.two_maps != 0 ? S::kVfBytes / 2 : 1024u;
+      constexpr uint32_t v_group = S::kGroup;
+      constexpr uint32_t v_block = S::kVfBytes / 2;
       const uint32_t v_hi = (v_group >> 4) | (1u << 14) | (kSmemSwizzle128 << 29), v_step = 2 * v_group >> 4;
       const uint32_t v0 = (smem_addr(smem + S::kOffVf) >> 4) | (v_block >> 4) << 16;
       const uint32_t s_col = tmem + mk_s(a), o_col = tmem + mk_o(a);
@@ -1667,27 +1661,16 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
   p.k_scales = c.k_scales;
   p.v_scales = c.v_scales;
   p.err_flags = a.err_flags;
-  // one map over both planes, whichever comes first in memory; planes that are too far
-  // apart for a map's stride have one each
-  const uint8_t *low = std::min(c.k_codes, c.v_codes), *high = std::max(c.k_codes, c.v_codes);
+  // Boxes no larger than the planes: of fewer KV heads than a unit has places, the others'
+  // keys are not loaded (their scores reach no row, their values are cleared).
+  p.box_heads = std::min(heads, H);
+  // A map per plane.  (One over both, with the planes' distance as a stride, would describe
+  // an array that spans memory between them which is not the cache's.)
   const int64_t slots = static_cast<int64_t>(p.num_blocks) << a.log2_block;
   CUtensorMap map, map_v;
-  p.two_maps = high - low < 128 || high - low >= (int64_t(1) << 40);
-  bool ok;
-  if (p.two_maps) {
-    ok = encode_plane_tensor_map(&map, c.k_codes, 0, slots, H, p.box, heads) &&
-         encode_plane_tensor_map(&map_v, c.v_codes, 0, slots, H, p.box, heads);
-    p.group = 1024;
-    p.k_off = 0;
-    p.v_off = kMkTok * kHeadDim;
-  } else {
-    ok = encode_plane_tensor_map(&map, low, high - low, slots, H, p.box, heads);
-    map_v = map;
-    p.group = 2048;
-    p.k_off = low == c.k_codes ? 0 : 1024;
-    p.v_off = 1024 - p.k_off;
-  }
-  if (!ok) return cudaErrorInvalidValue;
+  if (!encode_plane_tensor_map(&map, c.k_codes, slots, H, p.box, p.box_heads) ||
+      !encode_plane_tensor_map(&map_v, c.v_codes, slots, H, p.box, p.box_heads))
+    return cudaErrorInvalidValue;
   const int grid = a.sms;
   for (int r0 = 0; r0 < a.num_requests; r0 += kMkMaxRequests) {
     p.N = std::min(a.num_requests - r0, kMkMaxRequests);

@@ -484,3 +484,36 @@ def test_more_chunks_than_16_bits_count():
     got = window(on_gpu(c), torch.zeros(n, 1, 128, dtype=torch.bfloat16), tables, [most] * n, most, 0, 1)
     want = v.double().mean(0)
     assert bool(((got.cpu().double() - want).abs() <= (2.0 ** -8 + 2.0 ** -19) * want).all())
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 5])
+def test_few_heads_in_planes_far_apart(H):
+    # the planes' copies stay in their planes: fewer heads than a unit has places, a gap of
+    # other memory between the planes, the values' plane in front of the keys'
+    lens = [123, 1, 40]
+    c, tables = make(lens, H, 16, 107 + H)
+    q = queries(3, H, 107)
+    n = c["k_codes"].numel()
+    memory = torch.empty(1700 << 20, dtype=torch.uint8, device="cuda")
+    k, v = memory[-n:].view(c["k_codes"].shape), memory[:n].view(c["k_codes"].shape)
+    k.copy_(c["k_codes"])
+    v.copy_(c["v_codes"])
+    cache = kvq.Cache(k, v, c["k_scales"].cuda(), c["v_scales"].cuda(), 16)
+    want = plain.attention(c, q, tables, lens, 1, SCALE, plain.window_rule(5, 1))
+    for _ in range(20):
+        assert_close(window(cache, q, tables, lens, 5, 1, 1), want, lens)
+
+
+def test_small_calls_on_memory_that_changes():
+    # caches of few pages and heads, new tensors each time: equal results twice, all finite
+    g = torch.Generator().manual_seed(11)
+    for i in range(150):
+        H, G, R, n = (int(torch.randint(1, b, (1,), generator=g)) for b in (6, 5, 10, 4))
+        lens = [int(torch.randint(0, 300, (1,), generator=g)) for _ in range(n)]
+        c, tables = make(lens, H, 16, i)
+        q = queries(n * R, H * G, i)
+        cache = on_gpu(c)
+        a = window(cache, q, tables, lens, 50, 3, R, most=max(max(lens), 1))
+        b = tree(cache, q, random_mask(n, R, i), tables, lens, R, most=max(max(lens), 1))
+        again = window(cache, q, tables, lens, 50, 3, R, most=max(max(lens), 1))
+        assert torch.equal(a, again) and bool(torch.isfinite(a.float()).all() & torch.isfinite(b.float()).all())
