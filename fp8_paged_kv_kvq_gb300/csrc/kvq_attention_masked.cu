@@ -24,8 +24,9 @@
 //    (normalised output, reference, denominator) in the workspace, which a second
 //    launch joins, with all SMs (joined by the block whose piece came last, 175 rows in
 //    7 pieces took it 34 us).
-//  * Stages.  A chunk's K and V codes are copied by TMA, 8 rows of K and 8 of V in
-//    turns, 16 tokens (a tree's whole page) a copy.  kPair: two stages, values converted
+//  * Stages.  A chunk's K and V codes are copied by TMA, 16 tokens (of a tree and one head
+//    the whole page) and all the unit's heads a copy, boxes that lie within their plane but
+//    for heads behind its last.  kPair: two stages, values converted
 //    into two f16 buffers of their own.  Else five stages, values converted in place,
 //    over the chunk's own keys (once its scores are made) and codes: the copies in flight
 //    are what bounds a step's time with few rows (with separate buffers and three stages
@@ -63,7 +64,7 @@
 //    warp per scheduler, is as long as its products and the other chain's together, and no
 //    single part of it is the limit (without loading scales 554 us instead of 582, without
 //    exponentials 584, without the search for the largest 569, with a quarter of the
-//    conversion's stores 571).  4 x 2,048 rows of 32 / 8 heads, window 4,096: 586 us, half
+//    conversion's stores 571).  4 x 2,048 rows of 32 / 8 heads, window 4,096: 591 us, half
 //    the measured bf16 product rate.  Small calls are latency: one row over 1,028 tokens 16 us:
 //    set-up 1, unit 2.4, pages 3.3, keys 4.2, queries 5.3, then three chunks, epilogue, and 4
 //    us of the join.
