@@ -982,17 +982,21 @@ bool encode_code_tensor_map_strided(CUtensorMap *map, const uint8_t *codes, int6
 }
 
 bool encode_plane_tensor_map(CUtensorMap *map, const uint8_t *codes, int64_t num_slots, int H,
-                             int rows, int heads) {
+                             int first, int count, int rows, int heads) {
   EncodeTiledFn f = encode_tiled_fn();
-  if (f == nullptr || heads > H || rows > num_slots) return false;
+  if (f == nullptr || heads < 1 || count < heads || count % heads != 0 || first < 0 ||
+      first + count > H || rows > num_slots)
+    return false;
   const cuuint64_t row = static_cast<cuuint64_t>(H) * kHeadDim;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), 8u,
-                              static_cast<cuuint64_t>(num_slots / 8), static_cast<cuuint64_t>(H)};
+                              static_cast<cuuint64_t>(num_slots / 8),
+                              static_cast<cuuint64_t>(count)};
   const cuuint64_t strides[3] = {row, 8 * row, static_cast<cuuint64_t>(kHeadDim)};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(kHeadDim), 8u, static_cast<cuuint32_t>(rows / 8),
                              static_cast<cuuint32_t>(heads)};
   const cuuint32_t estride[4] = {1u, 1u, 1u, 1u};
-  return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(codes), dims, strides, box,
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+           const_cast<uint8_t *>(codes) + static_cast<int64_t>(first) * kHeadDim, dims, strides, box,
            estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

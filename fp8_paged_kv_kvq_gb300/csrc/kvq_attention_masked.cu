@@ -25,8 +25,8 @@
 //    launch joins, with all SMs (joined by the block whose piece came last, 175 rows in
 //    7 pieces took it 34 us).
 //  * Stages.  A chunk's K and V codes are copied by TMA, 16 tokens (of a tree and one head
-//    the whole page) and all the unit's heads a copy, boxes that lie within their plane but
-//    for heads behind its last.  kPair: two stages, values converted
+//    the whole page) and all the unit's heads a copy; of a last group of fewer heads the
+//    boxes are those heads wide, so that every box lies within its plane.  kPair: two stages, values converted
 //    into two f16 buffers of their own.  Else five stages, values converted in place,
 //    over the chunk's own keys (once its scores are made) and codes: the copies in flight
 //    are what bounds a step's time with few rows (with separate buffers and three stages
@@ -228,7 +228,7 @@ struct MkParams {
   int32_t T, HG;                                       // units of a request and group of heads, groups
   int32_t width;                                       // max_blocks_per_req
   int32_t ctx_limit, num_blocks, log2_bs, box;
-  int32_t box_heads;                                   // heads of a copy
+  int32_t tail;                                        // the first head of a last group of fewer heads, else H
   int32_t window, sinks, words;
   float scale2;                                        // |sm_scale| log2(e)
   uint32_t flip;                                       // sign bits of a negative sm_scale
@@ -237,6 +237,11 @@ struct MkParams {
   int4 *cuts;                                          // [grid]: the unit that block b is the first of several to work on
   int32_t *err_flags;
   int32_t least;                                       // positions of a block's range
+};
+
+// The planes' maps: whole groups of heads, and the last group's where it has fewer.
+struct MkMaps {
+  CUtensorMap k, v, k_tail, v_tail;
 };
 
 // m / G, m < 2^13: exact, since m (inv_g G - 2^32) < 2^26
@@ -683,8 +688,7 @@ __device__ __forceinline__ float mk_query_pieces(uint8_t *tile, int row, int c0,
 
 template <bool kPair, int kRows>
 __global__ void __launch_bounds__(kMkThreads, 1)
-attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
-                   const __grid_constant__ CUtensorMap tm_v) {
+attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
   using S = MkShape<kPair, kRows>;
   extern __shared__ uint8_t smem_raw[];
   // (an offset from the array, not a rounded address: the compiler keeps to shared memory)
@@ -1245,14 +1249,17 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ CUtensorMap tm,
         if (mk_elect()) {
           const uint32_t dst = smem_addr(smem + S::kOffKv) + b * S::kStage;
           const uint32_t full = BAR(S::kKvFull + b), step = p.box * S::kHeads / 8 * S::kGroup;
-          mbar_arrive_expect_tx(full, __popc(now) * 2 * p.box * p.box_heads * kHeadDim);
+          const bool tail = S::kHeads > 1 && uh >= p.tail;
+          const int head = tail ? 0 : uh, heads = tail ? p.H - p.tail : S::kHeads;
+          mbar_arrive_expect_tx(full, __popc(now) * 2 * p.box * heads * kHeadDim);
 #pragma unroll 1
           for (int plane = 0; plane < 2; ++plane) {
-            const CUtensorMap *map = plane == 0 ? &tm : &tm_v;
+            const CUtensorMap *map = plane == 0 ? (tail ? &maps.k_tail : &maps.k)
+                                                : (tail ? &maps.v_tail : &maps.v);
 #pragma unroll
             for (int i = 0; i < kBoxes; ++i)
               if ((now >> i) & 1u)
-                mk_load_box(dst + plane * S::kVOff + i * step, map, z[i], uh, full, pol);
+                mk_load_box(dst + plane * S::kVOff + i * step, map, z[i], head, full, pol);
           }
         }
         __syncwarp();
@@ -1583,8 +1590,7 @@ int mk_charge(int rows) { return rows > 128 ? MkShape<true, 128>::kCharge : MkSh
 int mk_heads(int rows) { return rows >= 128 ? 1 : 128 / rows; }
 
 template <bool kPair, int kRows>
-cudaError_t mk_launch(const MkParams &p, const CUtensorMap &map, const CUtensorMap &map_v, int grid,
-                      cudaStream_t stream) {
+cudaError_t mk_launch(const MkParams &p, const MkMaps &maps, int grid, cudaStream_t stream) {
   constexpr int kSmem = MkShape<kPair, kRows>::kSmem;
   const auto kernel = attn_masked_kernel<kPair, kRows>;
   static std::atomic<uint64_t> configured{0};
@@ -1598,7 +1604,7 @@ cudaError_t mk_launch(const MkParams &p, const CUtensorMap &map, const CUtensorM
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
   e = launch_overlapped(kernel, dim3(static_cast<unsigned>(grid)), dim3(kMkThreads), kSmem, stream, p,
-                        map, map_v);
+                        maps);
   if (e != cudaSuccess) return e;
   using S = MkShape<kPair, kRows>;
   const int rows = S::kHeads * std::min(p.M, S::kTileRows);
@@ -1662,15 +1668,19 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
   p.k_scales = c.k_scales;
   p.v_scales = c.v_scales;
   p.err_flags = a.err_flags;
-  // Boxes no larger than the planes: of fewer KV heads than a unit has places, the others'
-  // keys are not loaded (their scores reach no row, their values are cleared).
-  p.box_heads = std::min(heads, H);
-  // A map per plane.  (One over both, with the planes' distance as a stride, would describe
-  // an array that spans memory between them which is not the cache's.)
+  // A map per plane for the whole groups of heads, and one for a last group of fewer: the
+  // keys of its other places are not loaded (their scores reach no row, their values are
+  // cleared).
   const int64_t slots = static_cast<int64_t>(p.num_blocks) << a.log2_block;
-  CUtensorMap map, map_v;
-  if (!encode_plane_tensor_map(&map, c.k_codes, slots, H, p.box, p.box_heads) ||
-      !encode_plane_tensor_map(&map_v, c.v_codes, slots, H, p.box, p.box_heads))
+  const int last = H % heads;
+  p.tail = H - last;
+  MkMaps maps{};
+  if ((p.tail > 0 &&
+       (!encode_plane_tensor_map(&maps.k, c.k_codes, slots, H, 0, p.tail, p.box, heads) ||
+        !encode_plane_tensor_map(&maps.v, c.v_codes, slots, H, 0, p.tail, p.box, heads))) ||
+      (last > 0 &&
+       (!encode_plane_tensor_map(&maps.k_tail, c.k_codes, slots, H, p.tail, last, p.box, last) ||
+        !encode_plane_tensor_map(&maps.v_tail, c.v_codes, slots, H, p.tail, last, p.box, last))))
     return cudaErrorInvalidValue;
   const int grid = a.sms;
   for (int r0 = 0; r0 < a.num_requests; r0 += kMkMaxRequests) {
@@ -1688,10 +1698,10 @@ cudaError_t launch_attn_masked(const kvq_cache &c, const MaskedArgs &a, cudaStre
     p.o_part = reinterpret_cast<float *>(ws);
     ws += mk_round(slots_ws * kHeadDim * sizeof(float));
     p.ml_part = reinterpret_cast<float2 *>(ws);
-    const cudaError_t e = rows == 32    ? mk_launch<false, 32>(p, map, map_v, grid, stream)
-                          : rows == 64  ? mk_launch<false, 64>(p, map, map_v, grid, stream)
-                          : rows == 128 ? mk_launch<false, 128>(p, map, map_v, grid, stream)
-                                        : mk_launch<true, 128>(p, map, map_v, grid, stream);
+    const cudaError_t e = rows == 32    ? mk_launch<false, 32>(p, maps, grid, stream)
+                          : rows == 64  ? mk_launch<false, 64>(p, maps, grid, stream)
+                          : rows == 128 ? mk_launch<false, 128>(p, maps, grid, stream)
+                                        : mk_launch<true, 128>(p, maps, grid, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -183,11 +183,12 @@ bool encode_scale_tensor_map(CUtensorMap *map, const float *scales, int64_t num_
 bool encode_code_tensor_map_strided(CUtensorMap *map, const uint8_t *codes, int64_t num_slots,
                                     int H);
 
-// Tensor map over a code plane [num_slots, H, 128] uint8: boxes of `rows` slots (a multiple
-// of 8) of `heads` <= H heads (those past H are filled with 0), head by head in groups of 8
-// rows (coordinates: 0, 0, slot / 8, head), 128-byte swizzled.
+// Tensor map over `count` heads of a code plane [num_slots, H, 128] uint8, from head `first`
+// on: boxes of `rows` slots (a multiple of 8) of `heads` heads, head by head in groups of 8
+// rows (coordinates: 0, 0, slot / 8, head - first), 128-byte swizzled.  `heads` divides
+// `count`, so that no box passes the last head.
 bool encode_plane_tensor_map(CUtensorMap *map, const uint8_t *codes, int64_t num_slots, int H,
-                             int rows, int heads);
+                             int first, int count, int rows, int heads);
 
 // Tensor map over bf16 rows [num_tokens, heads, 128] with a token stride in
 // elements: boxes of `tokens` tokens of one head as two halves of 64 dims
