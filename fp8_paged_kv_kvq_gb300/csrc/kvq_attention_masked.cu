@@ -878,7 +878,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
           const uint16_t *bad_sc = reinterpret_cast<const uint16_t *>(bad_s + 4 * (S::kVfs + sc));
           const bool see_all = whole.at(k), edge = !all_whole.at(k);
           // where some row of the unit does not see all of the chunk, value rows with a NaN
-          // code or such a scale have been cleared
+          // code have been cleared (scales that are not finite in every chunk)
           if (edge) {
             ok = kPair ? mk_wait_all(BAR(S::kVfFull + seq % S::kVfs), (seq / S::kVfs) & 1, abort_s)
                        : mk_wait_all(BAR(S::kVfFull + a), edge_par, abort_s);
@@ -889,11 +889,11 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
             }
           }
           if (see_all) {
-            if (edge) {
+            if (edge || meta.w != 0.0f) {
 #pragma unroll 1
               for (int g = 0; g < 8 / S::kHeads; ++g) {
                 const int c = mk_col<S::kHeads>(g, hu) >> 4;
-                nan_row |= (bad[c] | (meta.w != 0.0f ? bad_sc[c] : 0)) != 0;
+                nan_row |= ((edge ? bad[c] : 0) | (meta.w != 0.0f ? bad_sc[c] : 0)) != 0;
               }
             }
             mk_softmax<S::kHeads, kPair>(scol, ocol, ks, meta, rowf, hu, fresh, ready, lane, row);
@@ -1289,8 +1289,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
       int slot = -1, eg = 0;
       const float *kp = p.k_scales, *vp = p.v_scales;
       int left = 0;                                    // tokens of the unit from the lane's first on
-      MkWhole all_whole{0, 0, 0};
-      uint32_t n = 0u, done = 0u, hist = 0u;           // hist: 2 bits a chunk: a unit's first, edge
+      uint32_t n = 0u, done = 0u, hist = 0u;           // hist: a bit a chunk: a unit's first
       bool more = ok;
 #pragma unroll 1
       for (;;) {
@@ -1309,7 +1308,6 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
             vp = p.v_scales + u.h + head_of;
             // (keys 4 lane ..: box, head, tokens from `tok` of the box on)
             left = head_of < p.H - u.h ? u.X - (u.c0 + kb) * S::kTok - box_of * p.box - tok_of : INT_MIN;
-            if (kb == 0) all_whole = mk_unit_whole<S>(p, u);
             next_kb = kb + per;
             if (next_kb >= un) {
               next_kb = 0;
@@ -1337,8 +1335,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
             cp_async_4(ks + i, kp + at + of, size);
             cp_async_4(ks + kMkTok + i, vp + at + of, size);
           }
-          const int k = kb + j;
-          hist = (hist << 2) | (k == 0 ? 1u : 0u) | (all_whole.at(k) ? 0u : 2u);
+          hist = (hist << 1) | (kb + j == 0 ? 1u : 0u);
           if (left > INT_MIN / 2) left -= S::kTok;
           ++j;
           ++n;
@@ -1355,24 +1352,23 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
         const float4 kk = ks[0];
         const float4 v4 = ks[kMkTok / 4];
         float vv[4] = {v4.x, v4.y, v4.z, v4.w}, lg[4];
-        const uint32_t what = hist >> (2 * (n - 1 - done));
+        const bool first_chunk = ((hist >> (n - 1 - done)) & 1u) != 0u;
+        // Scales that are not finite reach nobody by a product (an infinite one would put the
+        // references so high that every weight, and with them the denominator, is 0); rows that
+        // see them become NaN.
         float flagged = 0.0f;
-        if (what & 2u) {
-          // scales that are not finite reach nobody by a product; rows that see them become
-          // NaN
-          uint32_t bad = 0u;
+        uint32_t bad = 0u;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(vv[i] - vv[i] == 0.0f)) {
-              vv[i] = 0.0f;
-              bad |= 1u << i;
-            }
-          if (__any_sync(0xFFFFFFFFu, bad != 0u)) {
-            flagged = 1.0f;
-            if (lane < 4) bad_s[4 * (S::kVfs + b) + lane] = 0u;
-            __syncwarp();
-            if (bad != 0u) atomicOr(bad_s + 4 * (S::kVfs + b) + (lane >> 3), bad << (4 * (lane & 7)));
+        for (int i = 0; i < 4; ++i)
+          if (!(vv[i] - vv[i] == 0.0f)) {
+            vv[i] = 0.0f;
+            bad |= 1u << i;
           }
+        if (__any_sync(0xFFFFFFFFu, bad != 0u)) {
+          flagged = 1.0f;
+          if (lane < 4) bad_s[4 * (S::kVfs + b) + lane] = 0u;
+          __syncwarp();
+          if (bad != 0u) atomicOr(bad_s + 4 * (S::kVfs + b) + (lane >> 3), bad << (4 * (lane & 7)));
         }
         // (fmaxf leaves NaN out)
         const float km4 = fmaxf(fmaxf(kk.x, kk.y), fmaxf(kk.z, kk.w));
@@ -1380,7 +1376,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
         const uint32_t km = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(km4, 0.0f)));
         const uint32_t vm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(vm4, 0.0f)));
         const int ev = min(mk_ceil_log2(__uint_as_float(vm)), 126);
-        if (what & 1u) eg = min(ev, kMkMaxEg);
+        if (first_chunk) eg = min(ev, kMkMaxEg);
         else if (ev > eg) eg = min(ev + 2, kMkMaxEg);
         const float down = mk_pow2(-eg);
 #pragma unroll

@@ -6,7 +6,7 @@ import torch
 import fp8_paged_kv_kvq_gb300 as kvq
 import oracle.masked as plain
 from test_gpu_masked import (SCALE, assert_close, check_tree, check_window, make, on_gpu, queries, tree,
-                             window)
+                             window, words_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,44 @@ def test_last_groups_at_the_end_of_memory(H):
     mask = torch.tensor([[[0b001], [0b011], [0b101]]] * 2, dtype=torch.int32)
     assert_close(tree(cache, q, mask, tables, lens, R),
                  plain.attention(c, q, tables, lens, R, SCALE, plain.tree_rule(mask)), lens)
+
+
+def slot_of(tables, r, j, bs):
+    return int(tables[r, j // bs]) * bs + j % bs
+
+
+def heads_of(got, H):
+    """[rows, H, G, 128]"""
+    return got.cpu().view(got.shape[0], H, -1, 128)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("H,G,R", [(1, 1, 1), (1, 4, 2), (3, 5, 3), (4, 4, 8), (5, 4, 2), (2, 3, 11), (2, 4, 16), (1, 5, 13),
+                                   (2, 5, 20), (1, 4, 40), (2, 5, 64)])
+def test_value_scales_that_are_not_finite(H, G, R, value):
+    """One such scale, of a token that every row sees, in the first chunk, in later ones that every row
+    sees whole and in the last: no row that sees it is finite, all others (of other heads, requests and
+    branches) are right."""
+    bs, lens, h = 16, [300 + R, R, 141 + R], H // 2
+    c, tables = make(lens, H, bs, 511 + H)
+    q = queries(len(lens) * R, H * G, 13 * R + G)
+    bits = torch.zeros(len(lens), R, -(-R // 32) * 32, dtype=torch.int64)
+    for i in range(R):
+        bits[:, i, i] = 1
+        bits[:, i, i % 2:i:2] = 1
+    mask = words_of(bits)
+    rules = (plain.window_rule(10 ** 6, 0), plain.tree_rule(mask))
+    want = [plain.attention(c, q, tables, lens, R, SCALE, rule) for rule in rules]
+    for j, request in ((0, 0), (70, 0), (201, 2), (300 + R - 1, 0)):
+        j = min(j, lens[request] - 1)
+        was = c["v_scales"].clone()
+        c["v_scales"][slot_of(tables, request, j, bs), h] = value
+        cache = on_gpu(c)
+        c["v_scales"] = was
+        outs = (window(cache, q, tables, lens, 10 ** 6, 0, R), tree(cache, q, mask, tables, lens, R))
+        for got, ref, rule in zip(outs, want, rules):
+            hit = torch.zeros(len(lens) * R, H, dtype=torch.bool)
+            hit[request * R:(request + 1) * R, h] = rule(lens[request], R, request)[:, j]
+            rows = heads_of(got, H)
+            assert_close(rows[~hit], tuple(x.view(*rows.shape[:3], -1)[~hit] for x in ref), lens)
+            assert bool(hit.any()) and not bool(torch.isfinite(rows[hit]).any())
