@@ -45,10 +45,12 @@
 //    of tokens of value 0 stay finite) and at most 97.  A token that a row does not
 //    see can raise Eg to 30, no more, so that it costs no precision to rows of values
 //    above 2^-60.
-//  * Unseen tokens take no part: their scores are -infinity, their weights are set
-//    to 0 after the product with the scale (which may be NaN), and in chunks that
-//    some row of the unit does not see whole, value rows with a NaN code are cleared
-//    (0 times NaN is NaN) and noted; a row that does see one becomes NaN.
+//  * Unseen tokens take no part: their scores become -infinity before the exponential,
+//    value scales that are not finite become 0, and value rows with a NaN code are cleared
+//    (0 times NaN is NaN) in chunks that some row of the unit does not see whole and, where
+//    a unit has several heads, in all chunks, since the product runs over the other heads'
+//    keys with weights of 0.  What was cleared is noted, and a row that sees it becomes NaN:
+//    by its softmax warp, or, of a chunk that all rows see, by the epilogue for the head.
 //  * Roles, 512 threads: warps 0-3 and 4-7 the softmax of chain 0 and 1 (a thread owns
 //    a TMEM lane, a row), 8-11 the value codes' conversion and the epilogue, 12 the
 //    units and the copies of codes, 13 and 14 the MMAs of chain 0 and 1, 15 the scales.
@@ -139,13 +141,16 @@ struct MkShape {
   static constexpr int kOffUnit = kOffMeta + kScales * 16;
   static constexpr int kOffBad = kOffUnit + kMkUnits * static_cast<int>(sizeof(MkUnit));   // [Vf][4 words], [scales][4 words]
   static constexpr int kOffMisc = kOffBad + (kVfs + kScales) * 16;              // tmem base, abort
-  static constexpr int kOffScan = kOffMisc + 16;             // a warp's sum each
+  static constexpr int kOffNan = kOffMisc + 16;              // [unit, odd or even][warp] heads with a NaN
+  static constexpr int kOffScan = kOffNan + 2 * 4 * 4;       // a warp's sum each
   static constexpr int kOffPre = kOffScan + kMkThreads / 32 * 4;
   static constexpr int kOffBar = (kOffPre + (kMkMaxRequests + 1) * 4 + 7) / 8 * 8;
   static constexpr int kKvFull = 0;
   static constexpr int kKvEmpty = kKvFull + kStages;
   static constexpr int kVfFull = kKvEmpty + kStages;
-  static constexpr int kVfEmpty = kVfFull + 2;               // (kPair; else kVfFull: cleared values noted, per chain)
+  // (kPair; else kVfFull: cleared values of a chunk noted, per chain, kVfEmpty: those of a
+  // unit's whole chunks, odd and even units)
+  static constexpr int kVfEmpty = kVfFull + 2;
   static constexpr int kScFull = kVfEmpty + 2;
   static constexpr int kScEmpty = kScFull + kScales;
   static constexpr int kQFull = kScEmpty + kScales;        // per chain from here on
@@ -703,6 +708,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
   volatile float *ref_s = reinterpret_cast<volatile float *>(smem + S::kOffRef);
   volatile int *eg_s = reinterpret_cast<volatile int *>(smem + S::kOffEg);
   uint32_t *bad_s = reinterpret_cast<uint32_t *>(smem + S::kOffBad);
+  volatile uint32_t *nan_s = reinterpret_cast<volatile uint32_t *>(smem + S::kOffNan);
   int *pre = reinterpret_cast<int *>(smem + S::kOffPre);
 
   allow_dependents_launch();
@@ -710,7 +716,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
     uint32_t count = 1;
     const int i = tid;
     // commits of the chains that read it, and arrivals of the converting warps
-    if (i >= S::kVfEmpty && i < S::kVfEmpty + 2) count = 2;
+    if (i >= S::kVfEmpty && i < S::kVfEmpty + 2) count = kPair ? 2 : 4;
     if (i >= S::kVfFull && i < S::kVfFull + 2) count = 4;
     if (i >= S::kKvFull && i < S::kKvFull + S::kStages) count = kPair ? 1 : 2;   // copies, scales
     if (i >= S::kKvEmpty && i < S::kKvEmpty + S::kStages) count = kPair ? 4 + 2 : 1;
@@ -936,7 +942,13 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
       const int i = mk_query(p, m);
       return p.out + ((static_cast<int64_t>(r) * p.R + i) * p.Hq + h * p.G + (m - i * p.G)) * kHeadDim;
     };
-    auto epilogue = [&](const MkUnit &u) -> bool {
+    auto epilogue = [&](const MkUnit &u, int t) -> bool {
+      // heads that had a NaN code in a chunk that all rows see whole
+      uint32_t nan_heads = 0u;
+      if (S::kHeads > 1) {
+        if (!mk_wait_all(BAR(S::kVfEmpty + (t & 1)), (t >> 1) & 1, abort_s)) return false;
+        for (int i = 0; i < 4; ++i) nan_heads |= nan_s[4 * (t & 1) + i];
+      }
       const int64_t piece = static_cast<int64_t>(u.slot) * S::kLanes;
       const bool both = !kPair && u.n >= 2;
 #pragma unroll 1
@@ -958,6 +970,7 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
         const float w0 = m0 == -INFINITY ? 0.0f : mk_ex2(m0 - top), w1 = m1 == -INFINITY ? 0.0f : mk_ex2(m1 - top);
         float all = m0 == -INFINITY ? sum_s[128 * a + lane_row] : w0 * sum_s[128 * a + lane_row];
         if (both) all += m1 == -INFINITY ? sum_s[128 + lane_row] : w1 * sum_s[128 + lane_row];
+        if (S::kHeads > 1 && (nan_heads >> (lane_row / kRows)) & 1u) all = __uint_as_float(0x7FC00000u);
         const bool none = all == 0.0f;                 // (the row has seen nothing)
         const float f0 = w0 / all * mk_pow2(eg_s[a]), f1 = both ? w1 / all * mk_pow2(eg_s[1]) : 0.0f;
         const int head = u.h + (kPair ? 0 : lane_row / kRows);
@@ -1008,10 +1021,12 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
     };
     // chunk k of a unit, the seq-th of all: thread j converts key j, MN-major and 128-byte
     // swizzled, dims 0-63 and 64-127 in a block each; tokens past the unit's are cleared,
-    // and where some row does not see all of the chunk, values with a NaN code.  In place
-    // the blocks are the key's and the value's own codes, which one thread reads before it
-    // writes.
+    // and where some row does not see all of the chunk, values with a NaN code.  Of several
+    // heads all are: the product runs over the other heads' keys too, whose weights are 0.
+    // In place the blocks are the key's and the value's own codes, which one thread reads
+    // before it writes.
     const int j = lane_row;
+    uint32_t nan_heads = 0u;                           // of the warp's keys in whole chunks of the unit
     uint32_t chain_par = 0;                            // parity of chain a's chunks, bit a
     auto convert = [&](const MkUnit &u, int k, uint32_t seq, bool whole) -> bool {
       const uint32_t b = seq % S::kStages, v = seq % S::kVfs;
@@ -1036,18 +1051,26 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + ((c ^ (j & 7)) << 4));
       bool keep = x < u.X && (S::kHeads == 1 || (j >> 4) % S::kHeads < p.H - u.h);
-      if (!whole) {
+      if (S::kHeads > 1 || !whole) {
+        // (a NaN code is 0x7F but for its sign: one more carries into bit 7, and no further)
         uint32_t bad = 0u;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          bad |= __vcmpeq4(w[c].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w[c].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                 __vcmpeq4(w[c].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w[c].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        const uint32_t word = __ballot_sync(0xFFFFFFFFu, keep && bad != 0u);
-        if (lane == 0) {
-          bad_s[4 * v + q4] = word;
-          if (!kPair) mbar_arrive(BAR(S::kVfFull + (k & 1)));
+          bad |= ((w[c].x & 0x7F7F7F7Fu) + 0x01010101u) | ((w[c].y & 0x7F7F7F7Fu) + 0x01010101u) |
+                 ((w[c].z & 0x7F7F7F7Fu) + 0x01010101u) | ((w[c].w & 0x7F7F7F7Fu) + 0x01010101u);
+        const bool clear = (bad & 0x80808080u) != 0u;
+        const uint32_t word = __ballot_sync(0xFFFFFFFFu, keep && clear);
+        if (!whole) {
+          if (lane == 0) {
+            bad_s[4 * v + q4] = word;
+            if (!kPair) mbar_arrive(BAR(S::kVfFull + (k & 1)));
+          }
+        } else {
+          // (the warp's keys: 16 of a head, 16 of the next)
+          if ((word & 0xFFFFu) != 0u) nan_heads |= 1u << (2 * q4 % S::kHeads);
+          if ((word >> 16) != 0u) nan_heads |= 1u << ((2 * q4 + 1) % S::kHeads);
         }
-        keep = keep && bad == 0u;
+        keep = keep && !clear;
       }
       if (!keep) {
 #pragma unroll
@@ -1086,9 +1109,18 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
         if (un != 0) {
           gave_up = !convert(u, k, seq, all_whole.at(k));
           ++seq;
+          // (the slot of the unit before the last is read by now: this unit's first scores
+          // come after all warps' epilogues of it)
+          if (S::kHeads > 1 && k == un - 1) {
+            if (lane == 0) {
+              nan_s[4 * (t & 1) + q4] = nan_heads;
+              mbar_arrive(BAR(S::kVfEmpty + (t & 1)));
+            }
+            nan_heads = 0u;
+          }
         }
         if (k == 0 && last >= 0 && !gave_up) {
-          gave_up = !epilogue(unit_s[last % kMkUnits]);
+          gave_up = !epilogue(unit_s[last % kMkUnits], last);
           release_unit(last);
         }
       }

@@ -78,3 +78,89 @@ def test_value_scales_that_are_not_finite(H, G, R, value):
             rows = heads_of(got, H)
             assert_close(rows[~hit], tuple(x.view(*rows.shape[:3], -1)[~hit] for x in ref), lens)
             assert bool(hit.any()) and not bool(torch.isfinite(rows[hit]).any())
+
+
+def spoil(c, slot, h, how):
+    """A row of one head: one NaN code, or what the store makes of a row with a NaN."""
+    if how == "code":
+        c["v_codes"][slot, h, 5] = 0x7F
+    else:
+        for x in ("k", "v"):
+            c[x + "_codes"][slot, h] = 0x7F
+            c[x + "_scales"][slot, h] = float("nan")
+
+
+@pytest.mark.parametrize("how", ["code", "row"])
+@pytest.mark.parametrize("G,R", [(1, 1), (4, 2), (4, 8), (3, 11), (4, 16), (5, 13), (4, 40)])
+@pytest.mark.parametrize("H", [2, 3, 4, 5, 8])
+def test_what_one_head_holds_does_not_reach_the_others(H, G, R, how):
+    """A row of one head of a context token that every row sees, in a chunk that every row sees whole
+    (token 70 and 201) and in one that some rows do not (a drafted token): its own head's rows that see
+    it become NaN, all other rows are what they were (bit for bit where only a code
+    changed; a scale can move the power of two that a unit's weights are held over, which moves
+    roundings)."""
+    bs, lens, h = 16, [300 + R, R, 41 + R], H - 1 if H != 4 else 2
+    c, tables = make(lens, H, bs, 211 + H)
+    q = queries(len(lens) * R, H * G, 13 * R + G)
+    bits = torch.zeros(len(lens), R, -(-R // 32) * 32, dtype=torch.int64)
+    for i in range(R):
+        bits[:, i, i] = 1
+        bits[:, i, i % 2:i:2] = 1
+    mask = words_of(bits)
+    rules = (plain.window_rule(10 ** 6, 0), plain.tree_rule(mask))
+    want = [plain.attention(c, q, tables, lens, R, SCALE, rule) for rule in rules]
+
+    def calls(cache):
+        return window(cache, q, tables, lens, 10 ** 6, 0, R), tree(cache, q, mask, tables, lens, R)
+
+    clean = calls(on_gpu(c))
+    for j, request in ((70, 0), (201, 0), (300 + R - 1, 0), (41, 2)):
+        spoiled = {n: x.clone() if n != "block_size" else x for n, x in c.items()}
+        spoil(spoiled, slot_of(tables, request, j, bs), h, how)
+        for got, was, ref, rule in zip(calls(on_gpu(spoiled)), clean, want, rules):
+            sees = rule(lens[request], R, request)[:, j]
+            hit = torch.zeros(len(lens) * R, H, dtype=torch.bool)
+            hit[request * R:(request + 1) * R, h] = sees
+            rows, others = heads_of(got, H), ~hit
+            if how == "code":
+                assert torch.equal(rows[others], heads_of(was, H)[others])
+                assert bool(torch.isnan(rows[hit][..., 5]).all())
+            else:
+                assert_close(rows[others], tuple(x.view(*rows.shape[:3], -1)[others] for x in ref), lens)
+                assert bool(torch.isnan(rows[hit]).all())
+
+
+@pytest.mark.parametrize("H,G", [(4, 4), (5, 2), (2, 16)])
+def test_nan_of_one_of_many_units(H, G):
+    """Blocks with many units of one chunk and of several, one request and head of them with a NaN: the
+    units before and after it are what they were."""
+    bs = 16
+    lens = [(32, 64, 1, 100)[i % 4] for i in range(900)]
+    c, tables = make(lens, H, bs, 311)
+    q = queries(len(lens), H * G, 311)
+    clean = heads_of(window(on_gpu(c), q, tables, lens, 10 ** 6, 0, 1), H)
+    for request, j, h in ((0, 3, 0), (4, 31, H - 1), (441, 40, 1), (640, 0, H - 1), (899, 99, 0), (898, 0, 1)):
+        codes = c["v_codes"].clone()
+        c["v_codes"][slot_of(tables, request, j, bs), h, 5] = 0xFF
+        got = heads_of(window(on_gpu(c), q, tables, lens, 10 ** 6, 0, 1), H)
+        c["v_codes"] = codes
+        hit = torch.zeros(len(lens), H, dtype=torch.bool)
+        hit[request, h] = True
+        assert torch.equal(got[~hit], clean[~hit])
+        assert bool(torch.isnan(got[hit][..., 5]).all())
+
+
+def test_nan_in_pieces_of_a_split_unit():
+    """One request whose chunks are shared out over the whole GPU and joined."""
+    H, bs, lens = 6, 16, [9000]
+    c, tables = make(lens, H, bs, 401)
+    q = queries(3, 4 * H, 401)
+    clean = heads_of(window(on_gpu(c), q, tables, lens, 10 ** 6, 0, 3), H)
+    for j, h in ((0, 0), (4321, 2), (8000, 5), (8996, 4)):
+        codes = c["v_codes"].clone()
+        c["v_codes"][slot_of(tables, 0, j, bs), h, 5] = 0x7F
+        got = heads_of(window(on_gpu(c), q, tables, lens, 10 ** 6, 0, 3), H)
+        c["v_codes"] = codes
+        other = torch.arange(H) != h
+        assert torch.equal(got[:, other], clean[:, other])
+        assert bool(torch.isnan(got[:, h, :, 5]).all())
