@@ -29,19 +29,24 @@ __device__ __forceinline__ void flag(int32_t *err_flags, int32_t bit) {
 
 // Whether this block is the last of the grid to get here (all threads of the
 // block; the counter is 0 again afterwards).  What the blocks read and wrote
-// before is finished for the last one.
-__device__ bool last_block(int32_t *counter) {
-  __shared__ int last;
+// before is finished for the last one.  The counter's upper bits add up the
+// blocks' `mine` (thread 0's), its lower kBits count them; `all` gets the sum.
+template <int kBits>
+__device__ bool last_block(int32_t *counter, uint32_t mine, uint32_t *all) {
+  __shared__ uint32_t last, sum;
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    const int n = static_cast<int>(gridDim.x);
-    last = atomicAdd(counter, 1) == n - 1;
+    const uint32_t now =
+        atomicAdd(reinterpret_cast<uint32_t *>(counter), 1u + (mine << kBits)) + 1u + (mine << kBits);
+    last = (now & ((1u << kBits) - 1u)) == gridDim.x;
+    sum = now >> kBits;
     if (last) *counter = 0;
     __threadfence();
   }
   __syncthreads();
-  return last != 0;
+  *all = sum;
+  return last != 0u;
 }
 
 // Inclusive sums over a warp.
@@ -166,7 +171,8 @@ pages_free_kernel(const kvq_page_pool pool, const int32_t *tables, int32_t width
       }
     }
   }
-  if (!last_block(pool.state + 1)) return;
+  uint32_t none;
+  if (!last_block<31>(pool.state + 1, 0u, &none)) return;
   const int words = (pool.num_pages + 31) / 32;
   int num_free = min(max(pool.state[0], 0), pool.num_pages);
   uint32_t next = tid < words ? static_cast<uint32_t>(__ldcg(pool.marks + tid)) : 0u;
@@ -235,13 +241,20 @@ __global__ void __launch_bounds__(kPgThreads) pages_fork_kernel(const ForkParams
   allow_dependents_launch();
   grid_dependency_wait();
   const int num_free = min(max(p.pool.state[0], 0), p.pool.num_pages);
-  // children before this one that need a page
+  // Children before this one that take a page: for their parents' last ones, partly filled
+  // and the pool's.
+  auto held = [&](int page) -> bool { return page >= 0 && page < p.pool.num_pages; };
   int rank = 0;
   for (int j0 = 0; j0 < i; j0 += kPgThreads) {
     const int j = j0 + tid;
-    int len = 0;
-    if (j < i) fork_parent(p, j, &len);
-    rank += __syncthreads_count((len & (bs - 1)) != 0);
+    bool takes = false;
+    if (j < i) {
+      int l;
+      const int of = fork_parent(p, j, &l);
+      if ((l & (bs - 1)) != 0)
+        takes = held(p.tables[static_cast<int64_t>(of) * p.width + (l >> p.log2_bs)]);
+    }
+    rank += __syncthreads_count(takes);
   }
   int len;
   int parent = fork_parent(p, i, &len);
@@ -251,10 +264,11 @@ __global__ void __launch_bounds__(kPgThreads) pages_fork_kernel(const ForkParams
     else if (want >= 0) flag(p.err_flags, KVQ_ERRF_CONTEXT_RANGE);
   }
   const int rest = len & (bs - 1), full = len >> p.log2_bs;
-  if (rest != 0 && rank >= num_free) {
+  if (rest != 0 && rank >= num_free && held(p.tables[static_cast<int64_t>(parent) * p.width + full])) {
     if (part == 0 && tid == 0) flag(p.err_flags, KVQ_ERRF_NO_PAGES);
     parent = -1;
   }
+  bool takes = false;
   if (part == 0 && tid == 0) p.child_lens[i] = parent < 0 ? 0 : len;
   if (parent >= 0) {
     const int32_t *from = p.tables + static_cast<int64_t>(parent) * p.width;
@@ -263,17 +277,21 @@ __global__ void __launch_bounds__(kPgThreads) pages_fork_kernel(const ForkParams
       for (int k = tid; k < full; k += kPgThreads) {
         const int page = from[k];
         to[k] = page;
-        if (page >= 0 && page < p.pool.num_pages) atomicAdd(p.pool.ref_counts + page, 1);
+        if (held(page)) atomicAdd(p.pool.ref_counts + page, 1);
         else flag(p.err_flags, KVQ_ERRF_BLOCK_RANGE);
       }
     }
     if (rest != 0) {
-      const int src = from[full], dst = p.pool.free_pages[num_free - 1 - rank];
-      const bool ok = src >= 0 && src < p.pool.num_pages && dst >= 0 && dst < p.pool.num_pages;
+      // (a parent's page outside the pool is passed on.  Read here, not with the parent's
+      // length: with the read up there a fork 1 -> 8 took 2 us more)
+      const int src = from[full];
+      takes = held(src);
+      const int dst = takes ? p.pool.free_pages[num_free - 1 - rank] : src;
+      const bool ok = takes && held(dst);
       if (part == 0 && tid == 0) {
         to[full] = dst;
-        if (dst >= 0 && dst < p.pool.num_pages) p.pool.ref_counts[dst] = 1;
-        if (!ok) flag(p.err_flags, KVQ_ERRF_BLOCK_RANGE);
+        if (ok) p.pool.ref_counts[dst] = 1;
+        else flag(p.err_flags, KVQ_ERRF_BLOCK_RANGE);
       }
       if (ok) {
         // a page's rows lie one behind the other
@@ -287,15 +305,10 @@ __global__ void __launch_bounds__(kPgThreads) pages_fork_kernel(const ForkParams
       }
     }
   }
-  if (!last_block(p.pool.state + 1)) return;
-  int need = 0;
-  for (int j0 = 0; j0 < p.children; j0 += kPgThreads) {
-    const int j = j0 + tid;
-    int l = 0;
-    if (j < p.children) fork_parent(p, j, &l);
-    need += __syncthreads_count((l & (bs - 1)) != 0);
-  }
-  if (tid == 0) p.pool.state[0] = num_free - min(need, num_free);
+  // (at most 2^12 children, 2^12 blocks or a few an SM)
+  uint32_t taken;
+  if (!last_block<16>(p.pool.state + 1, takes && part == 0 ? 1u : 0u, &taken)) return;
+  if (tid == 0) p.pool.state[0] = num_free - static_cast<int>(taken);
 }
 
 // ---------------------------------------------------------------------------

@@ -612,7 +612,8 @@ kvq_status kvq_pages_free(const kvq_page_pool *pool, const int32_t *block_tables
  * num_parents or of a length outside [0, max_blocks_per_req * block_size], is no
  * child, as above, and sets KVQ_ERRF_NO_PAGES, KVQ_ERRF_PATH_RANGE or
  * KVQ_ERRF_CONTEXT_RANGE; a parent's page outside the pool sets
- * KVQ_ERRF_BLOCK_RANGE, is passed on as it is and neither counted nor copied.
+ * KVQ_ERRF_BLOCK_RANGE, is passed on as it is and neither counted nor copied (no
+ * page is taken for it, also where it is the last one and partly filled).
  * The cache holds the pool's pages (num_slots >= num_pages * block_size).
  * At most 4096 children. */
 kvq_status kvq_pages_fork(const kvq_cache *cache, const kvq_page_pool *pool,
