@@ -432,6 +432,12 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     return out
 
 
+def _int32(n: int) -> int:
+    """n, or the nearest number that 32 bits hold: ctypes would drop the upper bits of a
+    window that means all tokens (2**32 + 5: five)."""
+    return n if -0x80000000 <= n <= 0x7FFFFFFF else (0x7FFFFFFF if n > 0 else -0x80000000)
+
+
 def _masked_args(cache: Cache, q, block_tables, context_lens, R: int):
     """Requests, query heads, KV heads and table width of a windowed or tree call."""
     if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
@@ -472,7 +478,7 @@ def paged_decode_window_workspace_size(num_requests: int, rows_per_request: int,
                                        num_sinks: int = 0) -> int:
     return load().kvq_paged_decode_window_workspace_size(
         num_requests, rows_per_request, num_q_heads, num_kv_heads, head_dim, block_size,
-        max_context_len, window, num_sinks)
+        _int32(max_context_len), _int32(window), _int32(num_sinks))
 
 
 def paged_decode_window(cache: Cache, q: torch.Tensor, block_tables: torch.Tensor,
@@ -487,6 +493,7 @@ def paged_decode_window(cache: Cache, q: torch.Tensor, block_tables: torch.Tenso
     paged_decode_window_workspace_size) are allocated here when not given."""
     R = rows_per_request
     n, hq, h, width = _masked_args(cache, q, block_tables, context_lens, R)
+    max_context_len, window, num_sinks = _int32(max_context_len), _int32(window), _int32(num_sinks)
     lib = load()
     size = 0 if workspace is not None else lib.kvq_paged_decode_window_workspace_size(
         n, R, hq, h, 128, cache.block_size, max_context_len, window, num_sinks)
@@ -509,7 +516,7 @@ def paged_decode_tree_workspace_size(num_requests: int, rows_per_request: int, n
                                      max_context_len: int) -> int:
     return load().kvq_paged_decode_tree_workspace_size(
         num_requests, rows_per_request, num_q_heads, num_kv_heads, head_dim, block_size,
-        max_context_len)
+        _int32(max_context_len))
 
 
 def paged_decode_tree(cache: Cache, q: torch.Tensor, tree_mask: torch.Tensor,
@@ -525,6 +532,7 @@ def paged_decode_tree(cache: Cache, q: torch.Tensor, tree_mask: torch.Tensor,
     R = rows_per_request
     n, hq, h, width = _masked_args(cache, q, block_tables, context_lens, R)
     _flat(tree_mask, "tree_mask", torch.int32, n * R * ((R + 31) // 32))
+    max_context_len = _int32(max_context_len)
     lib = load()
     size = 0 if workspace is not None else lib.kvq_paged_decode_tree_workspace_size(
         n, R, hq, h, 128, cache.block_size, max_context_len)

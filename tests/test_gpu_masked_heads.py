@@ -164,3 +164,13 @@ def test_nan_in_pieces_of_a_split_unit():
         other = torch.arange(H) != h
         assert torch.equal(got[:, other], clean[:, other])
         assert bool(torch.isnan(got[:, h, :, 5]).all())
+
+
+@pytest.mark.parametrize("w,sinks", [(2 ** 32 + 5, 0), (2 ** 40, 2 ** 32 + 1), (10 ** 12, 10 ** 10), (7, 2 ** 33)])
+def test_windows_and_sinks_beyond_32_bits(w, sinks):
+    """Numbers that mean every token, whatever their lower 32 bits are."""
+    lens, H, R = [200, 33], 2, 2
+    c, tables = make(lens, H, 16, 601)
+    q = queries(len(lens) * R, 4, 601)
+    assert_close(window(on_gpu(c), q, tables, lens, w, sinks, R),
+                 plain.attention(c, q, tables, lens, R, SCALE, plain.window_rule(10 ** 6, 0)), lens)
