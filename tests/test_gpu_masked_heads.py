@@ -5,8 +5,8 @@ import torch
 
 import fp8_paged_kv_kvq_gb300 as kvq
 import oracle.masked as plain
-from test_gpu_masked import (SCALE, assert_close, check_tree, check_window, make, on_gpu, queries, tree,
-                             window, words_of)
+from test_gpu_masked import (SCALE, assert_close, check_tree, check_window, make, on_gpu, queries,
+                             random_mask, tree, window, words_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -174,3 +174,43 @@ def test_windows_and_sinks_beyond_32_bits(w, sinks):
     q = queries(len(lens) * R, 4, 601)
     assert_close(window(on_gpu(c), q, tables, lens, w, sinks, R),
                  plain.attention(c, q, tables, lens, R, SCALE, plain.window_rule(10 ** 6, 0)), lens)
+
+
+@pytest.mark.parametrize("H,G,R", [(2, 5, 40), (3, 4, 40), (5, 2, 65), (4, 8, 64), (2, 1, 300), (3, 16, 9), (2, 64, 2)])
+def test_row_tiles_of_several_heads(H, G, R):
+    """From 128 stacked rows on: units of one or two row tiles, a unit per head and tile."""
+    lens = [R + 500, R, 0, R + 70]
+    check_window(lens, H, H * G, R, 200, 5, seed=H * R)
+    check_window(lens, H, H * G, R, 33, 0, bs=64, seed=H + R)
+    check_tree(lens, H, H * G, R, seed=G * R)
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("H,G,R", [(1, 4, 20), (3, 4, 32), (2, 8, 17), (2, 4, 70), (1, 16, 33)])
+def test_trees_over_large_pages(bs, H, G, R):
+    """Trees of one head a unit, whose copies bring whole pages (of at most 128 tokens): pages that end
+    inside a chunk, at its end and behind it, and contexts that end in each of their parts."""
+    for lens in ([R + 4 * bs, R + bs - 1, R], [R + 3 * bs + 1, 700 + R, R + 2 * bs + 17], [R + 1, R + 127, R + 128]):
+        check_tree(lens, H, H * G, R, bs=bs, seed=bs + R + len(lens))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_small_calls_of_all_shapes(seed):
+    """Random heads, groups, rows, pages and lengths, new tensors each time, each call twice."""
+    g = torch.Generator().manual_seed(700 + seed)
+
+    def one(*values):
+        return values[int(torch.randint(0, len(values), (1,), generator=g))]
+
+    for i in range(12):
+        H, G, R, n = one(1, 2, 3, 4, 5, 6, 7, 9), one(1, 2, 3, 4, 7), one(1, 1, 2, 3, 5, 9, 10, 17, 40), one(1, 2, 3)
+        bs, w, sinks = one(16, 32, 64), one(1, 16, 50, 1000), one(0, 1, 3, 40)
+        lens = [one(0, R - 1, R, R + 31, R + int(torch.randint(0, 300, (1,), generator=g))) for _ in range(n)]
+        c, tables = make(lens, H, bs, 1000 * seed + i)
+        q, mask, most = queries(n * R, H * G, i), random_mask(n, R, i), max(max(lens), 1)
+        cache = on_gpu(c)
+        for call, rule in ((lambda: window(cache, q, tables, lens, w, sinks, R, most=most), plain.window_rule(w, sinks)),
+                           (lambda: tree(cache, q, mask, tables, lens, R, most=most), plain.tree_rule(mask))):
+            got = call()
+            assert_close(got, plain.attention(c, q, tables, lens, R, SCALE, rule), lens)
+            assert torch.equal(got, call())
