@@ -899,7 +899,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
 #pragma unroll 1
               for (int g = 0; g < 8 / S::kHeads; ++g) {
                 const int c = mk_col<S::kHeads>(g, hu) >> 4;
-                nan_row |= ((edge ? bad[c] : 0) | (meta.w != 0.0f ? bad_sc[c] : 0)) != 0;
+                if (edge) nan_row |= bad[c] != 0;
+                if (meta.w != 0.0f) nan_row |= bad_sc[c] != 0;
               }
             }
             mk_softmax<S::kHeads, kPair>(scol, ocol, ks, meta, rowf, hu, fresh, ready, lane, row);
