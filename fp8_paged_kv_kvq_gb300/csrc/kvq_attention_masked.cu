@@ -43,8 +43,8 @@
 //    log2 so far but at most 30, so that no weight or sum leaves binary32: weights
 //    reach 2^(14 - lg) for a scale of 2^(Eg + lg), with lg taken as at least -90 (sums
 //    of tokens of value 0 stay finite) and at most 97.  A token that a row does not
-//    see can raise Eg to 30, no more, so that it costs no precision to rows of values
-//    above 2^-60.
+//    see, or one of another head of the unit, can raise Eg to 30, no more, so that it costs
+//    no precision to rows of values above 2^-60 (it can move the roundings of others).
 //  * Unseen tokens take no part: their scores become -infinity before the exponential,
 //    value scales that are not finite become 0, and value rows with a NaN code are cleared
 //    (0 times NaN is NaN) in chunks that some row of the unit does not see whole and, where
@@ -58,18 +58,22 @@
 //    MMAs in flight complete, the block frees its tensor memory (KVQ_ERRF_WAIT_TIMEOUT).
 //  * What bounds it.  Few rows: memory, once the batch is large; a chunk of 32 KB costs
 //    1,094 tensor cycles (two pieces of the query, all 128 rows), 1,460 at the measured
-//    copy rate, and takes 1,900: two chains in flight, whose score, softmax, product and
+//    copy rate, and takes some 1,850: two chains in flight, whose score, softmax, product and
 //    their hand-overs follow one another, and five stages.  Window of 4,096 over 64 requests
-//    (421 MB): 89 us in a graph, 70% of the measured copy rate; trees of 8 nodes over 128
-//    requests (891 MB) 184 us, 71%.  kPair: a step of both chains costs 2,190 tensor cycles
-//    and takes 4,950; the softmax of a chain, 2,900 cycles of dependent instructions in one
-//    warp per scheduler, is as long as its products and the other chain's together, and no
-//    single part of it is the limit (without loading scales 554 us instead of 582, without
-//    exponentials 584, without the search for the largest 569, with a quarter of the
-//    conversion's stores 571).  4 x 2,048 rows of 32 / 8 heads, window 4,096: 591 us, half
-//    the measured bf16 product rate.  Small calls are latency: one row over 1,028 tokens 16 us:
-//    set-up 1, unit 2.4, pages 3.3, keys 4.2, queries 5.3, then three chunks, epilogue, and 4
-//    us of the join.
+//    (421 MB): 87 us replayed in a graph, 72% of the measured copy rate, 89 us and 70% in calls
+//    on other inputs each time; trees of 8 nodes over 128 requests (891 MB) 180 us and 73%, 190
+//    us and 69%.  That is this form's limit, not the operator's: attn_stream_kernel copies the
+//    same boxes for at most 8 stacked rows at 77%.  kPair: a step of both chains costs 2,190
+//    tensor cycles and takes some 5,000; the softmax of a chain, 2,900 cycles of dependent
+//    instructions in one warp per scheduler, is as long as its products and the other chain's
+//    together, and no single part of it is the limit (taken out of a form of 582 us: loading
+//    scales 554, exponentials 584, the search for the largest 569, three quarters of the
+//    conversion's stores 571).  The nearest limit is instruction fetch (84% of its peak, 90% of
+//    requests hit): layouts of the same code differ by several percent.  4 x 2,048 rows of 32 /
+//    8 heads, window 4,096: 596 us in a graph, 48% of the measured bf16 product rate.  Small
+//    calls are latency: one row over 1,028 tokens 16 us: set-up 1, unit 2.4, pages 3.3, keys
+//    4.2, queries 5.3, then three chunks, epilogue, and 4 us of the join, a second launch that
+//    every call makes.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -732,8 +736,8 @@ attn_masked_kernel(const MkParams p, const __grid_constant__ MkMaps maps) {
     fence_mbarrier_init();
   }
   if (tid == 0) *abort_s = 0;
-  // (the maps are not prefetched: nothing can wait for that, and a block without work would
-  // leave it behind, a read of the launch's parameters that may outlive the launch)
+  // (The maps are not prefetched: a form that did, with other maps, faulted now and then for a
+  // reason that was not found.)
   if (warp == kMkWarpLoad) {
     tmem_alloc(smem_addr(tmem_slot), kMkTmemCols);
     tmem_relinquish();

@@ -468,10 +468,11 @@ kvq_status kvq_prompt_attention(const void *q, int64_t q_token_stride,
  * with the scores and weights of kvq_paged_decode; rows that see no token
  * (p < 0) are zero.  Two launches (the second joins the rows whose tokens SMs have
  * shared), for more than 1,024 requests two for every 1,024; capturable.  Only the
- * tokens that some row of a request sees are read, so block-table entries of the others may hold anything (pages
- * given back, -1).  Tokens that a row does not see do not reach it, whatever
- * their slots hold; a NaN code in a value row that it does see makes that element
- * of its output NaN, or all of them.
+ * tokens that some row of a request sees are read, so block-table entries of the
+ * others may hold anything (pages given back, -1).  Tokens that a row does not see,
+ * and other KV heads than its own, do not reach it, whatever their slots hold.  A NaN
+ * code in a value row that it does see makes that element of its output NaN, or all
+ * of them; a value scale that is not finite makes all of them NaN.
  *   rows_per_request R >= 1, R * num_q_heads / num_kv_heads <= 8192: a decode or
  *                   verify step, a chunk of a prompt
  *   window          >= 1, the row's own token included
@@ -507,8 +508,7 @@ kvq_status kvq_paged_decode_window(const kvq_cache *cache, const void *q,
  * with the scores and weights of kvq_paged_decode.  For a tree the mask holds a
  * node's ancestors and the node itself, but any mask is allowed; rows that see
  * no token are zero.  Nodes at negative positions (L_r < R) do not exist.
- * Launches as for kvq_paged_decode_window.  Tokens that a row does not see do not reach it, whatever their slots
- * hold.
+ * Launches, and what NaN and infinities reach, as for kvq_paged_decode_window.
  *   tree_mask       device int32 [num_requests, R, ceil(R / 32)]: bit b % 32 of
  *                   word b / 32 of row i is set where row i sees node b; bits of
  *                   nodes >= R are ignored
